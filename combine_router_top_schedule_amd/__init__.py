@@ -55,6 +55,36 @@ class MokSizes(ctypes.Structure):
 
 _P = ctypes.c_void_p
 
+MOK_ELEM_F32, MOK_ELEM_BF16 = 0, 1
+MOK_SCORE_SOFTMAX, MOK_SCORE_SIGMOID = 0, 1
+MOK_GROUP_MAX, MOK_GROUP_TOP2 = 0, 1
+MOK_STATE_F32, MOK_STATE_MX8 = 0, 1
+
+
+class MokRouteDesc(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int64), ("logits_stride", ctypes.c_int64),
+                ("num_experts", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("score", ctypes.c_int32), ("num_groups", ctypes.c_int32),
+                ("top_groups", ctypes.c_int32), ("group_score", ctypes.c_int32),
+                ("renorm", ctypes.c_int32), ("elem", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class MokSumsqTensor(ctypes.Structure):
+    _fields_ = [("g", _P), ("n", ctypes.c_int64)]
+
+
+class MokAdamwTensor(ctypes.Structure):
+    _fields_ = [("p", _P), ("copy", _P), ("g", _P), ("m", _P), ("v", _P), ("m_scale", _P),
+                ("v_scale", _P), ("n", ctypes.c_int64)]
+
+
+class MokAdamwConfig(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double),
+                ("max_norm", ctypes.c_double), ("step", ctypes.c_int64), ("seed", ctypes.c_uint32),
+                ("grad_elem", ctypes.c_int32), ("param_elem", ctypes.c_int32),
+                ("state", ctypes.c_int32), ("sumsq_dev", _P), ("lr_dev", _P), ("step_dev", _P)]
+
 
 class MokWeights(ctypes.Structure):
     _fields_ = [(n, _P) for n in ("wg", "wu", "wd", "wg_q", "wg_s", "wu_q", "wu_s", "wd_q",
@@ -109,6 +139,11 @@ _SIGS = {
                                     ctypes.POINTER(MokDesc), ctypes.POINTER(ctypes.c_float),
                                     ctypes.POINTER(MokTuneResult), ctypes.c_int32,
                                     ctypes.POINTER(ctypes.c_int32)]),
+    "mok_route_fwd": (ctypes.c_int, [ctypes.POINTER(MokRouteDesc), _P, _P, _P, _P, _P, _P, _P]),
+    "mok_route_bwd": (ctypes.c_int, [ctypes.POINTER(MokRouteDesc), _P, _P, _P, _P, _P]),
+    "mok_sumsq_ws_size": (ctypes.c_int, [ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)]),
+    "mok_grad_sumsq": (ctypes.c_int, [ctypes.c_int32, _P, ctypes.c_int32, _P, _P, _P]),
+    "mok_adamw": (ctypes.c_int, [ctypes.c_int32, _P, ctypes.POINTER(MokAdamwConfig), _P]),
     "mok_device_cus": (ctypes.c_int32, []),
     "mok_trace_kernel": (ctypes.c_int, [ctypes.c_int32, _P, _P]),
 }
@@ -362,3 +397,216 @@ def mok_trace_kernel(kernel: int, before=None, after=None):
     b = None if before is None else int(before.cuda_event)
     a = None if after is None else int(after.cuda_event)
     _check("mok_trace_kernel", lib().mok_trace_kernel(int(kernel), b, a))
+
+
+# ------------------------------------------------------------------------ expert routing
+
+def route_desc(E: int, K: int, score: str = "softmax", groups: int = 1, top_groups: int = 1,
+               group_score: str = "max", renorm: bool = True, scale: float = 1.0) -> MokRouteDesc:
+    """What stays the same from call to call of mok_route_fwd / mok_route_bwd: experts, choices per
+    token, score ("softmax" or "sigmoid"), groups of experts ("max" or "top2" scored) and weights.
+    The tokens, their row stride and type are taken from the logits of each call."""
+    return MokRouteDesc(0, E, E, K, {"softmax": MOK_SCORE_SOFTMAX, "sigmoid": MOK_SCORE_SIGMOID}[score],
+                        groups, top_groups, {"max": MOK_GROUP_MAX, "top2": MOK_GROUP_TOP2}[group_score],
+                        int(renorm), MOK_ELEM_F32, scale)
+
+
+def _elem(t, name: str) -> int:
+    import torch
+    if t.dtype == torch.float32:
+        return MOK_ELEM_F32
+    if t.dtype == torch.bfloat16:
+        return MOK_ELEM_BF16
+    raise ValueError(f"{name} must be float32 or bfloat16, not {t.dtype}")
+
+
+def _want(t, name: str, dtype: str, shape, device):
+    import torch
+    if t.dtype != getattr(torch, dtype) or t.numel() != _count(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {shape}, not {t.dtype} "
+                         f"{tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _count(shape):
+    n = 1
+    for v in shape:
+        n *= v
+    return n
+
+
+class _on_device:
+    """Makes `device` current around a call (the library launches on the current device) and gives the
+    stream to use: the one asked for, or the device's current one."""
+
+    def __init__(self, device, stream):
+        import torch
+        if stream is not None and stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+        self.stream = stream
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return _stream(self.stream)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _route_call(d: MokRouteDesc, logits, topk_idx) -> MokRouteDesc:
+    """`d` for these logits [N][E] (rows may be strided)."""
+    N, E = logits.shape
+    if E != d.num_experts:
+        raise ValueError(f"logits have {E} columns, the descriptor {d.num_experts} experts")
+    if (E > 1 and logits.stride(1) != 1) or (N > 1 and logits.stride(0) < E):
+        raise ValueError("logits rows must be contiguous and must not overlap")
+    _want(topk_idx, "topk_idx", "int32", (N, d.top_k), logits.device)
+    return MokRouteDesc(N, logits.stride(0) if N > 1 else E, E, d.top_k, d.score, d.num_groups,
+                        d.top_groups, d.group_score, d.renorm, _elem(logits, "logits"), d.scale)
+
+
+def mok_route_fwd(d: MokRouteDesc, logits, topk_idx, topk_w, bias=None, token_mask=None, load=None,
+                  stream=None):
+    _need_cuda(logits, topk_idx, topk_w, bias, token_mask, load)
+    c, dev = _route_call(d, logits, topk_idx), logits.device
+    _want(topk_w, "topk_w", "float32", (c.num_tokens, c.top_k), dev)
+    if bias is not None:
+        _want(bias, "bias", "float32", (c.num_experts,), dev)
+    if token_mask is not None:
+        import torch
+        if token_mask.dtype == torch.bool:
+            token_mask = token_mask.view(torch.uint8)
+        _want(token_mask, "token_mask", "uint8", (c.num_tokens,), dev)
+    if load is not None:
+        _want(load, "load", "int32", (c.num_experts,), dev)
+    with _on_device(dev, stream) as s:
+        _check("mok_route_fwd", lib().mok_route_fwd(ctypes.byref(c), _ptr(logits), _ptr(bias),
+                                                    _ptr(token_mask), _ptr(topk_idx), _ptr(topk_w),
+                                                    _ptr(load), s))
+
+
+def mok_route_bwd(d: MokRouteDesc, logits, topk_idx, dw, dlogits, stream=None):
+    _need_cuda(logits, topk_idx, dw, dlogits)
+    c, dev = _route_call(d, logits, topk_idx), logits.device
+    _want(dw, "dw", "float32", (c.num_tokens, c.top_k), dev)
+    _want(dlogits, "dlogits", str(logits.dtype).replace("torch.", ""), tuple(logits.shape), dev)
+    with _on_device(dev, stream) as s:
+        _check("mok_route_bwd", lib().mok_route_bwd(ctypes.byref(c), _ptr(logits), _ptr(topk_idx),
+                                                    _ptr(dw), _ptr(dlogits), s))
+
+
+# ------------------------------------------------------------------------ the optimizer step
+
+class SumsqPlan:
+    """The tensors of a mok_grad_sumsq call, and scratch for it."""
+
+    def __init__(self, grads):
+        import torch
+        if not grads:
+            raise ValueError("no tensors")
+        _need_cuda(*grads)
+        self.keep, self.device, self.elem = list(grads), grads[0].device, _elem(grads[0], "a gradient")
+        for g in grads:
+            if g.dtype != grads[0].dtype:
+                raise ValueError("gradients of one call have one type")
+            _want(g, "a gradient", str(g.dtype).replace("torch.", ""), tuple(g.shape), self.device)
+        self.table = (MokSumsqTensor * len(grads))(*[MokSumsqTensor(g.data_ptr(), g.numel()) for g in grads])
+        n = ctypes.c_size_t()
+        _check("mok_sumsq_ws_size", lib().mok_sumsq_ws_size(len(grads), ctypes.byref(n)))
+        self.ws = torch.empty(int(n.value), dtype=torch.uint8, device=self.device)
+
+
+def sumsq_plan(grads) -> SumsqPlan:
+    return SumsqPlan(grads)
+
+
+def mok_grad_sumsq(plan: SumsqPlan, out, ws=None, stream=None):
+    """out (float64 [1]) = sum of squares over every tensor of the plan. Calls that may overlap in time
+    need scratch `ws` of their own (as large as plan.ws, which is used without it)."""
+    _need_cuda(out, ws)
+    _want(out, "out", "float64", (1,), plan.device)
+    if ws is not None:
+        if ws.numel() * ws.element_size() < plan.ws.numel():
+            raise ValueError(f"ws must hold {plan.ws.numel()} bytes")
+        _want(ws, "ws", str(ws.dtype).replace("torch.", ""), tuple(ws.shape), plan.device)
+    with _on_device(plan.device, stream) as s:
+        _check("mok_grad_sumsq", lib().mok_grad_sumsq(len(plan.table), plan.table, plan.elem, _ptr(out),
+                                                      _ptr(plan.ws if ws is None else ws), s))
+
+
+class AdamwPlan:
+    """The tensors of a mok_adamw call, checked once: lists of equal length of parameters (float32 or
+    bfloat16), gradients (float32 or bfloat16), moments (float32; or uint8 E4M3 codes, with their uint8
+    scales of 32 elements in m_scale and v_scale) and, for float32 parameters, bfloat16 copies."""
+
+    def __init__(self, p, g, m, v, copy=None, m_scale=None, v_scale=None):
+        import torch
+        if not p:
+            raise ValueError("no tensors")
+        if (m_scale is None) != (v_scale is None):
+            raise ValueError("m_scale and v_scale go together")
+        mx = m_scale is not None
+        lists = dict(p=p, g=g, m=m, v=v, copy=copy, m_scale=m_scale, v_scale=v_scale)
+        for name, ts in lists.items():
+            if ts is not None and len(ts) != len(p):
+                raise ValueError(f"{name} has {len(ts)} tensors, p {len(p)}")
+        self.keep = {k: list(ts) for k, ts in lists.items() if ts is not None}
+        _need_cuda(*[t for ts in self.keep.values() for t in ts])
+        self.device = p[0].device
+        self.param, self.grad = _elem(p[0], "a parameter"), _elem(g[0], "a gradient")
+        self.state = MOK_STATE_MX8 if mx else MOK_STATE_F32
+        if copy is not None and self.param != MOK_ELEM_F32:
+            raise ValueError("only float32 parameters have a bfloat16 copy")
+        text = lambda t: str(t.dtype).replace("torch.", "")
+        types = dict(p=text(p[0]), g=text(g[0]), copy="bfloat16", m="uint8" if mx else "float32",
+                     v="uint8" if mx else "float32", m_scale="uint8", v_scale="uint8")
+        spans = []
+        for i in range(len(p)):
+            n = p[i].numel()
+            for name, ts in self.keep.items():
+                want = (-(-n // 32),) if name.endswith("_scale") else (n,)
+                _want(ts[i], f"{name}[{i}]", types[name], want, self.device)
+                if name != "g" and n:
+                    spans.append((ts[i].data_ptr(), ts[i].numel() * ts[i].element_size(), f"{name}[{i}]"))
+        spans.sort()
+        for (a, size, x), (b, _, y) in zip(spans, spans[1:]):
+            if a + size > b:
+                raise ValueError(f"{x} and {y} share memory")
+        at = lambda name, i: self.keep[name][i].data_ptr() if name in self.keep else None
+        self.table = (MokAdamwTensor * len(p))(*[
+            MokAdamwTensor(at("p", i), at("copy", i), at("g", i), at("m", i), at("v", i), at("m_scale", i),
+                           at("v_scale", i), p[i].numel()) for i in range(len(p))])
+
+
+def adamw_plan(p, g, m, v, copy=None, m_scale=None, v_scale=None) -> AdamwPlan:
+    return AdamwPlan(p, g, m, v, copy, m_scale, v_scale)
+
+
+def mok_adamw(plan: AdamwPlan, lr, step, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+              weight_decay: float = 0.0, seed: int = 0, sumsq=None, max_norm: Optional[float] = None,
+              stream=None):
+    """One AdamW step over the plan's tensors, in place. `lr` and `step` may be device tensors (float64
+    [1], int64 [1]), read when the step runs. With `sumsq` (float64 [1], the squared norm of all
+    gradients) gradients are clipped to `max_norm` (None: not clipped) and a step whose norm is not
+    finite changes nothing."""
+    import torch
+    dev = {}
+    for name, x, dtype in (("lr", lr, "float64"), ("step", step, "int64"), ("sumsq", sumsq, "float64")):
+        if isinstance(x, torch.Tensor):
+            _need_cuda(x)
+            _want(x, name, dtype, (1,), plan.device)
+            dev[name] = x.data_ptr()
+        elif name == "sumsq" and x is not None:
+            raise ValueError("sumsq is a device tensor")
+    if max_norm is not None and sumsq is None:
+        raise ValueError("max_norm needs sumsq, the squared norm of all gradients")
+    c = MokAdamwConfig(0.0 if "lr" in dev else lr, beta1, beta2, eps, weight_decay,
+                       float("inf") if max_norm is None else max_norm, 1 if "step" in dev else step,
+                       seed & 0xFFFFFFFF, plan.grad, plan.param, plan.state, dev.get("sumsq"),
+                       dev.get("lr"), dev.get("step"))
+    with _on_device(plan.device, stream) as s:
+        _check("mok_adamw", lib().mok_adamw(len(plan.table), plan.table, ctypes.byref(c), s))

@@ -1,0 +1,426 @@
+// The optimizer step: the squared norm of all gradients, and AdamW over many tensors with moments
+// in fp32 or in MXFP8 (E4M3 codes, one UE8M0 scale per 32 elements).
+//
+// Both stream their tensors once and do little arithmetic per byte, so HBM bounds them. Tensors are
+// described in kernel arguments (no device table to upload, so a call can be captured); a workgroup finds its
+// tensor by searching the prefix sums of their chunk counts.
+#include <algorithm>
+#include <cmath>
+
+#include "mok_internal.h"
+#include "mok_device.h"
+
+// Every product and sum is rounded on its own: contracted into fused multiply-adds, results would
+// depend on what the compiler chose to fuse in each of the variants below.
+#pragma clang fp contract(off)
+
+namespace mok {
+namespace {
+
+// ---- sum of squares -------------------------------------------------------------------------
+constexpr int kSqTensors = 160;      // tensors a launch takes (kernel arguments hold 4 KB)
+constexpr int kSqBlocks = 1024;      // workgroups of a launch; fixed, so sums do not depend on the device
+constexpr int kSqChunk = 4096;       // elements of a chunk
+
+struct SqArgs {
+  const void* g[kSqTensors];
+  int64_t n[kSqTensors];
+  int32_t first[kSqTensors + 1];     // chunks before tensor t
+  int32_t count;
+  double* part;
+};
+
+template <int CAP>
+__device__ __forceinline__ int find_tensor(const int32_t (&first)[CAP], int count, int c) {
+  int lo = 0, hi = count;   // first[lo] <= c < first[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first[mid] <= c) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// Sum over a workgroup of 256, in a fixed order; the result in thread 0.
+__device__ __forceinline__ double block_sum(double v) {
+  __shared__ double s[4];
+  for (int off = 32; off; off >>= 1) v += __shfl_xor(v, off, 64);
+  if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return s[0] + s[1] + s[2] + s[3];
+}
+
+template <bool BF16>
+__global__ __launch_bounds__(256) void k_sumsq(SqArgs a) {
+  double sum = 0;
+  for (int c = blockIdx.x; c < a.first[a.count]; c += gridDim.x) {
+    const int t = find_tensor(a.first, a.count, c);
+    const int64_t i0 = int64_t(c - a.first[t]) * kSqChunk, n = a.n[t];
+    for (int u = 0; u < kSqChunk / 1024; ++u) {
+      const int64_t i = i0 + u * 1024 + threadIdx.x * 4;
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
+      if (i + 4 <= n) {
+        if constexpr (BF16) {
+          const uint2 b = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.g[t]) + i);
+          v[0] = bf2f(uint16_t(b.x)); v[1] = bf2f(uint16_t(b.x >> 16));
+          v[2] = bf2f(uint16_t(b.y)); v[3] = bf2f(uint16_t(b.y >> 16));
+        } else {
+          const f32x4 b = *reinterpret_cast<const f32x4*>(static_cast<const float*>(a.g[t]) + i);
+          for (int j = 0; j < 4; ++j) v[j] = b[j];
+        }
+      } else {
+        for (int j = 0; j < 4; ++j)
+          if (i + j < n) {
+            if constexpr (BF16) v[j] = bf2f(static_cast<const uint16_t*>(a.g[t])[i + j]);
+            else v[j] = static_cast<const float*>(a.g[t])[i + j];
+          }
+      }
+      for (int j = 0; j < 4; ++j) sum = fma(double(v[j]), double(v[j]), sum);
+    }
+  }
+  sum = block_sum(sum);
+  if (threadIdx.x == 0) a.part[blockIdx.x] = sum;
+}
+
+__global__ __launch_bounds__(256) void k_sumsq_join(const double* part, int64_t n, double* out) {
+  double sum = 0;
+  for (int64_t i = threadIdx.x; i < n; i += 256) sum += part[i];
+  sum = block_sum(sum);
+  if (threadIdx.x == 0) *out = sum;
+}
+
+// ---- AdamW ------------------------------------------------------------------------------------
+constexpr int kAdTensors = 48;       // tensors a launch takes
+constexpr int kAdChunk = 4096;       // elements a workgroup updates
+
+struct AdamArgs {
+  void* p[kAdTensors];
+  uint16_t* copy[kAdTensors];
+  const void* g[kAdTensors];
+  void* m[kAdTensors];
+  void* v[kAdTensors];
+  uint8_t* ms[kAdTensors];
+  uint8_t* vs[kAdTensors];
+  int64_t n[kAdTensors];
+  int32_t first[kAdTensors + 1];
+  int32_t count, number0;            // number0: position of this launch's first tensor in the call
+  uint32_t seed;
+  float b1, c1, b2, c2, eps;         // c = 1 - b
+  float rbc2;                        // 1 / sqrt(1 - beta2^step)
+  float decay, rate;                 // 1 - lr weight_decay, lr / (1 - beta1^step)
+  const double* sumsq;
+  const double* lr_dev;
+  const int64_t* step_dev;
+  double max_norm, lr, beta1, beta2, weight_decay;
+  int64_t step;
+};
+
+// Random bits: a hash by xor-shifts and odd multiplications (the fractional bits of sqrt 2 and
+// sqrt 3), which map 32 bits one to one.
+__host__ __device__ inline uint32_t mix(uint32_t h) {
+  h ^= h >> 16;
+  h *= 0x6A09E667u;
+  h ^= h >> 15;
+  h *= 0xBB67AE85u;
+  return h ^ (h >> 16);
+}
+
+// 2^e, e in [-127, 127]
+__device__ __forceinline__ float pow2(int e) {
+  return e >= -126 ? __uint_as_float(uint32_t(e + 127) << 23) : __uint_as_float(1u << 22);
+}
+
+// Exponent code of a run whose largest magnitude has these fp32 bits: the smallest power of two 2^(c-127)
+// that keeps it at most 448 = 1.75 * 2^8; 0 for a run of zeros, 0xFF if it is not finite.
+__device__ __forceinline__ uint32_t scale_code(uint32_t amax) {
+  if (amax >= 0x7F800000u) return 0xFFu;
+  const int c = int(amax >> 23) - 8 + ((amax & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return amax < 0x800000u || c < 0 ? 0u : uint32_t(c);
+}
+
+// |x| <= 448 rounded to an E4M3 value: to the multiple below of the step at |x|, or the one above when
+// the rest is at least 1 - u / 2^16 steps. POSITIVE: not to zero from above zero.
+template <bool POSITIVE>
+__device__ __forceinline__ float round_e4m3(float x, uint32_t u) {
+  const uint32_t b = __float_as_uint(x) & 0x7FFFFFFFu;
+  const int f = max(int(b >> 23), 121);                      // the exponent field, at least 2^-6's
+  const float y = __uint_as_float(b) * __uint_as_float(uint32_t(257 - f) << 23);   // over the step 2^(f-130)
+  float k = floorf(y + float(u) * (1.f / 65536.f));
+  if (POSITIVE) k = b ? fmaxf(k, 1.f) : k;
+  return copysignf(k * __uint_as_float(uint32_t(f - 3) << 23), x);
+}
+
+__device__ __forceinline__ uint32_t max_xor(uint32_t v, int off) {
+  const uint32_t o = uint32_t(__shfl_xor(int(v), off, 64));
+  return v > o ? v : o;
+}
+
+// Four values of a run held by 8 consecutive lanes -> their codes, and the run's scale code.
+template <bool POSITIVE>
+__device__ __forceinline__ uint32_t encode4(const float (&x)[4], const uint32_t (&u)[4], uint32_t* scale) {
+  uint32_t amax = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) amax = max(amax, __float_as_uint(x[j]) & 0x7FFFFFFFu);
+  amax = max_xor(amax, 1);
+  amax = max_xor(amax, 2);
+  amax = max_xor(amax, 4);
+  const uint32_t c = scale_code(amax);
+  *scale = c;
+  if (c == 0xFFu) return 0u;
+  const float inv = pow2(127 - int(c));
+  float r[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) r[j] = round_e4m3<POSITIVE>(x[j] * inv, u[j]);
+  const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(r[0], r[1], 0, false);
+  return uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(r[2], r[3], lo, true));
+}
+
+__device__ __forceinline__ void decode4(uint32_t code, uint32_t scale, float (&x)[4]) {
+  const float s = scale == 0xFFu ? NAN : pow2(int(scale) - 127);
+  x[0] = __builtin_amdgcn_cvt_f32_fp8(int(code), 0) * s;
+  x[1] = __builtin_amdgcn_cvt_f32_fp8(int(code), 1) * s;
+  x[2] = __builtin_amdgcn_cvt_f32_fp8(int(code), 2) * s;
+  x[3] = __builtin_amdgcn_cvt_f32_fp8(int(code), 3) * s;
+}
+
+// Four consecutive elements from i on, those past n as zero.
+__device__ __forceinline__ void load4(const float* p, int64_t i, int64_t n, float (&x)[4]) {
+  if (i + 4 <= n) {
+    const f32x4 v = *reinterpret_cast<const f32x4*>(p + i);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = v[j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = i + j < n ? p[i + j] : 0.f;
+  }
+}
+__device__ __forceinline__ void load4(const uint16_t* p, int64_t i, int64_t n, float (&x)[4]) {
+  if (i + 4 <= n) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p + i);
+    x[0] = bf2f(uint16_t(v.x)); x[1] = bf2f(uint16_t(v.x >> 16));
+    x[2] = bf2f(uint16_t(v.y)); x[3] = bf2f(uint16_t(v.y >> 16));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = i + j < n ? bf2f(p[i + j]) : 0.f;
+  }
+}
+__device__ __forceinline__ uint32_t load4(const uint8_t* p, int64_t i, int64_t n) {
+  if (i + 4 <= n) return *reinterpret_cast<const uint32_t*>(p + i);
+  uint32_t x = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (i + j < n) x |= uint32_t(p[i + j]) << (8 * j);
+  return x;
+}
+__device__ __forceinline__ void store4(float* p, int64_t i, int64_t n, const float (&x)[4]) {
+  if (i + 4 <= n) *reinterpret_cast<f32x4*>(p + i) = f32x4{x[0], x[1], x[2], x[3]};
+  else
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i + j < n) p[i + j] = x[j];
+}
+__device__ __forceinline__ void store4(uint16_t* p, int64_t i, int64_t n, uint2 x) {
+  if (i + 4 <= n) *reinterpret_cast<uint2*>(p + i) = x;
+  else
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i + j < n) p[i + j] = uint16_t((j & 2 ? x.y : x.x) >> (16 * (j & 1)));
+}
+__device__ __forceinline__ void store4(uint8_t* p, int64_t i, int64_t n, uint32_t x) {
+  if (i + 4 <= n) *reinterpret_cast<uint32_t*>(p + i) = x;
+  else
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i + j < n) p[i + j] = uint8_t(x >> (8 * j));
+}
+
+// fp32 -> BF16 bits by adding 16 random bits below the kept ones (infinities and NaN as they are).
+__device__ __forceinline__ uint32_t bf16_random(float x, uint32_t u) {
+  const uint32_t b = __float_as_uint(x);
+  if ((b & 0x7F800000u) == 0x7F800000u) return f2bf(x);
+  return (b + u) >> 16;
+}
+
+template <bool GBF, bool PBF, bool MX8>
+__global__ __launch_bounds__(256) void k_adamw(AdamArgs a) {
+  float clip = 1.f;
+  if (a.sumsq) {
+    const double sq = *a.sumsq;
+    if (!(sq < INFINITY)) return;   // NaN, too
+    const double norm = sqrt(sq);
+    clip = norm > a.max_norm ? float(a.max_norm / norm) : 1.f;
+  }
+  float decay = a.decay, rate = a.rate, rbc2 = a.rbc2;
+  if (a.lr_dev || a.step_dev) {
+    const double lr = a.lr_dev ? *a.lr_dev : a.lr;
+    const double step = double(a.step_dev ? *a.step_dev : a.step);
+    decay = float(1.0 - lr * a.weight_decay);
+    rate = float(lr / (1.0 - pow(a.beta1, step)));
+    rbc2 = float(1.0 / sqrt(1.0 - pow(a.beta2, step)));
+  }
+  const int c = blockIdx.x;
+  const int t = find_tensor(a.first, a.count, c);
+  const int64_t n = a.n[t];
+  const uint32_t salt = mix(a.seed + uint32_t(a.number0 + t) * 0x9E3779B1u);
+  for (int q = 0; q < kAdChunk / 1024; ++q) {
+    const int64_t i = int64_t(c - a.first[t]) * kAdChunk + q * 1024 + threadIdx.x * 4;
+    if (__ballot(i < n) == 0) break;
+    float g[4], p[4], m[4], v[4];
+    load4(static_cast<const std::conditional_t<GBF, uint16_t, float>*>(a.g[t]), i, n, g);
+    load4(static_cast<const std::conditional_t<PBF, uint16_t, float>*>(a.p[t]), i, n, p);
+    if constexpr (MX8) {
+      const uint32_t cm = load4(static_cast<const uint8_t*>(a.m[t]), i, n);
+      const uint32_t cv = load4(static_cast<const uint8_t*>(a.v[t]), i, n);
+      decode4(cm, i < n ? a.ms[t][i >> 5] : 0u, m);
+      decode4(cv, i < n ? a.vs[t][i >> 5] : 0u, v);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = v[j] * v[j];
+    } else {
+      load4(static_cast<const float*>(a.m[t]), i, n, m);
+      load4(static_cast<const float*>(a.v[t]), i, n, v);
+    }
+    float r[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float gj = g[j] * clip;
+      m[j] = m[j] * a.b1 + gj * a.c1;
+      v[j] = v[j] * a.b2 + (gj * gj) * a.c2;
+      r[j] = sqrtf(v[j]);
+      p[j] = p[j] * decay - (m[j] / (r[j] * rbc2 + a.eps)) * rate;
+    }
+    uint32_t h[4], u[4];
+    if constexpr (MX8 || PBF) {
+      const uint32_t base = mix(salt + uint32_t(i >> 32));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[j] = mix((uint32_t(i) + j) ^ base);
+    }
+    if constexpr (PBF) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) u[j] = bf16_random(p[j], mix(h[j] ^ 0x3C6EF372u) & 0xFFFFu);
+      store4(static_cast<uint16_t*>(a.p[t]), i, n, uint2{u[0] | u[1] << 16, u[2] | u[3] << 16});
+    } else {
+      store4(static_cast<float*>(a.p[t]), i, n, p);
+      if (a.copy[t]) store4(a.copy[t], i, n, uint2{pack_bf2(p[0], p[1]), pack_bf2(p[2], p[3])});
+    }
+    if constexpr (MX8) {
+      uint32_t sm, sv;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) u[j] = h[j] & 0xFFFFu;
+      const uint32_t cm = encode4<false>(m, u, &sm);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) u[j] = h[j] >> 16;
+      const uint32_t cv = encode4<true>(r, u, &sv);
+      store4(static_cast<uint8_t*>(a.m[t]), i, n, cm);
+      store4(static_cast<uint8_t*>(a.v[t]), i, n, cv);
+      if ((threadIdx.x & 7) == 0 && i < n) {
+        a.ms[t][i >> 5] = uint8_t(sm);
+        a.vs[t][i >> 5] = uint8_t(sv);
+      }
+    } else {
+      store4(static_cast<float*>(a.m[t]), i, n, m);
+      store4(static_cast<float*>(a.v[t]), i, n, v);
+    }
+  }
+}
+
+template <bool GBF, bool PBF>
+void adamw_kernel(bool mx, const AdamArgs& a, int blocks, hipStream_t s) {
+  if (mx) hipLaunchKernelGGL((k_adamw<GBF, PBF, true>), dim3(blocks), dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((k_adamw<GBF, PBF, false>), dim3(blocks), dim3(256), 0, s, a);
+}
+
+}  // namespace
+
+int64_t sumsq_ws_bytes(int count) {
+  return 8 * int64_t(kSqBlocks) * std::max<int64_t>(1, cdiv(count, kSqTensors));
+}
+
+hipError_t launch_sumsq(int count, const mok_sumsq_tensor* t, bool bf16, double* out, double* ws,
+                        hipStream_t s) {
+  int64_t parts = 0;
+  for (int t0 = 0; t0 < count;) {
+    SqArgs a;
+    a.count = 0;
+    int64_t chunks = 0;
+    a.first[0] = 0;
+    // (chunk numbers stay within 31 bits: a tensor of at most 2^35 elements has 2^23)
+    for (; t0 < count && a.count < kSqTensors; ++t0) {
+      if (t[t0].n == 0) continue;
+      a.g[a.count] = t[t0].g;
+      a.n[a.count] = t[t0].n;
+      chunks += cdiv(t[t0].n, kSqChunk);
+      a.first[++a.count] = int32_t(chunks);
+    }
+    if (a.count == 0) break;
+    a.part = ws + parts;
+    const int blocks = int(std::min<int64_t>(chunks, kSqBlocks));
+    if (bf16) hipLaunchKernelGGL(k_sumsq<true>, dim3(blocks), dim3(256), 0, s, a);
+    else hipLaunchKernelGGL(k_sumsq<false>, dim3(blocks), dim3(256), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    parts += blocks;
+  }
+  hipLaunchKernelGGL(k_sumsq_join, dim3(1), dim3(256), 0, s, ws, parts, out);
+  return hipGetLastError();
+}
+
+hipError_t launch_adamw(int count, const mok_adamw_tensor* t, const mok_adamw_config& c, hipStream_t s) {
+  AdamArgs a;
+  a.seed = c.seed;
+  a.b1 = float(c.beta1);
+  a.c1 = float(1.0 - c.beta1);
+  a.b2 = float(c.beta2);
+  a.c2 = float(1.0 - c.beta2);
+  a.eps = float(c.eps);
+  a.lr = c.lr;
+  a.beta1 = c.beta1;
+  a.beta2 = c.beta2;
+  a.weight_decay = c.weight_decay;
+  a.max_norm = c.max_norm;
+  a.step = c.step;
+  a.sumsq = c.sumsq_dev;
+  a.lr_dev = c.lr_dev;
+  a.step_dev = c.step_dev;
+  const double step = double(c.step);
+  a.decay = float(1.0 - c.lr * c.weight_decay);
+  a.rate = float(c.lr / (1.0 - std::pow(c.beta1, step)));
+  a.rbc2 = float(1.0 / std::sqrt(1.0 - std::pow(c.beta2, step)));
+  const bool mx = c.state == MOK_STATE_MX8, gbf = c.grad_elem == MOK_ELEM_BF16,
+             pbf = c.param_elem == MOK_ELEM_BF16;
+  for (int t0 = 0; t0 < count;) {
+    a.count = 0;
+    a.number0 = t0;
+    int64_t chunks = 0;
+    a.first[0] = 0;
+    for (; t0 < count && a.count < kAdTensors; ++t0) {
+      // a launch has fewer than 2^32 threads
+      const int64_t more = cdiv(t[t0].n, kAdChunk);
+      if (a.count > 0 && chunks + more >= (int64_t(1) << 24)) break;
+      const int k = a.count++;
+      a.p[k] = t[t0].p;
+      a.copy[k] = static_cast<uint16_t*>(t[t0].copy);
+      a.g[k] = t[t0].g;
+      a.m[k] = t[t0].m;
+      a.v[k] = t[t0].v;
+      a.ms[k] = t[t0].m_scale;
+      a.vs[k] = t[t0].v_scale;
+      a.n[k] = t[t0].n;
+      chunks += more;   // (an empty tensor has no chunk, so no workgroup finds it)
+      a.first[a.count] = int32_t(chunks);
+    }
+    if (chunks == 0) continue;
+    const int blocks = int(chunks);
+    if (gbf) {
+      if (pbf) adamw_kernel<true, true>(mx, a, blocks, s);
+      else adamw_kernel<true, false>(mx, a, blocks, s);
+    } else {
+      if (pbf) adamw_kernel<false, true>(mx, a, blocks, s);
+      else adamw_kernel<false, false>(mx, a, blocks, s);
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace mok

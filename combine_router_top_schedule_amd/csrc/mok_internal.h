@@ -450,6 +450,18 @@ hipError_t launch_router_bwd(const Layout& L, const void* const* x_seg, const ui
                              const float* dlogits, float* dwr, void* const* dx_seg, uint8_t* ws,
                              hipStream_t s);
 
+// Expert routing (k_route.hip) and the optimizer step (k_optim.hip); arguments are checked by the
+// host code (mok_train.cpp).
+hipError_t launch_route_fwd(const mok_route_desc& d, const void* x, const float* bias,
+                            const uint8_t* mask, int32_t* idx, float* w, int32_t* load, hipStream_t s);
+hipError_t launch_route_bwd(const mok_route_desc& d, const void* x, const int32_t* idx, const float* dw,
+                            void* dx, hipStream_t s);
+constexpr int64_t kMaxOptElements = int64_t(1) << 35;   // of one tensor
+int64_t sumsq_ws_bytes(int count);
+hipError_t launch_sumsq(int count, const mok_sumsq_tensor* t, bool bf16, double* out, double* ws,
+                        hipStream_t s);
+hipError_t launch_adamw(int count, const mok_adamw_tensor* t, const mok_adamw_config& c, hipStream_t s);
+
 int device_cus();
 
 // One-time set-up per device (kernel attributes are set for the device that is current when

@@ -413,6 +413,130 @@ mok_status mok_device_status(const void* ws_dev, void* stream, mok_status* out);
 /* Number of compute units of the current device (0 if unknown). */
 int32_t mok_device_cus(void);
 
+/* Element types of the calls below. */
+typedef enum { MOK_ELEM_F32 = 0, MOK_ELEM_BF16 = 1 } mok_elem;
+
+/* ---- expert routing: scores, balancing bias, groups, top-k, weights ----------------------------
+ *
+ * For a token with logits x_e (e = 0..E-1):
+ *   score      s_e = sigmoid(x_e), or softmax over all E logits;
+ *   key        s_e + b_e with a bias, x_e without one (a score rises with its logit);
+ *   able       x_e > -inf and key_e > -inf (so a logit of -inf bars the expert for the token, a bias
+ *              of -inf for all tokens, and NaN is never chosen);
+ *   groups     num_groups runs of E / num_groups consecutive experts. With more than one, a group's
+ *              score is the largest key of its able experts (MOK_GROUP_MAX) or the sum of their two
+ *              largest s_e + b_e (MOK_GROUP_TOP2; the only one where just one is able), and only the
+ *              top_groups best groups stay (ties: lower group first);
+ *   choice     the top_k largest keys among the able experts left, best first, ties to the lower
+ *              id; slots that no expert fills get id -1 and weight 0;
+ *   weight     renorm: scale * s_e / (sum of s over the chosen); else scale * s_e. The bias takes
+ *              part in the choice only.
+ * Choices are those of exact arithmetic on the given values: keys that fp32 cannot tell apart are
+ * compared in fp64. Weights are fp32 arithmetic; the renormalised ones are formed as a softmax over
+ * the chosen of x_e, or of log sigmoid(x_e), so they hold for logits of any size. (A NaN or +inf logit
+ * makes the row's softmax weights NaN; with a bias too, such a row chooses nothing.) */
+typedef enum { MOK_SCORE_SOFTMAX = 0, MOK_SCORE_SIGMOID = 1 } mok_score;
+typedef enum { MOK_GROUP_MAX = 0, MOK_GROUP_TOP2 = 1 } mok_group_score;
+
+typedef struct {
+  int64_t num_tokens;      /* N; 0..2^31 - 1                                                  */
+  int64_t logits_stride;   /* elements from one token's logits to the next's, >= E             */
+  int32_t num_experts;     /* E; 1..1024                                                       */
+  int32_t top_k;           /* K; 1..min(16, top_groups * E / num_groups)                       */
+  int32_t score;           /* mok_score                                                        */
+  int32_t num_groups;      /* 1..64, a divisor of E                                            */
+  int32_t top_groups;      /* 1..num_groups                                                    */
+  int32_t group_score;     /* mok_group_score                                                  */
+  int32_t renorm;          /* 0 or 1                                                           */
+  int32_t elem;            /* mok_elem of the logits and of dlogits                            */
+  float scale;             /* finite, > 0                                                      */
+} mok_route_desc;
+
+/* Choice and weights of every token.
+ *   logits_dev     [N] rows of E logits, logits_stride apart (aligned to their element)
+ *   bias_dev       fp32 [E] or NULL
+ *   token_mask_dev uint8 [N] or NULL; a token whose byte is 0 (padding) chooses nothing and is
+ *                  not counted, whatever its logits hold
+ *   topk_idx_dev   int32 [N][K] out, topk_w_dev fp32 [N][K] out: what mok_schedule_routed and
+ *                  mok_layer_fwd_routed take
+ *   load_dev       int32 [E] out or NULL: tokens that chose each expert (the counts that a balancing
+ *                  bias is steered by); overwritten */
+mok_status mok_route_fwd(const mok_route_desc* desc, const void* logits_dev, const float* bias_dev,
+                         const uint8_t* token_mask_dev, int32_t* topk_idx_dev, float* topk_w_dev,
+                         int32_t* load_dev, void* stream);
+
+/* Gradient of the weights with respect to the logits, the choice held fixed (the bias gets none).
+ *   dw_dev       fp32 [N][K]: the weights' gradient (mok_layer_bwd's dp); where topk_idx is -1 (or
+ *                names no expert, or one that an earlier slot of the token names) it is not used
+ *   dlogits_dev  [N][E] out, contiguous, of the logits' type, 16-byte aligned: zero wherever no
+ *                gradient flows; rows without a chosen expert are zero whatever their logits hold
+ * The other arguments are those of the forward. */
+mok_status mok_route_bwd(const mok_route_desc* desc, const void* logits_dev,
+                         const int32_t* topk_idx_dev, const float* dw_dev, void* dlogits_dev,
+                         void* stream);
+
+/* ---- the optimizer step -------------------------------------------------------------------------
+ * Tensors are described by HOST arrays, which are read before the call returns and travel as kernel
+ * arguments: no device table, no copy, and the calls can be captured into a HIP graph. Tensors are
+ * contiguous, 16-byte aligned (bf16 ones too) and do not overlap; a length may be 0. */
+typedef struct {
+  const void* g;
+  int64_t n;
+} mok_sumsq_tensor;
+
+/* *out_dev = sum over every element of every tensor of g^2, in fp64 and in a fixed order: the squared
+ * norm that mok_adamw clips by (add up over ranks first where tensors are sharded).
+ *   elem    mok_elem of the tensors
+ *   ws_dev  mok_sumsq_ws_size bytes of scratch (calls that overlap in time need their own) */
+mok_status mok_sumsq_ws_size(int32_t num_tensors, size_t* ws_bytes);
+mok_status mok_grad_sumsq(int32_t num_tensors, const mok_sumsq_tensor* tensors, int32_t elem,
+                          double* out_dev, void* ws_dev, void* stream);
+
+/* Moments kept in 32 bits: m, v fp32 [n]. In 8 bits (MXFP8, block 32): m and sqrt(v) as E4M3 codes
+ * [n], each run of 32 elements (the last may be shorter) with one UE8M0 scale, uint8 [ceil(n / 32)]: the
+ * smallest power of two that keeps the run's largest value at most 448 (2^-127 if all are zero; 0xFF,
+ * NaN, if one is not finite). Zero-filled memory is the zero state of both. */
+typedef enum { MOK_STATE_F32 = 0, MOK_STATE_MX8 = 1 } mok_opt_state;
+
+typedef struct {
+  void* p;            /* parameters, updated in place                                          */
+  void* copy;         /* bf16 copy of fp32 parameters, written (nearest even); NULL: none      */
+  const void* g;      /* gradient                                                              */
+  void* m;            /* first moment                                                          */
+  void* v;            /* second moment (MX8: its square root)                                  */
+  uint8_t* m_scale;   /* MX8 only                                                              */
+  uint8_t* v_scale;
+  int64_t n;
+} mok_adamw_tensor;
+
+typedef struct {
+  double lr, beta1, beta2, eps, weight_decay;   /* lr, weight_decay >= 0; betas in [0, 1); eps > 0  */
+  double max_norm;          /* with sumsq_dev: gradients are scaled by min(1, max_norm / norm); > 0,
+                               may be infinite (no clipping, only the check for finite values)   */
+  int64_t step;             /* 1, 2, ...: the bias correction's exponent                         */
+  uint32_t seed;            /* of the stochastic roundings: another one for each step            */
+  int32_t grad_elem;        /* mok_elem                                                          */
+  int32_t param_elem;       /* mok_elem; bf16 parameters are rounded stochastically               */
+  int32_t state;            /* mok_opt_state                                                     */
+  const double* sumsq_dev;  /* squared norm of all gradients, or NULL (no clipping). When it is not
+                               finite the call changes nothing                                   */
+  const double* lr_dev;     /* NULL, or where the device finds lr (a captured step whose rate changes) */
+  const int64_t* step_dev;  /* NULL, or where the device finds step                              */
+} mok_adamw_config;
+
+/* One AdamW step over all tensors, in few launches (48 tensors each):
+ *   g' = g min(1, max_norm / sqrt(*sumsq)),  m = beta1 m + (1 - beta1) g',
+ *   v = beta2 v + (1 - beta2) g'^2,
+ *   p = p (1 - lr weight_decay) - lr / (1 - beta1^step) m / (sqrt(v) / sqrt(1 - beta2^step) + eps).
+ * Arithmetic is fp32; p is updated with m and v before these are rounded to 8 bits. Stochastic
+ * rounding takes a value up when its distance from the value below, in steps of the target format,
+ * is at least 1 - u, u = 16 random bits / 2^16 made from (seed, position of the tensor in the call,
+ * element); it keeps small updates alive on average where rounding to nearest would drop them all (a
+ * second moment moves by 0.1 % a step, an E4M3 code by 6 % or more). A positive sqrt(v) never rounds
+ * to 0. Results do not depend on launch shapes. */
+mok_status mok_adamw(int32_t num_tensors, const mok_adamw_tensor* tensors,
+                     const mok_adamw_config* config, void* stream);
+
 /* Measurement hook (benchmarks only): from the next call on, the library records `before`
  * (a hipEvent_t) on the call's stream right before it launches the kernel `kernel` and `after`
  * right after it; MOK_TRACE_NONE (or NULL events) switches it off. Kernels:

@@ -1,0 +1,320 @@
+"""mok_grad_sumsq and mok_adamw on the GPU.
+
+The step rounds every operation to fp32 on its own, in the order that the header states, so it is
+compared bit for bit with the same operations in numpy's fp32 (oracle.optim.step32, encode), and with
+the definition in fp64. The latter's tolerance: a moment is two products and a sum of terms of one sign
+or less, 2 roundings of 2^-24 of the terms' sizes each, plus the coefficients' own roundings; the update adds a root, a
+product, a sum, a quotient and a product, so at most 12 units of 2^-24 of the update, and p two roundings."""
+import math
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from oracle import optim as oo
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover - CPU container
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+import combine_router_top_schedule_amd as mok
+
+U = 2.0 ** -24
+HYPER = dict(lr=3e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.1)
+
+
+def host(t):
+    return t.cpu().view(torch.uint16).numpy() if t.dtype == torch.bfloat16 else t.cpu().numpy()
+
+
+class Step:
+    """Tensors of the given lengths, each with guard elements behind, and their host copies."""
+
+    def __init__(self, sizes, grad="float32", param="float32", copy=True, mx=False, seed=0, g_scale=1.0):
+        rng = np.random.default_rng(seed)
+        self.sizes, self.mx, self.copy, self.bf = sizes, mx, copy, param == "bfloat16"
+        self.full = {k: [] for k in ("p", "g", "m", "v", "copy", "m_scale", "v_scale")}
+        self.h = []
+        for n in sizes:
+            val = lambda std: (rng.standard_normal(n + 40) * std).astype(np.float32)
+            p, m, r = val(0.02), val(1e-3), np.abs(val(2e-3))
+            g = (val(1e-3) * np.exp(2 * rng.standard_normal(n + 40)) * g_scale).astype(np.float32)
+            up = lambda a, dt: torch.from_numpy(np.ascontiguousarray(a)).cuda().to(getattr(torch, dt))
+            self.full["p"].append(up(p, param))
+            self.full["g"].append(up(g, grad))
+            if copy:
+                self.full["copy"].append(torch.full((n + 40,), -7.0, dtype=torch.bfloat16, device="cuda"))
+            if mx:
+                ns = -(-n // 32)
+                for k, a, pos in (("m", m, False), ("v", r, True)):
+                    c, s = oo.encode(a[:n], np.zeros(n), pos)
+                    self.full[k].append(up(np.concatenate([c, np.full(40, 99, np.uint8)]), "uint8"))
+                    self.full[k + "_scale"].append(up(np.concatenate([s, np.full(8, 99, np.uint8)]), "uint8"))
+                m, r = (oo.decode(host(self.full[k][-1])[:n], host(self.full[k + "_scale"][-1])[:ns])
+                        .astype(np.float32) for k in ("m", "v"))
+                v = r * r
+            else:
+                self.full["m"].append(up(m, "float32"))
+                self.full["v"].append(up(r * r, "float32"))
+                m, v = m[:n], (r * r)[:n]
+            f32 = lambda t: t.float().cpu().numpy()[:n]
+            self.h.append((f32(self.full["p"][-1]), f32(self.full["g"][-1]), m, v))
+        live = lambda k: [t[:-(-n // 32) if k.endswith("_scale") else n] for t, n in zip(self.full[k], sizes)]
+        self.t = {k: live(k) for k in self.full if self.full[k]}
+        self.plan = mok.adamw_plan(**self.t)
+
+    def check(self, step, seed, sumsq=None, max_norm=math.inf, exact64=True):
+        for k, (n, (p, g, m, v)) in enumerate(zip(self.sizes, self.h)):
+            a = (HYPER["lr"], 0.9, 0.999, 1e-8, 0.1, step)
+            with np.errstate(all="ignore"):
+                ep, em, ev, er = oo.step32(p, g, m, v, *a, sumsq, max_norm)
+            b = oo.bits(seed, k, n)
+            got = {q: host(self.t[q][k]) for q in self.t}
+            if self.bf:
+                assert np.array_equal(got["p"], oo.bf16_random(ep, oo.mix(b ^ 0x3C6EF372) & 0xFFFF))
+            else:
+                assert np.array_equal(got["p"], ep, equal_nan=True)
+                if self.copy:
+                    # (as values: a NaN may be any)
+                    assert np.array_equal(self.t["copy"][k].float().cpu().numpy(),
+                                          torch.from_numpy(ep).bfloat16().float().numpy(), equal_nan=True)
+            if self.mx:
+                for q, x, u, pos in (("m", em, b & 0xFFFF, False), ("v", er, b >> 16, True)):
+                    c, s = oo.encode(x, u, pos)
+                    assert np.array_equal(got[q + "_scale"], s)
+                    assert np.array_equal(got[q], c)
+            else:
+                assert np.array_equal(got["m"], em, equal_nan=True)
+                assert np.array_equal(got["v"], ev, equal_nan=True)
+            if exact64 and not self.bf:
+                norm = None if sumsq is None else math.sqrt(sumsq)
+                rp, rm, rv = oo.step(p, g, m, v, *a, norm, max_norm)
+                upd = np.abs(rp - p)
+                assert (np.abs(got["p"] - rp) <= 16 * U * upd + 3 * U * np.abs(p) + 1e-30).all()
+                if not self.mx:
+                    assert (np.abs(got["m"] - rm) <= 4 * U * (np.abs(m) + np.abs(g)) + 1e-38).all()
+                    assert (np.abs(got["v"] - rv) <= 6 * U * rv + 1e-38).all()
+            # what lies behind is as it was
+            for q, t in self.full.items():
+                if t and q not in ("p", "g"):
+                    ns = -(-n // 32) if q.endswith("_scale") else n
+                    if q == "copy" or t[k].dtype == torch.uint8:
+                        assert (t[k][ns:].float() == (-7 if q == "copy" else 99)).all()
+
+
+KINDS = [dict(mx=mx, param=p, copy=c, grad=g) for mx in (False, True)
+         for p, c in (("float32", True), ("float32", False), ("bfloat16", False)) for g in ("float32", "bfloat16")]
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=lambda k: "-".join(str(v) for v in k.values()))
+def test_adamw(kind):
+    s = Step([1, 3, 4, 31, 32, 33, 257, 1024, 4096, 4099, 0, 10007], **kind)
+    tail = [t.clone() for t in s.full["p"]]
+    mok.mok_adamw(s.plan, step=3, seed=11, **HYPER)
+    torch.cuda.synchronize()
+    s.check(3, 11)
+    for n, a, b in zip(s.sizes, tail, s.full["p"]):
+        assert torch.equal(a[n:], b[n:])
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_adamw_many_tensors_clipped(mx):
+    # more than one launch takes, with empty ones in between and at the ends
+    rng = np.random.default_rng(3)
+    sizes = [0, 0] + [int(v) for v in rng.integers(0, 200, 130)] + [0]
+    s = Step(sizes, mx=mx)
+    sumsq = sum(float((g.astype(np.float64) ** 2).sum()) for _, g, _, _ in s.h)
+    out = torch.zeros(1, dtype=torch.float64, device="cuda")
+    mok.mok_grad_sumsq(mok.sumsq_plan(s.t["g"]), out)
+    assert abs(out.item() - sumsq) <= 1e-12 * sumsq
+    mok.mok_adamw(s.plan, step=1, seed=5, sumsq=out, max_norm=0.25 * math.sqrt(sumsq), **HYPER)
+    torch.cuda.synchronize()
+    s.check(1, 5, out.item(), 0.25 * math.sqrt(sumsq))
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("bad", [math.inf, math.nan])
+def test_adamw_a_norm_that_is_not_finite_changes_nothing(mx, bad):
+    s = Step([1000, 77], mx=mx)
+    before = {k: [t.clone() for t in ts] for k, ts in s.full.items()}
+    s.t["g"][0][3] = bad
+    out = torch.zeros(1, dtype=torch.float64, device="cuda")
+    mok.mok_grad_sumsq(mok.sumsq_plan(s.t["g"]), out)
+    assert not math.isfinite(out.item())
+    for max_norm in (None, 1.0):
+        mok.mok_adamw(s.plan, step=1, sumsq=out, max_norm=max_norm, **HYPER)
+    for k, ts in s.full.items():
+        if k != "g":
+            assert all(torch.equal(a, b) for a, b in zip(ts, before[k])), k
+
+
+def test_adamw_extreme_gradients_in_8_bits():
+    # zeros, subnormals, values that overflow a square, infinities and NaN: the kernel gives what the
+    # same fp32 operations give; a run with a value that is not finite says so by its scale
+    s = Step([320], mx=True)
+    g = np.zeros(320, np.float32)
+    g[32:64] = 1e-42
+    g[64:96] = np.logspace(-44, 37, 32)
+    g[96] = 3e38
+    g[128] = np.inf
+    g[160] = np.nan
+    g[192:224:3] = -1e-20
+    g[224:256] = 2.0 ** np.arange(-16, 16)
+    s.t["g"][0].copy_(torch.from_numpy(g))
+    s.h[0] = (s.h[0][0], g, s.h[0][2], s.h[0][3])
+    mok.mok_adamw(s.plan, step=2, seed=9, **HYPER)
+    torch.cuda.synchronize()
+    s.check(2, 9, exact64=False)
+    sc = host(s.t["v_scale"][0])
+    # (run 2 holds 1e37, whose square is beyond fp32)
+    assert (sc[2:6] == 255).all() and (np.delete(sc, [2, 3, 4, 5]) != 255).all()
+    # and the next step keeps saying so
+    mok.mok_adamw(s.plan, step=3, seed=10, **HYPER)
+    assert torch.isnan(s.t["p"][0][128:192]).sum() == 64
+
+
+def test_adamw_from_zero_state_in_8_bits_follows_32_bits():
+    """200 steps on a quadratic's gradient plus noise: the mean distance between the 8-bit and the
+    32-bit run stays small against the way both have gone. A code is off by at most one step, 1/8 of its
+    value, without bias, so an update by at most about 1/8 + 1/8 of itself; errors of 200 steps add up to
+    at most a quarter of the way."""
+    n = 4096
+    goal = torch.randn(n, device="cuda")
+    runs = []
+    for mx in (False, True):
+        p = torch.zeros(n, device="cuda")
+        z = lambda k, dt: torch.zeros(k, dtype=dt, device="cuda")
+        st = dict(m=[z(n, torch.uint8)], v=[z(n, torch.uint8)], m_scale=[z(n // 32, torch.uint8)],
+                  v_scale=[z(n // 32, torch.uint8)]) if mx else dict(m=[z(n, torch.float32)], v=[z(n, torch.float32)])
+        g = z(n, torch.float32)
+        plan = mok.adamw_plan(p=[p], g=[g], **st)
+        gen = torch.Generator(device="cuda").manual_seed(1)
+        for t in range(1, 201):
+            g.copy_(p - goal + 0.1 * torch.randn(n, generator=gen, device="cuda"))
+            mok.mok_adamw(plan, lr=1e-3, step=t, seed=t, weight_decay=0.0)
+        runs.append(p)
+    way, apart = runs[0].abs().mean().item(), (runs[0] - runs[1]).abs().mean().item()
+    assert way > 0.05 and apart <= 0.25 * way, (way, apart)
+
+
+def test_adamw_rates_and_steps_on_the_device():
+    a, b = Step([5000]), Step([5000])
+    lr = torch.tensor([HYPER["lr"]], dtype=torch.float64, device="cuda")
+    t = torch.tensor([7], dtype=torch.int64, device="cuda")
+    rest = {k: v for k, v in HYPER.items() if k != "lr"}
+    mok.mok_adamw(a.plan, step=7, **HYPER)
+    mok.mok_adamw(b.plan, lr=lr, step=t, **rest)
+    # the device's pow may round a coefficient's last bit the other way: one unit of 2^-23 of the update
+    for k in ("p", "m", "v"):
+        x, y = a.t[k][0], b.t[k][0]
+        assert (x - y).abs().max() <= 2.0 ** -22 * x.abs().max()
+        if k != "p":
+            assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_adamw_captured(mx):
+    """Norm and step in a graph, with the rate and the step count on the device, replayed; against the
+    same calls made one by one."""
+    runs = []
+    for captured in (False, True):
+        s = Step([3000, 17, 4096], mx=mx, seed=4)
+        lr = torch.tensor([1e-3], dtype=torch.float64, device="cuda")
+        t = torch.ones(1, dtype=torch.int64, device="cuda")
+        out = torch.zeros(1, dtype=torch.float64, device="cuda")
+        sq = mok.sumsq_plan(s.t["g"])
+
+        def one():
+            mok.mok_grad_sumsq(sq, out)
+            mok.mok_adamw(s.plan, lr=lr, step=t, sumsq=out, max_norm=0.5, seed=3)
+            t.add_(1)
+
+        if captured:
+            graph = torch.cuda.CUDAGraph()
+            side = torch.cuda.Stream()
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side), torch.cuda.graph(graph, stream=side):
+                one()
+            torch.cuda.current_stream().wait_stream(side)
+        seen = []
+        for k in range(4):
+            lr.fill_(1e-3 / (k + 1))
+            s.t["g"][0].mul_(1.5)
+            graph.replay() if captured else one()
+            torch.cuda.synchronize()
+            seen += [t_.clone() for ts in s.t.values() for t_ in ts] + [out.clone(), t.clone()]
+        runs.append(seen)
+    assert all(torch.equal(a, b) for a, b in zip(*runs))
+
+
+def test_adamw_on_another_stream_and_twice_alike():
+    a, b = Step([100001], mx=True), Step([100001], mx=True)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    mok.mok_adamw(a.plan, step=1, seed=1, stream=s, **HYPER)
+    mok.mok_adamw(b.plan, step=1, seed=1, **HYPER)
+    torch.cuda.synchronize()
+    for k in a.t:
+        assert torch.equal(a.t[k][0], b.t[k][0]), k
+    c = Step([100001], mx=True)
+    mok.mok_adamw(c.plan, step=1, seed=2, **HYPER)
+    assert not torch.equal(a.t["m"][0], c.t["m"][0]) and torch.equal(a.t["p"][0], c.t["p"][0])
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("sizes", [[1], [0], [0, 5, 0], [3, 4, 5], [4095, 4096, 4097], [2000003],
+                                   [7] * 500, [9_000_001, 3]])
+def test_sumsq(sizes, dtype):
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    # 1e30 squared is beyond fp32
+    ts = [(torch.randn(n + 8, generator=gen, device="cuda") * 10.0 ** (30 if k % 2 else -3)).to(getattr(torch, dtype))[:n]
+          for k, n in enumerate(sizes)]
+    plan, out = mok.sumsq_plan(ts), torch.full((3,), -5.0, dtype=torch.float64, device="cuda")
+    mok.mok_grad_sumsq(plan, out[:1])
+    ref = math.fsum(float((t.double() ** 2).sum()) for t in ts)
+    # a sum of n positive terms in fp64: at most n units of 2^-53
+    assert abs(out[0].item() - ref) <= 2.0 ** -53 * (sum(sizes) + 8) * ref
+    assert out[1] == -5 and out[2] == -5
+    first = out.clone()
+    ws = torch.full_like(plan.ws, 255)
+    mok.mok_grad_sumsq(plan, out[:1], ws=ws)
+    assert torch.equal(first, out)
+
+
+def test_bindings_refuse():
+    z = lambda n, dt=torch.float32: torch.zeros(n, dtype=dt, device="cuda")
+    p, g, m, v = z(64), z(64), z(64), z(64)
+    u8 = lambda n: z(n, torch.uint8)
+    ok = dict(p=[p], g=[g], m=[m], v=[v])
+    for bad in (dict(p=[p.half()]), dict(g=[g.double()]), dict(g=[g[:63]]), dict(m=[m.bfloat16()]),
+                dict(v=[z(128)[::2]]), dict(g=[]), dict(g=[g, g]), dict(v=[m]), dict(m=[z(80)[:64], ][:0]),
+                dict(copy=[z(64)]), dict(copy=[z(63, torch.bfloat16)]), dict(m_scale=[u8(2)]),
+                dict(m=[u8(64)], v=[u8(64)]), dict(m=[u8(64)], v=[u8(64)], m_scale=[u8(2)], v_scale=[u8(3)]),
+                dict(p=[p.bfloat16()], copy=[z(64, torch.bfloat16)]), dict(p=[p.cpu()])):
+        with pytest.raises(ValueError):
+            mok.adamw_plan(**{**ok, **bad})
+    both = z(100)
+    with pytest.raises(ValueError):
+        mok.adamw_plan(p=[both[:64]], g=[g], m=[both[32:96]], v=[v])
+    with pytest.raises(ValueError):
+        mok.adamw_plan(p=[p, p], g=[g, g], m=[m, z(64)], v=[v, z(64)])
+    plan = mok.adamw_plan(**ok)
+    sq = z(1, torch.float64)
+    for bad in (dict(sumsq=z(1)), dict(sumsq=1.0), dict(max_norm=1.0), dict(step=z(1)), dict(lr=z(1)),
+                dict(sumsq=z(2, torch.float64))):
+        with pytest.raises(ValueError):
+            mok.mok_adamw(plan, **{**dict(lr=1e-3, step=1), **bad})
+    for bad in (dict(step=0), dict(lr=-1.0), dict(eps=0.0), dict(sumsq=sq, max_norm=-1.0)):
+        with pytest.raises(mok.MokError):
+            mok.mok_adamw(plan, **{**dict(lr=1e-3, step=1), **bad})
+    odd = z(65)[1:]
+    with pytest.raises(mok.MokError):
+        mok.mok_adamw(mok.adamw_plan(p=[odd], g=[g], m=[m], v=[v]), lr=1e-3, step=1)
+    with pytest.raises(ValueError):
+        mok.sumsq_plan([g, g.bfloat16()])
+    sp = mok.sumsq_plan([g])
+    for bad in (dict(out=z(1)), dict(out=z(2, torch.float64)), dict(ws=u8(8))):
+        with pytest.raises(ValueError):
+            mok.mok_grad_sumsq(sp, **{**dict(out=sq), **bad})
