@@ -24,6 +24,7 @@ struct RouteArgs {
   int64_t N, ld;
   int E, K, G, Kg, gs;   // gs: experts per group
   int sigmoid, top2, renorm;
+  int vec;               // rows allow loads of 4 logits
   float scale;
 };
 
@@ -157,6 +158,369 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_fwd(RouteArgs a) {
       a.w[n * a.K + lane] = w;
       if (a.load && e >= 0) atomicAdd(&s_load[e], 1);
     }
+  }
+  if (a.load) {
+    // integer sums: their order changes nothing
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += 64 * kWaves) {
+      if (gridDim.x == 1) a.load[e] = s_load[e];
+      else if (s_load[e]) atomicAdd(&a.load[e], s_load[e]);
+    }
+  }
+}
+
+// ---- many tokens per wave ---------------------------------------------------------------------
+// L lanes share a token, each with V of its experts in registers (lane j holds experts 4 (j + L i) + c), so
+// a wave reads whole rows of 64 / L tokens and keeps enough loads in flight. Comparing every key in
+// fp64 would cost 256 exponentials in fp64 a token; instead
+//   1. keys are formed in fp32 with an error of at most eps (0 without a bias: the logits themselves);
+//   2. the groups are ranked by their fp32 scores; a token whose border between staying and leaving groups
+//      is not wider than the error goes to choose_wave;
+//   3. tau, the K-th largest fp32 key, comes from sorting networks: each lane's V keys to a sorted list of
+//      KM, then the lists of the L lanes merged pairwise. The K best in exact arithmetic all have an fp32
+//      key of at least tau - 2 eps (of the keys above kappa + eps, kappa the exact K-th, fewer than K exist, so
+//      tau <= kappa + eps; and theirs are at least kappa - eps);
+//   4. those few candidates (nearly always exactly K) are ranked by their fp64 keys. More than 2 KM of
+//      them (rows of equal logits) go to choose_wave.
+template <int OFF>
+__device__ __forceinline__ float lane_xor(float v) {
+  const int x = __float_as_int(v);
+  // (after the steps below it, a partner in the mirrored place of the other half holds what the xor-ed
+  // lane holds)
+  if constexpr (OFF == 1) return __int_as_float(__builtin_amdgcn_mov_dpp(x, 0xB1, 0xF, 0xF, true));
+  else if constexpr (OFF == 2) return __int_as_float(__builtin_amdgcn_mov_dpp(x, 0x4E, 0xF, 0xF, true));
+  else if constexpr (OFF == 4) return __int_as_float(__builtin_amdgcn_mov_dpp(x, 0x141, 0xF, 0xF, true));
+  else if constexpr (OFF == 8) return __int_as_float(__builtin_amdgcn_mov_dpp(x, 0x140, 0xF, 0xF, true));
+  else return __shfl_xor(v, OFF, 64);
+}
+template <int L>
+__device__ __forceinline__ float lanes_max(float v) {
+  v = fmaxf(v, lane_xor<1>(v));
+  v = fmaxf(v, lane_xor<2>(v));
+  v = fmaxf(v, lane_xor<4>(v));
+  if constexpr (L > 8) v = fmaxf(v, lane_xor<8>(v));
+  if constexpr (L > 16) v = fmaxf(v, lane_xor<16>(v));
+  return v;
+}
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+  v += lane_xor<1>(v);
+  v += lane_xor<2>(v);
+  v += lane_xor<4>(v);
+  if constexpr (L > 8) v += lane_xor<8>(v);
+  if constexpr (L > 16) v += lane_xor<16>(v);
+  return v;
+}
+
+// Larger value to a, smaller to b.
+__device__ __forceinline__ void order(float& a, float& b) {
+  const float hi = fmaxf(a, b), lo = fminf(a, b);
+  a = hi;
+  b = lo;
+}
+
+// Sorts v[0..M) downwards: Batcher's odd-even merge network (M a power of two).
+template <int M>
+__device__ __forceinline__ void sort_down(float* v) {
+#pragma unroll
+  for (int p = 1; p < M; p *= 2)
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int j = k % p; j + k < M; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (i + j + k < M && (i + j) / (p * 2) == (i + j + k) / (p * 2)) order(v[i + j], v[i + j + k]);
+}
+
+// The M largest of two lists sorted downwards, sorted: the larger of v[i] and w[M-1-i] form a bitonic
+// sequence, which log2 M half-cleaners sort.
+template <int M>
+__device__ __forceinline__ void merge_down(float* v, const float* w) {
+#pragma unroll
+  for (int i = 0; i < M; ++i) v[i] = fmaxf(v[i], w[M - 1 - i]);
+#pragma unroll
+  for (int k = M / 2; k >= 1; k /= 2)
+#pragma unroll
+    for (int i = 0; i < M; ++i)
+      if (!(i & k)) order(v[i], v[i + k]);
+}
+template <int OFF, int M>
+__device__ __forceinline__ void merge_lanes(float* v) {
+  float w[M];
+#pragma unroll
+  for (int i = 0; i < M; ++i) w[i] = lane_xor<OFF>(v[i]);
+  merge_down<M>(v, w);
+}
+
+template <int L, int V, int KM>
+struct FastLds {   // of one wave
+  static constexpr int T = 64 / L, CAP = 2 * KM, CH = L * V / 4;
+  union {
+    float2 pair[T][CH + 1];       // the two largest of every 4 experts
+    struct {
+      double key[T][CAP];
+      int expert[T][CAP];
+    } cand;
+    double slow[L * V];
+  };
+  float group[T][L];
+  int out[T][KM];
+};
+
+template <bool BF16, int L, int V, int KM>
+__global__ __launch_bounds__(64 * kWaves) void k_route_fast(RouteArgs a) {
+  using Lds = FastLds<L, V, KM>;
+  constexpr int T = Lds::T, CAP = Lds::CAP, SL = CAP > L ? CAP / L : 1;
+  __shared__ Lds s_wave[kWaves];
+  __shared__ __attribute__((aligned(16))) float s_bias[L * V];
+  __shared__ int s_load[L * V];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int j = lane % L, t = lane / L;
+  Lds& s = s_wave[wave];
+  for (int e = threadIdx.x; e < L * V; e += 64 * kWaves) {
+    s_bias[e] = a.bias && e < a.E ? a.bias[e] : 0.f;
+    s_load[e] = 0;
+  }
+  __syncthreads();
+  // eps: the sigmoid's exponential, sum and reciprocal are off by a few units of 2^-23 of 1 (the
+  // exponent's rounding, x 2^-24, meets s (1 - s) < e^-|x|); the softmax's V-term sums by a few more; then
+  // the sum with the bias is rounded
+  float eps = a.sigmoid ? 0x1p-20f : 0x1p-17f;
+  if (a.bias) {
+    float big = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float b = fabsf(s_bias[j + L * i]);
+      big = fmaxf(big, b < INFINITY ? b : 0.f);
+    }
+    eps += lanes_max<L>(big) * 0x1p-23f;
+  }
+  const float key_eps = a.bias ? eps : 0.f;
+  const float group_gap = a.top2 ? 6.f * eps : 2.f * key_eps;
+  const bool sums = !a.sigmoid && (a.bias || (a.G > 1 && a.top2) || !a.renorm);
+  const int per = a.gs >> 2;   // chunks of 4 experts per group
+  const int64_t tiles = (a.N + T - 1) / T;
+  for (int64_t tile = int64_t(blockIdx.x) * kWaves + wave; tile < tiles; tile += int64_t(gridDim.x) * kWaves) {
+    const int64_t n = tile * T + t, nc = n < a.N ? n : a.N - 1;
+    const bool live = n < a.N && (!a.mask || a.mask[nc]);
+    float x[V];
+    // loads from clamped places, so that all of them are in flight together
+    if (a.vec) {
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i) {
+        const int e = min(4 * (j + L * i), a.E - 4);
+        if constexpr (BF16) {
+          const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.x) + nc * a.ld + e);
+          x[4 * i] = bf2f(uint16_t(v.x));
+          x[4 * i + 1] = bf2f(uint16_t(v.x >> 16));
+          x[4 * i + 2] = bf2f(uint16_t(v.y));
+          x[4 * i + 3] = bf2f(uint16_t(v.y >> 16));
+        } else {
+          const f32x4 v = *reinterpret_cast<const f32x4*>(static_cast<const float*>(a.x) + nc * a.ld + e);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) x[4 * i + c] = v[c];
+        }
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < V; ++u) x[u] = logit<BF16>(a.x, nc * a.ld + min(4 * (j + L * (u >> 2)) + (u & 3), a.E - 1));
+    }
+#pragma unroll
+    for (int u = 0; u < V; ++u)
+      x[u] = live && 4 * (j + L * (u >> 2)) + (u & 3) < a.E ? x[u] : -INFINITY;
+    float top = 0.f, sum = 1.f, rsum = 1.f;
+    double sum64 = 1.0;
+    if (sums) {
+      top = x[0];
+#pragma unroll
+      for (int u = 1; u < V; ++u) top = fmaxf(top, x[u]);
+      top = lanes_max<L>(top);
+      if (top == -INFINITY) top = 0.f;
+      sum = 0.f;
+#pragma unroll
+      for (int u = 0; u < V; ++u) sum += __expf(x[u] - top);
+      sum = lanes_sum<L>(sum);
+      rsum = 1.f / sum;
+      if (a.bias) {
+        sum64 = 0.0;
+#pragma unroll 1
+        for (int e = j; e < a.E; e += L)
+          if (live) sum64 += exp(double(logit<BF16>(a.x, n * a.ld + e)) - double(top));
+#pragma unroll
+        for (int off = 1; off < L; off *= 2) sum64 += __shfl_xor(sum64, off, 64);
+      }
+    }
+    auto score32 = [&](float v) {
+      return a.sigmoid ? __builtin_amdgcn_rcpf(1.f + __expf(-v)) : __expf(v - top) * rsum;
+    };
+    bool slow = false;
+    uint32_t stay = 0xFFFFFFFFu;
+    if (a.bias) {
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i) {
+        const f32x4 b = *reinterpret_cast<const f32x4*>(s_bias + 4 * (j + L * i));
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float k = score32(x[4 * i + c]) + b[c];
+          x[4 * i + c] = x[4 * i + c] > -INFINITY && k > -INFINITY ? k : -INFINITY;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < V; ++u) x[u] = x[u] > -INFINITY ? x[u] : -INFINITY;
+    }
+    if (a.G > 1) {
+      const bool scored = a.top2 && !a.bias;
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i) {
+        float g[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          g[c] = x[4 * i + c];
+          if (scored && g[c] > -INFINITY) g[c] = score32(g[c]);
+        }
+        const float h0 = fmaxf(g[0], g[1]), l0 = fminf(g[0], g[1]);
+        const float h1 = fmaxf(g[2], g[3]), l1 = fminf(g[2], g[3]);
+        s.pair[t][j + L * i] = float2{fmaxf(h0, h1), fmaxf(fminf(h0, h1), fmaxf(l0, l1))};
+      }
+      wave_sync();
+      float best = -INFINITY, second = -INFINITY;
+      if (j < a.G) {
+        for (int r = 0, q = j % per; r < per; ++r, q = q + 1 == per ? 0 : q + 1) {
+          const float2 p = s.pair[t][j * per + q];
+          second = fmaxf(fmaxf(second, p.y), fminf(best, p.x));
+          best = fmaxf(best, p.x);
+        }
+        if (a.top2 && second > -INFINITY) best += second;
+      }
+      s.group[t][j] = best;
+      wave_sync();
+      int above = 0, maybe = 0;   // groups that certainly, or possibly, come before this one
+      for (int g = 0; g < a.G; ++g) {
+        const float o = s.group[t][g];
+        if (group_gap > 0.f) {
+          above += o > best + group_gap;
+          maybe += g != j && o > best - group_gap;
+        } else {
+          const bool before = o > best || (o == best && g < j);
+          above += before;
+          maybe += before;
+        }
+      }
+      const bool in = j < a.G && above < a.Kg;
+      const bool unsure = j < a.G && best > -INFINITY &&
+                          ((in && maybe >= a.Kg) || (group_gap > 0.f && !(best < INFINITY)));
+      const uint64_t here = (L == 64 ? ~0ull : ((1ull << (L & 63)) - 1)) << (t * L);
+      slow = (__ballot(unsure) & here) != 0;
+      stay = uint32_t((__ballot(in) & here) >> (t * L));
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i) {
+        const int g = (j + L * i) / per;
+        const bool keep = g < 32 && ((stay >> (g & 31)) & 1);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[4 * i + c] = keep ? x[4 * i + c] : -INFINITY;
+      }
+    }
+    // tau
+    float list[V];
+#pragma unroll
+    for (int u = 0; u < V; ++u) list[u] = x[u];
+#pragma unroll
+    for (int i = 0; i < V; i += KM) sort_down<KM>(list + i);
+#pragma unroll
+    for (int i = KM; i < V; i += KM) merge_down<KM>(list, list + i);
+    merge_lanes<1, KM>(list);
+    merge_lanes<2, KM>(list);
+    merge_lanes<4, KM>(list);
+    if constexpr (L > 8) merge_lanes<8, KM>(list);
+    if constexpr (L > 16) merge_lanes<16, KM>(list);
+    float tau = list[0];
+#pragma unroll
+    for (int i = 1; i < KM; ++i) tau = i < a.K ? list[i] : tau;
+    const float cut = tau - 2.f * key_eps;
+    uint32_t mine = 0;
+#pragma unroll
+    for (int u = 0; u < V; ++u) mine |= uint32_t(x[u] >= cut && x[u] > -INFINITY) << u;
+    int upto = __popc(mine);
+    const int own = upto;
+#pragma unroll
+    for (int off = 1; off < L; off *= 2) {
+      const int o = __shfl_up(upto, off, L);
+      if (j >= off) upto += o;
+    }
+    const int count = __shfl(upto, L - 1, L);
+    slow = slow || count > CAP;
+    if (!slow) {
+      int slot = upto - own;
+      while (mine) {
+        const int u = __builtin_ctz(mine);
+        mine &= mine - 1;
+        s.cand.expert[t][slot++] = 4 * (j + L * (u >> 2)) + (u & 3);
+      }
+    }
+    const int have = slow ? 0 : count;
+    wave_sync();
+    double key[SL];
+    int ex[SL], rank[SL];
+#pragma unroll
+    for (int q = 0; q < SL; ++q) {
+      const int c = j + L * q;
+      ex[q] = -1;
+      rank[q] = KM;
+      key[q] = 0;
+      if (c < have) {
+        ex[q] = s.cand.expert[t][c];
+        rank[q] = 0;
+        const float v = logit<BF16>(a.x, n * a.ld + ex[q]);
+        key[q] = v;
+        if (a.bias) {
+          const double sc = a.sigmoid ? 1.0 / (1.0 + exp(-double(v))) : exp(double(v) - double(top)) / sum64;
+          key[q] = sc + double(s_bias[ex[q]]);
+        }
+        s.cand.key[t][c] = key[q];
+      }
+    }
+    wave_sync();
+    for (int c = 0; __ballot(c < have) != 0; ++c) {
+      if (c < have) {
+        const double ok = s.cand.key[t][c];
+        const int oe = s.cand.expert[t][c];
+#pragma unroll
+        for (int q = 0; q < SL; ++q) rank[q] += ok > key[q] || (ok == key[q] && oe < ex[q]);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < SL; ++q)
+      if (ex[q] >= 0 && rank[q] < a.K) s.out[t][rank[q]] = ex[q];
+    int filled = have < a.K ? have : a.K;
+    wave_sync();
+    for (uint64_t left = __ballot(slow && j == 0); left; left &= left - 1) {
+      const int st = __builtin_ctzll(left) / L;
+      const int e = choose_wave<BF16>(a, tile * T + st, lane, s.slow);
+      if (lane < a.K) s.out[st][lane] = e;
+      if (st == t) filled = a.K;
+      wave_sync();
+    }
+    // weights of the slots, one a lane
+    const int e = j < filled ? s.out[t][j] : -1;
+    const bool some = e >= 0;
+    const float v = some ? logit<BF16>(a.x, n * a.ld + e) : -INFINITY;
+    float w;
+    if (a.renorm) {
+      const float f = a.sigmoid ? log_sigmoid(v) : v;
+      const float first = lanes_max<L>(f);
+      const float q = some ? expf(f - first) : 0.f;
+      w = q / lanes_sum<L>(q);
+    } else {
+      w = a.sigmoid ? 1.f / (1.f + expf(-v)) : expf(v - top) / sum;
+    }
+    if (n < a.N && j < a.K) {
+      a.idx[n * a.K + j] = e;
+      a.w[n * a.K + j] = some ? w * a.scale : 0.f;
+      if (a.load && some) atomicAdd(&s_load[e], 1);
+    }
+    wave_sync();
   }
   if (a.load) {
     // integer sums: their order changes nothing
@@ -314,25 +678,59 @@ int grid_of(int64_t items, int per, int cap) {
   return int(b < 1 ? 1 : (b > cap ? cap : b));
 }
 
+template <bool BF16, int L, int V, int KM>
+void fast(const RouteArgs& a, int grid, hipStream_t s) {
+  hipLaunchKernelGGL((k_route_fast<BF16, L, V, KM>), dim3(grid), dim3(64 * kWaves), 0, s, a);
+}
+
+template <bool BF16>
+void route_fwd(const RouteArgs& a, bool quick, int lanes, int grid, hipStream_t s) {
+  if (!quick) {
+    const size_t lds = size_t(kWaves) * a.E * 8 + size_t(a.E) * 4;   // at most 36 KB
+    hipLaunchKernelGGL(k_route_fwd<BF16>, dim3(grid), dim3(64 * kWaves), lds, s, a);
+  } else if (a.K <= 8) {
+    if (lanes == 8) {
+      if (a.E <= 64) fast<BF16, 8, 8, 8>(a, grid, s);
+      else if (a.E <= 128) fast<BF16, 8, 16, 8>(a, grid, s);
+      else fast<BF16, 8, 32, 8>(a, grid, s);
+    } else if (lanes == 16) {
+      if (a.E <= 384) fast<BF16, 16, 24, 8>(a, grid, s);
+      else fast<BF16, 16, 32, 8>(a, grid, s);
+    } else {
+      fast<BF16, 32, 32, 8>(a, grid, s);
+    }
+  } else {
+    if (lanes == 16) {
+      if (a.E <= 256) fast<BF16, 16, 16, 16>(a, grid, s);
+      else fast<BF16, 16, 32, 16>(a, grid, s);
+    } else {
+      fast<BF16, 32, 32, 16>(a, grid, s);
+    }
+  }
+}
+
 }  // namespace
 
 hipError_t launch_route_fwd(const mok_route_desc& d, const void* x, const float* bias,
                             const uint8_t* mask, int32_t* idx, float* w, int32_t* load, hipStream_t s) {
   RouteArgs a{x, bias, mask, idx, w, load, d.num_tokens, d.logits_stride, d.num_experts, d.top_k,
               d.num_groups, d.top_groups, d.num_experts / d.num_groups, d.score == MOK_SCORE_SIGMOID,
-              d.group_score == MOK_GROUP_TOP2, d.renorm, d.scale};
+              d.group_score == MOK_GROUP_TOP2, d.renorm, 0, d.scale};
+  const bool bf = d.elem == MOK_ELEM_BF16;
+  a.vec = a.E % 4 == 0 && a.ld % 4 == 0 && (reinterpret_cast<uintptr_t>(x) & (bf ? 7 : 15)) == 0;
   const int cus = device_cus() > 0 ? device_cus() : 256;
-  const int grid = grid_of(a.N, kWaves, 8 * cus);
+  // lanes of a token: as many as its experts need at 32 a lane, and its choices at one a lane
+  const int lanes = a.E <= (a.K <= 8 ? 256 : 0) ? 8 : a.E <= 512 ? 16 : 32;
+  // groups that are not made of whole runs of 4 experts, or more of them than lanes, go one token a wave
+  const bool fast = a.G == 1 || (a.gs % 4 == 0 && a.G <= lanes);
+  const int grid = grid_of(a.N, fast ? kWaves * 64 / lanes : kWaves, 8 * cus);
   if (load && (grid > 1 || a.N == 0)) {
     const hipError_t e = launch_fill_u32(reinterpret_cast<uint32_t*>(load), 0u, a.E, s);
     if (e != hipSuccess) return e;
   }
   if (a.N == 0) return hipSuccess;
-  const size_t lds = size_t(kWaves) * a.E * 8 + size_t(a.E) * 4;   // at most 36 KB
-  if (d.elem == MOK_ELEM_BF16)
-    hipLaunchKernelGGL(k_route_fwd<true>, dim3(grid), dim3(64 * kWaves), lds, s, a);
-  else
-    hipLaunchKernelGGL(k_route_fwd<false>, dim3(grid), dim3(64 * kWaves), lds, s, a);
+  if (bf) route_fwd<true>(a, fast, lanes, grid, s);
+  else route_fwd<false>(a, fast, lanes, grid, s);
   return hipGetLastError();
 }
 
