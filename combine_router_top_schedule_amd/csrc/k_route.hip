@@ -6,6 +6,8 @@
 // Backward: the chosen weights are q = softmax over the chosen of f(x), f = x or log sigmoid(x), so
 // dx_k = scale q_k (dw_k - sum_j dw_j q_j) f'(x_k) with f' = 1 or sigmoid(-x_k), zero elsewhere; without
 // renormalisation the scores' own derivatives.
+#include <cfloat>
+
 #include "mok_internal.h"
 #include "mok_device.h"
 
@@ -34,6 +36,24 @@ __device__ __forceinline__ float logit(const void* x, int64_t at) {
   else return static_cast<const float*>(x)[at];
 }
 
+// Four consecutive logits, aligned for one load.
+template <bool BF16>
+__device__ __forceinline__ void load_logits4(const void* x, int64_t at, float* v) {
+  if constexpr (BF16) {
+    const uint2 b = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(x) + at);
+    v[0] = bf2f(uint16_t(b.x));
+    v[1] = bf2f(uint16_t(b.x >> 16));
+    v[2] = bf2f(uint16_t(b.y));
+    v[3] = bf2f(uint16_t(b.y >> 16));
+  } else {
+    const f32x4 b = *reinterpret_cast<const f32x4*>(static_cast<const float*>(x) + at);
+    v[0] = b[0];
+    v[1] = b[1];
+    v[2] = b[2];
+    v[3] = b[3];
+  }
+}
+
 // Orders LDS accesses of the lanes of one wave (which runs them in order) for the compiler.
 __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -47,9 +67,10 @@ __device__ __forceinline__ float log_sigmoid(float x) {
 
 // ---- one token by a whole wave, keys in fp64 -----------------------------------------------------
 // key: LDS, one double per expert, private to the wave. Returns the expert chosen by slot `lane`
-// (lane < K), -1 where none is left.
+// (lane < K), -1 where none is left. (Not inlined: the constants of its fp64 exponentials would be kept
+// in registers throughout the callers' loops.)
 template <bool BF16>
-__device__ __forceinline__ int choose_wave(const RouteArgs& a, int64_t n, int lane, double* key) {
+__device__ __attribute__((noinline)) int choose_wave(const RouteArgs a, int64_t n, int lane, double* key) {
   const double kNone = -INFINITY;
   const int64_t row = n * a.ld;
   double top = kNone, sum = 0;
@@ -180,8 +201,9 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_fwd(RouteArgs a) {
 //      KM, then the lists of the L lanes merged pairwise. The K best in exact arithmetic all have an fp32
 //      key of at least tau - 2 eps (of the keys above kappa + eps, kappa the exact K-th, fewer than K exist, so
 //      tau <= kappa + eps; and theirs are at least kappa - eps);
-//   4. those few candidates (nearly always exactly K) are ranked by their fp64 keys. More than 2 KM of
-//      them (rows of equal logits) go to choose_wave.
+//   4. those few candidates (nearly always exactly K) are ranked by counting. Two whose fp32 keys are
+//      further apart than 2 eps are in that order; two of the same logit and bias are tied; a token
+//      with two others, or with more than 2 KM candidates, goes to choose_wave.
 template <int OFF>
 __device__ __forceinline__ float lane_xor(float v) {
   const int x = __float_as_int(v);
@@ -258,80 +280,86 @@ struct FastLds {   // of one wave
   static constexpr int T = 64 / L, CAP = 2 * KM, CH = L * V / 4;
   union {
     float2 pair[T][CH + 1];       // the two largest of every 4 experts
-    struct {
-      double key[T][CAP];
-      int expert[T][CAP];
-    } cand;
+    f32x4 cand[T][CAP];           // key, logit, bias, expert
     double slow[L * V];
   };
   float group[T][L];
   int out[T][KM];
 };
 
-template <bool BF16, int L, int V, int KM>
-__global__ __launch_bounds__(64 * kWaves) void k_route_fast(RouteArgs a) {
+// What a kernel forms scores of: of nothing (keys are the logits), of nothing but the softmax's sum (for plain
+// softmax weights), or of every expert, for keys with a bias or for groups ranked by their two largest.
+enum ScoreMode { kLogits, kLogitsAndSum, kSigmoidBias, kSoftmaxBias, kSigmoidTop2, kSoftmaxTop2 };
+
+template <bool BF16, int L, int V, int KM, int MODE>
+__global__ __launch_bounds__(64 * kWaves, 4) void k_route_fast(RouteArgs a) {
   using Lds = FastLds<L, V, KM>;
   constexpr int T = Lds::T, CAP = Lds::CAP, SL = CAP > L ? CAP / L : 1;
+  constexpr bool kBias = MODE == kSigmoidBias || MODE == kSoftmaxBias;
+  constexpr bool kTop2 = MODE == kSigmoidTop2 || MODE == kSoftmaxTop2;   // scores for the groups only
+  constexpr bool kSigmoid = MODE == kSigmoidBias || MODE == kSigmoidTop2;
+  constexpr bool kSum = MODE == kLogitsAndSum || MODE == kSoftmaxBias || MODE == kSoftmaxTop2;
   __shared__ Lds s_wave[kWaves];
-  __shared__ __attribute__((aligned(16))) float s_bias[L * V];
+  __shared__ __attribute__((aligned(16))) float s_bias[kBias ? L * V : 4];
   __shared__ int s_load[L * V];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int j = lane % L, t = lane / L;
   Lds& s = s_wave[wave];
   for (int e = threadIdx.x; e < L * V; e += 64 * kWaves) {
-    s_bias[e] = a.bias && e < a.E ? a.bias[e] : 0.f;
+    if constexpr (kBias) {
+      const float b = e < a.E ? a.bias[e] : 0.f;
+      s_bias[e] = b == b ? b : -INFINITY;   // NaN bars the expert, as -inf does
+    }
     s_load[e] = 0;
   }
   __syncthreads();
-  // eps: the sigmoid's exponential, sum and reciprocal are off by a few units of 2^-23 of 1 (the
-  // exponent's rounding, x 2^-24, meets s (1 - s) < e^-|x|); the softmax's V-term sums by a few more; then
-  // the sum with the bias is rounded
-  float eps = a.sigmoid ? 0x1p-20f : 0x1p-17f;
-  if (a.bias) {
-    float big = 0.f;
-#pragma unroll
+  float big = 0.f;   // largest finite bias
+  if constexpr (kBias) {
+#pragma unroll 1
     for (int i = 0; i < V; ++i) {
       const float b = fabsf(s_bias[j + L * i]);
       big = fmaxf(big, b < INFINITY ? b : 0.f);
     }
-    eps += lanes_max<L>(big) * 0x1p-23f;
+    big = lanes_max<L>(big);
   }
-  const float key_eps = a.bias ? eps : 0.f;
-  const float group_gap = a.top2 ? 6.f * eps : 2.f * key_eps;
-  const bool sums = !a.sigmoid && (a.bias || (a.G > 1 && a.top2) || !a.renorm);
   const int per = a.gs >> 2;   // chunks of 4 experts per group
+  // group of each of the lane's chunks, a byte each (31: none that can stay)
+  uint32_t of_group[2] = {0, 0};
+  if (a.G > 1)
+#pragma unroll 1
+    for (int i = 0; i < V / 4; ++i) {
+      const uint32_t g = uint32_t(min((j + L * i) / per, 31)) << (8 * (i & 3));
+      if (i < 4) of_group[0] |= g;
+      else of_group[1] |= g;
+    }
+  const uint64_t here = ((1ull << L) - 1) << (t * L);   // the token's lanes
   const int64_t tiles = (a.N + T - 1) / T;
   for (int64_t tile = int64_t(blockIdx.x) * kWaves + wave; tile < tiles; tile += int64_t(gridDim.x) * kWaves) {
-    const int64_t n = tile * T + t, nc = n < a.N ? n : a.N - 1;
-    const bool live = n < a.N && (!a.mask || a.mask[nc]);
+    const int64_t n = tile * T + t;
+    const bool live = n < a.N && (!a.mask || a.mask[n]);
+    // experts past E, and all of a masked token, are barred and not read: expert 4 (j + L i) + c of
+    // this lane if 4 L i + c >= lim
+    const int lim = live ? a.E - 4 * j : 0;
+    const int64_t at = n * a.ld + 4 * j;
     float x[V];
-    // loads from clamped places, so that all of them are in flight together
-    if (a.vec) {
+    if (a.vec && a.E == L * V && __all(live)) {
 #pragma unroll
-      for (int i = 0; i < V / 4; ++i) {
-        const int e = min(4 * (j + L * i), a.E - 4);
-        if constexpr (BF16) {
-          const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.x) + nc * a.ld + e);
-          x[4 * i] = bf2f(uint16_t(v.x));
-          x[4 * i + 1] = bf2f(uint16_t(v.x >> 16));
-          x[4 * i + 2] = bf2f(uint16_t(v.y));
-          x[4 * i + 3] = bf2f(uint16_t(v.y >> 16));
-        } else {
-          const f32x4 v = *reinterpret_cast<const f32x4*>(static_cast<const float*>(a.x) + nc * a.ld + e);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) x[4 * i + c] = v[c];
-        }
-      }
+      for (int i = 0; i < V / 4; ++i) load_logits4<BF16>(a.x, at + 4 * L * i, x + 4 * i);
     } else {
 #pragma unroll
-      for (int u = 0; u < V; ++u) x[u] = logit<BF16>(a.x, nc * a.ld + min(4 * (j + L * (u >> 2)) + (u & 3), a.E - 1));
-    }
+      for (int u = 0; u < V; ++u) x[u] = -INFINITY;
+      if (a.vec) {
 #pragma unroll
-    for (int u = 0; u < V; ++u)
-      x[u] = live && 4 * (j + L * (u >> 2)) + (u & 3) < a.E ? x[u] : -INFINITY;
+        for (int i = 0; i < V / 4; ++i)
+          if (4 * L * i < lim) load_logits4<BF16>(a.x, at + 4 * L * i, x + 4 * i);
+      } else {
+#pragma unroll
+        for (int u = 0; u < V; ++u)
+          if (4 * L * (u >> 2) + (u & 3) < lim) x[u] = logit<BF16>(a.x, at + 4 * L * (u >> 2) + (u & 3));
+      }
+    }
     float top = 0.f, sum = 1.f, rsum = 1.f;
-    double sum64 = 1.0;
-    if (sums) {
+    if constexpr (kSum) {
       top = x[0];
 #pragma unroll
       for (int u = 1; u < V; ++u) top = fmaxf(top, x[u]);
@@ -342,57 +370,51 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_fast(RouteArgs a) {
       for (int u = 0; u < V; ++u) sum += __expf(x[u] - top);
       sum = lanes_sum<L>(sum);
       rsum = 1.f / sum;
-      if (a.bias) {
-        sum64 = 0.0;
-#pragma unroll 1
-        for (int e = j; e < a.E; e += L)
-          if (live) sum64 += exp(double(logit<BF16>(a.x, n * a.ld + e)) - double(top));
-#pragma unroll
-        for (int off = 1; off < L; off *= 2) sum64 += __shfl_xor(sum64, off, 64);
-      }
     }
+    // eps: the sigmoid's exponential, sum and reciprocal are off by a few units of 2^-23 of 1 (the
+    // exponent's rounding, x 2^-24, meets s (1 - s) < e^-|x|); the softmax's exponentials likewise of the
+    // largest score, 1 / sum, and its sum of at most 1024 positive terms (V in a row, then a tree) by
+    // 40 units of 2^-24; then the sum with the bias is rounded
+    const float eps = (kSigmoid ? 0x1p-20f : 0x1p-17f * rsum) + 0x1p-23f * big;
+    const float key_eps = kBias ? eps : 0.f;
+    const float group_gap = kTop2 || (kBias && a.top2) ? 6.f * eps : 2.f * key_eps;
     auto score32 = [&](float v) {
-      return a.sigmoid ? __builtin_amdgcn_rcpf(1.f + __expf(-v)) : __expf(v - top) * rsum;
+      return kSigmoid ? __builtin_amdgcn_rcpf(1.f + __expf(-v)) : __expf(v - top) * rsum;
     };
     bool slow = false;
-    uint32_t stay = 0xFFFFFFFFu;
-    if (a.bias) {
+    // keys (in x from here on) and, through LDS, the groups' scores
 #pragma unroll
-      for (int i = 0; i < V / 4; ++i) {
-        const f32x4 b = *reinterpret_cast<const f32x4*>(s_bias + 4 * (j + L * i));
+    for (int i = 0; i < V / 4; ++i) {
+      float g[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float k = score32(x[4 * i + c]) + b[c];
-          x[4 * i + c] = x[4 * i + c] > -INFINITY && k > -INFINITY ? k : -INFINITY;
-        }
+      for (int c = 0; c < 4; ++c) {
+        const float v = x[4 * i + c];
+        float k = v;
+        if constexpr (kBias) k = score32(v) + s_bias[4 * (j + L * i) + c];
+        bool able = v > -INFINITY;                            // NaN is not
+        if constexpr (MODE == kSoftmaxBias) able = able && k > -INFINITY;   // (the row's sum may be NaN)
+        x[4 * i + c] = able ? k : -INFINITY;
+        g[c] = x[4 * i + c];
+        if constexpr (kTop2) g[c] = able ? score32(v) : -INFINITY;
       }
-    } else {
-#pragma unroll
-      for (int u = 0; u < V; ++u) x[u] = x[u] > -INFINITY ? x[u] : -INFINITY;
-    }
-    if (a.G > 1) {
-      const bool scored = a.top2 && !a.bias;
-#pragma unroll
-      for (int i = 0; i < V / 4; ++i) {
-        float g[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          g[c] = x[4 * i + c];
-          if (scored && g[c] > -INFINITY) g[c] = score32(g[c]);
-        }
+      if (a.G > 1) {
         const float h0 = fmaxf(g[0], g[1]), l0 = fminf(g[0], g[1]);
         const float h1 = fmaxf(g[2], g[3]), l1 = fminf(g[2], g[3]);
         s.pair[t][j + L * i] = float2{fmaxf(h0, h1), fmaxf(fminf(h0, h1), fmaxf(l0, l1))};
       }
+    }
+    if (a.G > 1) {
       wave_sync();
       float best = -INFINITY, second = -INFINITY;
       if (j < a.G) {
-        for (int r = 0, q = j % per; r < per; ++r, q = q + 1 == per ? 0 : q + 1) {
+        int q = j;   // (lanes begin at different chunks of their groups: fewer bank conflicts)
+        while (q >= per) q -= per;
+        for (int r = 0; r < per; ++r, q = q + 1 == per ? 0 : q + 1) {
           const float2 p = s.pair[t][j * per + q];
           second = fmaxf(fmaxf(second, p.y), fminf(best, p.x));
           best = fmaxf(best, p.x);
         }
-        if (a.top2 && second > -INFINITY) best += second;
+        if ((kBias || kTop2) && a.top2 && second > -INFINITY) best += second;
       }
       s.group[t][j] = best;
       wave_sync();
@@ -411,13 +433,11 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_fast(RouteArgs a) {
       const bool in = j < a.G && above < a.Kg;
       const bool unsure = j < a.G && best > -INFINITY &&
                           ((in && maybe >= a.Kg) || (group_gap > 0.f && !(best < INFINITY)));
-      const uint64_t here = (L == 64 ? ~0ull : ((1ull << (L & 63)) - 1)) << (t * L);
       slow = (__ballot(unsure) & here) != 0;
-      stay = uint32_t((__ballot(in) & here) >> (t * L));
+      const uint32_t stay = uint32_t((__ballot(in) & here) >> (t * L));
 #pragma unroll
       for (int i = 0; i < V / 4; ++i) {
-        const int g = (j + L * i) / per;
-        const bool keep = g < 32 && ((stay >> (g & 31)) & 1);
+        const bool keep = (stay >> ((of_group[i >> 2] >> (8 * (i & 3))) & 31)) & 1;
 #pragma unroll
         for (int c = 0; c < 4; ++c) x[4 * i + c] = keep ? x[4 * i + c] : -INFINITY;
       }
@@ -438,10 +458,10 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_fast(RouteArgs a) {
     float tau = list[0];
 #pragma unroll
     for (int i = 1; i < KM; ++i) tau = i < a.K ? list[i] : tau;
-    const float cut = tau - 2.f * key_eps;
+    const float cut = fmaxf(tau - 2.f * key_eps, -FLT_MAX);
     uint32_t mine = 0;
 #pragma unroll
-    for (int u = 0; u < V; ++u) mine |= uint32_t(x[u] >= cut && x[u] > -INFINITY) << u;
+    for (int u = 0; u < V; ++u) mine |= uint32_t(x[u] >= cut) << u;
     int upto = __popc(mine);
     const int own = upto;
 #pragma unroll
@@ -451,48 +471,55 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_fast(RouteArgs a) {
     }
     const int count = __shfl(upto, L - 1, L);
     slow = slow || count > CAP;
+    const int have = slow ? 0 : count;
     if (!slow) {
       int slot = upto - own;
       while (mine) {
         const int u = __builtin_ctz(mine);
         mine &= mine - 1;
-        s.cand.expert[t][slot++] = 4 * (j + L * (u >> 2)) + (u & 3);
+        s.cand[t][slot++][3] = __int_as_float(4 * (j + L * (u >> 2)) + (u & 3));
       }
     }
-    const int have = slow ? 0 : count;
     wave_sync();
-    double key[SL];
-    int ex[SL], rank[SL];
+    f32x4 me[SL];
+    int rank[SL];
 #pragma unroll
     for (int q = 0; q < SL; ++q) {
       const int c = j + L * q;
-      ex[q] = -1;
-      rank[q] = KM;
-      key[q] = 0;
+      me[q] = f32x4{0.f, 0.f, 0.f, __int_as_float(-1)};
+      rank[q] = 0;
       if (c < have) {
-        ex[q] = s.cand.expert[t][c];
-        rank[q] = 0;
-        const float v = logit<BF16>(a.x, n * a.ld + ex[q]);
-        key[q] = v;
-        if (a.bias) {
-          const double sc = a.sigmoid ? 1.0 / (1.0 + exp(-double(v))) : exp(double(v) - double(top)) / sum64;
-          key[q] = sc + double(s_bias[ex[q]]);
+        const int e = __float_as_int(s.cand[t][c][3]);
+        const float v = logit<BF16>(a.x, n * a.ld + e);
+        float k = v, b = 0.f;
+        if constexpr (kBias) {
+          b = s_bias[e];
+          k = score32(v) + b;
         }
-        s.cand.key[t][c] = key[q];
+        me[q] = f32x4{k, v, b, __int_as_float(e)};
+        s.cand[t][c] = me[q];
       }
     }
     wave_sync();
+    bool unsure = false;
     for (int c = 0; __ballot(c < have) != 0; ++c) {
       if (c < have) {
-        const double ok = s.cand.key[t][c];
-        const int oe = s.cand.expert[t][c];
+        const f32x4 o = s.cand[t][c];
 #pragma unroll
-        for (int q = 0; q < SL; ++q) rank[q] += ok > key[q] || (ok == key[q] && oe < ex[q]);
+        for (int q = 0; q < SL; ++q) {
+          const bool lower = __float_as_int(o[3]) < __float_as_int(me[q][3]);
+          const bool same = o[1] == me[q][1] && o[2] == me[q][2];
+          rank[q] += same ? lower : o[0] > me[q][0];
+          // (keys of -inf and NaN are no candidates; with +inf the difference is not a number)
+          if constexpr (kBias)
+            unsure |= !same && !(fabsf(o[0] - me[q][0]) > 2.f * key_eps) && j + L * q < have;
+        }
       }
     }
+    slow = slow || (kBias && (__ballot(unsure) & here) != 0);
 #pragma unroll
     for (int q = 0; q < SL; ++q)
-      if (ex[q] >= 0 && rank[q] < a.K) s.out[t][rank[q]] = ex[q];
+      if (j + L * q < have && rank[q] < a.K) s.out[t][rank[q]] = __float_as_int(me[q][3]);
     int filled = have < a.K ? have : a.K;
     wave_sync();
     for (uint64_t left = __ballot(slow && j == 0); left; left &= left - 1) {
@@ -680,7 +707,19 @@ int grid_of(int64_t items, int per, int cap) {
 
 template <bool BF16, int L, int V, int KM>
 void fast(const RouteArgs& a, int grid, hipStream_t s) {
-  hipLaunchKernelGGL((k_route_fast<BF16, L, V, KM>), dim3(grid), dim3(64 * kWaves), 0, s, a);
+  const dim3 g(grid), b(64 * kWaves);
+  const bool top2 = a.G > 1 && a.top2;
+  if (a.bias) {
+    if (a.sigmoid) hipLaunchKernelGGL((k_route_fast<BF16, L, V, KM, kSigmoidBias>), g, b, 0, s, a);
+    else hipLaunchKernelGGL((k_route_fast<BF16, L, V, KM, kSoftmaxBias>), g, b, 0, s, a);
+  } else if (top2) {
+    if (a.sigmoid) hipLaunchKernelGGL((k_route_fast<BF16, L, V, KM, kSigmoidTop2>), g, b, 0, s, a);
+    else hipLaunchKernelGGL((k_route_fast<BF16, L, V, KM, kSoftmaxTop2>), g, b, 0, s, a);
+  } else if (a.sigmoid || a.renorm) {
+    hipLaunchKernelGGL((k_route_fast<BF16, L, V, KM, kLogits>), g, b, 0, s, a);
+  } else {
+    hipLaunchKernelGGL((k_route_fast<BF16, L, V, KM, kLogitsAndSum>), g, b, 0, s, a);
+  }
 }
 
 template <bool BF16>
