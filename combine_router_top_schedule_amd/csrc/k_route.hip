@@ -27,6 +27,7 @@ struct RouteArgs {
   int E, K, G, Kg, gs;   // gs: experts per group
   int sigmoid, top2, renorm;
   int vec;               // rows allow loads of 4 logits
+  uint32_t chunk_magic;  // ceil(2^16 / (gs / 4)): a chunk's group is (chunk * magic) >> 16 (chunks < 256)
   float scale;
 };
 
@@ -65,22 +66,44 @@ __device__ __forceinline__ float log_sigmoid(float x) {
   return fminf(x, 0.f) - log1pf(expf(-fabsf(x)));
 }
 
+// exp in fp64 to a few units in the last place: x = n ln 2 + r with |r| <= ln 2 / 2, and the Taylor sum of
+// e^r to r^13 / 13! (the rest is below 2^-57). Its constants are read from memory where they are used: as
+// literals they are hoisted out of every loop around the call, which costs the common path, where
+// nothing is computed in fp64, 30 registers.
+__device__ const double kExp[16] = {
+    1.4426950408889634,         // 1 / ln 2
+    -6.93147180369123816490e-01,  // -ln 2, the first 32 bits
+    -1.90821492927058770002e-10,  // -ln 2, the rest
+    1.0 / 6227020800, 1.0 / 479001600, 1.0 / 39916800, 1.0 / 3628800, 1.0 / 362880, 1.0 / 40320,
+    1.0 / 5040, 1.0 / 720, 1.0 / 120, 1.0 / 24, 1.0 / 6, 0.5, 1.0};
+__device__ __forceinline__ double exp64(double x) {
+  const double* c = kExp;
+  asm volatile("" : "+s"(c));
+  if (x > 709.8) return INFINITY;
+  if (x < -745.2) return 0.0;
+  const double n = rint(x * c[0]);
+  const double r = fma(n, c[2], fma(n, c[1], x));
+  double s = c[3];
+#pragma unroll
+  for (int i = 4; i < 16; ++i) s = fma(s, r, c[i]);
+  return ldexp(fma(s, r, 1.0), int(n));
+}
+
 // ---- one token by a whole wave, keys in fp64 -----------------------------------------------------
 // key: LDS, one double per expert, private to the wave. Returns the expert chosen by slot `lane`
-// (lane < K), -1 where none is left. (Not inlined: the constants of its fp64 exponentials would be kept
-// in registers throughout the callers' loops.)
+// (lane < K), -1 where none is left.
 template <bool BF16>
-__device__ __attribute__((noinline)) int choose_wave(const RouteArgs a, int64_t n, int lane, double* key) {
+__device__ __forceinline__ int choose_wave(const RouteArgs& a, int64_t n, int lane, double* key) {
   const double kNone = -INFINITY;
   const int64_t row = n * a.ld;
   double top = kNone, sum = 0;
   if (!a.sigmoid && (a.bias || (a.G > 1 && a.top2))) {
     for (int e = lane; e < a.E; e += 64) top = fmax(top, double(logit<BF16>(a.x, row + e)));
     for (int off = 32; off; off >>= 1) top = fmax(top, __shfl_xor(top, off, 64));
-    for (int e = lane; e < a.E; e += 64) sum += exp(double(logit<BF16>(a.x, row + e)) - top);
+    for (int e = lane; e < a.E; e += 64) sum += exp64(double(logit<BF16>(a.x, row + e)) - top);
     for (int off = 32; off; off >>= 1) sum += __shfl_xor(sum, off, 64);
   }
-  auto score = [&](double x) { return a.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - top) / sum; };
+  auto score = [&](double x) { return a.sigmoid ? 1.0 / (1.0 + exp64(-x)) : exp64(x - top) / sum; };
   for (int e = lane; e < a.E; e += 64) {
     const double x = logit<BF16>(a.x, row + e);
     const double k = a.bias ? score(x) + double(a.bias[e]) : x;
@@ -316,25 +339,28 @@ __global__ __launch_bounds__(64 * kWaves, 4) void k_route_fast(RouteArgs a) {
   float big = 0.f;   // largest finite bias
   if constexpr (kBias) {
 #pragma unroll 1
-    for (int i = 0; i < V; ++i) {
-      const float b = fabsf(s_bias[j + L * i]);
+    for (int e = lane; e < a.E; e += 64) {
+      const float b = fabsf(s_bias[e]);
       big = fmaxf(big, b < INFINITY ? b : 0.f);
     }
-    big = lanes_max<L>(big);
+#pragma unroll
+    for (int off = 32; off; off >>= 1) big = fmaxf(big, __shfl_xor(big, off, 64));
   }
   const int per = a.gs >> 2;   // chunks of 4 experts per group
   // group of each of the lane's chunks, a byte each (31: none that can stay)
   uint32_t of_group[2] = {0, 0};
   if (a.G > 1)
-#pragma unroll 1
-    for (int i = 0; i < V / 4; ++i) {
-      const uint32_t g = uint32_t(min((j + L * i) / per, 31)) << (8 * (i & 3));
-      if (i < 4) of_group[0] |= g;
-      else of_group[1] |= g;
-    }
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i)
+      of_group[i >> 2] |= min(((j + L * i) * a.chunk_magic) >> 16, 31u) << (8 * (i & 3));
   const uint64_t here = ((1ull << L) - 1) << (t * L);   // the token's lanes
   const int64_t tiles = (a.N + T - 1) / T;
-  for (int64_t tile = int64_t(blockIdx.x) * kWaves + wave; tile < tiles; tile += int64_t(gridDim.x) * kWaves) {
+  const int64_t stride = int64_t(gridDim.x) * kWaves;
+  for (int64_t tile0 = int64_t(blockIdx.x) * kWaves + wave; tile0 < tiles; tile0 += 8 * stride) {
+  uint64_t left = 0;   // tokens of these 8 tiles that go one a wave, T bits a tile
+  for (int step = 0; step < 8; ++step) {
+    const int64_t tile = tile0 + step * stride;
+    if (tile >= tiles) break;
     const int64_t n = tile * T + t;
     const bool live = n < a.N && (!a.mask || a.mask[n]);
     // experts past E, and all of a masked token, are barred and not read: expert 4 (j + L i) + c of
@@ -418,21 +444,23 @@ __global__ __launch_bounds__(64 * kWaves, 4) void k_route_fast(RouteArgs a) {
       }
       s.group[t][j] = best;
       wave_sync();
-      int above = 0, maybe = 0;   // groups that certainly, or possibly, come before this one
-      for (int g = 0; g < a.G; ++g) {
+      // groups that certainly, or possibly, come before this one (places past G hold -inf)
+      int above = 0, maybe = 0;
+#pragma unroll
+      for (int g = 0; g < L; ++g) {
         const float o = s.group[t][g];
-        if (group_gap > 0.f) {
+        if constexpr (kBias || kTop2) {
           above += o > best + group_gap;
-          maybe += g != j && o > best - group_gap;
+          maybe += o > best - group_gap;   // (this one counts itself)
         } else {
-          const bool before = o > best || (o == best && g < j);
-          above += before;
-          maybe += before;
+          above += o > best || (o == best && g < j);
         }
       }
+      if constexpr (kBias || kTop2) maybe -= best > best - group_gap;
+      else maybe = above;
       const bool in = j < a.G && above < a.Kg;
       const bool unsure = j < a.G && best > -INFINITY &&
-                          ((in && maybe >= a.Kg) || (group_gap > 0.f && !(best < INFINITY)));
+                          ((in && maybe >= a.Kg) || ((kBias || kTop2) && !(best < INFINITY)));
       slow = (__ballot(unsure) & here) != 0;
       const uint32_t stay = uint32_t((__ballot(in) & here) >> (t * L));
 #pragma unroll
@@ -443,13 +471,17 @@ __global__ __launch_bounds__(64 * kWaves, 4) void k_route_fast(RouteArgs a) {
       }
     }
     // tau
-    float list[V];
+    float list[KM], next[KM];
 #pragma unroll
-    for (int u = 0; u < V; ++u) list[u] = x[u];
+    for (int u = 0; u < KM; ++u) list[u] = x[u];
+    sort_down<KM>(list);
 #pragma unroll
-    for (int i = 0; i < V; i += KM) sort_down<KM>(list + i);
+    for (int i = KM; i < V; i += KM) {
 #pragma unroll
-    for (int i = KM; i < V; i += KM) merge_down<KM>(list, list + i);
+      for (int u = 0; u < KM; ++u) next[u] = x[i + u];
+      sort_down<KM>(next);
+      merge_down<KM>(list, next);
+    }
     merge_lanes<1, KM>(list);
     merge_lanes<2, KM>(list);
     merge_lanes<4, KM>(list);
@@ -459,9 +491,11 @@ __global__ __launch_bounds__(64 * kWaves, 4) void k_route_fast(RouteArgs a) {
 #pragma unroll
     for (int i = 1; i < KM; ++i) tau = i < a.K ? list[i] : tau;
     const float cut = fmaxf(tau - 2.f * key_eps, -FLT_MAX);
+    // a bit per expert of the lane: shifted in with the comparison's carry
     uint32_t mine = 0;
 #pragma unroll
-    for (int u = 0; u < V; ++u) mine |= uint32_t(x[u] >= cut) << u;
+    for (int u = V - 1; u >= 0; --u)
+      asm("v_cmp_ge_f32 vcc, %1, %2\n\tv_addc_co_u32 %0, vcc, %0, %0, vcc" : "+v"(mine) : "v"(x[u]), "v"(cut) : "vcc");
     int upto = __popc(mine);
     const int own = upto;
 #pragma unroll
@@ -483,11 +517,13 @@ __global__ __launch_bounds__(64 * kWaves, 4) void k_route_fast(RouteArgs a) {
     wave_sync();
     f32x4 me[SL];
     int rank[SL];
+    const bool more = SL > 1 && __any(have > L);
 #pragma unroll
     for (int q = 0; q < SL; ++q) {
       const int c = j + L * q;
       me[q] = f32x4{0.f, 0.f, 0.f, __int_as_float(-1)};
       rank[q] = 0;
+      if (q > 0 && !more) break;
       if (c < have) {
         const int e = __float_as_int(s.cand[t][c][3]);
         const float v = logit<BF16>(a.x, n * a.ld + e);
@@ -507,6 +543,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void k_route_fast(RouteArgs a) {
         const f32x4 o = s.cand[t][c];
 #pragma unroll
         for (int q = 0; q < SL; ++q) {
+          if (q > 0 && !more) break;
           const bool lower = __float_as_int(o[3]) < __float_as_int(me[q][3]);
           const bool same = o[1] == me[q][1] && o[2] == me[q][2];
           rank[q] += same ? lower : o[0] > me[q][0];
@@ -520,34 +557,44 @@ __global__ __launch_bounds__(64 * kWaves, 4) void k_route_fast(RouteArgs a) {
 #pragma unroll
     for (int q = 0; q < SL; ++q)
       if (j + L * q < have && rank[q] < a.K) s.out[t][rank[q]] = __float_as_int(me[q][3]);
-    int filled = have < a.K ? have : a.K;
+    const uint64_t skip = __ballot(slow && j == 0);   // a bit per token, L apart
+#pragma unroll
+    for (int i = 0; i < T; ++i) left |= ((skip >> (i * L)) & 1) << (step * T + i);
+    // (a token that leaves here may have ranks that do not fill its slots)
+    const int filled = slow ? 0 : have < a.K ? have : a.K;
     wave_sync();
-    for (uint64_t left = __ballot(slow && j == 0); left; left &= left - 1) {
-      const int st = __builtin_ctzll(left) / L;
-      const int e = choose_wave<BF16>(a, tile * T + st, lane, s.slow);
-      if (lane < a.K) s.out[st][lane] = e;
-      if (st == t) filled = a.K;
-      wave_sync();
-    }
     // weights of the slots, one a lane
     const int e = j < filled ? s.out[t][j] : -1;
     const bool some = e >= 0;
     const float v = some ? logit<BF16>(a.x, n * a.ld + e) : -INFINITY;
     float w;
     if (a.renorm) {
-      const float f = a.sigmoid ? log_sigmoid(v) : v;
+      // (log sigmoid, to a few units of 2^-23 of max(1, |f|): it goes into an exponential)
+      const float f = a.sigmoid ? fminf(v, 0.f) - __logf(1.f + __expf(-fabsf(v))) : v;
       const float first = lanes_max<L>(f);
-      const float q = some ? expf(f - first) : 0.f;
+      const float q = some ? __expf(f - first) : 0.f;
       w = q / lanes_sum<L>(q);
     } else {
-      w = a.sigmoid ? 1.f / (1.f + expf(-v)) : expf(v - top) / sum;
+      w = a.sigmoid ? 1.f / (1.f + __expf(-v)) : __expf(v - top) / sum;
     }
-    if (n < a.N && j < a.K) {
+    if (n < a.N && j < a.K && !slow) {
       a.idx[n * a.K + j] = e;
       a.w[n * a.K + j] = some ? w * a.scale : 0.f;
       if (a.load && some) atomicAdd(&s_load[e], 1);
     }
     wave_sync();
+  }
+  for (; left; left &= left - 1) {
+    const int b = __builtin_ctzll(left);
+    const int64_t n = (tile0 + b / T * stride) * T + b % T;
+    const int e = choose_wave<BF16>(a, n, lane, s.slow);
+    const float w = weight_wave<BF16>(a, n, lane, e);
+    if (lane < a.K) {
+      a.idx[n * a.K + lane] = e;
+      a.w[n * a.K + lane] = w;
+      if (a.load && e >= 0) atomicAdd(&s_load[e], 1);
+    }
+  }
   }
   if (a.load) {
     // integer sums: their order changes nothing
@@ -754,7 +801,7 @@ hipError_t launch_route_fwd(const mok_route_desc& d, const void* x, const float*
                             const uint8_t* mask, int32_t* idx, float* w, int32_t* load, hipStream_t s) {
   RouteArgs a{x, bias, mask, idx, w, load, d.num_tokens, d.logits_stride, d.num_experts, d.top_k,
               d.num_groups, d.top_groups, d.num_experts / d.num_groups, d.score == MOK_SCORE_SIGMOID,
-              d.group_score == MOK_GROUP_TOP2, d.renorm, 0, d.scale};
+              d.group_score == MOK_GROUP_TOP2, d.renorm, 0, 0, d.scale};
   const bool bf = d.elem == MOK_ELEM_BF16;
   a.vec = a.E % 4 == 0 && a.ld % 4 == 0 && (reinterpret_cast<uintptr_t>(x) & (bf ? 7 : 15)) == 0;
   const int cus = device_cus() > 0 ? device_cus() : 256;
@@ -762,7 +809,8 @@ hipError_t launch_route_fwd(const mok_route_desc& d, const void* x, const float*
   const int lanes = a.E <= (a.K <= 8 ? 256 : 0) ? 8 : a.E <= 512 ? 16 : 32;
   // groups that are not made of whole runs of 4 experts, or more of them than lanes, go one token a wave
   const bool fast = a.G == 1 || (a.gs % 4 == 0 && a.G <= lanes);
-  const int grid = grid_of(a.N, fast ? kWaves * 64 / lanes : kWaves, 8 * cus);
+  if (a.gs >= 4) a.chunk_magic = uint32_t(cdiv(65536, a.gs / 4));
+  const int grid = grid_of(a.N, fast ? kWaves * 64 / lanes : kWaves, (fast ? 4 : 8) * cus);
   if (load && (grid > 1 || a.N == 0)) {
     const hipError_t e = launch_fill_u32(reinterpret_cast<uint32_t*>(load), 0u, a.E, s);
     if (e != hipSuccess) return e;
