@@ -66,29 +66,6 @@ __device__ __forceinline__ float log_sigmoid(float x) {
   return fminf(x, 0.f) - log1pf(expf(-fabsf(x)));
 }
 
-// exp in fp64 to a few units in the last place: x = n ln 2 + r with |r| <= ln 2 / 2, and the Taylor sum of
-// e^r to r^13 / 13! (the rest is below 2^-57). Its constants are read from memory where they are used: as
-// literals they are hoisted out of every loop around the call, which costs the common path, where
-// nothing is computed in fp64, 30 registers.
-__device__ const double kExp[16] = {
-    1.4426950408889634,         // 1 / ln 2
-    -6.93147180369123816490e-01,  // -ln 2, the first 32 bits
-    -1.90821492927058770002e-10,  // -ln 2, the rest
-    1.0 / 6227020800, 1.0 / 479001600, 1.0 / 39916800, 1.0 / 3628800, 1.0 / 362880, 1.0 / 40320,
-    1.0 / 5040, 1.0 / 720, 1.0 / 120, 1.0 / 24, 1.0 / 6, 0.5, 1.0};
-__device__ __forceinline__ double exp64(double x) {
-  const double* c = kExp;
-  asm volatile("" : "+s"(c));
-  if (x > 709.8) return INFINITY;
-  if (x < -745.2) return 0.0;
-  const double n = rint(x * c[0]);
-  const double r = fma(n, c[2], fma(n, c[1], x));
-  double s = c[3];
-#pragma unroll
-  for (int i = 4; i < 16; ++i) s = fma(s, r, c[i]);
-  return ldexp(fma(s, r, 1.0), int(n));
-}
-
 // ---- one token by a whole wave, keys in fp64 -----------------------------------------------------
 // key: LDS, one double per expert, private to the wave. Returns the expert chosen by slot `lane`
 // (lane < K), -1 where none is left.
@@ -100,10 +77,10 @@ __device__ __forceinline__ int choose_wave(const RouteArgs& a, int64_t n, int la
   if (!a.sigmoid && (a.bias || (a.G > 1 && a.top2))) {
     for (int e = lane; e < a.E; e += 64) top = fmax(top, double(logit<BF16>(a.x, row + e)));
     for (int off = 32; off; off >>= 1) top = fmax(top, __shfl_xor(top, off, 64));
-    for (int e = lane; e < a.E; e += 64) sum += exp64(double(logit<BF16>(a.x, row + e)) - top);
+    for (int e = lane; e < a.E; e += 64) sum += exp(double(logit<BF16>(a.x, row + e)) - top);
     for (int off = 32; off; off >>= 1) sum += __shfl_xor(sum, off, 64);
   }
-  auto score = [&](double x) { return a.sigmoid ? 1.0 / (1.0 + exp64(-x)) : exp64(x - top) / sum; };
+  auto score = [&](double x) { return a.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - top) / sum; };
   for (int e = lane; e < a.E; e += 64) {
     const double x = logit<BF16>(a.x, row + e);
     const double k = a.bias ? score(x) + double(a.bias[e]) : x;
@@ -298,13 +275,45 @@ __device__ __forceinline__ void merge_lanes(float* v) {
   merge_down<M>(v, w);
 }
 
+// The tokens of a wave's tiles (of T tokens: tile0, tile0 + stride, ...) that it has left with kLater in
+// their first slot. Called once, when all else is done, and not inlined: inside the tile loop, the constants
+// of its fp64 exponentials were kept in 80 registers throughout (84 us instead of 71 us for 131,072 tokens
+// of 256 experts).
+constexpr int32_t kLater = -2;
+template <bool BF16>
+__device__ __attribute__((noinline)) void choose_later(const RouteArgs* args, double* key, int* load,
+                                                       int64_t tile0, int64_t stride, int T) {
+  const RouteArgs& a = *args;
+  const int lane = threadIdx.x & 63;
+  // this wave's own stores, read back past the CU's cache
+  __builtin_amdgcn_s_waitcnt(0);
+  for (; tile0 * T < a.N; tile0 += stride * (64 / T)) {
+    const int64_t n = (tile0 + lane / T * stride) * T + lane % T;
+    const bool mine = n < a.N && ld_relaxed(a.idx + n * a.K) == kLater;
+    for (uint64_t left = __ballot(mine); left; left &= left - 1) {
+      const int b = __builtin_ctzll(left);
+      const int64_t m = (tile0 + b / T * stride) * T + b % T;
+      const int e = choose_wave<BF16>(a, m, lane, key);
+      const float w = weight_wave<BF16>(a, m, lane, e);
+      if (lane < a.K) {
+        a.idx[m * a.K + lane] = e;
+        a.w[m * a.K + lane] = w;
+        if (a.load && e >= 0) atomicAdd(&load[e], 1);
+      }
+    }
+  }
+}
+
 template <int L, int V, int KM>
 struct FastLds {   // of one wave
   static constexpr int T = 64 / L, CAP = 2 * KM, CH = L * V / 4;
   union {
     float2 pair[T][CH + 1];       // the two largest of every 4 experts
     f32x4 cand[T][CAP];           // key, logit, bias, expert
-    double slow[L * V];
+    struct {
+      double key[L * V];
+      RouteArgs args;
+    } slow;
   };
   float group[T][L];
   int out[T][KM];
@@ -315,7 +324,7 @@ struct FastLds {   // of one wave
 enum ScoreMode { kLogits, kLogitsAndSum, kSigmoidBias, kSoftmaxBias, kSigmoidTop2, kSoftmaxTop2 };
 
 template <bool BF16, int L, int V, int KM, int MODE>
-__global__ __launch_bounds__(64 * kWaves, 4) void k_route_fast(RouteArgs a) {
+__global__ __launch_bounds__(64 * kWaves, L * V >= 1024 ? 3 : 4) void k_route_fast(RouteArgs a) {
   using Lds = FastLds<L, V, KM>;
   constexpr int T = Lds::T, CAP = Lds::CAP, SL = CAP > L ? CAP / L : 1;
   constexpr bool kBias = MODE == kSigmoidBias || MODE == kSoftmaxBias;
@@ -354,13 +363,10 @@ __global__ __launch_bounds__(64 * kWaves, 4) void k_route_fast(RouteArgs a) {
     for (int i = 0; i < V / 4; ++i)
       of_group[i >> 2] |= min(((j + L * i) * a.chunk_magic) >> 16, 31u) << (8 * (i & 3));
   const uint64_t here = ((1ull << L) - 1) << (t * L);   // the token's lanes
+  bool any_slow = false;
   const int64_t tiles = (a.N + T - 1) / T;
   const int64_t stride = int64_t(gridDim.x) * kWaves;
-  for (int64_t tile0 = int64_t(blockIdx.x) * kWaves + wave; tile0 < tiles; tile0 += 8 * stride) {
-  uint64_t left = 0;   // tokens of these 8 tiles that go one a wave, T bits a tile
-  for (int step = 0; step < 8; ++step) {
-    const int64_t tile = tile0 + step * stride;
-    if (tile >= tiles) break;
+  for (int64_t tile = int64_t(blockIdx.x) * kWaves + wave; tile < tiles; tile += stride) {
     const int64_t n = tile * T + t;
     const bool live = n < a.N && (!a.mask || a.mask[n]);
     // experts past E, and all of a masked token, are barred and not read: expert 4 (j + L i) + c of
@@ -557,9 +563,6 @@ __global__ __launch_bounds__(64 * kWaves, 4) void k_route_fast(RouteArgs a) {
 #pragma unroll
     for (int q = 0; q < SL; ++q)
       if (j + L * q < have && rank[q] < a.K) s.out[t][rank[q]] = __float_as_int(me[q][3]);
-    const uint64_t skip = __ballot(slow && j == 0);   // a bit per token, L apart
-#pragma unroll
-    for (int i = 0; i < T; ++i) left |= ((skip >> (i * L)) & 1) << (step * T + i);
     // (a token that leaves here may have ranks that do not fill its slots)
     const int filled = slow ? 0 : have < a.K ? have : a.K;
     wave_sync();
@@ -577,24 +580,18 @@ __global__ __launch_bounds__(64 * kWaves, 4) void k_route_fast(RouteArgs a) {
     } else {
       w = a.sigmoid ? 1.f / (1.f + __expf(-v)) : __expf(v - top) / sum;
     }
-    if (n < a.N && j < a.K && !slow) {
-      a.idx[n * a.K + j] = e;
+    any_slow |= __any(slow);
+    if (n < a.N && j < a.K) {
+      a.idx[n * a.K + j] = slow ? kLater : e;
       a.w[n * a.K + j] = some ? w * a.scale : 0.f;
       if (a.load && some) atomicAdd(&s_load[e], 1);
     }
     wave_sync();
   }
-  for (; left; left &= left - 1) {
-    const int b = __builtin_ctzll(left);
-    const int64_t n = (tile0 + b / T * stride) * T + b % T;
-    const int e = choose_wave<BF16>(a, n, lane, s.slow);
-    const float w = weight_wave<BF16>(a, n, lane, e);
-    if (lane < a.K) {
-      a.idx[n * a.K + lane] = e;
-      a.w[n * a.K + lane] = w;
-      if (a.load && e >= 0) atomicAdd(&s_load[e], 1);
-    }
-  }
+  if (any_slow) {
+    if (lane == 0) s.slow.args = a;
+    wave_sync();
+    choose_later<BF16>(&s.slow.args, s.slow.key, s_load, int64_t(blockIdx.x) * kWaves + wave, stride, T);
   }
   if (a.load) {
     // integer sums: their order changes nothing
