@@ -67,6 +67,30 @@ __device__ __forceinline__ float log_sigmoid(float x) {
 }
 
 // ---- one token by a whole wave, keys in fp64 -----------------------------------------------------
+// Largest of the wave's values, in every lane: shifts within rows of 16 lanes, then broadcasts of a row's
+// last lane to the next rows; lanes without a source keep their own value.
+template <int CTRL>
+__device__ __forceinline__ double max_dpp(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const int lo = int(uint32_t(b)), hi = int(uint32_t(b >> 32));
+  const uint32_t l = uint32_t(__builtin_amdgcn_update_dpp(lo, lo, CTRL, 0xF, 0xF, false));
+  const uint32_t h = uint32_t(__builtin_amdgcn_update_dpp(hi, hi, CTRL, 0xF, 0xF, false));
+  const double o = __builtin_bit_cast(double, uint64_t(h) << 32 | l);
+  return o > v ? o : v;
+}
+__device__ __forceinline__ double wave_max(double v) {
+  v = max_dpp<0x111>(v);   // row_shr:1
+  v = max_dpp<0x112>(v);   // row_shr:2
+  v = max_dpp<0x114>(v);   // row_shr:4
+  v = max_dpp<0x118>(v);   // row_shr:8
+  v = max_dpp<0x142>(v);   // row_bcast:15
+  v = max_dpp<0x143>(v);   // row_bcast:31
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = uint32_t(__builtin_amdgcn_readlane(int(uint32_t(b)), 63));
+  const uint32_t hi = uint32_t(__builtin_amdgcn_readlane(int(uint32_t(b >> 32)), 63));
+  return __builtin_bit_cast(double, uint64_t(hi) << 32 | lo);
+}
+
 // key: LDS, one double per expert, private to the wave. Returns the expert chosen by slot `lane`
 // (lane < K), -1 where none is left.
 template <bool BF16>
@@ -88,26 +112,35 @@ __device__ __forceinline__ int choose_wave(const RouteArgs& a, int64_t n, int la
   }
   wave_sync();
   if (a.G > 1) {
-    // lane g < G: the group's score, then its place among all groups
+    // P lanes a group: each the two largest of its experts, then those of the P lanes
+    int P = 64;
+    while (P * a.G > 64) P >>= 1;
+    const int g = lane / P;
     double best = kNone, second = kNone;
-    if (lane < a.G) {
-      for (int i = 0; i < a.gs; ++i) {
-        double k = key[lane * a.gs + i];
+    if (g < a.G)
+      for (int i = lane % P; i < a.gs; i += P) {
+        double k = key[g * a.gs + i];
         if (a.top2 && !a.bias && k > kNone) k = score(k);
         if (k > best) { second = best; best = k; }
         else if (k > second) second = k;
       }
-      if (a.top2 && second > kNone) best += second;
+    for (int off = P >> 1; off; off >>= 1) {
+      const double b = __shfl_xor(best, off, 64), c = __shfl_xor(second, off, 64);
+      const double low = b < best ? b : best;
+      second = c > second ? c : second;
+      second = low > second ? low : second;
+      best = b > best ? b : best;
     }
+    if (a.top2 && second > kNone) best += second;
     int place = 0;
-    for (int g = 0; g < a.G; ++g) {
-      const double other = __shfl(best, g, 64);
-      place += other > best || (other == best && g < lane);
+    for (int o = 0; o < a.G; ++o) {
+      const double other = __shfl(best, o * P, 64);
+      place += other > best || (other == best && o < g);
     }
-    const uint64_t stay = __ballot(lane < a.G && place < a.Kg);
+    const uint64_t stay = __ballot(g < a.G && place < a.Kg);
     wave_sync();
     for (int e = lane; e < a.E; e += 64)
-      if (!((stay >> (e / a.gs)) & 1)) key[e] = kNone;
+      if (!((stay >> (e / a.gs * P)) & 1)) key[e] = kNone;
     wave_sync();
   }
   int mine = -1;
@@ -116,14 +149,15 @@ __device__ __forceinline__ int choose_wave(const RouteArgs& a, int64_t n, int la
     int at = a.E;
     for (int e = lane; e < a.E; e += 64)
       if (key[e] > best) { best = key[e]; at = e; }
-    for (int off = 32; off; off >>= 1) {
-      const double b = __shfl_xor(best, off, 64);
-      const int i = __shfl_xor(at, off, 64);
-      if (b > best || (b == best && i < at)) { best = b; at = i; }
-    }
-    if (!(best > kNone)) break;   // the same in every lane
-    if (lane == k) mine = at;
-    if ((at & 63) == lane) key[at] = kNone;
+    const double all = wave_max(best);
+    if (!(all > kNone)) break;   // the same in every lane
+    int first = best == all ? at : a.E;
+    if (__popcll(__ballot(best == all)) > 1)
+      for (int off = 32; off; off >>= 1) first = min(first, __shfl_xor(first, off, 64));
+    const uint64_t who = __ballot(best == all && at == first);
+    first = __builtin_amdgcn_readlane(at, __builtin_ctzll(who));
+    if (lane == k) mine = first;
+    if ((first & 63) == lane) key[first] = kNone;
     wave_sync();
   }
   wave_sync();
@@ -283,7 +317,15 @@ constexpr int32_t kLater = -2;
 template <bool BF16>
 __device__ __attribute__((noinline)) void choose_later(const RouteArgs* args, double* key, int* load,
                                                        int64_t tile0, int64_t stride, int T) {
-  const RouteArgs& a = *args;
+  // the same in every lane, and so in scalar registers
+  RouteArgs a;
+  {
+    const int* from = reinterpret_cast<const int*>(args);
+    int* to = reinterpret_cast<int*>(&a);
+    static_assert(sizeof(RouteArgs) % 4 == 0, "copied by words");
+#pragma unroll
+    for (int i = 0; i < int(sizeof(RouteArgs) / 4); ++i) to[i] = __builtin_amdgcn_readfirstlane(from[i]);
+  }
   const int lane = threadIdx.x & 63;
   // this wave's own stores, read back past the CU's cache
   __builtin_amdgcn_s_waitcnt(0);
@@ -403,11 +445,12 @@ __global__ __launch_bounds__(64 * kWaves, L * V >= 1024 ? 3 : 4) void k_route_fa
       sum = lanes_sum<L>(sum);
       rsum = 1.f / sum;
     }
-    // eps: the sigmoid's exponential, sum and reciprocal are off by a few units of 2^-23 of 1 (the
-    // exponent's rounding, x 2^-24, meets s (1 - s) < e^-|x|); the softmax's exponentials likewise of the
-    // largest score, 1 / sum, and its sum of at most 1024 positive terms (V in a row, then a tree) by
-    // 40 units of 2^-24; then the sum with the bias is rounded
-    const float eps = (kSigmoid ? 0x1p-20f : 0x1p-17f * rsum) + 0x1p-23f * big;
+    // eps, in units u = 2^-24. Sigmoid: t = e^-v is off by 1.5 u |v| (two roundings of the exponent) and
+    // 2 u (the instruction) of itself, which moves s by s (1 - s) <= 1/4 times that, and s (1 - s) |v| <= 0.23:
+    // under 0.9 u; 1 + t and the reciprocal by another 1 u each (the last place of a number below 1). Softmax:
+    // exponentials and the sum of at most 1024 positive terms (V in a row, then a tree) by 100 u of the
+    // largest score, 1 / sum. The sum with the bias is rounded once more, to 1 u of at most 1 + |b|.
+    const float eps = (kSigmoid ? 3.f : 100.f * rsum) * 0x1p-24f + (1.f + big) * 0x1p-24f;
     const float key_eps = kBias ? eps : 0.f;
     const float group_gap = kTop2 || (kBias && a.top2) ? 6.f * eps : 2.f * key_eps;
     auto score32 = [&](float v) {
