@@ -249,6 +249,10 @@ __device__ __forceinline__ float lane_xor(float v) {
   else if constexpr (OFF == 8) return __int_as_float(__builtin_amdgcn_mov_dpp(x, 0x140, 0xF, 0xF, true));
   else return __shfl_xor(v, OFF, 64);
 }
+template <int CTRL>   // a permutation of every 4 lanes
+__device__ __forceinline__ int quad(int v) { return __builtin_amdgcn_mov_dpp(v, CTRL, 0xF, 0xF, true); }
+template <int CTRL>
+__device__ __forceinline__ float quad(float v) { return __int_as_float(quad<CTRL>(__float_as_int(v))); }
 template <int L>
 __device__ __forceinline__ float lanes_max(float v) {
   v = fmaxf(v, lane_xor<1>(v));
@@ -585,20 +589,46 @@ __global__ __launch_bounds__(64 * kWaves, L * V >= 1024 ? 3 : 4) void k_route_fa
         s.cand[t][c] = me[q];
       }
     }
-    wave_sync();
-    bool unsure = false;
-    for (int c = 0; __ballot(c < have) != 0; ++c) {
-      if (c < have) {
-        const f32x4 o = s.cand[t][c];
+    // At most 8 candidates, all in the token's first 8 lanes: each meets the other 7 by lane exchanges. If all
+    // keys are further apart than the error, or exact, that is their order; else, and for more candidates,
+    // the loop below looks at logits and biases too.
+    bool unsure = false, again = __any(have > 8);
+    if (!again) {
+      const float k0 = j < have ? me[0][0] : -INFINITY;
+      const int e0 = __float_as_int(me[0][3]);
+      const float k7 = lane_xor<4>(k0);   // (lane 7 - j)
+      const int e7 = __float_as_int(lane_xor<4>(__int_as_float(e0)));
+      bool near = false;
+      auto meet = [&](float ko, int eo) {
+        rank[0] += ko > k0 || (ko == k0 && eo < e0);
+        if constexpr (kBias) near |= fabsf(ko - k0) <= 2.f * key_eps;
+      };
+      meet(quad<0xB1>(k0), quad<0xB1>(e0));
+      meet(quad<0x4E>(k0), quad<0x4E>(e0));
+      meet(quad<0x1B>(k0), quad<0x1B>(e0));
+      meet(k7, e7);
+      meet(quad<0xB1>(k7), quad<0xB1>(e7));
+      meet(quad<0x4E>(k7), quad<0x4E>(e7));
+      meet(quad<0x1B>(k7), quad<0x1B>(e7));
+      // (two +inf: their difference is not a number)
+      if constexpr (kBias) again = __any(j < have && (near || k0 == INFINITY));
+      if (again) rank[0] = 0;
+    }
+    if (again) {
+      wave_sync();
+      for (int c = 0; __ballot(c < have) != 0; ++c) {
+        if (c < have) {
+          const f32x4 o = s.cand[t][c];
 #pragma unroll
-        for (int q = 0; q < SL; ++q) {
-          if (q > 0 && !more) break;
-          const bool lower = __float_as_int(o[3]) < __float_as_int(me[q][3]);
-          const bool same = o[1] == me[q][1] && o[2] == me[q][2];
-          rank[q] += same ? lower : o[0] > me[q][0];
-          // (keys of -inf and NaN are no candidates; with +inf the difference is not a number)
-          if constexpr (kBias)
-            unsure |= !same && !(fabsf(o[0] - me[q][0]) > 2.f * key_eps) && j + L * q < have;
+          for (int q = 0; q < SL; ++q) {
+            if (q > 0 && !more) break;
+            const bool lower = __float_as_int(o[3]) < __float_as_int(me[q][3]);
+            const bool same = o[1] == me[q][1] && o[2] == me[q][2];
+            rank[q] += same ? lower : o[0] > me[q][0];
+            // (keys of -inf and NaN are no candidates; with +inf the difference is not a number)
+            if constexpr (kBias)
+              unsure |= !same && !(fabsf(o[0] - me[q][0]) > 2.f * key_eps) && j + L * q < have;
+          }
         }
       }
     }
