@@ -105,10 +105,25 @@ __device__ __forceinline__ int choose_wave(const RouteArgs& a, int64_t n, int la
     for (int off = 32; off; off >>= 1) sum += __shfl_xor(sum, off, 64);
   }
   auto score = [&](double x) { return a.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - top) / sum; };
-  for (int e = lane; e < a.E; e += 64) {
-    const double x = logit<BF16>(a.x, row + e);
-    const double k = a.bias ? score(x) + double(a.bias[e]) : x;
-    key[e] = x > kNone && k > kNone ? k : kNone;
+  // (four at a time: their loads, and then their exponentials, overlap)
+  for (int e0 = lane; e0 < a.E; e0 += 256) {
+    float x[4], b[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int e = min(e0 + 64 * q, a.E - 1);
+      x[q] = logit<BF16>(a.x, row + e);
+      b[q] = a.bias ? a.bias[e] : 0.f;
+    }
+    double k[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) k[q] = x[q];
+    if (a.bias) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) k[q] = score(k[q]) + double(b[q]);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (e0 + 64 * q < a.E) key[e0 + 64 * q] = x[q] > -INFINITY && k[q] > kNone ? k[q] : kNone;
   }
   wave_sync();
   if (a.G > 1) {
@@ -118,6 +133,7 @@ __device__ __forceinline__ int choose_wave(const RouteArgs& a, int64_t n, int la
     const int g = lane / P;
     double best = kNone, second = kNone;
     if (g < a.G)
+#pragma unroll 4
       for (int i = lane % P; i < a.gs; i += P) {
         double k = key[g * a.gs + i];
         if (a.top2 && !a.bias && k > kNone) k = score(k);
@@ -147,8 +163,11 @@ __device__ __forceinline__ int choose_wave(const RouteArgs& a, int64_t n, int la
   for (int k = 0; k < a.K; ++k) {
     double best = kNone;
     int at = a.E;
-    for (int e = lane; e < a.E; e += 64)
-      if (key[e] > best) { best = key[e]; at = e; }
+#pragma unroll 4
+    for (int e = lane; e < a.E; e += 64) {
+      const double v = key[e];
+      if (v > best) { best = v; at = e; }
+    }
     const double all = wave_max(best);
     if (!(all > kNone)) break;   // the same in every lane
     int first = best == all ? at : a.E;
@@ -313,14 +332,16 @@ __device__ __forceinline__ void merge_lanes(float* v) {
   merge_down<M>(v, w);
 }
 
-// The tokens of a wave's tiles (of T tokens: tile0, tile0 + stride, ...) that it has left with kLater in
-// their first slot. Called once, when all else is done, and not inlined: inside the tile loop, the constants
-// of its fp64 exponentials were kept in 80 registers throughout (84 us instead of 71 us for 131,072 tokens
-// of 256 experts).
+// The tokens that a wave has left with kLater in their first slot: `count` of them, in `list` if that holds
+// them; else all tokens of the wave's tiles (tile0, tile0 + stride, ..., of T tokens) are looked at. Called once, when all else is done, and not inlined: inside the
+// tile loop, the constants of its fp64 exponentials were kept in 80 registers throughout (84 us instead of
+// 71 us for 131,072 tokens of 256 experts).
 constexpr int32_t kLater = -2;
+constexpr int kListed = 32;
 template <bool BF16>
 __device__ __attribute__((noinline)) void choose_later(const RouteArgs* args, double* key, int* load,
-                                                       int64_t tile0, int64_t stride, int T) {
+                                                       const int64_t* list, int count, int64_t tile0,
+                                                       int64_t stride, int T) {
   // the same in every lane, and so in scalar registers
   RouteArgs a;
   {
@@ -331,14 +352,16 @@ __device__ __attribute__((noinline)) void choose_later(const RouteArgs* args, do
     for (int i = 0; i < int(sizeof(RouteArgs) / 4); ++i) to[i] = __builtin_amdgcn_readfirstlane(from[i]);
   }
   const int lane = threadIdx.x & 63;
-  // this wave's own stores, read back past the CU's cache
-  __builtin_amdgcn_s_waitcnt(0);
-  for (; tile0 * T < a.N; tile0 += stride * (64 / T)) {
-    const int64_t n = (tile0 + lane / T * stride) * T + lane % T;
-    const bool mine = n < a.N && ld_relaxed(a.idx + n * a.K) == kLater;
+  const bool listed = count <= kListed;
+  if (!listed) __builtin_amdgcn_s_waitcnt(0);   // this wave's own stores, read back past the CU's cache
+  for (int64_t i0 = 0;; i0 += 64) {
+    // 64 numbers at a time: those of the list, or all
+    const int64_t i = i0 + lane;
+    const int64_t n = listed ? (i < count ? list[i] : a.N) : (tile0 + i / T * stride) * T + i % T;
+    if (__all(n >= a.N)) break;
+    const bool mine = n < a.N && (listed || ld_relaxed(a.idx + n * a.K) == kLater);
     for (uint64_t left = __ballot(mine); left; left &= left - 1) {
-      const int b = __builtin_ctzll(left);
-      const int64_t m = (tile0 + b / T * stride) * T + b % T;
+      const int64_t m = __shfl(n, __builtin_ctzll(left), 64);
       const int e = choose_wave<BF16>(a, m, lane, key);
       const float w = weight_wave<BF16>(a, m, lane, e);
       if (lane < a.K) {
@@ -363,6 +386,7 @@ struct FastLds {   // of one wave
   };
   float group[T][L];
   int out[T][KM];
+  int64_t later[kListed];
 };
 
 // What a kernel forms scores of: of nothing (keys are the logits), of nothing but the softmax's sum (for plain
@@ -409,7 +433,7 @@ __global__ __launch_bounds__(64 * kWaves, L * V >= 1024 ? 3 : 4) void k_route_fa
     for (int i = 0; i < V / 4; ++i)
       of_group[i >> 2] |= min(((j + L * i) * a.chunk_magic) >> 16, 31u) << (8 * (i & 3));
   const uint64_t here = ((1ull << L) - 1) << (t * L);   // the token's lanes
-  bool any_slow = false;
+  int later = 0;   // tokens left for the end, the same in every lane
   const int64_t tiles = (a.N + T - 1) / T;
   const int64_t stride = int64_t(gridDim.x) * kWaves;
   for (int64_t tile = int64_t(blockIdx.x) * kWaves + wave; tile < tiles; tile += stride) {
@@ -653,7 +677,11 @@ __global__ __launch_bounds__(64 * kWaves, L * V >= 1024 ? 3 : 4) void k_route_fa
     } else {
       w = a.sigmoid ? 1.f / (1.f + __expf(-v)) : __expf(v - top) / sum;
     }
-    any_slow |= __any(slow);
+    if (const uint64_t who = __ballot(slow && j == 0)) {
+      const int at = later + __popcll(who & ((1ull << lane) - 1));
+      if (slow && j == 0 && at < kListed) s.later[at] = n;
+      later += __popcll(who);
+    }
     if (n < a.N && j < a.K) {
       a.idx[n * a.K + j] = slow ? kLater : e;
       a.w[n * a.K + j] = some ? w * a.scale : 0.f;
@@ -661,10 +689,11 @@ __global__ __launch_bounds__(64 * kWaves, L * V >= 1024 ? 3 : 4) void k_route_fa
     }
     wave_sync();
   }
-  if (any_slow) {
+  if (later) {
     if (lane == 0) s.slow.args = a;
     wave_sync();
-    choose_later<BF16>(&s.slow.args, s.slow.key, s_load, int64_t(blockIdx.x) * kWaves + wave, stride, T);
+    choose_later<BF16>(&s.slow.args, s.slow.key, s_load, s.later, later, int64_t(blockIdx.x) * kWaves + wave,
+                       stride, T);
   }
   if (a.load) {
     // integer sums: their order changes nothing

@@ -192,6 +192,27 @@ def test_route_choices_closer_than_fp32(name):
     r.check_forward()
 
 
+@pytest.mark.parametrize("bias", [False, True])
+def test_route_many_rows_of_equal_logits(bias):
+    """More tokens without a decision in fp32 than a wave keeps a list of (a few dozen of its 48), and
+    others between them."""
+    gate, n = G(64, 8, "sigmoid", 8, 4, "top2", True, 2.5), 200001
+    x = torch.zeros(n, 64, device="cuda")
+    some = torch.arange(0, n, 17, device="cuda")
+    x[some] = torch.randn(len(some), 64, device="cuda")
+    b = torch.zeros(64, device="cuda") if bias else None
+    idx = torch.full((n, 8), -5, dtype=torch.int32, device="cuda")
+    w, load = torch.empty(n, 8, device="cuda"), torch.empty(64, dtype=torch.int32, device="cuda")
+    mok.mok_route_fwd(desc(gate), x, idx, w, bias=b, load=load)
+    rest = torch.ones(n, dtype=torch.bool, device="cuda")
+    rest[some] = False
+    assert (idx[rest] == torch.arange(8, device="cuda")).all() and (w[rest] == 2.5 / 8).all()
+    pick = some[:300]
+    ref, _, _ = orr.forward(gate, x[pick].double().cpu().numpy(), None if b is None else np.zeros(64))
+    assert np.array_equal(idx[pick].cpu().numpy(), ref)
+    assert torch.equal(load.long(), torch.bincount(idx.flatten().long(), minlength=64))
+
+
 def test_route_bias_bars_and_forces_experts():
     gate = GATES["kimi"]
     rng = np.random.default_rng(7)
