@@ -411,92 +411,107 @@ def route_desc(E: int, K: int, score: str = "softmax", groups: int = 1, top_grou
                         int(renorm), MOK_ELEM_F32, scale)
 
 
+_torch = None
+
+
+def _tch():
+    """torch, imported at the first call that needs it."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
 def _elem(t, name: str) -> int:
-    import torch
-    if t.dtype == torch.float32:
+    torch = _tch()
+    if t.dtype is torch.float32:
         return MOK_ELEM_F32
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return MOK_ELEM_BF16
     raise ValueError(f"{name} must be float32 or bfloat16, not {t.dtype}")
 
 
-def _want(t, name: str, dtype: str, shape, device):
-    import torch
-    if t.dtype != getattr(torch, dtype) or t.numel() != _count(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {shape}, not {t.dtype} "
-                         f"{tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
+def _want(t, name: str, dtype, count: int, dev: int) -> int:
+    """Address of a contiguous tensor of `count` elements of `dtype` on device number `dev`."""
+    if t.dtype is not dtype or t.numel() != count or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {count} elements on device {dev}, "
+                         f"not {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+    return t.data_ptr()
 
 
-def _count(shape):
-    n = 1
-    for v in shape:
-        n *= v
-    return n
+def _device_of(t) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("libmok takes device tensors only")
+    return dev
 
 
 class _on_device:
-    """Makes `device` current around a call (the library launches on the current device) and gives the
-    stream to use: the one asked for, or the device's current one."""
+    """Makes device number `dev` current around a call (the library launches on the current device) and
+    gives the stream to use: the one asked for, or the device's current one."""
 
-    def __init__(self, device, stream):
-        import torch
-        if stream is not None and stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
-        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-        self.stream = stream
+    __slots__ = ("guard", "raw")
+
+    def __init__(self, dev: int, stream):
+        torch = _tch()
+        if stream is None:
+            stream = torch.cuda.current_stream(dev)
+        elif stream.device.index != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors are on device {dev}")
+        self.raw = stream.cuda_stream
+        self.guard = None if torch.cuda.current_device() == dev else torch.cuda.device(dev)
 
     def __enter__(self):
         if self.guard is not None:
             self.guard.__enter__()
-        return _stream(self.stream)
+        return self.raw
 
     def __exit__(self, *exc):
         if self.guard is not None:
             self.guard.__exit__(*exc)
 
 
-def _route_call(d: MokRouteDesc, logits, topk_idx) -> MokRouteDesc:
-    """`d` for these logits [N][E] (rows may be strided)."""
+def _route_call(d: MokRouteDesc, logits, topk_idx, dev: int):
+    """(`d` for these logits [N][E], whose rows may be strided; address of topk_idx)"""
+    if logits.dim() != 2 or logits.shape[1] != d.num_experts:
+        raise ValueError(f"logits must be [N][{d.num_experts}], not {tuple(logits.shape)}")
     N, E = logits.shape
-    if E != d.num_experts:
-        raise ValueError(f"logits have {E} columns, the descriptor {d.num_experts} experts")
-    if (E > 1 and logits.stride(1) != 1) or (N > 1 and logits.stride(0) < E):
+    ld, step = logits.stride()
+    if (E > 1 and step != 1) or (N > 1 and ld < E):
         raise ValueError("logits rows must be contiguous and must not overlap")
-    _want(topk_idx, "topk_idx", "int32", (N, d.top_k), logits.device)
-    return MokRouteDesc(N, logits.stride(0) if N > 1 else E, E, d.top_k, d.score, d.num_groups,
-                        d.top_groups, d.group_score, d.renorm, _elem(logits, "logits"), d.scale)
+    c = MokRouteDesc.from_buffer_copy(d)
+    c.num_tokens = N
+    c.logits_stride = ld if N > 1 else E
+    c.elem = _elem(logits, "logits")
+    return c, _want(topk_idx, "topk_idx", _torch.int32, N * d.top_k, dev)
 
 
 def mok_route_fwd(d: MokRouteDesc, logits, topk_idx, topk_w, bias=None, token_mask=None, load=None,
                   stream=None):
-    _need_cuda(logits, topk_idx, topk_w, bias, token_mask, load)
-    c, dev = _route_call(d, logits, topk_idx), logits.device
-    _want(topk_w, "topk_w", "float32", (c.num_tokens, c.top_k), dev)
+    torch, dev = _tch(), _device_of(logits)
+    c, idx = _route_call(d, logits, topk_idx, dev)
+    N, E = c.num_tokens, c.num_experts
+    w = _want(topk_w, "topk_w", torch.float32, N * c.top_k, dev)
     if bias is not None:
-        _want(bias, "bias", "float32", (c.num_experts,), dev)
+        bias = _want(bias, "bias", torch.float32, E, dev)
     if token_mask is not None:
-        import torch
-        if token_mask.dtype == torch.bool:
-            token_mask = token_mask.view(torch.uint8)
-        _want(token_mask, "token_mask", "uint8", (c.num_tokens,), dev)
+        token_mask = _want(token_mask.view(torch.uint8) if token_mask.dtype is torch.bool else token_mask,
+                           "token_mask", torch.uint8, N, dev)
     if load is not None:
-        _want(load, "load", "int32", (c.num_experts,), dev)
+        load = _want(load, "load", torch.int32, E, dev)
     with _on_device(dev, stream) as s:
-        _check("mok_route_fwd", lib().mok_route_fwd(ctypes.byref(c), _ptr(logits), _ptr(bias),
-                                                    _ptr(token_mask), _ptr(topk_idx), _ptr(topk_w),
-                                                    _ptr(load), s))
+        _check("mok_route_fwd", lib().mok_route_fwd(ctypes.byref(c), logits.data_ptr(), bias, token_mask,
+                                                    idx, w, load, s))
 
 
 def mok_route_bwd(d: MokRouteDesc, logits, topk_idx, dw, dlogits, stream=None):
-    _need_cuda(logits, topk_idx, dw, dlogits)
-    c, dev = _route_call(d, logits, topk_idx), logits.device
-    _want(dw, "dw", "float32", (c.num_tokens, c.top_k), dev)
-    _want(dlogits, "dlogits", str(logits.dtype).replace("torch.", ""), tuple(logits.shape), dev)
+    torch, dev = _tch(), _device_of(logits)
+    c, idx = _route_call(d, logits, topk_idx, dev)
+    w = _want(dw, "dw", torch.float32, c.num_tokens * c.top_k, dev)
+    dx = _want(dlogits, "dlogits", logits.dtype, c.num_tokens * c.num_experts, dev)
     with _on_device(dev, stream) as s:
-        _check("mok_route_bwd", lib().mok_route_bwd(ctypes.byref(c), _ptr(logits), _ptr(topk_idx),
-                                                    _ptr(dw), _ptr(dlogits), s))
+        _check("mok_route_bwd", lib().mok_route_bwd(ctypes.byref(c), logits.data_ptr(), idx, w, dx, s))
 
 
 # ------------------------------------------------------------------------ the optimizer step
@@ -505,19 +520,16 @@ class SumsqPlan:
     """The tensors of a mok_grad_sumsq call, and scratch for it."""
 
     def __init__(self, grads):
-        import torch
         if not grads:
             raise ValueError("no tensors")
-        _need_cuda(*grads)
-        self.keep, self.device, self.elem = list(grads), grads[0].device, _elem(grads[0], "a gradient")
-        for g in grads:
-            if g.dtype != grads[0].dtype:
-                raise ValueError("gradients of one call have one type")
-            _want(g, "a gradient", str(g.dtype).replace("torch.", ""), tuple(g.shape), self.device)
-        self.table = (MokSumsqTensor * len(grads))(*[MokSumsqTensor(g.data_ptr(), g.numel()) for g in grads])
+        self.keep, self.dev, self.elem = list(grads), _device_of(grads[0]), _elem(grads[0], "a gradient")
+        self.table = (MokSumsqTensor * len(grads))(*[
+            MokSumsqTensor(_want(g, f"gradient {i}", grads[0].dtype, g.numel(), self.dev), g.numel())
+            for i, g in enumerate(grads)])
         n = ctypes.c_size_t()
         _check("mok_sumsq_ws_size", lib().mok_sumsq_ws_size(len(grads), ctypes.byref(n)))
-        self.ws = torch.empty(int(n.value), dtype=torch.uint8, device=self.device)
+        self.ws = _tch().empty(int(n.value), dtype=_torch.uint8, device=grads[0].device)
+        self.ws_at = self.ws.data_ptr()
 
 
 def sumsq_plan(grads) -> SumsqPlan:
@@ -527,15 +539,14 @@ def sumsq_plan(grads) -> SumsqPlan:
 def mok_grad_sumsq(plan: SumsqPlan, out, ws=None, stream=None):
     """out (float64 [1]) = sum of squares over every tensor of the plan. Calls that may overlap in time
     need scratch `ws` of their own (as large as plan.ws, which is used without it)."""
-    _need_cuda(out, ws)
-    _want(out, "out", "float64", (1,), plan.device)
+    at = _want(out, "out", _tch().float64, 1, plan.dev)
+    ws_at = plan.ws_at
     if ws is not None:
         if ws.numel() * ws.element_size() < plan.ws.numel():
             raise ValueError(f"ws must hold {plan.ws.numel()} bytes")
-        _want(ws, "ws", str(ws.dtype).replace("torch.", ""), tuple(ws.shape), plan.device)
-    with _on_device(plan.device, stream) as s:
-        _check("mok_grad_sumsq", lib().mok_grad_sumsq(len(plan.table), plan.table, plan.elem, _ptr(out),
-                                                      _ptr(plan.ws if ws is None else ws), s))
+        ws_at = _want(ws, "ws", ws.dtype, ws.numel(), plan.dev)
+    with _on_device(plan.dev, stream) as s:
+        _check("mok_grad_sumsq", lib().mok_grad_sumsq(len(plan.table), plan.table, plan.elem, at, ws_at, s))
 
 
 class AdamwPlan:
@@ -544,42 +555,40 @@ class AdamwPlan:
     scales of 32 elements in m_scale and v_scale) and, for float32 parameters, bfloat16 copies."""
 
     def __init__(self, p, g, m, v, copy=None, m_scale=None, v_scale=None):
-        import torch
+        torch = _tch()
         if not p:
             raise ValueError("no tensors")
         if (m_scale is None) != (v_scale is None):
             raise ValueError("m_scale and v_scale go together")
-        mx = m_scale is not None
         lists = dict(p=p, g=g, m=m, v=v, copy=copy, m_scale=m_scale, v_scale=v_scale)
-        for name, ts in lists.items():
-            if ts is not None and len(ts) != len(p):
-                raise ValueError(f"{name} has {len(ts)} tensors, p {len(p)}")
         self.keep = {k: list(ts) for k, ts in lists.items() if ts is not None}
-        _need_cuda(*[t for ts in self.keep.values() for t in ts])
-        self.device = p[0].device
-        self.param, self.grad = _elem(p[0], "a parameter"), _elem(g[0], "a gradient")
-        self.state = MOK_STATE_MX8 if mx else MOK_STATE_F32
-        if copy is not None and self.param != MOK_ELEM_F32:
+        for name, ts in self.keep.items():
+            if len(ts) != len(p):
+                raise ValueError(f"{name} has {len(ts)} tensors, p {len(p)}")
+        mx = m_scale is not None
+        self.dev, param, grad = _device_of(p[0]), _elem(p[0], "a parameter"), _elem(g[0], "a gradient")
+        if copy is not None and param != MOK_ELEM_F32:
             raise ValueError("only float32 parameters have a bfloat16 copy")
-        text = lambda t: str(t.dtype).replace("torch.", "")
-        types = dict(p=text(p[0]), g=text(g[0]), copy="bfloat16", m="uint8" if mx else "float32",
-                     v="uint8" if mx else "float32", m_scale="uint8", v_scale="uint8")
-        spans = []
+        types = dict(p=p[0].dtype, g=g[0].dtype, copy=torch.bfloat16, m=torch.uint8 if mx else torch.float32,
+                     v=torch.uint8 if mx else torch.float32, m_scale=torch.uint8, v_scale=torch.uint8)
+        rows, spans = [], []
         for i in range(len(p)):
-            n = p[i].numel()
+            n, row = p[i].numel(), MokAdamwTensor()
             for name, ts in self.keep.items():
-                want = (-(-n // 32),) if name.endswith("_scale") else (n,)
-                _want(ts[i], f"{name}[{i}]", types[name], want, self.device)
+                count = -(-n // 32) if name.endswith("_scale") else n
+                at = _want(ts[i], f"{name}[{i}]", types[name], count, self.dev)
+                setattr(row, name, at)
                 if name != "g" and n:
-                    spans.append((ts[i].data_ptr(), ts[i].numel() * ts[i].element_size(), f"{name}[{i}]"))
+                    spans.append((at, count * ts[i].element_size(), f"{name}[{i}]"))
+            row.n = n
+            rows.append(row)
         spans.sort()
         for (a, size, x), (b, _, y) in zip(spans, spans[1:]):
             if a + size > b:
                 raise ValueError(f"{x} and {y} share memory")
-        at = lambda name, i: self.keep[name][i].data_ptr() if name in self.keep else None
-        self.table = (MokAdamwTensor * len(p))(*[
-            MokAdamwTensor(at("p", i), at("copy", i), at("g", i), at("m", i), at("v", i), at("m_scale", i),
-                           at("v_scale", i), p[i].numel()) for i in range(len(p))])
+        self.table = (MokAdamwTensor * len(p))(*rows)
+        self.config = MokAdamwConfig(grad_elem=grad, param_elem=param,
+                                     state=MOK_STATE_MX8 if mx else MOK_STATE_F32)
 
 
 def adamw_plan(p, g, m, v, copy=None, m_scale=None, v_scale=None) -> AdamwPlan:
@@ -593,20 +602,24 @@ def mok_adamw(plan: AdamwPlan, lr, step, beta1: float = 0.9, beta2: float = 0.99
     [1], int64 [1]), read when the step runs. With `sumsq` (float64 [1], the squared norm of all
     gradients) gradients are clipped to `max_norm` (None: not clipped) and a step whose norm is not
     finite changes nothing."""
-    import torch
-    dev = {}
-    for name, x, dtype in (("lr", lr, "float64"), ("step", step, "int64"), ("sumsq", sumsq, "float64")):
-        if isinstance(x, torch.Tensor):
-            _need_cuda(x)
-            _want(x, name, dtype, (1,), plan.device)
-            dev[name] = x.data_ptr()
-        elif name == "sumsq" and x is not None:
+    torch = _tch()
+    c = MokAdamwConfig.from_buffer_copy(plan.config)
+    if isinstance(lr, torch.Tensor):
+        c.lr_dev = _want(lr, "lr", torch.float64, 1, plan.dev)
+    else:
+        c.lr = lr
+    if isinstance(step, torch.Tensor):
+        c.step_dev, c.step = _want(step, "step", torch.int64, 1, plan.dev), 1
+    else:
+        c.step = step
+    if sumsq is not None:
+        if not isinstance(sumsq, torch.Tensor):
             raise ValueError("sumsq is a device tensor")
-    if max_norm is not None and sumsq is None:
+        c.sumsq_dev = _want(sumsq, "sumsq", torch.float64, 1, plan.dev)
+    elif max_norm is not None:
         raise ValueError("max_norm needs sumsq, the squared norm of all gradients")
-    c = MokAdamwConfig(0.0 if "lr" in dev else lr, beta1, beta2, eps, weight_decay,
-                       float("inf") if max_norm is None else max_norm, 1 if "step" in dev else step,
-                       seed & 0xFFFFFFFF, plan.grad, plan.param, plan.state, dev.get("sumsq"),
-                       dev.get("lr"), dev.get("step"))
-    with _on_device(plan.device, stream) as s:
+    c.beta1, c.beta2, c.eps, c.weight_decay = beta1, beta2, eps, weight_decay
+    c.max_norm = float("inf") if max_norm is None else max_norm
+    c.seed = seed & 0xFFFFFFFF
+    with _on_device(plan.dev, stream) as s:
         _check("mok_adamw", lib().mok_adamw(len(plan.table), plan.table, ctypes.byref(c), s))

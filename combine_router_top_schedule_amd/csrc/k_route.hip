@@ -66,6 +66,41 @@ __device__ __forceinline__ float log_sigmoid(float x) {
   return fminf(x, 0.f) - log1pf(expf(-fabsf(x)));
 }
 
+// ---- exchanges between lanes
+template <int OFF>
+__device__ __forceinline__ float lane_xor(float v) {
+  const int x = __float_as_int(v);
+  // (after the steps below it, a partner in the mirrored place of the other half holds what the xor-ed
+  // lane holds)
+  if constexpr (OFF == 1) return __int_as_float(__builtin_amdgcn_mov_dpp(x, 0xB1, 0xF, 0xF, true));
+  else if constexpr (OFF == 2) return __int_as_float(__builtin_amdgcn_mov_dpp(x, 0x4E, 0xF, 0xF, true));
+  else if constexpr (OFF == 4) return __int_as_float(__builtin_amdgcn_mov_dpp(x, 0x141, 0xF, 0xF, true));
+  else if constexpr (OFF == 8) return __int_as_float(__builtin_amdgcn_mov_dpp(x, 0x140, 0xF, 0xF, true));
+  else return __shfl_xor(v, OFF, 64);
+}
+template <int CTRL>   // a permutation of every 4 lanes
+__device__ __forceinline__ int quad(int v) { return __builtin_amdgcn_mov_dpp(v, CTRL, 0xF, 0xF, true); }
+template <int CTRL>
+__device__ __forceinline__ float quad(float v) { return __int_as_float(quad<CTRL>(__float_as_int(v))); }
+template <int L>
+__device__ __forceinline__ float lanes_max(float v) {
+  v = fmaxf(v, lane_xor<1>(v));
+  v = fmaxf(v, lane_xor<2>(v));
+  v = fmaxf(v, lane_xor<4>(v));
+  if constexpr (L > 8) v = fmaxf(v, lane_xor<8>(v));
+  if constexpr (L > 16) v = fmaxf(v, lane_xor<16>(v));
+  return v;
+}
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+  v += lane_xor<1>(v);
+  v += lane_xor<2>(v);
+  v += lane_xor<4>(v);
+  if constexpr (L > 8) v += lane_xor<8>(v);
+  if constexpr (L > 16) v += lane_xor<16>(v);
+  return v;
+}
+
 // ---- one token by a whole wave, keys in fp64 -----------------------------------------------------
 // Largest of the wave's values, in every lane: shifts within rows of 16 lanes, then broadcasts of a row's
 // last lane to the next rows; lanes without a source keep their own value.
@@ -92,39 +127,42 @@ __device__ __forceinline__ double wave_max(double v) {
 }
 
 // key: LDS, one double per expert, private to the wave. Returns the expert chosen by slot `lane`
-// (lane < K), -1 where none is left.
+// (lane < K), -1 where none is left. Written for few instructions (one exponential, one quotient): where
+// a token in ten thousand needs it, most of its time goes into fetching them (11 us with the loops unrolled).
 template <bool BF16>
 __device__ __forceinline__ int choose_wave(const RouteArgs& a, int64_t n, int lane, double* key) {
   const double kNone = -INFINITY;
   const int64_t row = n * a.ld;
-  double top = kNone, sum = 0;
-  if (!a.sigmoid && (a.bias || (a.G > 1 && a.top2))) {
-    for (int e = lane; e < a.E; e += 64) top = fmax(top, double(logit<BF16>(a.x, row + e)));
-    for (int off = 32; off; off >>= 1) top = fmax(top, __shfl_xor(top, off, 64));
-    for (int e = lane; e < a.E; e += 64) sum += exp(double(logit<BF16>(a.x, row + e)) - top);
+  const bool top2 = a.G > 1 && a.top2;
+  double sum = 0;
+  // logits
+  float most = -INFINITY;
+  for (int e = lane; e < a.E; e += 64) {
+    const float x = logit<BF16>(a.x, row + e);
+    key[e] = x;
+    most = fmaxf(most, x);
+  }
+  if (a.bias || top2) {
+    // exp(-x), or exp(x - largest) and their sum
+    for (int off = 32; off; off >>= 1) most = fmaxf(most, __shfl_xor(most, off, 64));
+#pragma unroll 1
+    for (int e = lane; e < a.E; e += 64) {
+      const double t = exp(a.sigmoid ? -key[e] : key[e] - double(most));
+      key[e] = t;
+      sum += t;
+    }
     for (int off = 32; off; off >>= 1) sum += __shfl_xor(sum, off, 64);
-  }
-  auto score = [&](double x) { return a.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - top) / sum; };
-  // (four at a time: their loads, and then their exponentials, overlap)
-  for (int e0 = lane; e0 < a.E; e0 += 256) {
-    float x[4], b[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int e = min(e0 + 64 * q, a.E - 1);
-      x[q] = logit<BF16>(a.x, row + e);
-      b[q] = a.bias ? a.bias[e] : 0.f;
+    // scores, with their bias
+#pragma unroll 1
+    for (int e = lane; e < a.E; e += 64) {
+      const float x = logit<BF16>(a.x, row + e), b = a.bias ? a.bias[e] : 0.f;
+      const double t = key[e];
+      const double k = (a.sigmoid ? 1.0 : t) / (a.sigmoid ? 1.0 + t : sum) + double(b);
+      key[e] = x > -INFINITY && k > kNone ? k : kNone;
     }
-    double k[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) k[q] = x[q];
-    if (a.bias) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) k[q] = score(k[q]) + double(b[q]);
-    }
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (e0 + 64 * q < a.E) key[e0 + 64 * q] = x[q] > -INFINITY && k[q] > kNone ? k[q] : kNone;
   }
+  if (!a.bias && !top2)
+    for (int e = lane; e < a.E; e += 64) key[e] = key[e] > kNone ? key[e] : kNone;   // NaN is not able
   wave_sync();
   if (a.G > 1) {
     // P lanes a group: each the two largest of its experts, then those of the P lanes
@@ -133,13 +171,14 @@ __device__ __forceinline__ int choose_wave(const RouteArgs& a, int64_t n, int la
     const int g = lane / P;
     double best = kNone, second = kNone;
     if (g < a.G)
-#pragma unroll 4
+#pragma unroll 2
       for (int i = lane % P; i < a.gs; i += P) {
-        double k = key[g * a.gs + i];
-        if (a.top2 && !a.bias && k > kNone) k = score(k);
-        if (k > best) { second = best; best = k; }
-        else if (k > second) second = k;
+        const double k = key[g * a.gs + i];
+        const double low = k < best ? k : best;
+        second = low > second ? low : second;
+        best = k > best ? k : best;
       }
+#pragma unroll 1
     for (int off = P >> 1; off; off >>= 1) {
       const double b = __shfl_xor(best, off, 64), c = __shfl_xor(second, off, 64);
       const double low = b < best ? b : best;
@@ -149,21 +188,27 @@ __device__ __forceinline__ int choose_wave(const RouteArgs& a, int64_t n, int la
     }
     if (a.top2 && second > kNone) best += second;
     int place = 0;
+#pragma unroll 2
     for (int o = 0; o < a.G; ++o) {
       const double other = __shfl(best, o * P, 64);
       place += other > best || (other == best && o < g);
     }
     const uint64_t stay = __ballot(g < a.G && place < a.Kg);
     wave_sync();
-    for (int e = lane; e < a.E; e += 64)
-      if (!((stay >> (e / a.gs * P)) & 1)) key[e] = kNone;
+#pragma unroll 1
+    for (int e = lane; e < a.E; e += 64) {
+      const bool in = (stay >> (e / a.gs * P)) & 1;
+      // (groups ranked by scores: from here on the logits decide)
+      if (in && !a.bias && top2 && key[e] > kNone) key[e] = logit<BF16>(a.x, row + e);
+      if (!in) key[e] = kNone;
+    }
     wave_sync();
   }
   int mine = -1;
+#pragma unroll 1
   for (int k = 0; k < a.K; ++k) {
     double best = kNone;
     int at = a.E;
-#pragma unroll 4
     for (int e = lane; e < a.E; e += 64) {
       const double v = key[e];
       if (v > best) { best = v; at = e; }
@@ -183,32 +228,39 @@ __device__ __forceinline__ int choose_wave(const RouteArgs& a, int64_t n, int la
   return mine;
 }
 
+// Weight from a chosen expert's logit v: a softmax over the chosen of v or log sigmoid(v) among the `W` lanes
+// of its token, or the score itself (top, sum: the row's largest logit and the sum of its
+// exponentials).
+template <int W>
+__device__ __forceinline__ float slot_weight(const RouteArgs& a, bool some, float v, float top, float sum) {
+  float w;
+  if (a.renorm) {
+    // (log sigmoid, to a few units of 2^-23 of max(1, |f|): it goes into an exponential)
+    const float f = a.sigmoid ? fminf(v, 0.f) - __logf(1.f + __expf(-fabsf(v))) : v;
+    const float top_f = lanes_max<W>(f);   // (every lane takes part in the exchanges)
+    const float q = some ? __expf(f - top_f) : 0.f;
+    w = q / lanes_sum<W>(q);
+  } else {
+    w = a.sigmoid ? 1.f / (1.f + __expf(-v)) : __expf(v - top) / sum;
+  }
+  return some ? w * a.scale : 0.f;
+}
+
 // Weight of the expert in slot `lane` (lane < K; e < 0: none), by a whole wave.
 template <bool BF16>
 __device__ __forceinline__ float weight_wave(const RouteArgs& a, int64_t n, int lane, int e) {
   const int64_t row = n * a.ld;
   const bool some = lane < a.K && e >= 0;
-  const float x = some ? logit<BF16>(a.x, row + e) : -INFINITY;
-  float w;
-  if (a.renorm) {
-    const float f = a.sigmoid ? log_sigmoid(x) : x;
-    float top = f;
-    for (int off = 8; off; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 16));
-    const float q = some ? expf(f - top) : 0.f;
-    float sum = q;
-    for (int off = 8; off; off >>= 1) sum += __shfl_xor(sum, off, 16);
-    w = q / sum;
-  } else if (a.sigmoid) {
-    w = 1.f / (1.f + expf(-x));
-  } else {
-    float top = -INFINITY, sum = 0.f;
+  float top = 0.f, sum = 1.f;
+  if (!a.sigmoid && !a.renorm) {
+    top = -INFINITY;
+    sum = 0.f;
     for (int i = lane; i < a.E; i += 64) top = fmaxf(top, logit<BF16>(a.x, row + i));
     for (int off = 32; off; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
-    for (int i = lane; i < a.E; i += 64) sum += expf(logit<BF16>(a.x, row + i) - top);
+    for (int i = lane; i < a.E; i += 64) sum += __expf(logit<BF16>(a.x, row + i) - top);
     for (int off = 32; off; off >>= 1) sum += __shfl_xor(sum, off, 64);
-    w = expf(x - top) / sum;
   }
-  return some ? w * a.scale : 0.f;
+  return slot_weight<16>(a, some, some ? logit<BF16>(a.x, row + e) : -INFINITY, top, sum);
 }
 
 template <bool BF16>
@@ -257,40 +309,6 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_fwd(RouteArgs a) {
 //   4. those few candidates (nearly always exactly K) are ranked by counting. Two whose fp32 keys are
 //      further apart than 2 eps are in that order; two of the same logit and bias are tied; a token
 //      with two others, or with more than 2 KM candidates, goes to choose_wave.
-template <int OFF>
-__device__ __forceinline__ float lane_xor(float v) {
-  const int x = __float_as_int(v);
-  // (after the steps below it, a partner in the mirrored place of the other half holds what the xor-ed
-  // lane holds)
-  if constexpr (OFF == 1) return __int_as_float(__builtin_amdgcn_mov_dpp(x, 0xB1, 0xF, 0xF, true));
-  else if constexpr (OFF == 2) return __int_as_float(__builtin_amdgcn_mov_dpp(x, 0x4E, 0xF, 0xF, true));
-  else if constexpr (OFF == 4) return __int_as_float(__builtin_amdgcn_mov_dpp(x, 0x141, 0xF, 0xF, true));
-  else if constexpr (OFF == 8) return __int_as_float(__builtin_amdgcn_mov_dpp(x, 0x140, 0xF, 0xF, true));
-  else return __shfl_xor(v, OFF, 64);
-}
-template <int CTRL>   // a permutation of every 4 lanes
-__device__ __forceinline__ int quad(int v) { return __builtin_amdgcn_mov_dpp(v, CTRL, 0xF, 0xF, true); }
-template <int CTRL>
-__device__ __forceinline__ float quad(float v) { return __int_as_float(quad<CTRL>(__float_as_int(v))); }
-template <int L>
-__device__ __forceinline__ float lanes_max(float v) {
-  v = fmaxf(v, lane_xor<1>(v));
-  v = fmaxf(v, lane_xor<2>(v));
-  v = fmaxf(v, lane_xor<4>(v));
-  if constexpr (L > 8) v = fmaxf(v, lane_xor<8>(v));
-  if constexpr (L > 16) v = fmaxf(v, lane_xor<16>(v));
-  return v;
-}
-template <int L>
-__device__ __forceinline__ float lanes_sum(float v) {
-  v += lane_xor<1>(v);
-  v += lane_xor<2>(v);
-  v += lane_xor<4>(v);
-  if constexpr (L > 8) v += lane_xor<8>(v);
-  if constexpr (L > 16) v += lane_xor<16>(v);
-  return v;
-}
-
 // Larger value to a, smaller to b.
 __device__ __forceinline__ void order(float& a, float& b) {
   const float hi = fmaxf(a, b), lo = fminf(a, b);
@@ -667,16 +685,7 @@ __global__ __launch_bounds__(64 * kWaves, L * V >= 1024 ? 3 : 4) void k_route_fa
     const int e = j < filled ? s.out[t][j] : -1;
     const bool some = e >= 0;
     const float v = some ? logit<BF16>(a.x, n * a.ld + e) : -INFINITY;
-    float w;
-    if (a.renorm) {
-      // (log sigmoid, to a few units of 2^-23 of max(1, |f|): it goes into an exponential)
-      const float f = a.sigmoid ? fminf(v, 0.f) - __logf(1.f + __expf(-fabsf(v))) : v;
-      const float first = lanes_max<L>(f);
-      const float q = some ? __expf(f - first) : 0.f;
-      w = q / lanes_sum<L>(q);
-    } else {
-      w = a.sigmoid ? 1.f / (1.f + __expf(-v)) : __expf(v - top) / sum;
-    }
+    const float w = slot_weight<L>(a, some, v, top, sum);
     if (const uint64_t who = __ballot(slow && j == 0)) {
       const int at = later + __popcll(who & ((1ull << lane) - 1));
       if (slow && j == 0 && at < kListed) s.later[at] = n;
@@ -684,7 +693,7 @@ __global__ __launch_bounds__(64 * kWaves, L * V >= 1024 ? 3 : 4) void k_route_fa
     }
     if (n < a.N && j < a.K) {
       a.idx[n * a.K + j] = slow ? kLater : e;
-      a.w[n * a.K + j] = some ? w * a.scale : 0.f;
+      a.w[n * a.K + j] = w;
       if (a.load && some) atomicAdd(&s_load[e], 1);
     }
     wave_sync();
