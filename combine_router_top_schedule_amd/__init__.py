@@ -447,6 +447,13 @@ def _device_of(t) -> int:
     return dev
 
 
+def _raw_stream(dev: int) -> int:
+    """The current stream of device number `dev` (torch's own short way to its handle where it has one:
+    a tenth of a microsecond instead of one)."""
+    short = getattr(_torch._C, "_cuda_getCurrentRawStream", None)
+    return short(dev) if short is not None else _torch.cuda.current_stream(dev).cuda_stream
+
+
 class _on_device:
     """Makes device number `dev` current around a call (the library launches on the current device) and
     gives the stream to use: the one asked for, or the device's current one."""
@@ -456,10 +463,11 @@ class _on_device:
     def __init__(self, dev: int, stream):
         torch = _tch()
         if stream is None:
-            stream = torch.cuda.current_stream(dev)
+            self.raw = _raw_stream(dev)
         elif stream.device.index != dev:
             raise ValueError(f"the stream is on {stream.device}, the tensors are on device {dev}")
-        self.raw = stream.cuda_stream
+        else:
+            self.raw = stream.cuda_stream
         self.guard = None if torch.cuda.current_device() == dev else torch.cuda.device(dev)
 
     def __enter__(self):
@@ -528,7 +536,7 @@ class SumsqPlan:
             for i, g in enumerate(grads)])
         n = ctypes.c_size_t()
         _check("mok_sumsq_ws_size", lib().mok_sumsq_ws_size(len(grads), ctypes.byref(n)))
-        self.ws = _tch().empty(int(n.value), dtype=_torch.uint8, device=grads[0].device)
+        self.ws = _tch().zeros(int(n.value), dtype=_torch.uint8, device=grads[0].device)
         self.ws_at = self.ws.data_ptr()
 
 
@@ -538,7 +546,8 @@ def sumsq_plan(grads) -> SumsqPlan:
 
 def mok_grad_sumsq(plan: SumsqPlan, out, ws=None, stream=None):
     """out (float64 [1]) = sum of squares over every tensor of the plan. Calls that may overlap in time
-    need scratch `ws` of their own (as large as plan.ws, which is used without it)."""
+    need scratch `ws` of their own (as large as plan.ws, which is used without it, and zero-filled before its
+    first use)."""
     at = _want(out, "out", _tch().float64, 1, plan.dev)
     ws_at = plan.ws_at
     if ws is not None:

@@ -19,8 +19,9 @@ namespace {
 
 // ---- sum of squares -------------------------------------------------------------------------
 constexpr int kSqTensors = 160;      // tensors a launch takes (kernel arguments hold 4 KB)
-constexpr int kSqBlocks = 1024;      // workgroups of a launch; fixed, so sums do not depend on the device
-constexpr int kSqChunk = 4096;       // elements of a chunk
+constexpr int kSqThreads = 512;
+constexpr int kSqBlocks = 512;       // workgroups of a launch; fixed, so sums do not depend on the device
+constexpr int kSqChunk = 8192;       // elements of a chunk: 4 loads of 16 bytes a thread in flight
 
 struct SqArgs {
   const void* g[kSqTensors];
@@ -28,70 +29,102 @@ struct SqArgs {
   int32_t first[kSqTensors + 1];     // chunks before tensor t
   int32_t count;
   double* part;
+  uint32_t* ticket;                  // of the last launch: workgroups that have written their sum (else null)
+  int64_t parts;                     // sums of all launches
+  double* out;
 };
 
+// The tensor of chunk c: the last t with first[t] <= c. Every lane looks at one prefix sum (a binary search
+// took 6 dependent loads, each some 0.3 us).
 template <int CAP>
 __device__ __forceinline__ int find_tensor(const int32_t (&first)[CAP], int count, int c) {
-  int lo = 0, hi = count;   // first[lo] <= c < first[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (first[mid] <= c) lo = mid;
-    else hi = mid;
+  const int lane = threadIdx.x & 63;
+  int before = 0;
+#pragma unroll
+  for (int i = 0; i < CAP; i += 64) {
+    const bool in = i + lane < count && first[min(i + lane, CAP - 1)] <= c;
+    before += __popcll(__ballot(in));
   }
-  return lo;
+  return before - 1;
 }
 
-// Sum over a workgroup of 256, in a fixed order; the result in thread 0.
+// Sum over a workgroup, in a fixed order; the result in thread 0.
 __device__ __forceinline__ double block_sum(double v) {
-  __shared__ double s[4];
+  __shared__ double s[kSqThreads / 64];
   for (int off = 32; off; off >>= 1) v += __shfl_xor(v, off, 64);
+  __syncthreads();   // (an earlier call's readers)
   if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
   __syncthreads();
-  return s[0] + s[1] + s[2] + s[3];
+  double sum = 0;
+  for (int w = 0; w < kSqThreads / 64; ++w) sum += s[w];
+  return sum;
+}
+
+// Four consecutive elements from i on, those past n as zero.
+template <bool BF16>
+__device__ __forceinline__ void load_sq(const void* g, int64_t i, int64_t n, float (&v)[4]) {
+  if (i + 4 <= n) {
+    if constexpr (BF16) {
+      const uint2 b = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(g) + i);
+      v[0] = bf2f(uint16_t(b.x)); v[1] = bf2f(uint16_t(b.x >> 16));
+      v[2] = bf2f(uint16_t(b.y)); v[3] = bf2f(uint16_t(b.y >> 16));
+    } else {
+      const f32x4 b = *reinterpret_cast<const f32x4*>(static_cast<const float*>(g) + i);
+      for (int j = 0; j < 4; ++j) v[j] = b[j];
+    }
+  } else {
+    for (int j = 0; j < 4; ++j) {
+      v[j] = 0.f;
+      if (i + j < n) {
+        if constexpr (BF16) v[j] = bf2f(static_cast<const uint16_t*>(g)[i + j]);
+        else v[j] = static_cast<const float*>(g)[i + j];
+      }
+    }
+  }
 }
 
 template <bool BF16>
-__global__ __launch_bounds__(256) void k_sumsq(SqArgs a) {
+__global__ __launch_bounds__(kSqThreads) void k_sumsq(SqArgs a) {
   double sum = 0;
   for (int c = blockIdx.x; c < a.first[a.count]; c += gridDim.x) {
-    const int t = find_tensor(a.first, a.count, c);
-    const int64_t i0 = int64_t(c - a.first[t]) * kSqChunk, n = a.n[t];
-    for (int u = 0; u < kSqChunk / 1024; ++u) {
-      const int64_t i = i0 + u * 1024 + threadIdx.x * 4;
-      float v[4] = {0.f, 0.f, 0.f, 0.f};
-      if (i + 4 <= n) {
-        if constexpr (BF16) {
-          const uint2 b = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.g[t]) + i);
-          v[0] = bf2f(uint16_t(b.x)); v[1] = bf2f(uint16_t(b.x >> 16));
-          v[2] = bf2f(uint16_t(b.y)); v[3] = bf2f(uint16_t(b.y >> 16));
-        } else {
-          const f32x4 b = *reinterpret_cast<const f32x4*>(static_cast<const float*>(a.g[t]) + i);
-          for (int j = 0; j < 4; ++j) v[j] = b[j];
-        }
-      } else {
-        for (int j = 0; j < 4; ++j)
-          if (i + j < n) {
-            if constexpr (BF16) v[j] = bf2f(static_cast<const uint16_t*>(a.g[t])[i + j]);
-            else v[j] = static_cast<const float*>(a.g[t])[i + j];
-          }
-      }
-      for (int j = 0; j < 4; ++j) sum = fma(double(v[j]), double(v[j]), sum);
-    }
+    const int t = __builtin_amdgcn_readfirstlane(find_tensor(a.first, a.count, c));
+    const int64_t i0 = int64_t(c - a.first[t]) * kSqChunk + threadIdx.x * 4, n = a.n[t];
+    constexpr int U = kSqChunk / (4 * kSqThreads);
+    float v[U][4];
+#pragma unroll
+    for (int u = 0; u < U; ++u) load_sq<BF16>(a.g[t], i0 + u * 4 * kSqThreads, n, v[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      for (int j = 0; j < 4; ++j) sum = fma(double(v[u][j]), double(v[u][j]), sum);
   }
   sum = block_sum(sum);
-  if (threadIdx.x == 0) a.part[blockIdx.x] = sum;
-}
-
-__global__ __launch_bounds__(256) void k_sumsq_join(const double* part, int64_t n, double* out) {
-  double sum = 0;
-  for (int64_t i = threadIdx.x; i < n; i += 256) sum += part[i];
-  sum = block_sum(sum);
-  if (threadIdx.x == 0) *out = sum;
+  // The sums of all workgroups are joined, in the order of their numbers, by the one that comes last; a
+  // second launch for that took 4 us. Sums and ticket go through agent-scope accesses, which are coherent
+  // across XCDs: a sum has arrived (the wait) before its workgroup is counted.
+  __shared__ bool s_last;
+  if (threadIdx.x == 0) {
+    __hip_atomic_store(a.part + blockIdx.x, sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    s_last = a.ticket && __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                             gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!s_last) return;
+  double all = 0;
+  const double* first = a.part + gridDim.x - a.parts;   // this launch's sums are the last ones
+  for (int64_t i = threadIdx.x; i < a.parts; i += kSqThreads)
+    all += __hip_atomic_load(first + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  all = block_sum(all);
+  if (threadIdx.x == 0) {
+    *a.out = all;
+    st_relaxed_u(a.ticket, 0u);   // ready for the next call
+  }
 }
 
 // ---- AdamW ------------------------------------------------------------------------------------
 constexpr int kAdTensors = 48;       // tensors a launch takes
-constexpr int kAdChunk = 4096;       // elements a workgroup updates
+constexpr int kAdUnroll = 1;         // groups of 4 elements a thread updates
+constexpr int kAdChunk = 1024 * kAdUnroll;   // elements a workgroup updates
 
 struct AdamArgs {
   void* p[kAdTensors];
@@ -259,34 +292,44 @@ __global__ __launch_bounds__(256) void k_adamw(AdamArgs a) {
     rbc2 = float(1.0 / sqrt(1.0 - pow(a.beta2, step)));
   }
   const int c = blockIdx.x;
-  const int t = find_tensor(a.first, a.count, c);
+  const int t = __builtin_amdgcn_readfirstlane(find_tensor(a.first, a.count, c));
   const int64_t n = a.n[t];
+  const int64_t i0 = int64_t(c - a.first[t]) * kAdChunk + threadIdx.x * 4;
   const uint32_t salt = mix(a.seed + uint32_t(a.number0 + t) * 0x9E3779B1u);
-  for (int q = 0; q < kAdChunk / 1024; ++q) {
-    const int64_t i = int64_t(c - a.first[t]) * kAdChunk + q * 1024 + threadIdx.x * 4;
-    if (__ballot(i < n) == 0) break;
-    float g[4], p[4], m[4], v[4];
-    load4(static_cast<const std::conditional_t<GBF, uint16_t, float>*>(a.g[t]), i, n, g);
-    load4(static_cast<const std::conditional_t<PBF, uint16_t, float>*>(a.p[t]), i, n, p);
-    if constexpr (MX8) {
-      const uint32_t cm = load4(static_cast<const uint8_t*>(a.m[t]), i, n);
-      const uint32_t cv = load4(static_cast<const uint8_t*>(a.v[t]), i, n);
-      decode4(cm, i < n ? a.ms[t][i >> 5] : 0u, m);
-      decode4(cv, i < n ? a.vs[t][i >> 5] : 0u, v);
+  float g[kAdUnroll][4], p[kAdUnroll][4], m[kAdUnroll][4], v[kAdUnroll][4];
+  uint32_t code[kAdUnroll][2], scale[kAdUnroll][2];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = v[j] * v[j];
+  for (int q = 0; q < kAdUnroll; ++q) {
+    const int64_t i = i0 + 1024 * q;
+    load4(static_cast<const std::conditional_t<GBF, uint16_t, float>*>(a.g[t]), i, n, g[q]);
+    load4(static_cast<const std::conditional_t<PBF, uint16_t, float>*>(a.p[t]), i, n, p[q]);
+    if constexpr (MX8) {
+      code[q][0] = load4(static_cast<const uint8_t*>(a.m[t]), i, n);
+      code[q][1] = load4(static_cast<const uint8_t*>(a.v[t]), i, n);
+      scale[q][0] = i < n ? a.ms[t][i >> 5] : 0u;
+      scale[q][1] = i < n ? a.vs[t][i >> 5] : 0u;
     } else {
-      load4(static_cast<const float*>(a.m[t]), i, n, m);
-      load4(static_cast<const float*>(a.v[t]), i, n, v);
+      load4(static_cast<const float*>(a.m[t]), i, n, m[q]);
+      load4(static_cast<const float*>(a.v[t]), i, n, v[q]);
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < kAdUnroll; ++q) {
+    const int64_t i = i0 + 1024 * q;
+    if constexpr (MX8) {
+      decode4(code[q][0], scale[q][0], m[q]);
+      decode4(code[q][1], scale[q][1], v[q]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[q][j] = v[q][j] * v[q][j];
     }
     float r[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float gj = g[j] * clip;
-      m[j] = m[j] * a.b1 + gj * a.c1;
-      v[j] = v[j] * a.b2 + (gj * gj) * a.c2;
-      r[j] = sqrtf(v[j]);
-      p[j] = p[j] * decay - (m[j] / (r[j] * rbc2 + a.eps)) * rate;
+      const float gj = g[q][j] * clip;
+      m[q][j] = m[q][j] * a.b1 + gj * a.c1;
+      v[q][j] = v[q][j] * a.b2 + (gj * gj) * a.c2;
+      r[j] = sqrtf(v[q][j]);
+      p[q][j] = p[q][j] * decay - (m[q][j] / (r[j] * rbc2 + a.eps)) * rate;
     }
     uint32_t h[4], u[4];
     if constexpr (MX8 || PBF) {
@@ -296,17 +339,17 @@ __global__ __launch_bounds__(256) void k_adamw(AdamArgs a) {
     }
     if constexpr (PBF) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) u[j] = bf16_random(p[j], mix(h[j] ^ 0x3C6EF372u) & 0xFFFFu);
+      for (int j = 0; j < 4; ++j) u[j] = bf16_random(p[q][j], mix(h[j] ^ 0x3C6EF372u) & 0xFFFFu);
       store4(static_cast<uint16_t*>(a.p[t]), i, n, uint2{u[0] | u[1] << 16, u[2] | u[3] << 16});
     } else {
-      store4(static_cast<float*>(a.p[t]), i, n, p);
-      if (a.copy[t]) store4(a.copy[t], i, n, uint2{pack_bf2(p[0], p[1]), pack_bf2(p[2], p[3])});
+      store4(static_cast<float*>(a.p[t]), i, n, p[q]);
+      if (a.copy[t]) store4(a.copy[t], i, n, uint2{pack_bf2(p[q][0], p[q][1]), pack_bf2(p[q][2], p[q][3])});
     }
     if constexpr (MX8) {
       uint32_t sm, sv;
 #pragma unroll
       for (int j = 0; j < 4; ++j) u[j] = h[j] & 0xFFFFu;
-      const uint32_t cm = encode4<false>(m, u, &sm);
+      const uint32_t cm = encode4<false>(m[q], u, &sm);
 #pragma unroll
       for (int j = 0; j < 4; ++j) u[j] = h[j] >> 16;
       const uint32_t cv = encode4<true>(r, u, &sv);
@@ -317,8 +360,8 @@ __global__ __launch_bounds__(256) void k_adamw(AdamArgs a) {
         a.vs[t][i >> 5] = uint8_t(sv);
       }
     } else {
-      store4(static_cast<float*>(a.m[t]), i, n, m);
-      store4(static_cast<float*>(a.v[t]), i, n, v);
+      store4(static_cast<float*>(a.m[t]), i, n, m[q]);
+      store4(static_cast<float*>(a.v[t]), i, n, v[q]);
     }
   }
 }
@@ -331,15 +374,18 @@ void adamw_kernel(bool mx, const AdamArgs& a, int blocks, hipStream_t s) {
 
 }  // namespace
 
+// The ticket (64 bytes), then a sum per workgroup of every launch.
 int64_t sumsq_ws_bytes(int count) {
-  return 8 * int64_t(kSqBlocks) * std::max<int64_t>(1, cdiv(count, kSqTensors));
+  return 64 + 8 * int64_t(kSqBlocks) * std::max<int64_t>(1, cdiv(count, kSqTensors));
 }
 
-hipError_t launch_sumsq(int count, const mok_sumsq_tensor* t, bool bf16, double* out, double* ws,
+hipError_t launch_sumsq(int count, const mok_sumsq_tensor* t, bool bf16, double* out, uint8_t* ws,
                         hipStream_t s) {
-  int64_t parts = 0;
-  for (int t0 = 0; t0 < count;) {
-    SqArgs a;
+  SqArgs a;
+  a.out = out;
+  a.parts = 0;
+  int t0 = 0;
+  do {   // (without an element, one launch writes 0)
     a.count = 0;
     int64_t chunks = 0;
     a.first[0] = 0;
@@ -351,17 +397,17 @@ hipError_t launch_sumsq(int count, const mok_sumsq_tensor* t, bool bf16, double*
       chunks += cdiv(t[t0].n, kSqChunk);
       a.first[++a.count] = int32_t(chunks);
     }
-    if (a.count == 0) break;
-    a.part = ws + parts;
-    const int blocks = int(std::min<int64_t>(chunks, kSqBlocks));
-    if (bf16) hipLaunchKernelGGL(k_sumsq<true>, dim3(blocks), dim3(256), 0, s, a);
-    else hipLaunchKernelGGL(k_sumsq<false>, dim3(blocks), dim3(256), 0, s, a);
+    while (t0 < count && t[t0].n == 0) ++t0;
+    const int blocks = int(std::max<int64_t>(1, std::min<int64_t>(chunks, kSqBlocks)));
+    a.part = reinterpret_cast<double*>(ws + 64) + a.parts;
+    a.parts += blocks;
+    a.ticket = t0 < count ? nullptr : reinterpret_cast<uint32_t*>(ws);
+    if (bf16) hipLaunchKernelGGL(k_sumsq<true>, dim3(blocks), dim3(kSqThreads), 0, s, a);
+    else hipLaunchKernelGGL(k_sumsq<false>, dim3(blocks), dim3(kSqThreads), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    parts += blocks;
-  }
-  hipLaunchKernelGGL(k_sumsq_join, dim3(1), dim3(256), 0, s, ws, parts, out);
-  return hipGetLastError();
+  } while (t0 < count);
+  return hipSuccess;
 }
 
 hipError_t launch_adamw(int count, const mok_adamw_tensor* t, const mok_adamw_config& c, hipStream_t s) {

@@ -371,7 +371,8 @@ __device__ __attribute__((noinline)) void choose_later(const RouteArgs* args, do
   }
   const int lane = threadIdx.x & 63;
   const bool listed = count <= kListed;
-  if (!listed) __builtin_amdgcn_s_waitcnt(0);   // this wave's own stores, read back past the CU's cache
+  // (this wave's own stores, read back past the CU's cache)
+  if (!listed) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   for (int64_t i0 = 0;; i0 += 64) {
     // 64 numbers at a time: those of the list, or all
     const int64_t i = i0 + lane;
@@ -918,7 +919,10 @@ hipError_t launch_route_fwd(const mok_route_desc& d, const void* x, const float*
   // groups that are not made of whole runs of 4 experts, or more of them than lanes, go one token a wave
   const bool fast = a.G == 1 || (a.gs % 4 == 0 && a.G <= lanes);
   if (a.gs >= 4) a.chunk_magic = uint32_t(cdiv(65536, a.gs / 4));
-  const int grid = grid_of(a.N, fast ? kWaves * 64 / lanes : kWaves, (fast ? 4 : 8) * cus);
+  // One workgroup writes the load by itself; several add to it, which takes a launch that clears it first
+  // (3.8 us). Few enough tokens (4 steps of a workgroup, some 3 us each) are left to one.
+  const int per_step = fast ? kWaves * 64 / lanes : kWaves;
+  const int grid = load && a.N <= 4 * per_step ? 1 : grid_of(a.N, per_step, (fast ? 4 : 8) * cus);
   if (load && (grid > 1 || a.N == 0)) {
     const hipError_t e = launch_fill_u32(reinterpret_cast<uint32_t*>(load), 0u, a.E, s);
     if (e != hipSuccess) return e;

@@ -458,7 +458,7 @@ hipError_t launch_route_bwd(const mok_route_desc& d, const void* x, const int32_
                             void* dx, hipStream_t s);
 constexpr int64_t kMaxOptElements = int64_t(1) << 35;   // of one tensor
 int64_t sumsq_ws_bytes(int count);
-hipError_t launch_sumsq(int count, const mok_sumsq_tensor* t, bool bf16, double* out, double* ws,
+hipError_t launch_sumsq(int count, const mok_sumsq_tensor* t, bool bf16, double* out, uint8_t* ws,
                         hipStream_t s);
 hipError_t launch_adamw(int count, const mok_adamw_tensor* t, const mok_adamw_config& c, hipStream_t s);
 

@@ -85,7 +85,7 @@ mok_status mok_grad_sumsq(int32_t num_tensors, const mok_sumsq_tensor* tensors, 
     if (!aligned(tensors[t].g, 16)) return MOK_ERR_ALIGN;
   }
   return hip_status(launch_sumsq(num_tensors, tensors, elem == MOK_ELEM_BF16, out_dev,
-                                 static_cast<double*>(ws_dev), static_cast<hipStream_t>(stream)));
+                                 static_cast<uint8_t*>(ws_dev), static_cast<hipStream_t>(stream)));
 }
 
 mok_status mok_adamw(int32_t num_tensors, const mok_adamw_tensor* tensors,

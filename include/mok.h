@@ -487,7 +487,8 @@ typedef struct {
 /* *out_dev = sum over every element of every tensor of g^2, in fp64 and in a fixed order: the squared
  * norm that mok_adamw clips by (add up over ranks first where tensors are sharded).
  *   elem    mok_elem of the tensors
- *   ws_dev  mok_sumsq_ws_size bytes of scratch (calls that overlap in time need their own) */
+ *   ws_dev  mok_sumsq_ws_size bytes of scratch, zero-filled before its first use; every call leaves it
+ *           ready for the next one. Calls that overlap in time need their own. */
 mok_status mok_sumsq_ws_size(int32_t num_tensors, size_t* ws_bytes);
 mok_status mok_grad_sumsq(int32_t num_tensors, const mok_sumsq_tensor* tensors, int32_t elem,
                           double* out_dev, void* ws_dev, void* stream);
