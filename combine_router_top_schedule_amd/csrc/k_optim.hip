@@ -123,8 +123,8 @@ __global__ __launch_bounds__(kSqThreads) void k_sumsq(SqArgs a) {
 
 // ---- AdamW ------------------------------------------------------------------------------------
 constexpr int kAdTensors = 48;       // tensors a launch takes
-constexpr int kAdUnroll = 1;         // groups of 4 elements a thread updates
-constexpr int kAdChunk = 1024 * kAdUnroll;   // elements a workgroup updates
+constexpr int kAdChunk = 1024;       // elements a workgroup updates, 4 a thread (8 a thread, or 4 times 4, are
+                                     // 2 to 9 % slower at 100 M elements and more)
 
 struct AdamArgs {
   void* p[kAdTensors];
@@ -171,41 +171,37 @@ __device__ __forceinline__ uint32_t scale_code(uint32_t amax) {
   return amax < 0x800000u || c < 0 ? 0u : uint32_t(c);
 }
 
-// |x| <= 448 rounded to an E4M3 value: to the multiple below of the step at |x|, or the one above when
-// the rest is at least 1 - u / 2^16 steps. POSITIVE: not to zero from above zero.
-template <bool POSITIVE>
-__device__ __forceinline__ float round_e4m3(float x, uint32_t u) {
-  const uint32_t b = __float_as_uint(x) & 0x7FFFFFFFu;
-  const int f = max(int(b >> 23), 121);                      // the exponent field, at least 2^-6's
-  const float y = __uint_as_float(b) * __uint_as_float(uint32_t(257 - f) << 23);   // over the step 2^(f-130)
-  float k = floorf(y + float(u) * (1.f / 65536.f));
-  if (POSITIVE) k = b ? fmaxf(k, 1.f) : k;
-  return copysignf(k * __uint_as_float(uint32_t(f - 3) << 23), x);
+// The largest of 8 consecutive lanes: exchanges within 4 lanes, then with the mirrored lane of the other 4.
+__device__ __forceinline__ uint32_t max8(uint32_t v) {
+  v = max(v, uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0xB1, 0xF, 0xF, true)));
+  v = max(v, uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0x4E, 0xF, 0xF, true)));
+  return max(v, uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0x141, 0xF, 0xF, true)));
 }
 
-__device__ __forceinline__ uint32_t max_xor(uint32_t v, int off) {
-  const uint32_t o = uint32_t(__shfl_xor(int(v), off, 64));
-  return v > o ? v : o;
-}
-
-// Four values of a run held by 8 consecutive lanes -> their codes, and the run's scale code.
+// Four values of a run held by 8 consecutive lanes -> their codes, and the run's scale code. `u` holds 16
+// random bits in its upper half. The conversion adds the upper 20 bits of its seed below the kept
+// mantissa and cuts: |x| goes to floor(|x| / step + u / 2^16) steps, subnormal codes too. POSITIVE: what is above
+// zero does not become zero, as one step (2^-9) stays one step.
 template <bool POSITIVE>
 __device__ __forceinline__ uint32_t encode4(const float (&x)[4], const uint32_t (&u)[4], uint32_t* scale) {
   uint32_t amax = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) amax = max(amax, __float_as_uint(x[j]) & 0x7FFFFFFFu);
-  amax = max_xor(amax, 1);
-  amax = max_xor(amax, 2);
-  amax = max_xor(amax, 4);
+  amax = max8(amax);
   const uint32_t c = scale_code(amax);
   *scale = c;
-  if (c == 0xFFu) return 0u;
-  const float inv = pow2(127 - int(c));
+  const float inv = pow2(127 - int(min(c, 254u)));
   float r[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) r[j] = round_e4m3<POSITIVE>(x[j] * inv, u[j]);
-  const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(r[0], r[1], 0, false);
-  return uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(r[2], r[3], lo, true));
+  for (int j = 0; j < 4; ++j) {
+    r[j] = x[j] * inv;
+    if (POSITIVE) r[j] = r[j] > 0.f ? fmaxf(r[j], 0x1p-9f) : r[j];
+  }
+  int code = __builtin_amdgcn_cvt_sr_fp8_f32(r[0], int(u[0]), 0, 0);
+  code = __builtin_amdgcn_cvt_sr_fp8_f32(r[1], int(u[1]), code, 1);
+  code = __builtin_amdgcn_cvt_sr_fp8_f32(r[2], int(u[2]), code, 2);
+  code = __builtin_amdgcn_cvt_sr_fp8_f32(r[3], int(u[3]), code, 3);
+  return c == 0xFFu ? 0u : uint32_t(code);
 }
 
 __device__ __forceinline__ void decode4(uint32_t code, uint32_t scale, float (&x)[4]) {
@@ -216,9 +212,10 @@ __device__ __forceinline__ void decode4(uint32_t code, uint32_t scale, float (&x
   x[3] = __builtin_amdgcn_cvt_f32_fp8(int(code), 3) * s;
 }
 
-// Four consecutive elements from i on, those past n as zero.
+// Four consecutive elements from i on; without FULL, those past n read as zero and are not written.
+template <bool FULL>
 __device__ __forceinline__ void load4(const float* p, int64_t i, int64_t n, float (&x)[4]) {
-  if (i + 4 <= n) {
+  if (FULL || i + 4 <= n) {
     const f32x4 v = *reinterpret_cast<const f32x4*>(p + i);
 #pragma unroll
     for (int j = 0; j < 4; ++j) x[j] = v[j];
@@ -227,8 +224,9 @@ __device__ __forceinline__ void load4(const float* p, int64_t i, int64_t n, floa
     for (int j = 0; j < 4; ++j) x[j] = i + j < n ? p[i + j] : 0.f;
   }
 }
+template <bool FULL>
 __device__ __forceinline__ void load4(const uint16_t* p, int64_t i, int64_t n, float (&x)[4]) {
-  if (i + 4 <= n) {
+  if (FULL || i + 4 <= n) {
     const uint2 v = *reinterpret_cast<const uint2*>(p + i);
     x[0] = bf2f(uint16_t(v.x)); x[1] = bf2f(uint16_t(v.x >> 16));
     x[2] = bf2f(uint16_t(v.y)); x[3] = bf2f(uint16_t(v.y >> 16));
@@ -237,34 +235,44 @@ __device__ __forceinline__ void load4(const uint16_t* p, int64_t i, int64_t n, f
     for (int j = 0; j < 4; ++j) x[j] = i + j < n ? bf2f(p[i + j]) : 0.f;
   }
 }
+template <bool FULL>
 __device__ __forceinline__ uint32_t load4(const uint8_t* p, int64_t i, int64_t n) {
-  if (i + 4 <= n) return *reinterpret_cast<const uint32_t*>(p + i);
+  if (FULL || i + 4 <= n) return *reinterpret_cast<const uint32_t*>(p + i);
   uint32_t x = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     if (i + j < n) x |= uint32_t(p[i + j]) << (8 * j);
   return x;
 }
+template <bool FULL>
 __device__ __forceinline__ void store4(float* p, int64_t i, int64_t n, const float (&x)[4]) {
-  if (i + 4 <= n) *reinterpret_cast<f32x4*>(p + i) = f32x4{x[0], x[1], x[2], x[3]};
-  else
+  if (FULL || i + 4 <= n) {
+    *reinterpret_cast<f32x4*>(p + i) = f32x4{x[0], x[1], x[2], x[3]};
+  } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (i + j < n) p[i + j] = x[j];
+  }
 }
+template <bool FULL>
 __device__ __forceinline__ void store4(uint16_t* p, int64_t i, int64_t n, uint2 x) {
-  if (i + 4 <= n) *reinterpret_cast<uint2*>(p + i) = x;
-  else
+  if (FULL || i + 4 <= n) {
+    *reinterpret_cast<uint2*>(p + i) = x;
+  } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (i + j < n) p[i + j] = uint16_t((j & 2 ? x.y : x.x) >> (16 * (j & 1)));
+  }
 }
+template <bool FULL>
 __device__ __forceinline__ void store4(uint8_t* p, int64_t i, int64_t n, uint32_t x) {
-  if (i + 4 <= n) *reinterpret_cast<uint32_t*>(p + i) = x;
-  else
+  if (FULL || i + 4 <= n) {
+    *reinterpret_cast<uint32_t*>(p + i) = x;
+  } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (i + j < n) p[i + j] = uint8_t(x >> (8 * j));
+  }
 }
 
 // fp32 -> BF16 bits by adding 16 random bits below the kept ones (infinities and NaN as they are).
@@ -272,6 +280,68 @@ __device__ __forceinline__ uint32_t bf16_random(float x, uint32_t u) {
   const uint32_t b = __float_as_uint(x);
   if ((b & 0x7F800000u) == 0x7F800000u) return f2bf(x);
   return (b + u) >> 16;
+}
+
+// The step of 4 elements a thread, from i on, of tensor t.
+template <bool GBF, bool PBF, bool MX8, bool FULL>
+__device__ __forceinline__ void adamw4(const AdamArgs& a, int t, int64_t i, int64_t n, float clip, float decay,
+                                       float rate, float rbc2) {
+  float g[4], p[4], m[4], v[4], r[4];
+  load4<FULL>(static_cast<const std::conditional_t<GBF, uint16_t, float>*>(a.g[t]), i, n, g);
+  load4<FULL>(static_cast<const std::conditional_t<PBF, uint16_t, float>*>(a.p[t]), i, n, p);
+  if constexpr (MX8) {
+    const uint32_t cm = load4<FULL>(static_cast<const uint8_t*>(a.m[t]), i, n);
+    const uint32_t cv = load4<FULL>(static_cast<const uint8_t*>(a.v[t]), i, n);
+    const uint32_t sm = FULL || i < n ? a.ms[t][i >> 5] : 0u, sv = FULL || i < n ? a.vs[t][i >> 5] : 0u;
+    decode4(cm, sm, m);
+    decode4(cv, sv, v);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = v[j] * v[j];
+  } else {
+    load4<FULL>(static_cast<const float*>(a.m[t]), i, n, m);
+    load4<FULL>(static_cast<const float*>(a.v[t]), i, n, v);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float gj = g[j] * clip;
+    m[j] = m[j] * a.b1 + gj * a.c1;
+    v[j] = v[j] * a.b2 + (gj * gj) * a.c2;
+    r[j] = sqrtf(v[j]);
+    p[j] = p[j] * decay - (m[j] / (r[j] * rbc2 + a.eps)) * rate;
+  }
+  uint32_t h[4], u[4];
+  if constexpr (MX8 || PBF) {
+    const uint32_t salt = mix(a.seed + uint32_t(a.number0 + t) * 0x9E3779B1u);
+    const uint32_t base = mix(salt + uint32_t(i >> 32));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h[j] = mix((uint32_t(i) + j) ^ base);
+  }
+  if constexpr (PBF) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) u[j] = bf16_random(p[j], mix(h[j] ^ 0x3C6EF372u) & 0xFFFFu);
+    store4<FULL>(static_cast<uint16_t*>(a.p[t]), i, n, uint2{u[0] | u[1] << 16, u[2] | u[3] << 16});
+  } else {
+    store4<FULL>(static_cast<float*>(a.p[t]), i, n, p);
+    if (a.copy[t]) store4<FULL>(a.copy[t], i, n, uint2{pack_bf2(p[0], p[1]), pack_bf2(p[2], p[3])});
+  }
+  if constexpr (MX8) {
+    uint32_t sm, sv;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) u[j] = h[j] << 16;
+    const uint32_t cm = encode4<false>(m, u, &sm);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) u[j] = h[j] & 0xFFFF0000u;
+    const uint32_t cv = encode4<true>(r, u, &sv);
+    store4<FULL>(static_cast<uint8_t*>(a.m[t]), i, n, cm);
+    store4<FULL>(static_cast<uint8_t*>(a.v[t]), i, n, cv);
+    if ((threadIdx.x & 7) == 0 && (FULL || i < n)) {
+      a.ms[t][i >> 5] = uint8_t(sm);
+      a.vs[t][i >> 5] = uint8_t(sv);
+    }
+  } else {
+    store4<FULL>(static_cast<float*>(a.m[t]), i, n, m);
+    store4<FULL>(static_cast<float*>(a.v[t]), i, n, v);
+  }
 }
 
 template <bool GBF, bool PBF, bool MX8>
@@ -293,77 +363,9 @@ __global__ __launch_bounds__(256) void k_adamw(AdamArgs a) {
   }
   const int c = blockIdx.x;
   const int t = __builtin_amdgcn_readfirstlane(find_tensor(a.first, a.count, c));
-  const int64_t n = a.n[t];
-  const int64_t i0 = int64_t(c - a.first[t]) * kAdChunk + threadIdx.x * 4;
-  const uint32_t salt = mix(a.seed + uint32_t(a.number0 + t) * 0x9E3779B1u);
-  float g[kAdUnroll][4], p[kAdUnroll][4], m[kAdUnroll][4], v[kAdUnroll][4];
-  uint32_t code[kAdUnroll][2], scale[kAdUnroll][2];
-#pragma unroll
-  for (int q = 0; q < kAdUnroll; ++q) {
-    const int64_t i = i0 + 1024 * q;
-    load4(static_cast<const std::conditional_t<GBF, uint16_t, float>*>(a.g[t]), i, n, g[q]);
-    load4(static_cast<const std::conditional_t<PBF, uint16_t, float>*>(a.p[t]), i, n, p[q]);
-    if constexpr (MX8) {
-      code[q][0] = load4(static_cast<const uint8_t*>(a.m[t]), i, n);
-      code[q][1] = load4(static_cast<const uint8_t*>(a.v[t]), i, n);
-      scale[q][0] = i < n ? a.ms[t][i >> 5] : 0u;
-      scale[q][1] = i < n ? a.vs[t][i >> 5] : 0u;
-    } else {
-      load4(static_cast<const float*>(a.m[t]), i, n, m[q]);
-      load4(static_cast<const float*>(a.v[t]), i, n, v[q]);
-    }
-  }
-#pragma unroll
-  for (int q = 0; q < kAdUnroll; ++q) {
-    const int64_t i = i0 + 1024 * q;
-    if constexpr (MX8) {
-      decode4(code[q][0], scale[q][0], m[q]);
-      decode4(code[q][1], scale[q][1], v[q]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[q][j] = v[q][j] * v[q][j];
-    }
-    float r[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float gj = g[q][j] * clip;
-      m[q][j] = m[q][j] * a.b1 + gj * a.c1;
-      v[q][j] = v[q][j] * a.b2 + (gj * gj) * a.c2;
-      r[j] = sqrtf(v[q][j]);
-      p[q][j] = p[q][j] * decay - (m[q][j] / (r[j] * rbc2 + a.eps)) * rate;
-    }
-    uint32_t h[4], u[4];
-    if constexpr (MX8 || PBF) {
-      const uint32_t base = mix(salt + uint32_t(i >> 32));
-#pragma unroll
-      for (int j = 0; j < 4; ++j) h[j] = mix((uint32_t(i) + j) ^ base);
-    }
-    if constexpr (PBF) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) u[j] = bf16_random(p[q][j], mix(h[j] ^ 0x3C6EF372u) & 0xFFFFu);
-      store4(static_cast<uint16_t*>(a.p[t]), i, n, uint2{u[0] | u[1] << 16, u[2] | u[3] << 16});
-    } else {
-      store4(static_cast<float*>(a.p[t]), i, n, p[q]);
-      if (a.copy[t]) store4(a.copy[t], i, n, uint2{pack_bf2(p[q][0], p[q][1]), pack_bf2(p[q][2], p[q][3])});
-    }
-    if constexpr (MX8) {
-      uint32_t sm, sv;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) u[j] = h[j] & 0xFFFFu;
-      const uint32_t cm = encode4<false>(m[q], u, &sm);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) u[j] = h[j] >> 16;
-      const uint32_t cv = encode4<true>(r, u, &sv);
-      store4(static_cast<uint8_t*>(a.m[t]), i, n, cm);
-      store4(static_cast<uint8_t*>(a.v[t]), i, n, cv);
-      if ((threadIdx.x & 7) == 0 && i < n) {
-        a.ms[t][i >> 5] = uint8_t(sm);
-        a.vs[t][i >> 5] = uint8_t(sv);
-      }
-    } else {
-      store4(static_cast<float*>(a.m[t]), i, n, m[q]);
-      store4(static_cast<float*>(a.v[t]), i, n, v[q]);
-    }
-  }
+  const int64_t n = a.n[t], i0 = int64_t(c - a.first[t]) * kAdChunk, i = i0 + threadIdx.x * 4;
+  if (i0 + kAdChunk <= n) adamw4<GBF, PBF, MX8, true>(a, t, i, n, clip, decay, rate, rbc2);
+  else adamw4<GBF, PBF, MX8, false>(a, t, i, n, clip, decay, rate, rbc2);
 }
 
 template <bool GBF, bool PBF>
