@@ -756,41 +756,46 @@ __device__ __forceinline__ void store_run(void* dst, int64_t at, const float* s,
     int i = lane * 8;
     for (; i + 8 <= count; i += 512) {
       const f32x4 p = *reinterpret_cast<const f32x4*>(s + i), q = *reinterpret_cast<const f32x4*>(s + i + 4);
-      *reinterpret_cast<u32x4*>(d + i) =
-          u32x4{pack_bf2(p[0], p[1]), pack_bf2(p[2], p[3]), pack_bf2(q[0], q[1]), pack_bf2(q[2], q[3])};
+      __builtin_nontemporal_store(
+          u32x4{pack_bf2(p[0], p[1]), pack_bf2(p[2], p[3]), pack_bf2(q[0], q[1]), pack_bf2(q[2], q[3])},
+          reinterpret_cast<u32x4*>(d + i));
     }
     for (int j = i; j < count && j < i + 8; ++j) d[j] = f2bf(s[j]);
   } else {
     float* d = static_cast<float*>(dst) + at;
     int i = lane * 4;
-    for (; i + 4 <= count; i += 256) *reinterpret_cast<f32x4*>(d + i) = *reinterpret_cast<const f32x4*>(s + i);
+    for (; i + 4 <= count; i += 256)
+      __builtin_nontemporal_store(*reinterpret_cast<const f32x4*>(s + i), reinterpret_cast<f32x4*>(d + i));
     for (int j = i; j < count && j < i + 4; ++j) d[j] = s[j];
   }
 }
 
 // Gradients that reach the chosen logits only: every weight but the plain softmax's. A wave takes 8
-// tokens: their K slots in KP lanes each, the results scattered into 8 zeroed rows in LDS, and
-// the rows (consecutive in memory) stored with 16 bytes a lane. LDS goes back to zero by the same
-// scatter.
+// tokens: their K slots in KP lanes each, the results scattered into `rows` (4 or 8) zeroed rows in LDS at a
+// time, and the rows (consecutive in memory) stored with 16 bytes a lane. LDS goes back to zero by the
+// same scatter.
 template <bool BF16, int KP>
-__global__ __launch_bounds__(64 * kWaves) void k_route_bwd(RouteBwdArgs a) {
-  extern __shared__ __attribute__((aligned(16))) float s_row[];   // [waves][8][E]
+__global__ __launch_bounds__(64 * kWaves) void k_route_bwd(RouteBwdArgs a, int rows) {
+  extern __shared__ __attribute__((aligned(16))) float s_row[];   // [waves][rows][E]
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
-  float* s = s_row + wave * 8 * a.E;
-  for (int i = lane; i < 8 * a.E; i += 64) s[i] = 0.f;
+  float* s = s_row + wave * rows * a.E;
+  for (int i = lane; i < rows * a.E; i += 64) s[i] = 0.f;
   wave_sync();
   constexpr int kPass = KP / 8;   // passes of 64 / KP tokens
   for (int64_t n0 = (int64_t(blockIdx.x) * waves + wave) * 8; n0 < a.N;
        n0 += int64_t(gridDim.x) * waves * 8) {
-    int at[kPass];
+    int ex[kPass];
+    float dx[kPass];
 #pragma unroll
     for (int p = 0; p < kPass; ++p) {
       const int t = p * (64 / KP) + lane / KP, k = lane % KP;
       const int64_t n = n0 + t;
+      const bool in = n < a.N && k < a.K;
+      const float dw_in = in ? a.dw[n * a.K + k] : 0.f;
       const int e = slot_expert<KP>(a, n, k, n < a.N);
       const bool some = e >= 0;
       const float x = some ? logit<BF16>(a.x, n * a.ld + e) : -INFINITY;
-      const float dw = some ? a.dw[n * a.K + k] : 0.f;
+      const float dw = some ? dw_in : 0.f;
       float d;
       if (a.renorm) {
         const float f = a.sigmoid ? log_sigmoid(x) : x;
@@ -805,17 +810,26 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_bwd(RouteBwdArgs a) {
         const float sg = 1.f / (1.f + expf(-x));
         d = a.scale * dw * sg / (1.f + expf(x));
       }
-      at[p] = some ? t * a.E + e : -1;
-      if (some) s[at[p]] = d;
+      ex[p] = e;
+      dx[p] = d;
     }
-    wave_sync();
-    const int64_t left = a.N - n0;
-    store_run<BF16>(a.dx, n0 * a.E, s, int(left < 8 ? left : 8) * a.E, lane);
-    wave_sync();
+    for (int r0 = 0; r0 < 8 && n0 + r0 < a.N; r0 += rows) {
+      int at[kPass];
 #pragma unroll
-    for (int p = 0; p < kPass; ++p)
-      if (at[p] >= 0) s[at[p]] = 0.f;
-    wave_sync();
+      for (int p = 0; p < kPass; ++p) {
+        const int t = p * (64 / KP) + lane / KP - r0;
+        at[p] = ex[p] >= 0 && t >= 0 && t < rows ? t * a.E + ex[p] : -1;
+        if (at[p] >= 0) s[at[p]] = dx[p];
+      }
+      wave_sync();
+      const int64_t left = a.N - n0 - r0;
+      store_run<BF16>(a.dx, (n0 + r0) * a.E, s, int(left < rows ? left : rows) * a.E, lane);
+      wave_sync();
+#pragma unroll
+      for (int p = 0; p < kPass; ++p)
+        if (at[p] >= 0) s[at[p]] = 0.f;
+      wave_sync();
+    }
   }
 }
 
@@ -946,17 +960,20 @@ hipError_t launch_route_bwd(const mok_route_desc& d, const void* x, const int32_
     else hipLaunchKernelGGL(k_route_bwd_dense<false>, dim3(grid), dim3(64 * kWaves), 0, s, a);
     return hipGetLastError();
   }
-  // 32 E bytes of LDS per wave, within the 64 KB that a workgroup has without asking for more
-  const int waves = a.E <= 512 ? 4 : 2;
-  const int grid = grid_of(a.N, 8 * waves, 8 * cus);
-  const size_t lds = size_t(waves) * 8 * a.E * 4;
+  // 4 rows a wave at a time (16 E bytes of LDS, so that enough waves are resident); 8 where a run of 4
+  // bf16 rows would not end on 16 bytes, or where 8 are small. At most the 64 KB that a workgroup has
+  // without asking for more.
+  const int rows = (bf && a.E % 2) || a.E <= 64 ? 8 : 4;
+  const int waves = int64_t(kWaves) * rows * a.E * 4 <= 65536 ? kWaves : 2;
+  const int grid = grid_of(a.N, 8 * waves, 16 * cus);
+  const size_t lds = size_t(waves) * rows * a.E * 4;
   const dim3 t(64 * waves);
   if (a.K <= 8) {
-    if (bf) hipLaunchKernelGGL((k_route_bwd<true, 8>), dim3(grid), t, lds, s, a);
-    else hipLaunchKernelGGL((k_route_bwd<false, 8>), dim3(grid), t, lds, s, a);
+    if (bf) hipLaunchKernelGGL((k_route_bwd<true, 8>), dim3(grid), t, lds, s, a, rows);
+    else hipLaunchKernelGGL((k_route_bwd<false, 8>), dim3(grid), t, lds, s, a, rows);
   } else {
-    if (bf) hipLaunchKernelGGL((k_route_bwd<true, 16>), dim3(grid), t, lds, s, a);
-    else hipLaunchKernelGGL((k_route_bwd<false, 16>), dim3(grid), t, lds, s, a);
+    if (bf) hipLaunchKernelGGL((k_route_bwd<true, 16>), dim3(grid), t, lds, s, a, rows);
+    else hipLaunchKernelGGL((k_route_bwd<false, 16>), dim3(grid), t, lds, s, a, rows);
   }
   return hipGetLastError();
 }
