@@ -61,9 +61,10 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// x -> log sigmoid(x); the form that neither overflows nor cancels.
+// x -> log sigmoid(x), to a few units of 2^-23 of max(1, |result|): it goes into exponentials. The form
+// does not overflow.
 __device__ __forceinline__ float log_sigmoid(float x) {
-  return fminf(x, 0.f) - log1pf(expf(-fabsf(x)));
+  return fminf(x, 0.f) - __logf(1.f + __expf(-fabsf(x)));
 }
 
 // ---- exchanges between lanes
@@ -235,8 +236,7 @@ template <int W>
 __device__ __forceinline__ float slot_weight(const RouteArgs& a, bool some, float v, float top, float sum) {
   float w;
   if (a.renorm) {
-    // (log sigmoid, to a few units of 2^-23 of max(1, |f|): it goes into an exponential)
-    const float f = a.sigmoid ? fminf(v, 0.f) - __logf(1.f + __expf(-fabsf(v))) : v;
+    const float f = a.sigmoid ? log_sigmoid(v) : v;
     const float top_f = lanes_max<W>(f);   // (every lane takes part in the exchanges)
     const float q = some ? __expf(f - top_f) : 0.f;
     w = q / lanes_sum<W>(q);
@@ -724,28 +724,35 @@ struct RouteBwdArgs {
   int64_t N, ld;
   int E, K;
   int sigmoid, renorm;
+  int vec;   // rows allow loads of 4 logits
   float scale;
 };
 
-// Expert of slot k of a token; -1 if it names none, or one that an earlier slot named.
+// Expert of slot k of a token; -1 if it names none, or one that an earlier slot named. The token's KP
+// slots are in KP consecutive lanes.
 template <int KP>
 __device__ __forceinline__ int slot_expert(const RouteBwdArgs& a, int64_t n, int k, bool live) {
   int e = live && k < a.K ? a.idx[n * a.K + k] : -1;
   if (e >= a.E) e = -1;
   bool again = false;
+  if constexpr (KP == 8) {
+    auto meet = [&](int o, int other) { again |= other < k && o == e; };
+    const int m = __float_as_int(lane_xor<4>(__int_as_float(e)));   // (slot 7 - k)
+    meet(quad<0xB1>(e), k ^ 1);
+    meet(quad<0x4E>(e), k ^ 2);
+    meet(quad<0x1B>(e), k ^ 3);
+    meet(m, 7 - k);
+    meet(quad<0xB1>(m), 7 - (k ^ 1));
+    meet(quad<0x4E>(m), 7 - (k ^ 2));
+    meet(quad<0x1B>(m), 7 - (k ^ 3));
+  } else {
 #pragma unroll
-  for (int j = 0; j < KP; ++j) {
-    const int o = __shfl(e, j, KP);
-    again |= j < k && o == e;
+    for (int j = 0; j < KP; ++j) {
+      const int o = __shfl(e, j, KP);
+      again |= j < k && o == e;
+    }
   }
   return again ? -1 : e;
-}
-
-template <int KP>
-__device__ __forceinline__ float slots_sum(float v) {
-#pragma unroll
-  for (int off = KP / 2; off; off >>= 1) v += __shfl_xor(v, off, KP);
-  return v;
 }
 
 // Stores `count` consecutive values (fp32 in LDS) at a 16-byte aligned place, by a wave.
@@ -799,16 +806,14 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_bwd(RouteBwdArgs a, int r
       float d;
       if (a.renorm) {
         const float f = a.sigmoid ? log_sigmoid(x) : x;
-        float top = f;
-#pragma unroll
-        for (int off = KP / 2; off; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, KP));
-        const float u = some ? expf(f - top) : 0.f;
-        const float q = u / slots_sum<KP>(u);
-        d = a.scale * q * (dw - slots_sum<KP>(some ? dw * q : 0.f));
-        if (a.sigmoid) d /= 1.f + expf(x);
+        const float top = lanes_max<KP>(f);
+        const float u = some ? __expf(f - top) : 0.f;
+        const float q = u / lanes_sum<KP>(u);
+        d = a.scale * q * (dw - lanes_sum<KP>(some ? dw * q : 0.f));
+        if (a.sigmoid) d /= 1.f + __expf(x);
       } else {
-        const float sg = 1.f / (1.f + expf(-x));
-        d = a.scale * dw * sg / (1.f + expf(x));
+        const float sg = 1.f / (1.f + __expf(-x));
+        d = a.scale * dw * sg / (1.f + __expf(x));
       }
       ex[p] = e;
       dx[p] = d;
@@ -833,40 +838,115 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_bwd(RouteBwdArgs a, int r
   }
 }
 
-// The plain softmax's weights reach every logit: dx_e = scale s_e ([e chosen] dw_e - sum_j dw_j s_j).
-// One wave per token.
-template <bool BF16>
+// The plain softmax's weights reach every logit: dx_e = scale s_e ([e chosen] dw_e - sum_j dw_j s_j). As in the
+// forward, L lanes share a token, each with V of its experts in registers; the weights' gradients come to
+// their experts through a row in LDS, zero but for them.
+template <bool BF16, int L, int V>
 __global__ __launch_bounds__(64 * kWaves) void k_route_bwd_dense(RouteBwdArgs a) {
+  constexpr int T = 64 / L, SL = L < 16 ? 16 / L : 1;
+  __shared__ __attribute__((aligned(16))) float s_row[kWaves][T][L * V];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int64_t n = int64_t(blockIdx.x) * kWaves + wave; n < a.N; n += int64_t(gridDim.x) * kWaves) {
-    const int64_t row = n * a.ld;
-    const int e = slot_expert<16>(a, n, lane & 15, true);
-    const bool some = e >= 0;
-    const bool any = __ballot(some) != 0;
-    const float x = some ? logit<BF16>(a.x, row + e) : -INFINITY;
-    const float dw = some ? a.dw[n * a.K + (lane & 15)] : 0.f;
-    float top = -INFINITY, sum = 0.f;
-    if (any) {
-      for (int i = lane; i < a.E; i += 64) top = fmaxf(top, logit<BF16>(a.x, row + i));
-      for (int off = 32; off; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
-      for (int i = lane; i < a.E; i += 64) sum += expf(logit<BF16>(a.x, row + i) - top);
-      for (int off = 32; off; off >>= 1) sum += __shfl_xor(sum, off, 64);
+  const int j = lane % L, t = lane / L;
+  float* s = s_row[wave][t];
+#pragma unroll
+  for (int i = 0; i < V / 4; ++i) *reinterpret_cast<f32x4*>(s + 4 * (j + L * i)) = f32x4{0.f, 0.f, 0.f, 0.f};
+  wave_sync();
+  const uint64_t here = ((1ull << L) - 1) << (t * L);   // the token's lanes
+  const int64_t tiles = (a.N + T - 1) / T;
+  for (int64_t tile = int64_t(blockIdx.x) * kWaves + wave; tile < tiles; tile += int64_t(gridDim.x) * kWaves) {
+    const int64_t n = tile * T + t;
+    const bool live = n < a.N;
+    int ex[SL];
+    float dw[SL], xk[SL];
+    bool some = false;
+#pragma unroll
+    for (int p = 0; p < SL; ++p) {
+      const int k = j + L * p;
+      ex[p] = live && k < a.K ? a.idx[n * a.K + k] : -1;
+      dw[p] = live && k < a.K ? a.dw[n * a.K + k] : 0.f;
+      if (ex[p] >= a.E) ex[p] = -1;
     }
-    const float back = slots_sum<16>(some ? dw * (expf(x - top) / sum) : 0.f);
-    for (int i0 = 0; i0 < a.E; i0 += 64) {
-      const int i = i0 + lane;
-      float g = -back;
-      for (int k = 0; k < a.K; ++k) {
-        const int ek = __shfl(e, k, 64);
-        const float dk = __shfl(dw, k, 64);
-        if (ek == i) g += dk;
+    // an expert that an earlier slot named counts once
+    bool again[SL] = {};
+    for (int k = 0; k + 1 < a.K; ++k) {
+      const int o = SL > 1 && k >= L ? __shfl(ex[SL - 1], k - L, L) : __shfl(ex[0], k % L, L);
+#pragma unroll
+      for (int p = 0; p < SL; ++p) again[p] |= k < j + L * p && o == ex[p];
+    }
+#pragma unroll
+    for (int p = 0; p < SL; ++p) {
+      if (again[p]) ex[p] = -1;
+      some |= ex[p] >= 0;
+      xk[p] = ex[p] >= 0 ? logit<BF16>(a.x, n * a.ld + ex[p]) : -INFINITY;
+    }
+    // a row without a chosen expert is zero, whatever its logits hold
+    const bool any = (__ballot(some) & here) != 0;
+    const int lim = any ? a.E - 4 * j : 0;   // expert 4 (j + L i) + c of this lane exists if 4 L i + c < lim
+    const int64_t at = n * a.ld + 4 * j;
+    float x[V];
+#pragma unroll
+    for (int u = 0; u < V; ++u) x[u] = -INFINITY;
+    if (a.vec) {
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i)
+        if (4 * L * i < lim) load_logits4<BF16>(a.x, at + 4 * L * i, x + 4 * i);
+    } else {
+#pragma unroll
+      for (int u = 0; u < V; ++u)
+        if (4 * L * (u >> 2) + (u & 3) < lim) x[u] = logit<BF16>(a.x, at + 4 * L * (u >> 2) + (u & 3));
+    }
+    float top = x[0];
+#pragma unroll
+    for (int u = 1; u < V; ++u) top = fmaxf(top, x[u]);
+    top = lanes_max<L>(top);
+    float sum = 0.f;
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+      x[u] = __expf(x[u] - top);
+      sum += x[u];
+    }
+    sum = lanes_sum<L>(sum);
+    float back = 0.f;
+#pragma unroll
+    for (int p = 0; p < SL; ++p)
+      if (ex[p] >= 0) {
+        back += dw[p] * (__expf(xk[p] - top) / sum);
+        s[ex[p]] = dw[p];
       }
-      if (i < a.E) {
-        const float v = any ? a.scale * (expf(logit<BF16>(a.x, row + i) - top) / sum) * g : 0.f;
-        if constexpr (BF16) static_cast<uint16_t*>(a.dx)[n * a.E + i] = f2bf(v);
-        else static_cast<float*>(a.dx)[n * a.E + i] = v;
+    back = lanes_sum<L>(back);
+    wave_sync();
+    const float f = a.scale / sum;
+    const int end = live ? a.E - 4 * j : 0;
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) {
+      if (4 * L * i < end) {
+        const f32x4 g = *reinterpret_cast<const f32x4*>(s + 4 * (j + L * i));
+        float o[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[c] = any ? x[4 * i + c] * f * (g[c] - back) : 0.f;
+        const int64_t to = n * a.E + 4 * (j + L * i);
+        if (a.E % 4 == 0) {
+          if constexpr (BF16)
+            __builtin_nontemporal_store(uint64_t(pack_bf2(o[0], o[1])) | uint64_t(pack_bf2(o[2], o[3])) << 32,
+                                        reinterpret_cast<uint64_t*>(static_cast<uint16_t*>(a.dx) + to));
+          else
+            __builtin_nontemporal_store(f32x4{o[0], o[1], o[2], o[3]},
+                                        reinterpret_cast<f32x4*>(static_cast<float*>(a.dx) + to));
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (4 * L * i + c < end) {
+              if constexpr (BF16) static_cast<uint16_t*>(a.dx)[to + c] = f2bf(o[c]);
+              else static_cast<float*>(a.dx)[to + c] = o[c];
+            }
+        }
       }
     }
+    wave_sync();
+#pragma unroll
+    for (int p = 0; p < SL; ++p)
+      if (ex[p] >= 0) s[ex[p]] = 0.f;
+    wave_sync();
   }
 }
 
@@ -918,6 +998,18 @@ void route_fwd(const RouteArgs& a, bool quick, int lanes, int grid, hipStream_t 
   }
 }
 
+template <bool BF16>
+void route_bwd_dense(const RouteBwdArgs& a, int cus, hipStream_t s) {
+  const int lanes = a.E <= 256 ? 8 : a.E <= 512 ? 16 : 32;
+  const dim3 g(grid_of(a.N, kWaves * 64 / lanes, 8 * cus)), b(64 * kWaves);
+  if (a.E <= 64) hipLaunchKernelGGL((k_route_bwd_dense<BF16, 8, 8>), g, b, 0, s, a);
+  else if (a.E <= 128) hipLaunchKernelGGL((k_route_bwd_dense<BF16, 8, 16>), g, b, 0, s, a);
+  else if (a.E <= 256) hipLaunchKernelGGL((k_route_bwd_dense<BF16, 8, 32>), g, b, 0, s, a);
+  else if (a.E <= 384) hipLaunchKernelGGL((k_route_bwd_dense<BF16, 16, 24>), g, b, 0, s, a);
+  else if (a.E <= 512) hipLaunchKernelGGL((k_route_bwd_dense<BF16, 16, 32>), g, b, 0, s, a);
+  else hipLaunchKernelGGL((k_route_bwd_dense<BF16, 32, 32>), g, b, 0, s, a);
+}
+
 }  // namespace
 
 hipError_t launch_route_fwd(const mok_route_desc& d, const void* x, const float* bias,
@@ -950,14 +1042,14 @@ hipError_t launch_route_fwd(const mok_route_desc& d, const void* x, const float*
 hipError_t launch_route_bwd(const mok_route_desc& d, const void* x, const int32_t* idx, const float* dw,
                             void* dx, hipStream_t s) {
   RouteBwdArgs a{x, idx, dw, dx, d.num_tokens, d.logits_stride, d.num_experts, d.top_k,
-                 d.score == MOK_SCORE_SIGMOID, d.renorm, d.scale};
+                 d.score == MOK_SCORE_SIGMOID, d.renorm, 0, d.scale};
   if (a.N == 0) return hipSuccess;
   const int cus = device_cus() > 0 ? device_cus() : 256;
   const bool bf = d.elem == MOK_ELEM_BF16;
+  a.vec = a.E % 4 == 0 && a.ld % 4 == 0 && (reinterpret_cast<uintptr_t>(x) & (bf ? 7 : 15)) == 0;
   if (!a.sigmoid && !a.renorm) {
-    const int grid = grid_of(a.N, kWaves, 8 * cus);
-    if (bf) hipLaunchKernelGGL(k_route_bwd_dense<true>, dim3(grid), dim3(64 * kWaves), 0, s, a);
-    else hipLaunchKernelGGL(k_route_bwd_dense<false>, dim3(grid), dim3(64 * kWaves), 0, s, a);
+    if (bf) route_bwd_dense<true>(a, cus, s);
+    else route_bwd_dense<false>(a, cus, s);
     return hipGetLastError();
   }
   // 4 rows a wave at a time (16 E bytes of LDS, so that enough waves are resident); 8 where a run of 4
