@@ -111,6 +111,9 @@ _SIGS = {
                                           ctypes.POINTER(ctypes.c_size_t)]),
     "mok_two_wave_floor": (ctypes.c_int64, [ctypes.c_int32] * 4),
     "mok_schedule": (ctypes.c_int, [ctypes.POINTER(MokDesc), _P, _P, _P, _P, _P, _P]),
+    "mok_schedule_routed": (ctypes.c_int, [ctypes.POINTER(MokDesc), _P, _P, _P, _P, _P]),
+    "mok_layer_fwd_routed": (ctypes.c_int, [ctypes.POINTER(MokDesc), _P, ctypes.POINTER(MokWeights), _P,
+                                            _P, _P, _P, _P, _P, _P, _P]),
     "mok_schedule_noalloc": (ctypes.c_int, [ctypes.POINTER(MokDesc), _P, _P, _P, _P, _P]),
     "mok_router_fwd": (ctypes.c_int, [ctypes.POINTER(MokDesc), _P, _P, _P, _P]),
     "mok_router_ws_size": (ctypes.c_int, [ctypes.POINTER(MokDesc), ctypes.POINTER(ctypes.c_size_t)]),
@@ -262,6 +265,14 @@ def mok_schedule(d: MokDesc, logits, topk_idx, topk_p, saved, ws, stream=None):
                                               _ptr(topk_p), _ptr(saved), _ptr(ws), _stream(stream)))
 
 
+def mok_schedule_routed(d: MokDesc, topk_idx, topk_p, saved, ws, stream=None):
+    """The schedule table of a given choice (topk_idx int32, topk_p float32, both tidied in place)."""
+    _need_cuda(topk_idx, topk_p, saved, ws)
+    _check("mok_schedule_routed", lib().mok_schedule_routed(ctypes.byref(d), _ptr(topk_idx),
+                                                            _ptr(topk_p), _ptr(saved), _ptr(ws),
+                                                            _stream(stream)))
+
+
 def mok_schedule_noalloc(d: MokDesc, logits, topk_idx, topk_p, saved, stream=None):
     _need_cuda(logits, topk_idx, topk_p, saved)
     _check("mok_schedule_noalloc", lib().mok_schedule_noalloc(ctypes.byref(d), _ptr(logits),
@@ -315,6 +326,14 @@ def mok_layer_fwd(d: MokDesc, x_seg, logits, w: MokWeights, out_seg, topk_idx, t
                                                 ctypes.byref(w), _ptr(out_seg), _ptr(topk_idx),
                                                 _ptr(topk_p), _ptr(saved), _ptr(ring),
                                                 _ptr(slots), _ptr(ws), _stream(stream)))
+
+
+def mok_layer_fwd_routed(d: MokDesc, x_seg, w: MokWeights, out_seg, topk_idx, topk_p, saved, ring,
+                         slots, ws, stream=None):
+    _need_cuda(x_seg, out_seg, topk_idx, topk_p, saved, ring, slots, ws)
+    _check("mok_layer_fwd_routed", lib().mok_layer_fwd_routed(
+        ctypes.byref(d), _ptr(x_seg), ctypes.byref(w), _ptr(out_seg), _ptr(topk_idx), _ptr(topk_p),
+        _ptr(saved), _ptr(ring), _ptr(slots), _ptr(ws), _stream(stream)))
 
 
 def macro_ws_size(d: MokDesc, num_macro: int) -> int:

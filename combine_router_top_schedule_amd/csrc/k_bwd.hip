@@ -600,8 +600,13 @@ __global__ void k_dp_finalize(const int32_t* hdr, const int32_t* perm, const flo
   }
 }
 
-__global__ void k_dlogits(const int32_t* idx, const float* p, const float* dp, float* dl,
-                          int64_t N, int K, int E) {
+// After a forward with a given choice p is no softmax of logits: that is an error here.
+__global__ void k_dlogits(const int32_t* hdr, int32_t* err, const int32_t* idx, const float* p,
+                          const float* dp, float* dl, int64_t N, int K, int E) {
+  if (hdr[kHdrRouted]) {
+    if (threadIdx.x == 0) set_error(err, MOK_ERR_UNSUPPORTED);
+    return;
+  }
   for (int64_t n = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; n < N;
        n += int64_t(gridDim.x) * blockDim.x) {
     float s = 0.f;
@@ -789,8 +794,9 @@ hipError_t launch_backward(const Layout& L, const BwdBuffers& b, hipStream_t s) 
   hipLaunchKernelGGL(k_dp_finalize, dim3(grid_cap(L.rows_max / 256 + 1, 4096)), dim3(256), 0, s,
                      hdr, perm, b.dp_part, int(cdiv(I, kTileN)), b.dp, L.rows_max);
   if (b.dlogits)
-    hipLaunchKernelGGL(k_dlogits, dim3(grid_cap(L.N / 256 + 1, 4096)), dim3(256), 0, s, b.topk_idx,
-                       b.topk_p, b.dp, b.dlogits, L.N, L.K, L.E);
+    hipLaunchKernelGGL(k_dlogits, dim3(grid_cap(L.N / 256 + 1, 4096)), dim3(256), 0, s, hdr,
+                       reinterpret_cast<int32_t*>(b.ws) + kWsError, b.topk_idx, b.topk_p, b.dp,
+                       b.dlogits, L.N, L.K, L.E);
   if ((err = hipGetLastError()) != hipSuccess) return err;
   return hipSuccess;
 }

@@ -89,6 +89,9 @@ __device__ __forceinline__ void sort_desc(uint64_t (&key)[KM]) {
   }
 }
 
+// KM = 0: the choice is given (idx and p hold it: any experts and weights). Slots that name no expert, or
+// one that an earlier slot of the token names, become expert -1 with weight 0, so every later stage
+// sees each expert of a token once.
 // One thread per token: the block's 256 tokens stream their logits through LDS in chunks of
 // 32 experts (coalesced 128-byte row pieces in, conflict-free column reads out), and each
 // thread keeps its token's top-KM in registers. Two LDS chunk buffers: the loads of chunk
@@ -96,7 +99,6 @@ __device__ __forceinline__ void sort_desc(uint64_t (&key)[KM]) {
 template <int KM>
 __global__ __launch_bounds__(256) void k_topk_scan(RouterArgs a) {
   __shared__ int s_b;
-  __shared__ float s_l[2][kTopkTokensPerBlock][33];
   __shared__ uint64_t s_mask[kTopkTokensPerBlock];
   __shared__ int s_wcnt[4][kMaxLocalExperts + 2];
   __shared__ int s_excl[kMaxLocalExperts + 2];
@@ -107,7 +109,11 @@ __global__ __launch_bounds__(256) void k_topk_scan(RouterArgs a) {
   const int b = s_b;
   const int64_t n_base = int64_t(b) * kTopkTokensPerBlock;
   const int64_t n_me = n_base + tid;
+  uint64_t mask = 0;
+  bool raw_merge = false;   // a sole pair that the epilogue cannot weigh (its weight's sign marks raw rows)
 
+  if constexpr (KM > 0) {
+  __shared__ float s_l[2][kTopkTokensPerBlock][33];
   uint64_t key[KM];
 #pragma unroll
   for (int j = 0; j < KM; ++j) key[j] = 0;   // below every real key
@@ -192,7 +198,6 @@ __global__ __launch_bounds__(256) void k_topk_scan(RouterArgs a) {
     v[j] = key_value(key[j]);
     id[j] = key_expert(key[j]);
   }
-  uint64_t mask = 0;
   if (n_me < a.N) {
     // p_k = exp(l_k - l_0) / sum_j exp(l_j - l_0), fp32, k ascending
     float sum = 0.f;
@@ -209,6 +214,28 @@ __global__ __launch_bounds__(256) void k_topk_scan(RouterArgs a) {
       }
     }
   }
+  } else if (n_me < a.N) {
+    int id[kMaxTopK];
+#pragma unroll
+    for (int k = 0; k < kMaxTopK; ++k) {
+      id[k] = k < a.K ? a.idx[n_me * a.K + k] : -1;
+      bool ok = id[k] >= 0 && id[k] < a.E;
+#pragma unroll
+      for (int q = 0; q < k; ++q) ok = ok && id[q] != id[k];
+      if (k < a.K) {
+        if (ok) {
+          const int le = id[k] - a.e0;
+          if (le >= 0 && le < a.El) {
+            mask |= 1ull << le;
+            raw_merge = raw_merge || a.p[n_me * a.K + k] < 0.f;
+          }
+        } else {
+          a.idx[n_me * a.K + k] = -1;
+          a.p[n_me * a.K + k] = 0.f;
+        }
+      }
+    }
+  }
   s_mask[tid] = mask;
   __syncthreads();
 
@@ -217,8 +244,10 @@ __global__ __launch_bounds__(256) void k_topk_scan(RouterArgs a) {
   const uint64_t mymask = s_mask[tid];
   const uint64_t lt = (1ull << lane) - 1;
   const int nc = a.El + 2;   // counted values
+  // tokens whose output row the merge forms (the others' row comes straight from a GEMM epilogue)
+  const bool merged = __popcll(mymask) > 1 || (mymask != 0 && raw_merge);
   auto counted = [&](int e) -> bool {
-    return e < a.El ? ((mymask >> e) & 1) : e == a.El ? mymask != 0 : __popcll(mymask) > 1;
+    return e < a.El ? ((mymask >> e) & 1) : e == a.El ? mymask != 0 : merged;
   };
   for (int e = 0; e < nc; ++e) {
     bool bit = counted(e);
@@ -267,6 +296,7 @@ __global__ __launch_bounds__(256) void k_topk_scan(RouterArgs a) {
       if (b == a.nblocks - 1) {
         // Last block: inclusive values are the totals.
         const int total = int(excl + agg);
+        if (KM == 0) a.hdr[kHdrRouted] = 1;
         if (e < a.El) a.hdr[kHdrCounts + e] = total;
         else a.hdr[e == a.El ? kHdrU : kHdrUm] = total;
       }
@@ -286,7 +316,7 @@ __global__ __launch_bounds__(256) void k_topk_scan(RouterArgs a) {
         int k = 0;
         for (int q = 0; q < a.K; ++q)
           if (a.idx[n * a.K + q] == a.e0 + e) k = q;
-        a.rank[n * a.K + k] = r | (__popcll(mymask) == 1 ? kSoleFlag : 0);
+        a.rank[n * a.K + k] = r | (merged ? 0 : kSoleFlag);
       } else if (r < a.N) {
         (e == a.El ? a.touched : a.multi)[r] = int32_t(n);
       }
@@ -417,7 +447,8 @@ hipError_t launch_router(const Layout& L, const float* logits, int32_t* idx, flo
                state, wsh + kWsTicket, wsh + kWsError,
                L.N, L.E, L.K, L.e0, L.El, L.row_align, L.topk_blocks};
   // top-KM list with KM >= K; its first K entries are the top-K
-  if (L.K <= 1) hipLaunchKernelGGL(k_topk_scan<1>, dim3(L.topk_blocks), dim3(256), 0, s, a);
+  if (!logits) hipLaunchKernelGGL(k_topk_scan<0>, dim3(L.topk_blocks), dim3(256), 0, s, a);
+  else if (L.K <= 1) hipLaunchKernelGGL(k_topk_scan<1>, dim3(L.topk_blocks), dim3(256), 0, s, a);
   else if (L.K <= 2) hipLaunchKernelGGL(k_topk_scan<2>, dim3(L.topk_blocks), dim3(256), 0, s, a);
   else if (L.K <= 4) hipLaunchKernelGGL(k_topk_scan<4>, dim3(L.topk_blocks), dim3(256), 0, s, a);
   else if (L.K <= 8) hipLaunchKernelGGL(k_topk_scan<8>, dim3(L.topk_blocks), dim3(256), 0, s, a);

@@ -184,6 +184,18 @@ mok_status mok_schedule(const mok_desc* desc, const float* logits_dev, int32_t* 
                                   static_cast<uint8_t*>(saved_dev), static_cast<uint8_t*>(ws_dev), s));
 }
 
+mok_status mok_schedule_routed(const mok_desc* desc, int32_t* topk_idx_dev, float* topk_p_dev,
+                               void* saved_dev, void* ws_dev, void* stream) {
+  mok_status st = check_desc(desc);
+  if (st != MOK_OK) return st;
+  if (!topk_idx_dev || !topk_p_dev || !saved_dev || !ws_dev) return MOK_ERR_NULL;
+  if (!aligned16(saved_dev) || !aligned16(ws_dev)) return MOK_ERR_ALIGN;
+  const Layout L = layout_of(*desc);
+  return hip_status(launch_router(L, nullptr, topk_idx_dev, topk_p_dev,
+                                  static_cast<uint8_t*>(saved_dev), static_cast<uint8_t*>(ws_dev),
+                                  as_stream(stream)));
+}
+
 mok_status mok_schedule_noalloc(const mok_desc* desc, const float* logits_dev,
                                 int32_t* topk_idx_dev, float* topk_p_dev, void* saved_dev,
                                 void* stream) {
@@ -278,17 +290,17 @@ mok_status mok_device_status(const void* ws_dev, void* stream, mok_status* out) 
 
 }  // extern "C"
 
-extern "C" {
+namespace {
 
-mok_status mok_layer_fwd(const mok_desc* desc, const void* const* x_seg_dev,
-                         const float* logits_dev, const mok_weights* w,
-                         void* const* out_seg_dev, int32_t* topk_idx_dev, float* topk_p_dev,
-                         void* saved_dev, void* ring_dev, void* slots_dev, void* ws_dev,
-                         void* stream) {
+// mok_layer_fwd (logits given) and mok_layer_fwd_routed (logits null: idx and p given).
+mok_status layer_fwd(const mok_desc* desc, const void* const* x_seg_dev, const float* logits_dev,
+                     const mok_weights* w, void* const* out_seg_dev, int32_t* topk_idx_dev,
+                     float* topk_p_dev, void* saved_dev, void* ring_dev, void* slots_dev,
+                     void* ws_dev, void* stream) {
   mok_status st = check_desc(desc);
   if (st != MOK_OK) return st;
-  if (!x_seg_dev || !logits_dev || !w || !out_seg_dev || !topk_idx_dev || !topk_p_dev ||
-      !saved_dev || !ring_dev || !slots_dev || !ws_dev)
+  if (!x_seg_dev || !w || !out_seg_dev || !topk_idx_dev || !topk_p_dev || !saved_dev ||
+      !ring_dev || !slots_dev || !ws_dev)
     return MOK_ERR_NULL;
   st = check_weights(desc, w, false);
   if (st != MOK_OK) return st;
@@ -304,6 +316,30 @@ mok_status mok_layer_fwd(const mok_desc* desc, const void* const* x_seg_dev,
   if (st != MOK_OK) return st;
   return hip_status(launch_layer_fwd_macro(L, *desc, 1, &mb, wk, static_cast<uint8_t*>(ring_dev),
                                            static_cast<uint8_t*>(ws_dev), as_stream(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+mok_status mok_layer_fwd(const mok_desc* desc, const void* const* x_seg_dev,
+                         const float* logits_dev, const mok_weights* w,
+                         void* const* out_seg_dev, int32_t* topk_idx_dev, float* topk_p_dev,
+                         void* saved_dev, void* ring_dev, void* slots_dev, void* ws_dev,
+                         void* stream) {
+  const mok_status st = check_desc(desc);
+  if (st != MOK_OK) return st;
+  if (!logits_dev) return MOK_ERR_NULL;
+  return layer_fwd(desc, x_seg_dev, logits_dev, w, out_seg_dev, topk_idx_dev, topk_p_dev,
+                   saved_dev, ring_dev, slots_dev, ws_dev, stream);
+}
+
+mok_status mok_layer_fwd_routed(const mok_desc* desc, const void* const* x_seg_dev,
+                                const mok_weights* w, void* const* out_seg_dev,
+                                int32_t* topk_idx_dev, float* topk_p_dev, void* saved_dev,
+                                void* ring_dev, void* slots_dev, void* ws_dev, void* stream) {
+  return layer_fwd(desc, x_seg_dev, nullptr, w, out_seg_dev, topk_idx_dev, topk_p_dev, saved_dev,
+                   ring_dev, slots_dev, ws_dev, stream);
 }
 
 mok_status mok_macro_ws_size(const mok_desc* desc, int32_t num_macro, size_t* ws_bytes) {

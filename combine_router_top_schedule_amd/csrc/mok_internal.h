@@ -61,6 +61,7 @@ enum SavedHeader : int {
   kHdrU = 2,        // touched tokens
   kHdrUm = 3,       // touched tokens with more than one local pair
   kHdrStatus = 4,   // copy of the router's device-side status (0 if its scan finished)
+  kHdrRouted = 5,   // 1: the choice was given (mok_schedule_routed, mok_layer_fwd_routed)
   kHdrCounts = 16,  // [E_loc]
   kHdrOffsets = 96, // [E_loc + 1]
   kHdrWords = 192,
@@ -316,6 +317,7 @@ struct FillRange {
 };
 constexpr int kMaxFillRanges = 16;
 hipError_t launch_fill_ranges(const FillRange* r, int count, hipStream_t s);
+// logits null: idx and p hold the choice and are tidied (k_topk_scan<0>).
 // clear_error = false keeps a failure an earlier call recorded in the error word (the
 // routers of several macrobatches of one fused launch).
 hipError_t launch_router(const Layout& L, const float* logits, int32_t* idx, float* p,
@@ -394,7 +396,7 @@ int fused_slots_per_xcd(const Layout& L);
 // Buffers of one macrobatch (one layer call) of a fused forward launch.
 struct MacroBuffers {
   const void* const* x_seg;
-  const float* logits;
+  const float* logits;      // null: idx and p are given
   void* const* out_seg;
   int32_t* idx;
   float* p;

@@ -7,7 +7,8 @@ from typing import Optional
 import torch
 
 from . import (MOK_MXFP8, desc, mok_autotune, mok_combine, mok_dispatch, mok_expert_ffn,
-               mok_layer_bwd, mok_layer_fwd, mok_pack_weights, mok_quantize_mx, mok_schedule,
+               mok_layer_bwd, mok_layer_fwd, mok_layer_fwd_routed, mok_pack_weights,
+               mok_quantize_mx, mok_route_bwd, mok_route_fwd, mok_schedule, mok_schedule_routed,
                query_sizes, seg_table, weights_struct)
 
 
@@ -40,6 +41,8 @@ class MokLayer:
         self.bws = None
         self.w = None
         self._keep = []
+        self._quant = []      # (master, transposed, codes, scales) of the MXFP8 weights
+        self._packed = None
 
     # ---- weights ---------------------------------------------------------------------------
     def set_weights(self, wg, wu, wd, packed: bool = True):
@@ -49,6 +52,8 @@ class MokLayer:
         workspace)."""
         d = self.d
         self._keep = [wg, wu, wd]
+        self._quant = []
+        self._packed = None
         E, I, H = d.num_local_experts, d.intermediate, d.hidden
         dev = self.device
         if not self.mx:
@@ -59,7 +64,7 @@ class MokLayer:
                 c = torch.empty((E, orow, ocol), dtype=torch.uint8, device=dev)
                 s = torch.empty((E, orow, ocol // 32), dtype=torch.uint8, device=dev)
                 mok_quantize_mx(src, transpose, c, s)
-                self._keep += [c, s]
+                self._quant.append((src, transpose, c, s))
                 return c, s
 
             wg_q, wg_s = q(wg, I, H, False)
@@ -72,10 +77,17 @@ class MokLayer:
                                     wd_q=wd_q, wd_s=wd_s, wgt_q=wgt_q, wgt_s=wgt_s, wut_q=wut_q,
                                     wut_s=wut_s, wdt_q=wdt_q, wdt_s=wdt_s)
         if packed:
-            buf = _bytes(query_sizes(d).packed_bytes, dev)
-            mok_pack_weights(d, self.w, buf)
-            self._keep.append(buf)
-            self.w.packed = buf.data_ptr()
+            self._packed = _bytes(query_sizes(d).packed_bytes, dev)
+            mok_pack_weights(d, self.w, self._packed)
+            self.w.packed = self._packed.data_ptr()
+
+    def refresh_weights(self):
+        """After an update of the BF16 masters in place (an optimizer step): quantises (MXFP8) and packs
+        them again, into the buffers that set_weights made."""
+        for src, transpose, c, s in self._quant:
+            mok_quantize_mx(src, transpose, c, s)
+        if self._packed is not None:
+            mok_pack_weights(self.d, self.w, self._packed)
 
     # ---- segment pointer tables ---------------------------------------------------------------
     def segs(self, rows):
@@ -83,7 +95,23 @@ class MokLayer:
         self._keep.append(t)
         return t
 
+    # ---- gate ---------------------------------------------------------------------------------
+    def route(self, gate, logits, bias=None, token_mask=None, load=None):
+        """Chooses experts and weights by `gate` (a route_desc) for schedule_routed and
+        forward_routed."""
+        K = self.d.top_k
+        mok_route_fwd(gate, logits, self.idx.view(-1, K), self.p.view(-1, K), bias=bias,
+                      token_mask=token_mask, load=load)
+
+    def route_backward(self, gate, logits, dp, dlogits):
+        """dlogits from the backward's dp, for the choice that route made."""
+        K = self.d.top_k
+        mok_route_bwd(gate, logits, self.idx.view(-1, K), dp.view(-1, K), dlogits)
+
     # ---- staged path ------------------------------------------------------------------------
+    def schedule_routed(self):
+        mok_schedule_routed(self.d, self.idx, self.p, self.saved, self.ws)
+
     def schedule(self, logits):
         mok_schedule(self.d, logits, self.idx, self.p, self.saved, self.ws)
 
@@ -107,6 +135,11 @@ class MokLayer:
     def forward(self, x_seg, logits, out_seg):
         mok_layer_fwd(self.d, x_seg, logits, self.w, out_seg, self.idx, self.p, self.saved,
                       self.ring, self.slots, self.ws)
+
+    def forward_routed(self, x_seg, out_seg):
+        """Forward with the choice in self.idx and weights in self.p (see route)."""
+        mok_layer_fwd_routed(self.d, x_seg, self.w, out_seg, self.idx, self.p, self.saved, self.ring,
+                             self.slots, self.ws)
 
     def autotune(self, x_seg, logits, out_seg, reps: int = 3, apply: bool = True):
         """Time the fused forward over candidate minibatch sizes and dispatch-CU counts (this

@@ -130,7 +130,8 @@ typedef struct {
   int64_t slot_bytes;    /* bytes of one activation slot (g|u of 256 rows)                  */
   /* Layout of the schedule table inside `saved` (byte offsets). Words 0..191 are a header:
    * [0] P (local pairs), [1] rows (P plus MXFP8 padding), [2] U (touched tokens),
-   * [3] touched tokens with several local pairs, [4] the router's device-side status,
+   * [3] touched tokens with several local pairs, [4] the router's device-side status, [5] 1 if the
+   * choice was given (mok_schedule_routed),
    * [16 + e] count of local expert e, [96 + e] first row of expert e (e = 0..E_loc). */
   int64_t perm_offset;    /* int32 [rows_max]: expert-order row -> pair id (-1: pad row)     */
   int64_t tokpos_offset;  /* int32 [N*K]: pair id -> row (-1: not local)                     */
@@ -212,6 +213,17 @@ int64_t mok_two_wave_floor(int32_t cus, int32_t tile_m, int32_t tile_n, int32_t 
  *   ws_dev       scratch (ws_bytes) */
 mok_status mok_schedule(const mok_desc* desc, const float* logits_dev, int32_t* topk_idx_dev,
                         float* topk_p_dev, void* saved_dev, void* ws_dev, void* stream);
+
+/* The schedule table of a given choice, from any gate (mok_route_fwd's, or the caller's own):
+ *   topk_idx_dev int32 [N][K] in/out: experts, in any order; a slot that names none (outside 0..E-1)
+ *                or one that an earlier slot of the token names is rewritten to -1, with weight 0
+ *   topk_p_dev   fp32 [N][K] in/out: weights, of any sign
+ * The later stages take both as after mok_schedule. mok_layer_bwd's dp is then the gradient of these
+ * weights (not written at slots without an expert); its dlogits must be NULL, as the way from
+ * logits to weights is not known there (mok_route_bwd goes it back for mok_route_fwd): else it writes none
+ * and reports MOK_ERR_UNSUPPORTED through mok_device_status. */
+mok_status mok_schedule_routed(const mok_desc* desc, int32_t* topk_idx_dev, float* topk_p_dev,
+                               void* saved_dev, void* ws_dev, void* stream);
 
 /* mok_schedule for callers that cannot allocate device memory (code under HIP graph capture,
  * tight serving loops, harnesses that forbid allocation): the same outputs, bit for bit, with
@@ -301,6 +313,13 @@ mok_status mok_layer_fwd(const mok_desc* desc, const void* const* x_seg_dev,
                          void* saved_dev, void* ring_dev, void* slots_dev, void* ws_dev,
                          void* stream);
 
+/* mok_layer_fwd with a given choice instead of logits: topk_idx_dev and topk_p_dev as for
+ * mok_schedule_routed, everything else as for mok_layer_fwd. */
+mok_status mok_layer_fwd_routed(const mok_desc* desc, const void* const* x_seg_dev,
+                                const mok_weights* w, void* const* out_seg_dev,
+                                int32_t* topk_idx_dev, float* topk_p_dev, void* saved_dev,
+                                void* ring_dev, void* slots_dev, void* ws_dev, void* stream);
+
 /* Macrobatch interleave: `num_macro` consecutive layer calls (1..8 macrobatches, each with its
  * own tokens, logits, outputs, schedule table and slots, the same weights) in one persistent
  * launch. The pages' ring buffer interleaves dispatch and combine at macrobatch boundaries: the
@@ -335,7 +354,8 @@ mok_status mok_layer_fwd_macro(const mok_desc* desc, int32_t num_macro,
  * dX row written directly), and the weight gradients. Then the dX merge over k ascending of the
  * tokens with several local pairs and, when E_loc == E, dlogits.
  *   dp_dev       fp32 [N][K], written at local pairs only
- *   dlogits_dev  fp32 [N][E] or NULL; must be NULL unless E_loc == E
+ *   dlogits_dev  fp32 [N][E] or NULL; must be NULL unless E_loc == E, and after a forward with a given
+ *                choice (mok_schedule_routed)
  *   g            weight gradients, fully overwritten
  *   ring_dev     the ring the matching mok_layer_fwd used, untouched since (or NULL). Row tiles
  *                whose ring slot still holds them give back their g|u and h; all other rows
