@@ -308,7 +308,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_fwd(RouteArgs a) {
 //      tau <= kappa + eps; and theirs are at least kappa - eps);
 //   4. those few candidates (nearly always exactly K) are ranked by counting. Two whose fp32 keys are
 //      further apart than 2 eps are in that order; two of the same logit and bias are tied; a token
-//      with two others, or with more than 2 KM candidates, goes to choose_wave.
+//      with two others, or with more than 2 KM candidates, goes to choose_wave (choose_apart).
 // Larger value to a, smaller to b.
 __device__ __forceinline__ void order(float& a, float& b) {
   const float hi = fmaxf(a, b), lo = fminf(a, b);
@@ -350,16 +350,13 @@ __device__ __forceinline__ void merge_lanes(float* v) {
   merge_down<M>(v, w);
 }
 
-// The tokens that a wave has left with kLater in their first slot: `count` of them, in `list` if that holds
-// them; else all tokens of the wave's tiles (tile0, tile0 + stride, ..., of T tokens) are looked at. Called once, when all else is done, and not inlined: inside the
-// tile loop, the constants of its fp64 exponentials were kept in 80 registers throughout (84 us instead of
-// 71 us for 131,072 tokens of 256 experts).
-constexpr int32_t kLater = -2;
-constexpr int kListed = 32;
+// The tokens n0 + b / L for the set bits b of `left`, one after the other. Not inlined: the constants of its
+// fp64 exponentials would be kept in 80 registers throughout the tile loop (84 us instead of 71 us for
+// 131,072 tokens of 256 experts). Called from the loop and not behind it, so that the 10 us which a token
+// takes, nearly all of it latency, are filled by the other waves.
 template <bool BF16>
-__device__ __attribute__((noinline)) void choose_later(const RouteArgs* args, double* key, int* load,
-                                                       const int64_t* list, int count, int64_t tile0,
-                                                       int64_t stride, int T) {
+__device__ __attribute__((noinline)) void choose_apart(const RouteArgs* args, double* key, int* load,
+                                                       int64_t n0, uint64_t left, int L) {
   // the same in every lane, and so in scalar registers
   RouteArgs a;
   {
@@ -370,24 +367,14 @@ __device__ __attribute__((noinline)) void choose_later(const RouteArgs* args, do
     for (int i = 0; i < int(sizeof(RouteArgs) / 4); ++i) to[i] = __builtin_amdgcn_readfirstlane(from[i]);
   }
   const int lane = threadIdx.x & 63;
-  const bool listed = count <= kListed;
-  // (this wave's own stores, read back past the CU's cache)
-  if (!listed) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  for (int64_t i0 = 0;; i0 += 64) {
-    // 64 numbers at a time: those of the list, or all
-    const int64_t i = i0 + lane;
-    const int64_t n = listed ? (i < count ? list[i] : a.N) : (tile0 + i / T * stride) * T + i % T;
-    if (__all(n >= a.N)) break;
-    const bool mine = n < a.N && (listed || ld_relaxed(a.idx + n * a.K) == kLater);
-    for (uint64_t left = __ballot(mine); left; left &= left - 1) {
-      const int64_t m = __shfl(n, __builtin_ctzll(left), 64);
-      const int e = choose_wave<BF16>(a, m, lane, key);
-      const float w = weight_wave<BF16>(a, m, lane, e);
-      if (lane < a.K) {
-        a.idx[m * a.K + lane] = e;
-        a.w[m * a.K + lane] = w;
-        if (a.load && e >= 0) atomicAdd(&load[e], 1);
-      }
+  for (; left; left &= left - 1) {
+    const int64_t n = n0 + __builtin_ctzll(left) / L;
+    const int e = choose_wave<BF16>(a, n, lane, key);
+    const float w = weight_wave<BF16>(a, n, lane, e);
+    if (lane < a.K) {
+      a.idx[n * a.K + lane] = e;
+      a.w[n * a.K + lane] = w;
+      if (a.load && e >= 0) atomicAdd(&load[e], 1);
     }
   }
 }
@@ -405,7 +392,6 @@ struct FastLds {   // of one wave
   };
   float group[T][L];
   int out[T][KM];
-  int64_t later[kListed];
 };
 
 // What a kernel forms scores of: of nothing (keys are the logits), of nothing but the softmax's sum (for plain
@@ -452,7 +438,6 @@ __global__ __launch_bounds__(64 * kWaves, L * V >= 1024 ? 3 : 4) void k_route_fa
     for (int i = 0; i < V / 4; ++i)
       of_group[i >> 2] |= min(((j + L * i) * a.chunk_magic) >> 16, 31u) << (8 * (i & 3));
   const uint64_t here = ((1ull << L) - 1) << (t * L);   // the token's lanes
-  int later = 0;   // tokens left for the end, the same in every lane
   const int64_t tiles = (a.N + T - 1) / T;
   const int64_t stride = int64_t(gridDim.x) * kWaves;
   for (int64_t tile = int64_t(blockIdx.x) * kWaves + wave; tile < tiles; tile += stride) {
@@ -687,23 +672,18 @@ __global__ __launch_bounds__(64 * kWaves, L * V >= 1024 ? 3 : 4) void k_route_fa
     const bool some = e >= 0;
     const float v = some ? logit<BF16>(a.x, n * a.ld + e) : -INFINITY;
     const float w = slot_weight<L>(a, some, v, top, sum);
-    if (const uint64_t who = __ballot(slow && j == 0)) {
-      const int at = later + __popcll(who & ((1ull << lane) - 1));
-      if (slow && j == 0 && at < kListed) s.later[at] = n;
-      later += __popcll(who);
-    }
-    if (n < a.N && j < a.K) {
-      a.idx[n * a.K + j] = slow ? kLater : e;
+    if (n < a.N && j < a.K && !slow) {
+      a.idx[n * a.K + j] = e;
       a.w[n * a.K + j] = w;
       if (a.load && some) atomicAdd(&s_load[e], 1);
     }
     wave_sync();
-  }
-  if (later) {
-    if (lane == 0) s.slow.args = a;
-    wave_sync();
-    choose_later<BF16>(&s.slow.args, s.slow.key, s_load, s.later, later, int64_t(blockIdx.x) * kWaves + wave,
-                       stride, T);
+    if (const uint64_t apart = __ballot(slow && j == 0)) {
+      if (lane == 0) s.slow.args = a;
+      wave_sync();
+      choose_apart<BF16>(&s.slow.args, s.slow.key, s_load, tile * T, apart, L);
+      wave_sync();
+    }
   }
   if (a.load) {
     // integer sums: their order changes nothing
