@@ -28,6 +28,7 @@ struct RouteArgs {
   int sigmoid, top2, renorm;
   int vec;               // rows allow loads of 4 logits
   uint32_t chunk_magic;  // ceil(2^16 / (gs / 4)): a chunk's group is (chunk * magic) >> 16 (chunks < 256)
+  uint32_t group_magic;  // ceil(2^32 / gs), gs > 1: an expert's group is (expert * magic) >> 32
   float scale;
 };
 
@@ -127,57 +128,66 @@ __device__ __forceinline__ double wave_max(double v) {
   return __builtin_bit_cast(double, uint64_t(hi) << 32 | lo);
 }
 
-// key: LDS, one double per expert, private to the wave. Returns the expert chosen by slot `lane`
-// (lane < K), -1 where none is left. Written for few instructions (one exponential, one quotient): where
-// a token in ten thousand needs it, most of its time goes into fetching them (11 us with the loops unrolled).
-template <bool BF16>
-__device__ __forceinline__ int choose_wave(const RouteArgs& a, int64_t n, int lane, double* key) {
+// key: LDS, 64 Q doubles (Q = experts / 64, rounded up), private to the wave; bias: in LDS or memory. Returns
+// the expert chosen by slot `lane` (lane < K), -1 where none is left. Written for a short way through few
+// instructions: where a token in some thousands needs it, all but latency and the fetching of its
+// code is hidden.
+template <bool BF16, int Q>
+__device__ __forceinline__ int choose_wave(const RouteArgs& a, const float* bias, int64_t n, int lane,
+                                           double* key) {
   const double kNone = -INFINITY;
   const int64_t row = n * a.ld;
-  const bool top2 = a.G > 1 && a.top2;
-  double sum = 0;
-  // logits
-  float most = -INFINITY;
-  for (int e = lane; e < a.E; e += 64) {
-    const float x = logit<BF16>(a.x, row + e);
-    key[e] = x;
-    most = fmaxf(most, x);
-  }
-  if (a.bias || top2) {
-    // exp(-x), or exp(x - largest) and their sum
-    for (int off = 32; off; off >>= 1) most = fmaxf(most, __shfl_xor(most, off, 64));
+  const bool top2 = a.G > 1 && a.top2, scored = bias || top2;
+  float x[Q];
+#pragma unroll
+  for (int q = 0; q < Q; ++q) x[q] = lane + 64 * q < a.E ? logit<BF16>(a.x, row + lane + 64 * q) : -INFINITY;
+#pragma unroll
+  for (int q = 0; q < Q; ++q) key[lane + 64 * q] = x[q];
+  if (scored) {
+    float most = 0.f;
+    double sum = 0;
+    if (!a.sigmoid) {
+      most = x[0];
+#pragma unroll
+      for (int q = 1; q < Q; ++q) most = fmaxf(most, x[q]);
 #pragma unroll 1
-    for (int e = lane; e < a.E; e += 64) {
-      const double t = exp(a.sigmoid ? -key[e] : key[e] - double(most));
-      key[e] = t;
-      sum += t;
+      for (int off = 32; off; off >>= 1) most = fmaxf(most, __shfl_xor(most, off, 64));
     }
-    for (int off = 32; off; off >>= 1) sum += __shfl_xor(sum, off, 64);
-    // scores, with their bias
+    // exp(-x), or exp(x - largest), and the score with its bias; a softmax needs its sum before
 #pragma unroll 1
-    for (int e = lane; e < a.E; e += 64) {
-      const float x = logit<BF16>(a.x, row + e), b = a.bias ? a.bias[e] : 0.f;
-      const double t = key[e];
-      const double k = (a.sigmoid ? 1.0 : t) / (a.sigmoid ? 1.0 + t : sum) + double(b);
-      key[e] = x > -INFINITY && k > kNone ? k : kNone;
+    for (int pass = a.sigmoid; pass < 2; ++pass) {
+#pragma unroll 1
+      for (int e = lane; e < a.E; e += 64) {
+        const double v = key[e];
+        const double t = exp(a.sigmoid ? -v : v - double(most));
+        if (pass == 0) {
+          sum += t;
+        } else {
+          const double k = (a.sigmoid ? 1.0 : t) / (a.sigmoid ? 1.0 + t : sum) + (bias ? double(bias[e]) : 0.0);
+          key[e] = v > kNone && k > kNone ? k : kNone;
+        }
+      }
+      if (pass == 0)
+#pragma unroll 1
+        for (int off = 32; off; off >>= 1) sum += __shfl_xor(sum, off, 64);
     }
   }
-  if (!a.bias && !top2)
-    for (int e = lane; e < a.E; e += 64) key[e] = key[e] > kNone ? key[e] : kNone;   // NaN is not able
   wave_sync();
+  uint64_t stay = ~0ull;
+  int P = 64;   // lanes a group
   if (a.G > 1) {
-    // P lanes a group: each the two largest of its experts, then those of the P lanes
-    int P = 64;
     while (P * a.G > 64) P >>= 1;
+    // each lane the two largest of its experts, then those of the P lanes
     const int g = lane / P;
     double best = kNone, second = kNone;
     if (g < a.G)
 #pragma unroll 2
       for (int i = lane % P; i < a.gs; i += P) {
         const double k = key[g * a.gs + i];
+        const bool able = k > kNone;   // (NaN is not)
         const double low = k < best ? k : best;
-        second = low > second ? low : second;
-        best = k > best ? k : best;
+        second = able && low > second ? low : second;
+        best = able && k > best ? k : best;
       }
 #pragma unroll 1
     for (int off = P >> 1; off; off >>= 1) {
@@ -189,41 +199,46 @@ __device__ __forceinline__ int choose_wave(const RouteArgs& a, int64_t n, int la
     }
     if (a.top2 && second > kNone) best += second;
     int place = 0;
-#pragma unroll 2
+#pragma unroll 4
     for (int o = 0; o < a.G; ++o) {
       const double other = __shfl(best, o * P, 64);
       place += other > best || (other == best && o < g);
     }
-    const uint64_t stay = __ballot(g < a.G && place < a.Kg);
-    wave_sync();
-#pragma unroll 1
-    for (int e = lane; e < a.E; e += 64) {
-      const bool in = (stay >> (e / a.gs * P)) & 1;
-      // (groups ranked by scores: from here on the logits decide)
-      if (in && !a.bias && top2 && key[e] > kNone) key[e] = logit<BF16>(a.x, row + e);
-      if (!in) key[e] = kNone;
-    }
-    wave_sync();
+    stay = __ballot(g < a.G && place < a.Kg);
+  }
+  // From here on in registers. Without a bias the logits decide (groups may have gone by scores).
+  double k[Q];
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    const int e = lane + 64 * q;
+    const int g = a.gs > 1 ? int(__umulhi(uint32_t(e), a.group_magic)) : e;
+    const double v = e < a.E ? key[e] : kNone;
+    const bool in = e < a.E && v > kNone && (a.G == 1 || ((stay >> (g * P & 63)) & 1));
+    k[q] = in ? (bias ? v : double(x[q])) : kNone;
   }
   int mine = -1;
 #pragma unroll 1
-  for (int k = 0; k < a.K; ++k) {
-    double best = kNone;
-    int at = a.E;
-    for (int e = lane; e < a.E; e += 64) {
-      const double v = key[e];
-      if (v > best) { best = v; at = e; }
+  for (int slot = 0; slot < a.K; ++slot) {
+    double best = k[0];
+    int at = lane;
+#pragma unroll
+    for (int q = 1; q < Q; ++q) {
+      at = k[q] > best ? lane + 64 * q : at;
+      best = k[q] > best ? k[q] : best;
     }
     const double all = wave_max(best);
     if (!(all > kNone)) break;   // the same in every lane
-    int first = best == all ? at : a.E;
-    if (__popcll(__ballot(best == all)) > 1)
+    uint64_t who = __ballot(best == all);
+    if (who & (who - 1)) {       // several: the lowest expert
+      int first = best == all ? at : a.E;
+#pragma unroll 1
       for (int off = 32; off; off >>= 1) first = min(first, __shfl_xor(first, off, 64));
-    const uint64_t who = __ballot(best == all && at == first);
-    first = __builtin_amdgcn_readlane(at, __builtin_ctzll(who));
-    if (lane == k) mine = first;
-    if ((first & 63) == lane) key[first] = kNone;
-    wave_sync();
+      who = __ballot(best == all && at == first);
+    }
+    const int first = __builtin_amdgcn_readlane(at, __builtin_ctzll(who));
+    mine = lane == slot ? first : mine;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) k[q] = first == lane + 64 * q ? kNone : k[q];
   }
   wave_sync();
   return mine;
@@ -263,10 +278,10 @@ __device__ __forceinline__ float weight_wave(const RouteArgs& a, int64_t n, int 
   return slot_weight<16>(a, some, some ? logit<BF16>(a.x, row + e) : -INFINITY, top, sum);
 }
 
-template <bool BF16>
+template <bool BF16, int Q>
 __global__ __launch_bounds__(64 * kWaves) void k_route_fwd(RouteArgs a) {
-  extern __shared__ double s_key[];   // [kWaves][E], then int [E]
-  int* s_load = reinterpret_cast<int*>(s_key + kWaves * a.E);
+  __shared__ double s_key[kWaves][64 * Q];
+  __shared__ int s_load[64 * Q];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   if (a.load) {
     for (int e = threadIdx.x; e < a.E; e += 64 * kWaves) s_load[e] = 0;
@@ -276,7 +291,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_fwd(RouteArgs a) {
     int e = -1;
     float w = 0.f;
     if (!a.mask || a.mask[n]) {
-      e = choose_wave<BF16>(a, n, lane, s_key + wave * a.E);
+      e = choose_wave<BF16, Q>(a, a.bias, n, lane, s_key[wave]);
       w = weight_wave<BF16>(a, n, lane, e);
     }
     if (lane < a.K) {
@@ -354,9 +369,9 @@ __device__ __forceinline__ void merge_lanes(float* v) {
 // fp64 exponentials would be kept in 80 registers throughout the tile loop (84 us instead of 71 us for
 // 131,072 tokens of 256 experts). Called from the loop and not behind it, so that the 10 us which a token
 // takes, nearly all of it latency, are filled by the other waves.
-template <bool BF16>
-__device__ __attribute__((noinline)) void choose_apart(const RouteArgs* args, double* key, int* load,
-                                                       int64_t n0, uint64_t left, int L) {
+template <bool BF16, int Q>
+__device__ __attribute__((noinline)) void choose_apart(const RouteArgs* args, const float* bias, double* key,
+                                                       int* load, int64_t n0, uint64_t left, int L) {
   // the same in every lane, and so in scalar registers
   RouteArgs a;
   {
@@ -369,7 +384,7 @@ __device__ __attribute__((noinline)) void choose_apart(const RouteArgs* args, do
   const int lane = threadIdx.x & 63;
   for (; left; left &= left - 1) {
     const int64_t n = n0 + __builtin_ctzll(left) / L;
-    const int e = choose_wave<BF16>(a, n, lane, key);
+    const int e = choose_wave<BF16, Q>(a, bias, n, lane, key);
     const float w = weight_wave<BF16>(a, n, lane, e);
     if (lane < a.K) {
       a.idx[n * a.K + lane] = e;
@@ -681,7 +696,8 @@ __global__ __launch_bounds__(64 * kWaves, L * V >= 1024 ? 3 : 4) void k_route_fa
     if (const uint64_t apart = __ballot(slow && j == 0)) {
       if (lane == 0) s.slow.args = a;
       wave_sync();
-      choose_apart<BF16>(&s.slow.args, s.slow.key, s_load, tile * T, apart, L);
+      choose_apart<BF16, L * V / 64>(&s.slow.args, kBias ? s_bias : nullptr, s.slow.key, s_load, tile * T,
+                                     apart, L);
       wave_sync();
     }
   }
@@ -955,8 +971,8 @@ void fast(const RouteArgs& a, int grid, hipStream_t s) {
 template <bool BF16>
 void route_fwd(const RouteArgs& a, bool quick, int lanes, int grid, hipStream_t s) {
   if (!quick) {
-    const size_t lds = size_t(kWaves) * a.E * 8 + size_t(a.E) * 4;   // at most 36 KB
-    hipLaunchKernelGGL(k_route_fwd<BF16>, dim3(grid), dim3(64 * kWaves), lds, s, a);
+    if (a.E <= 256) hipLaunchKernelGGL((k_route_fwd<BF16, 4>), dim3(grid), dim3(64 * kWaves), 0, s, a);
+    else hipLaunchKernelGGL((k_route_fwd<BF16, 16>), dim3(grid), dim3(64 * kWaves), 0, s, a);
   } else if (a.K <= 8) {
     if (lanes == 8) {
       if (a.E <= 64) fast<BF16, 8, 8, 8>(a, grid, s);
@@ -996,7 +1012,7 @@ hipError_t launch_route_fwd(const mok_route_desc& d, const void* x, const float*
                             const uint8_t* mask, int32_t* idx, float* w, int32_t* load, hipStream_t s) {
   RouteArgs a{x, bias, mask, idx, w, load, d.num_tokens, d.logits_stride, d.num_experts, d.top_k,
               d.num_groups, d.top_groups, d.num_experts / d.num_groups, d.score == MOK_SCORE_SIGMOID,
-              d.group_score == MOK_GROUP_TOP2, d.renorm, 0, 0, d.scale};
+              d.group_score == MOK_GROUP_TOP2, d.renorm, 0, 0, 0, d.scale};
   const bool bf = d.elem == MOK_ELEM_BF16;
   a.vec = a.E % 4 == 0 && a.ld % 4 == 0 && (reinterpret_cast<uintptr_t>(x) & (bf ? 7 : 15)) == 0;
   const int cus = device_cus() > 0 ? device_cus() : 256;
@@ -1004,6 +1020,7 @@ hipError_t launch_route_fwd(const mok_route_desc& d, const void* x, const float*
   const int lanes = a.E <= (a.K <= 8 ? 256 : 0) ? 8 : a.E <= 512 ? 16 : 32;
   // groups that are not made of whole runs of 4 experts, or more of them than lanes, go one token a wave
   const bool fast = a.G == 1 || (a.gs % 4 == 0 && a.G <= lanes);
+  if (a.gs > 1) a.group_magic = uint32_t(cdiv(int64_t(1) << 32, a.gs));
   if (a.gs >= 4) a.chunk_magic = uint32_t(cdiv(65536, a.gs / 4));
   // One workgroup writes the load by itself; several add to it, which takes a launch that clears it first
   // (3.8 us). Few enough tokens (4 steps of a workgroup, some 3 us each) are left to one.
