@@ -322,8 +322,9 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_fwd(RouteArgs a) {
 //      key of at least tau - 2 eps (of the keys above kappa + eps, kappa the exact K-th, fewer than K exist, so
 //      tau <= kappa + eps; and theirs are at least kappa - eps);
 //   4. those few candidates (nearly always exactly K) are ranked by counting. Two whose fp32 keys are
-//      further apart than 2 eps are in that order; two of the same logit and bias are tied; a token
-//      with two others, or with more than 2 KM candidates, goes to choose_wave (choose_apart).
+//      further apart than 2 eps are in that order; two of the same logit and bias are tied; else
+//      the candidates are compared by fp64 keys. A token with more than 2 KM candidates goes to choose_wave
+//      (choose_apart), and so does one of softmax scores whose fp32 keys do not decide.
 // Larger value to a, smaller to b.
 __device__ __forceinline__ void order(float& a, float& b) {
   const float hi = fmaxf(a, b), lo = fminf(a, b);
@@ -392,6 +393,14 @@ __device__ __attribute__((noinline)) void choose_apart(const RouteArgs* args, co
       if (a.load && e >= 0) atomicAdd(&load[e], 1);
     }
   }
+}
+
+// (Not inlined for the same reason.)
+__device__ __attribute__((noinline)) double sigmoid64(float x) { return 1.0 / (1.0 + exp(-double(x))); }
+
+// The fp64 number in the first two components.
+__device__ __forceinline__ double pair64(const f32x4& v) {
+  return __builtin_bit_cast(double, uint64_t(__float_as_uint(v[1])) << 32 | __float_as_uint(v[0]));
 }
 
 template <int L, int V, int KM>
@@ -673,6 +682,35 @@ __global__ __launch_bounds__(64 * kWaves, L * V >= 1024 ? 3 : 4) void k_route_fa
               unsure |= !same && !(fabsf(o[0] - me[q][0]) > 2.f * key_eps) && j + L * q < have;
           }
         }
+      }
+    }
+    if constexpr (MODE == kSigmoidBias) {
+      if (__any(unsure)) {
+        // the candidates' keys in fp64, in the place of their fp32 key and logit
+        wave_sync();
+#pragma unroll
+        for (int q = 0; q < SL; ++q) {
+          const int c = j + L * q;
+          rank[q] = 0;
+          if (q > 0 && !more) break;
+          const uint64_t k = __builtin_bit_cast(uint64_t, sigmoid64(me[q][1]) + double(me[q][2]));
+          me[q][0] = __uint_as_float(uint32_t(k));
+          me[q][1] = __uint_as_float(uint32_t(k >> 32));
+          if (c < have) s.cand[t][c] = me[q];
+        }
+        wave_sync();
+        for (int c = 0; __ballot(c < have) != 0; ++c) {
+          if (c < have) {
+            const f32x4 o = s.cand[t][c];
+#pragma unroll
+            for (int q = 0; q < SL; ++q) {
+              if (q > 0 && !more) break;
+              const double ko = pair64(o), km = pair64(me[q]);
+              rank[q] += ko > km || (ko == km && __float_as_int(o[3]) < __float_as_int(me[q][3]));
+            }
+          }
+        }
+        unsure = false;
       }
     }
     slow = slow || (kBias && (__ballot(unsure) & here) != 0);
