@@ -423,7 +423,7 @@ struct FastLds {   // of one wave
 enum ScoreMode { kLogits, kLogitsAndSum, kSigmoidBias, kSoftmaxBias, kSigmoidTop2, kSoftmaxTop2 };
 
 template <bool BF16, int L, int V, int KM, int MODE>
-__global__ __launch_bounds__(64 * kWaves, L * V >= 1024 ? 3 : 4) void k_route_fast(RouteArgs a) {
+__global__ __launch_bounds__(64 * kWaves, L * V >= 1024 || V > 32 ? 3 : 4) void k_route_fast(RouteArgs a) {
   using Lds = FastLds<L, V, KM>;
   constexpr int T = Lds::T, CAP = Lds::CAP, SL = CAP > L ? CAP / L : 1;
   constexpr bool kBias = MODE == kSigmoidBias || MODE == kSoftmaxBias;
@@ -456,7 +456,7 @@ __global__ __launch_bounds__(64 * kWaves, L * V >= 1024 ? 3 : 4) void k_route_fa
   }
   const int per = a.gs >> 2;   // chunks of 4 experts per group
   // group of each of the lane's chunks, a byte each (31: none that can stay)
-  uint32_t of_group[2] = {0, 0};
+  uint32_t of_group[(V + 15) / 16] = {};
   if (a.G > 1)
 #pragma unroll
     for (int i = 0; i < V / 4; ++i)
@@ -597,11 +597,14 @@ __global__ __launch_bounds__(64 * kWaves, L * V >= 1024 ? 3 : 4) void k_route_fa
     for (int i = 1; i < KM; ++i) tau = i < a.K ? list[i] : tau;
     const float cut = fmaxf(tau - 2.f * key_eps, -FLT_MAX);
     // a bit per expert of the lane: shifted in with the comparison's carry
-    uint32_t mine = 0;
+    constexpr int W = (V + 31) / 32;
+    uint32_t mine[W] = {};
 #pragma unroll
     for (int u = V - 1; u >= 0; --u)
-      asm("v_cmp_ge_f32 vcc, %1, %2\n\tv_addc_co_u32 %0, vcc, %0, %0, vcc" : "+v"(mine) : "v"(x[u]), "v"(cut) : "vcc");
-    int upto = __popc(mine);
+      asm("v_cmp_ge_f32 vcc, %1, %2\n\tv_addc_co_u32 %0, vcc, %0, %0, vcc" : "+v"(mine[u / 32]) : "v"(x[u]), "v"(cut) : "vcc");
+    int upto = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) upto += __popc(mine[i]);
     const int own = upto;
 #pragma unroll
     for (int off = 1; off < L; off *= 2) {
@@ -613,11 +616,13 @@ __global__ __launch_bounds__(64 * kWaves, L * V >= 1024 ? 3 : 4) void k_route_fa
     const int have = slow ? 0 : count;
     if (!slow) {
       int slot = upto - own;
-      while (mine) {
-        const int u = __builtin_ctz(mine);
-        mine &= mine - 1;
-        s.cand[t][slot++][3] = __int_as_float(4 * (j + L * (u >> 2)) + (u & 3));
-      }
+#pragma unroll
+      for (int i = 0; i < W; ++i)
+        while (mine[i]) {
+          const int u = 32 * i + __builtin_ctz(mine[i]);
+          mine[i] &= mine[i] - 1;
+          s.cand[t][slot++][3] = __int_as_float(4 * (j + L * (u >> 2)) + (u & 3));
+        }
     }
     wave_sync();
     f32x4 me[SL];
@@ -1015,10 +1020,10 @@ void route_fwd(const RouteArgs& a, bool quick, int lanes, int grid, hipStream_t 
     if (lanes == 8) {
       if (a.E <= 64) fast<BF16, 8, 8, 8>(a, grid, s);
       else if (a.E <= 128) fast<BF16, 8, 16, 8>(a, grid, s);
-      else fast<BF16, 8, 32, 8>(a, grid, s);
+      else if (a.E <= 256) fast<BF16, 8, 32, 8>(a, grid, s);
+      else fast<BF16, 8, 48, 8>(a, grid, s);
     } else if (lanes == 16) {
-      if (a.E <= 384) fast<BF16, 16, 24, 8>(a, grid, s);
-      else fast<BF16, 16, 32, 8>(a, grid, s);
+      fast<BF16, 16, 32, 8>(a, grid, s);
     } else {
       fast<BF16, 32, 32, 8>(a, grid, s);
     }
@@ -1055,7 +1060,7 @@ hipError_t launch_route_fwd(const mok_route_desc& d, const void* x, const float*
   a.vec = a.E % 4 == 0 && a.ld % 4 == 0 && (reinterpret_cast<uintptr_t>(x) & (bf ? 7 : 15)) == 0;
   const int cus = device_cus() > 0 ? device_cus() : 256;
   // lanes of a token: as many as its experts need at 32 a lane, and its choices at one a lane
-  const int lanes = a.E <= (a.K <= 8 ? 256 : 0) ? 8 : a.E <= 512 ? 16 : 32;
+  const int lanes = a.E <= (a.K <= 8 ? 384 : 0) ? 8 : a.E <= 512 ? 16 : 32;
   // groups that are not made of whole runs of 4 experts, or more of them than lanes, go one token a wave
   const bool fast = a.G == 1 || (a.gs % 4 == 0 && a.G <= lanes);
   if (a.gs > 1) a.group_magic = uint32_t(cdiv(int64_t(1) << 32, a.gs));
