@@ -1068,7 +1068,10 @@ hipError_t launch_route_fwd(const mok_route_desc& d, const void* x, const float*
   // One workgroup writes the load by itself; several add to it, which takes a launch that clears it first
   // (3.8 us). Few enough tokens (4 steps of a workgroup, some 3 us each) are left to one.
   const int per_step = fast ? kWaves * 64 / lanes : kWaves;
-  const int grid = load && a.N <= 4 * per_step ? 1 : grid_of(a.N, per_step, (fast ? 4 : 8) * cus);
+  // as many workgroups as are resident: 4 a CU, 3 of the kernels with more registers (131,072 tokens of 384
+  // experts: 60 us, with 4 a CU 65 us)
+  const int per_cu = !fast ? 8 : a.E > 512 || (lanes == 8 && a.E > 256) ? 3 : 4;
+  const int grid = load && a.N <= 4 * per_step ? 1 : grid_of(a.N, per_step, per_cu * cus);
   if (load && (grid > 1 || a.N == 0)) {
     const hipError_t e = launch_fill_u32(reinterpret_cast<uint32_t*>(load), 0u, a.E, s);
     if (e != hipSuccess) return e;
