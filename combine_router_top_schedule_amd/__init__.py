@@ -606,14 +606,21 @@ class AdamwPlan:
                 count = -(-n // 32) if name.endswith("_scale") else n
                 at = _want(ts[i], f"{name}[{i}]", types[name], count, self.dev)
                 setattr(row, name, at)
-                if name != "g" and n:
-                    spans.append((at, count * ts[i].element_size(), f"{name}[{i}]"))
+                if n:
+                    spans.append((at, at + count * ts[i].element_size(), name == "g", f"{name}[{i}]"))
             row.n = n
             rows.append(row)
+        # what is written overlaps nothing else (gradients may be given twice)
         spans.sort()
-        for (a, size, x), (b, _, y) in zip(spans, spans[1:]):
-            if a + size > b:
-                raise ValueError(f"{x} and {y} share memory")
+        read, written = (0, ""), (0, "")   # the furthest ends so far
+        for a, end, is_read, name in spans:
+            for before in (written,) if is_read else (written, read):
+                if before[0] > a:
+                    raise ValueError(f"{before[1]} and {name} share memory")
+            if is_read:
+                read = max(read, (end, name))
+            else:
+                written = max(written, (end, name))
         self.table = (MokAdamwTensor * len(p))(*rows)
         self.config = MokAdamwConfig(grad_elem=grad, param_elem=param,
                                      state=MOK_STATE_MX8 if mx else MOK_STATE_F32)

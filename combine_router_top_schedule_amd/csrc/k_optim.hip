@@ -393,7 +393,7 @@ hipError_t launch_sumsq(int count, const mok_sumsq_tensor* t, bool bf16, double*
     a.count = 0;
     int64_t chunks = 0;
     a.first[0] = 0;
-    // (chunk numbers stay within 31 bits: a tensor of at most 2^35 elements has 2^23)
+    // (chunk numbers stay within 31 bits: a tensor of at most 2^33 elements has 2^20)
     for (; t0 < count && a.count < kSqTensors; ++t0) {
       if (t[t0].n == 0) continue;
       a.g[a.count] = t[t0].g;

@@ -113,107 +113,107 @@ __global__ __launch_bounds__(256) void k_topk_scan(RouterArgs a) {
   bool raw_merge = false;   // a sole pair that the epilogue cannot weigh (its weight's sign marks raw rows)
 
   if constexpr (KM > 0) {
-  __shared__ float s_l[2][kTopkTokensPerBlock][33];
-  uint64_t key[KM];
-#pragma unroll
-  for (int j = 0; j < KM; ++j) key[j] = 0;   // below every real key
-  const bool vec4 = (a.E & 3) == 0;
-  // Thread t covers rows t/8 + 32q, experts c0 + 4*(t%8) .. +3. Every load is issued
-  // unconditionally from a clamped (in-bounds) address and masked when stored, so all eight
-  // rows' loads are in flight together.
-  float4 val[8];
-  // (the branch on vec4 stays outside the row loop: inside it, the two paths were merged into
-  // four 4-byte loads per row)
-  auto load_chunk = [&](int c0) {
-    const int col = c0 + 4 * (tid & 7);
-    if (vec4) {
-      const int cc = min(col, a.E - 4);
-#pragma unroll
+    __shared__ float s_l[2][kTopkTokensPerBlock][33];
+    uint64_t key[KM];
+  #pragma unroll
+    for (int j = 0; j < KM; ++j) key[j] = 0;   // below every real key
+    const bool vec4 = (a.E & 3) == 0;
+    // Thread t covers rows t/8 + 32q, experts c0 + 4*(t%8) .. +3. Every load is issued
+    // unconditionally from a clamped (in-bounds) address and masked when stored, so all eight
+    // rows' loads are in flight together.
+    float4 val[8];
+    // (the branch on vec4 stays outside the row loop: inside it, the two paths were merged into
+    // four 4-byte loads per row)
+    auto load_chunk = [&](int c0) {
+      const int col = c0 + 4 * (tid & 7);
+      if (vec4) {
+        const int cc = min(col, a.E - 4);
+  #pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const int64_t n = min(n_base + (tid >> 3) + 32 * q, a.N - 1);
+          val[q] = *reinterpret_cast<const float4*>(a.logits + n * a.E + cc);
+        }
+      } else {
+  #pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const int64_t n = min(n_base + (tid >> 3) + 32 * q, a.N - 1);
+          val[q].x = a.logits[n * a.E + min(col, a.E - 1)];
+          val[q].y = a.logits[n * a.E + min(col + 1, a.E - 1)];
+          val[q].z = a.logits[n * a.E + min(col + 2, a.E - 1)];
+          val[q].w = a.logits[n * a.E + min(col + 3, a.E - 1)];
+        }
+      }
+    };
+    load_chunk(0);
+    for (int c0 = 0, buf = 0; c0 < a.E; c0 += 32, buf ^= 1) {
+      const int col = c0 + 4 * (tid & 7);
+  #pragma unroll
       for (int q = 0; q < 8; ++q) {
-        const int64_t n = min(n_base + (tid >> 3) + 32 * q, a.N - 1);
-        val[q] = *reinterpret_cast<const float4*>(a.logits + n * a.E + cc);
+        const int r = (tid >> 3) + 32 * q;
+        const bool rok = n_base + r < a.N;
+        s_l[buf][r][4 * (tid & 7) + 0] = (rok && col + 0 < a.E) ? val[q].x : -INFINITY;
+        s_l[buf][r][4 * (tid & 7) + 1] = (rok && col + 1 < a.E) ? val[q].y : -INFINITY;
+        s_l[buf][r][4 * (tid & 7) + 2] = (rok && col + 2 < a.E) ? val[q].z : -INFINITY;
+        s_l[buf][r][4 * (tid & 7) + 3] = (rok && col + 3 < a.E) ? val[q].w : -INFINITY;
       }
-    } else {
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const int64_t n = min(n_base + (tid >> 3) + 32 * q, a.N - 1);
-        val[q].x = a.logits[n * a.E + min(col, a.E - 1)];
-        val[q].y = a.logits[n * a.E + min(col + 1, a.E - 1)];
-        val[q].z = a.logits[n * a.E + min(col + 2, a.E - 1)];
-        val[q].w = a.logits[n * a.E + min(col + 3, a.E - 1)];
+      // One barrier per chunk suffices with two buffers: a thread writing buffer `buf` again
+      // (two chunks later) has passed the barrier after which every thread finished ranking it.
+      __syncthreads();
+      if (c0 + 32 < a.E) load_chunk(c0 + 32);
+      const int ce = min(32, a.E - c0);
+      // The token's 32 logits of the chunk, read together (one LDS round trip, not one per
+      // candidate).
+      float lv[32];
+  #pragma unroll
+      for (int u = 0; u < 32; ++u) lv[u] = s_l[buf][tid][u];
+      // The first chunk starts the list as its first KM candidates, sorted by a compare-exchange
+      // network instead of KM insertions.
+      int u0 = 0;
+      if (c0 == 0 && ce >= KM) {
+  #pragma unroll
+        for (int j = 0; j < KM; ++j) key[j] = rank_key(lv[j], j);
+        sort_desc<KM>(key);
+        u0 = KM;
       }
-    }
-  };
-  load_chunk(0);
-  for (int c0 = 0, buf = 0; c0 < a.E; c0 += 32, buf ^= 1) {
-    const int col = c0 + 4 * (tid & 7);
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const int r = (tid >> 3) + 32 * q;
-      const bool rok = n_base + r < a.N;
-      s_l[buf][r][4 * (tid & 7) + 0] = (rok && col + 0 < a.E) ? val[q].x : -INFINITY;
-      s_l[buf][r][4 * (tid & 7) + 1] = (rok && col + 1 < a.E) ? val[q].y : -INFINITY;
-      s_l[buf][r][4 * (tid & 7) + 2] = (rok && col + 2 < a.E) ? val[q].z : -INFINITY;
-      s_l[buf][r][4 * (tid & 7) + 3] = (rok && col + 3 < a.E) ? val[q].w : -INFINITY;
-    }
-    // One barrier per chunk suffices with two buffers: a thread writing buffer `buf` again
-    // (two chunks later) has passed the barrier after which every thread finished ranking it.
-    __syncthreads();
-    if (c0 + 32 < a.E) load_chunk(c0 + 32);
-    const int ce = min(32, a.E - c0);
-    // The token's 32 logits of the chunk, read together (one LDS round trip, not one per
-    // candidate).
-    float lv[32];
-#pragma unroll
-    for (int u = 0; u < 32; ++u) lv[u] = s_l[buf][tid][u];
-    // The first chunk starts the list as its first KM candidates, sorted by a compare-exchange
-    // network instead of KM insertions.
-    int u0 = 0;
-    if (c0 == 0 && ce >= KM) {
-#pragma unroll
-      for (int j = 0; j < KM; ++j) key[j] = rank_key(lv[j], j);
-      sort_desc<KM>(key);
-      u0 = KM;
-    }
-    // Only a candidate above the list's smallest key can enter it: one 64-bit compare per
-    // candidate builds the chunk's mask, and only those are inserted, in expert order (one the
-    // list has outgrown meanwhile passes through unchanged). A wave iterates as often as its
-    // busiest lane (a few times per chunk once the list has filled, against 32 insertions).
-    // The keys are unique, so the list is the one inserting every candidate gives.
-    const uint64_t kth = key[KM - 1];
-    uint32_t m = 0;
-#pragma unroll
-    for (int u = 0; u < 32; ++u) m |= uint32_t(rank_key(lv[u], c0 + u) > kth) << u;
-    m &= (ce >= 32 ? 0xFFFFFFFFu : (1u << ce) - 1u) & (0xFFFFFFFFu << u0);
-    while (m) {
-      const int u = __builtin_ctz(m);
-      m &= m - 1;
-      topk_insert<KM>(key, rank_key(s_l[buf][tid][u], c0 + u));
-    }
-  }
-  float v[KM];
-  int id[KM];
-#pragma unroll
-  for (int j = 0; j < KM; ++j) {
-    v[j] = key_value(key[j]);
-    id[j] = key_expert(key[j]);
-  }
-  if (n_me < a.N) {
-    // p_k = exp(l_k - l_0) / sum_j exp(l_j - l_0), fp32, k ascending
-    float sum = 0.f;
-#pragma unroll
-    for (int k = 0; k < KM; ++k)
-      if (k < a.K) sum += expf(v[k] - v[0]);
-#pragma unroll
-    for (int k = 0; k < KM; ++k) {
-      if (k < a.K) {
-        a.idx[n_me * a.K + k] = id[k];
-        a.p[n_me * a.K + k] = expf(v[k] - v[0]) / sum;
-        const int le = id[k] - a.e0;
-        if (le >= 0 && le < a.El) mask |= 1ull << le;
+      // Only a candidate above the list's smallest key can enter it: one 64-bit compare per
+      // candidate builds the chunk's mask, and only those are inserted, in expert order (one the
+      // list has outgrown meanwhile passes through unchanged). A wave iterates as often as its
+      // busiest lane (a few times per chunk once the list has filled, against 32 insertions).
+      // The keys are unique, so the list is the one inserting every candidate gives.
+      const uint64_t kth = key[KM - 1];
+      uint32_t m = 0;
+  #pragma unroll
+      for (int u = 0; u < 32; ++u) m |= uint32_t(rank_key(lv[u], c0 + u) > kth) << u;
+      m &= (ce >= 32 ? 0xFFFFFFFFu : (1u << ce) - 1u) & (0xFFFFFFFFu << u0);
+      while (m) {
+        const int u = __builtin_ctz(m);
+        m &= m - 1;
+        topk_insert<KM>(key, rank_key(s_l[buf][tid][u], c0 + u));
       }
     }
-  }
+    float v[KM];
+    int id[KM];
+  #pragma unroll
+    for (int j = 0; j < KM; ++j) {
+      v[j] = key_value(key[j]);
+      id[j] = key_expert(key[j]);
+    }
+    if (n_me < a.N) {
+      // p_k = exp(l_k - l_0) / sum_j exp(l_j - l_0), fp32, k ascending
+      float sum = 0.f;
+  #pragma unroll
+      for (int k = 0; k < KM; ++k)
+        if (k < a.K) sum += expf(v[k] - v[0]);
+  #pragma unroll
+      for (int k = 0; k < KM; ++k) {
+        if (k < a.K) {
+          a.idx[n_me * a.K + k] = id[k];
+          a.p[n_me * a.K + k] = expf(v[k] - v[0]) / sum;
+          const int le = id[k] - a.e0;
+          if (le >= 0 && le < a.El) mask |= 1ull << le;
+        }
+      }
+    }
   } else if (n_me < a.N) {
     int id[kMaxTopK];
 #pragma unroll

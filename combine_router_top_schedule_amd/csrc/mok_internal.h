@@ -458,7 +458,7 @@ hipError_t launch_route_fwd(const mok_route_desc& d, const void* x, const float*
                             const uint8_t* mask, int32_t* idx, float* w, int32_t* load, hipStream_t s);
 hipError_t launch_route_bwd(const mok_route_desc& d, const void* x, const int32_t* idx, const float* dw,
                             void* dx, hipStream_t s);
-constexpr int64_t kMaxOptElements = int64_t(1) << 35;   // of one tensor
+constexpr int64_t kMaxOptElements = int64_t(1) << 33;   // of one tensor: 2^23 workgroups of mok_adamw
 int64_t sumsq_ws_bytes(int count);
 hipError_t launch_sumsq(int count, const mok_sumsq_tensor* t, bool bf16, double* out, uint8_t* ws,
                         hipStream_t s);

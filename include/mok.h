@@ -460,7 +460,7 @@ typedef enum { MOK_GROUP_MAX = 0, MOK_GROUP_TOP2 = 1 } mok_group_score;
 
 typedef struct {
   int64_t num_tokens;      /* N; 0..2^31 - 1                                                  */
-  int64_t logits_stride;   /* elements from one token's logits to the next's, >= E             */
+  int64_t logits_stride;   /* elements from one token's logits to the next's; E..2^31          */
   int32_t num_experts;     /* E; 1..1024                                                       */
   int32_t top_k;           /* K; 1..min(16, top_groups * E / num_groups)                       */
   int32_t score;           /* mok_score                                                        */
@@ -490,7 +490,7 @@ mok_status mok_route_fwd(const mok_route_desc* desc, const void* logits_dev, con
  *                names no expert, or one that an earlier slot of the token names) it is not used
  *   dlogits_dev  [N][E] out, contiguous, of the logits' type, 16-byte aligned: zero wherever no
  *                gradient flows; rows without a chosen expert are zero whatever their logits hold
- * The other arguments are those of the forward. */
+ * The other arguments are those of the forward; no output of either call overlaps an input. */
 mok_status mok_route_bwd(const mok_route_desc* desc, const void* logits_dev,
                          const int32_t* topk_idx_dev, const float* dw_dev, void* dlogits_dev,
                          void* stream);
@@ -498,7 +498,8 @@ mok_status mok_route_bwd(const mok_route_desc* desc, const void* logits_dev,
 /* ---- the optimizer step -------------------------------------------------------------------------
  * Tensors are described by HOST arrays, which are read before the call returns and travel as kernel
  * arguments: no device table, no copy, and the calls can be captured into a HIP graph. Tensors are
- * contiguous, 16-byte aligned (bf16 ones too) and do not overlap; a length may be 0. */
+ * contiguous, 16-byte aligned (bf16 ones too), of 0..2^33 elements, and what is written overlaps nothing
+ * else. */
 typedef struct {
   const void* g;
   int64_t n;

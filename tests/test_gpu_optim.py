@@ -298,8 +298,11 @@ def test_bindings_refuse():
         with pytest.raises(ValueError):
             mok.adamw_plan(**{**ok, **bad})
     both = z(100)
-    with pytest.raises(ValueError):
-        mok.adamw_plan(p=[both[:64]], g=[g], m=[both[32:96]], v=[v])
+    for bad in (dict(p=[both[:64]], m=[both[32:96]]), dict(p=[both[:64]], g=[both[32:96]]),
+                dict(g=[both[:64]], v=[both[32:96]])):
+        with pytest.raises(ValueError):
+            mok.adamw_plan(**{**ok, **bad})
+    mok.adamw_plan(p=[p, z(64)], g=[g, g], m=[m, z(64)], v=[v, z(64)])   # (a gradient may be given twice)
     with pytest.raises(ValueError):
         mok.adamw_plan(p=[p, p], g=[g, g], m=[m, z(64)], v=[v, z(64)])
     plan = mok.adamw_plan(**ok)
@@ -320,3 +323,37 @@ def test_bindings_refuse():
     for bad in (dict(out=z(1)), dict(out=z(2, torch.float64)), dict(ws=u8(8))):
         with pytest.raises(ValueError):
             mok.mok_grad_sumsq(sp, **{**dict(out=sq), **bad})
+
+
+def test_lengths_beyond_32_bits():
+    """A tensor of more than 2^32 elements: bf16 parameters and gradients, 8-bit moments (26 GB). Checked
+    around the 2^31 and 2^32 borders and at the end."""
+    n = 2 ** 32 + 1001
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    z = lambda k, dt: torch.zeros(k, dtype=dt, device="cuda")
+    p, g = z(n, torch.bfloat16), z(n, torch.bfloat16)
+    m, v, ms, vs = z(n, torch.uint8), z(n, torch.uint8), z(-(-n // 32), torch.uint8), z(-(-n // 32), torch.uint8)
+    at = [0, 2 ** 31 - 64, 2 ** 32 - 64, n - 105]          # (each on a run's first element, n - 105 = 2^32 + 896)
+    rng = np.random.default_rng(1)
+    windows = []
+    for a in at:
+        k = min(128, n - a)
+        for t, std in ((p, 0.02), (g, 1e-3)):
+            t[a:a + k] = torch.from_numpy((rng.standard_normal(k) * std).astype(np.float32)).cuda().bfloat16()
+        windows.append((a, k, p[a:a + k].float().cpu().numpy(), g[a:a + k].float().cpu().numpy()))
+    out = z(1, torch.float64)
+    mok.mok_grad_sumsq(mok.sumsq_plan([g]), out)
+    sumsq = math.fsum(float((w[3].astype(np.float64) ** 2).sum()) for w in windows)
+    assert abs(out.item() - sumsq) <= 1e-13 * sumsq
+    mok.mok_adamw(mok.adamw_plan(p=[p], g=[g], m=[m], v=[v], m_scale=[ms], v_scale=[vs]), step=1, seed=4, **HYPER)
+    torch.cuda.synchronize()
+    for a, k, p0, g0 in windows:
+        zero = np.zeros(k, np.float32)
+        ep, em, _, er = oo.step32(p0, g0, zero, zero, HYPER["lr"], 0.9, 0.999, 1e-8, 0.1, 1)
+        b = oo.bits(4, 0, k, first=a)
+        assert np.array_equal(host(p[a:a + k]), oo.bf16_random(ep, oo.mix(b ^ 0x3C6EF372) & 0xFFFF)), a
+        for code, scale, x, u, pos in ((m, ms, em, b & 0xFFFF, False), (v, vs, er, b >> 16, True)):
+            c, s = oo.encode(x, u, pos)
+            assert np.array_equal(host(code[a:a + k]), c), a
+            assert np.array_equal(host(scale[a // 32:a // 32 + len(s)]), s), a

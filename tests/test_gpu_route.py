@@ -328,6 +328,21 @@ def test_route_on_a_stream_and_in_a_graph():
         assert all(torch.equal(a, b) for a, b in zip(got, (r.idx, r.w, r.load, r.dx)))
 
 
+@pytest.mark.parametrize("name", ["dsv3", "odd", "odd_groups"])
+def test_route_rows_beyond_32_bits(name):
+    """Rows so far apart that an element's number passes 2^32 (8.6 GB of bf16)."""
+    if torch.cuda.mem_get_info()[0] < 16 << 30:
+        pytest.skip("needs 16 GB")
+    gate, far = GATES[name], 2 ** 31
+    r = Run(gate, np.random.default_rng(12).standard_normal((3, gate.E)), None, None, "bfloat16")
+    x = torch.empty(2 * far + gate.E, dtype=torch.bfloat16, device="cuda").as_strided((3, gate.E), (far, 1))
+    x.copy_(r.x)
+    r.x = x
+    r.forward()
+    idx, _ = r.check_forward()
+    r.check_backward(idx)
+
+
 def test_route_binding_refusals():
     gate = GATES["dsv3"]
     x = torch.zeros(4, 256, device="cuda")

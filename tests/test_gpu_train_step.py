@@ -151,6 +151,39 @@ def test_given_choice_and_dlogits_is_reported():
     assert max_rel_err(case.dlogits.cpu().numpy().astype(np.float64), bw.dlogits) <= BF16_TOL
 
 
+def test_gate_and_layer_in_a_graph():
+    """Gate, layer forward and backward, gate backward, captured and replayed on changing logits, with the
+    calls made one by one in between."""
+    cfg = CFGS["wide"]
+    gate = mok.route_desc(cfg.E, cfg.K, "sigmoid", 4, 2, "top2", True, 2.5)
+    case = BwdCase(cfg, staged=False, fused=True)
+    L, dl = case.layer, torch.empty(cfg.N, cfg.E, device="cuda")
+    load = torch.empty(cfg.E, dtype=torch.int32, device="cuda")
+
+    def one():
+        L.route(gate, case.logits, None, None, load)
+        L.forward_routed(case.x_seg, case.out_seg)
+        mok.mok_layer_bwd(case.d, case.dout_seg, case.x_seg, L.w, L.idx, L.p, L.saved, L.ring, L.slots,
+                          case.dx_seg, case.dp, None, case.dwg, case.dwu, case.dwd, case.bws)
+        L.route_backward(gate, case.logits, case.dp, dl)
+
+    one()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        one()
+    outs = lambda: [t.clone() for t in (L.idx, L.p, load, case.out, case.dx, case.dp, dl, case.dwg, case.dwd)]
+    for k in range(4):
+        case.logits.copy_(torch.randn(cfg.N, cfg.E, generator=torch.Generator().manual_seed(k)))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = outs()
+        one()
+        torch.cuda.synchronize()
+        assert mok.mok_device_status(L.ws) == 0 and mok.mok_device_status(case.bws) == 0
+        assert all(torch.equal(a, b) for a, b in zip(got, outs()))
+
+
 def test_given_choice_host_refusals():
     lib, d = mok.lib(), mok.desc_from_config(TINY)
     w = mok.MokWeights()
