@@ -110,7 +110,7 @@ __global__ __launch_bounds__(256) void k_topk_scan(RouterArgs a) {
   const int64_t n_base = int64_t(b) * kTopkTokensPerBlock;
   const int64_t n_me = n_base + tid;
   uint64_t mask = 0;
-  bool raw_merge = false;   // a sole pair that the epilogue cannot weigh (its weight's sign marks raw rows)
+  bool raw_merge = false;   // a sole pair that the epilogue cannot weigh (negative or NaN: that marks raw rows)
 
   if constexpr (KM > 0) {
     __shared__ float s_l[2][kTopkTokensPerBlock][33];
@@ -227,7 +227,7 @@ __global__ __launch_bounds__(256) void k_topk_scan(RouterArgs a) {
           const int le = id[k] - a.e0;
           if (le >= 0 && le < a.El) {
             mask |= 1ull << le;
-            raw_merge = raw_merge || a.p[n_me * a.K + k] < 0.f;
+            raw_merge = raw_merge || !(a.p[n_me * a.K + k] >= 0.f);
           }
         } else {
           a.idx[n_me * a.K + k] = -1;

@@ -110,6 +110,35 @@ def test_layer_with_a_given_choice(name, fused, kind):
         assert err(got.cpu().numpy().astype(np.float64), ref) <= tol
 
 
+@pytest.mark.parametrize("fused", [False, True])
+def test_sole_pairs_of_weight_nan_and_minus_zero(fused):
+    """Tokens with one expert, whose weight the rows' epilogue cannot take as it is."""
+    cfg = CFGS["wide"]
+    idx, p, _, _ = choice(cfg, "plain")
+    idx[3, 1:] = idx[5, 1:] = -1
+    outs = []
+    for w3, w5 in ((1.0, 1.0), (np.nan, -0.0)):
+        p[3, 0], p[5, 0] = w3, w5
+        case = BwdCase(cfg, staged=not fused, fused=fused)
+        L = case.layer
+        L.idx.copy_(torch.from_numpy(idx).flatten())
+        L.p.copy_(torch.from_numpy(p).flatten())
+        if fused:
+            L.forward_routed(case.x_seg, case.out_seg)
+        else:
+            L.schedule_routed()
+            L.dispatch(case.x_seg)
+            L.expert_ffn()
+            L.combine(case.out_seg)
+        torch.cuda.synchronize()
+        assert mok.mok_device_status(L.ws) == 0
+        outs.append(mo.decode_bf16(host_u16(case.out)))
+    assert np.isfinite(outs[0]).all() and outs[0][3].any() and outs[0][5].any()
+    assert np.isnan(outs[1][3]).all() and not outs[1][5].any()
+    rest = np.setdiff1d(np.arange(cfg.N), [3, 5])
+    assert np.array_equal(outs[0][rest], outs[1][rest])
+
+
 def test_given_choice_equals_the_layers_own():
     """With the layer's own choice and weights given, every output is the same bit for bit."""
     cfg = CFGS["wide"]
