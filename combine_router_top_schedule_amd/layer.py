@@ -104,7 +104,9 @@ class MokLayer:
                       token_mask=token_mask, load=load)
 
     def route_backward(self, gate, logits, dp, dlogits):
-        """dlogits from the backward's dp, for the choice that route made."""
+        """dlogits from the backward's dp, for the choice that route made. Where this layer holds a
+        share of the experts, its backward writes dp at its own pairs only: put the shares' dp
+        together first."""
         K = self.d.top_k
         mok_route_bwd(gate, logits, self.idx.view(-1, K), dp.view(-1, K), dlogits)
 

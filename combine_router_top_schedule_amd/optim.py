@@ -41,7 +41,11 @@ class MokAdamW:
             self.sumsq = torch.zeros(1, dtype=torch.float64, device=self.params[0].device)
 
     def step(self, lr: Optional[float] = None):
-        """One step; `lr` replaces the rate given at the start, for this step."""
+        """One step; `lr` replaces the rate given at the start, for this step. Rate and step count are
+        the host's, which a graph would keep: to capture a step call mok_adamw on this object's
+        plan with both on the device."""
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("a captured step takes its number from the device: see mok_adamw")
         self.steps += 1
         if self.sumsq is not None:
             mok_grad_sumsq(self.sumsq_plan, self.sumsq)

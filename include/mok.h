@@ -536,14 +536,15 @@ typedef struct {
   double max_norm;          /* with sumsq_dev: gradients are scaled by min(1, max_norm / norm); > 0,
                                may be infinite (no clipping, only the check for finite values)   */
   int64_t step;             /* 1, 2, ...: the bias correction's exponent                         */
-  uint32_t seed;            /* of the stochastic roundings: another one for each step            */
+  uint32_t seed;            /* of the stochastic roundings: another one for each step. With step_dev the
+                               device adds the step to it, so a captured step may keep it        */
   int32_t grad_elem;        /* mok_elem                                                          */
   int32_t param_elem;       /* mok_elem; bf16 parameters are rounded stochastically               */
   int32_t state;            /* mok_opt_state                                                     */
   const double* sumsq_dev;  /* squared norm of all gradients, or NULL (no clipping). When it is not
                                finite the call changes nothing                                   */
   const double* lr_dev;     /* NULL, or where the device finds lr (a captured step whose rate changes) */
-  const int64_t* step_dev;  /* NULL, or where the device finds step                              */
+  const int64_t* step_dev;  /* NULL, or where the device finds step (and adds it to the seed)     */
 } mok_adamw_config;
 
 /* One AdamW step over all tensors, in few launches (48 tensors each):

@@ -214,6 +214,19 @@ def test_adamw_rates_and_steps_on_the_device():
             assert torch.equal(x, y)
 
 
+def test_adamw_step_on_the_device_joins_the_seed():
+    """Replays of one captured call round by other random bits: those of seed + step."""
+    a, b, c = (Step([5000], mx=True) for _ in range(3))
+    t = torch.tensor([7], dtype=torch.int64, device="cuda")
+    mok.mok_adamw(a.plan, step=t, seed=3, **HYPER)
+    mok.mok_adamw(b.plan, step=7, seed=10, **HYPER)
+    t.fill_(8)
+    mok.mok_adamw(c.plan, step=t, seed=3, **HYPER)
+    for k in ("m", "v", "m_scale", "v_scale"):   # (which depend on the step by their random bits alone)
+        assert torch.equal(a.t[k][0], b.t[k][0]), k
+    assert not torch.equal(a.t["m"][0], c.t["m"][0]) and not torch.equal(a.t["v"][0], c.t["v"][0])
+
+
 @pytest.mark.parametrize("mx", [False, True])
 def test_adamw_captured(mx):
     """Norm and step in a graph, with the rate and the step count on the device, replayed; against the
