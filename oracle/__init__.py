@@ -23,6 +23,10 @@ Modules:
   gradient taken inside SwiGLU backward.
 * ``mx``          the MXFP8 (E4M3 + UE8M0, 32-element blocks) quantiser, from the OCP
   Microscaling Formats v1.0 definition.
+* ``route``       the gate with scores, balancing bias, groups and renormalised weights, and its
+  gradient, in fp64.
+* ``optim``       the norm of all gradients and AdamW in fp64, and bit for bit the fp32 and 8-bit
+  arithmetic that ``include/mok.h`` states.
 * ``brute``       pure-Python loops over the same definitions, for tiny shapes only; it
   pins ``moe_oracle``.
 """

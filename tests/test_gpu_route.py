@@ -194,8 +194,7 @@ def test_route_choices_closer_than_fp32(name):
 
 @pytest.mark.parametrize("bias", [False, True])
 def test_route_many_rows_of_equal_logits(bias):
-    """More tokens without a decision in fp32 than a wave keeps a list of (a few dozen of its 48), and
-    others between them."""
+    """Many tokens that fp32 cannot decide (all their logits alike), and others between them."""
     gate, n = G(64, 8, "sigmoid", 8, 4, "top2", True, 2.5), 200001
     x = torch.zeros(n, 64, device="cuda")
     some = torch.arange(0, n, 17, device="cuda")
