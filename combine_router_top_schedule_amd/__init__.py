@@ -551,8 +551,7 @@ class SumsqPlan:
             raise ValueError("no tensors")
         self.keep, self.dev, self.elem = list(grads), _device_of(grads[0]), _elem(grads[0], "a gradient")
         self.table = (MokSumsqTensor * len(grads))(*[
-            MokSumsqTensor(_want(g, f"gradient {i}", grads[0].dtype, g.numel(), self.dev), g.numel())
-            for i, g in enumerate(grads)])
+            (_want(g, "a gradient", grads[0].dtype, g.numel(), self.dev), g.numel()) for g in grads])
         n = ctypes.c_size_t()
         _check("mok_sumsq_ws_size", lib().mok_sumsq_ws_size(len(grads), ctypes.byref(n)))
         self.ws = _tch().zeros(int(n.value), dtype=_torch.uint8, device=grads[0].device)
@@ -599,29 +598,29 @@ class AdamwPlan:
             raise ValueError("only float32 parameters have a bfloat16 copy")
         types = dict(p=p[0].dtype, g=g[0].dtype, copy=torch.bfloat16, m=torch.uint8 if mx else torch.float32,
                      v=torch.uint8 if mx else torch.float32, m_scale=torch.uint8, v_scale=torch.uint8)
-        rows, spans = [], []
-        for i in range(len(p)):
-            n, row = p[i].numel(), MokAdamwTensor()
-            for name, ts in self.keep.items():
-                count = -(-n // 32) if name.endswith("_scale") else n
-                at = _want(ts[i], f"{name}[{i}]", types[name], count, self.dev)
-                setattr(row, name, at)
-                if n:
-                    spans.append((at, at + count * ts[i].element_size(), name == "g", f"{name}[{i}]"))
-            row.n = n
-            rows.append(row)
+        sizes = [t.numel() for t in p]
+        runs = [-(-n // 32) for n in sizes]
+        columns, spans = {}, []
+        for name, ts in self.keep.items():
+            counts, dtype, read = runs if name.endswith("_scale") else sizes, types[name], name == "g"
+            columns[name] = at = [
+                t.data_ptr() if t.dtype is dtype and t.numel() == n and t.get_device() == self.dev
+                and t.is_contiguous() else _want(t, name, dtype, n, self.dev) for t, n in zip(ts, counts)]
+            size = ts[0].element_size()
+            spans += [(a, a + n * size, read, name) for a, n in zip(at, counts) if n]
         # what is written overlaps nothing else (gradients may be given twice)
         spans.sort()
-        read, written = (0, ""), (0, "")   # the furthest ends so far
-        for a, end, is_read, name in spans:
-            for before in (written,) if is_read else (written, read):
-                if before[0] > a:
-                    raise ValueError(f"{before[1]} and {name} share memory")
-            if is_read:
-                read = max(read, (end, name))
+        read_end = written_end = 0   # the furthest ends so far
+        for a, end, read, name in spans:
+            if a < written_end or a < read_end and not read:
+                raise ValueError(f"memory of {name} is shared with another tensor")
+            if read:
+                read_end = max(read_end, end)
             else:
-                written = max(written, (end, name))
-        self.table = (MokAdamwTensor * len(p))(*rows)
+                written_end = max(written_end, end)
+        none = [None] * len(p)
+        self.table = (MokAdamwTensor * len(p))(*zip(*[
+            columns.get(name, none) for name in ("p", "copy", "g", "m", "v", "m_scale", "v_scale")], sizes))
         self.config = MokAdamwConfig(grad_elem=grad, param_elem=param,
                                      state=MOK_STATE_MX8 if mx else MOK_STATE_F32)
 
@@ -634,9 +633,9 @@ def mok_adamw(plan: AdamwPlan, lr, step, beta1: float = 0.9, beta2: float = 0.99
               weight_decay: float = 0.0, seed: int = 0, sumsq=None, max_norm: Optional[float] = None,
               stream=None):
     """One AdamW step over the plan's tensors, in place. `lr` and `step` may be device tensors (float64
-    [1], int64 [1]), read when the step runs (a step's number is then added to `seed`). With `sumsq` (float64 [1], the squared norm of all
-    gradients) gradients are clipped to `max_norm` (None: not clipped) and a step whose norm is not
-    finite changes nothing."""
+    [1], int64 [1]), read when the step runs (a step's number is then added to `seed`). With `sumsq`
+    (float64 [1], the squared norm of all gradients) gradients are clipped to `max_norm` (None: not
+    clipped) and a step whose norm is not finite changes nothing."""
     torch = _tch()
     c = MokAdamwConfig.from_buffer_copy(plan.config)
     if isinstance(lr, torch.Tensor):
