@@ -63,28 +63,24 @@ __device__ __forceinline__ double block_sum(double v) {
   return sum;
 }
 
-// Four consecutive elements from i on, those past n as zero.
-template <bool BF16>
-__device__ __forceinline__ void load_sq(const void* g, int64_t i, int64_t n, float (&v)[4]) {
-  if (i + 4 <= n) {
-    if constexpr (BF16) {
-      const uint64_t b = __builtin_nontemporal_load(
-          reinterpret_cast<const uint64_t*>(static_cast<const uint16_t*>(g) + i));
-      for (int j = 0; j < 4; ++j) v[j] = bf2f(uint16_t(b >> (16 * j)));
-    } else {
-      const f32x4 b = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(static_cast<const float*>(g) + i));
-      for (int j = 0; j < 4; ++j) v[j] = b[j];
-    }
-  } else {
-    for (int j = 0; j < 4; ++j) {
-      v[j] = 0.f;
-      if (i + j < n) {
-        if constexpr (BF16) v[j] = bf2f(static_cast<const uint16_t*>(g)[i + j]);
-        else v[j] = static_cast<const float*>(g)[i + j];
-      }
-    }
-  }
+// Four consecutive elements from i on, as they lie in memory, those past n as zero. (Converted behind all loads:
+// in the branches each load would be waited for before the next.)
+__device__ __forceinline__ f32x4 load_sq(const float* g, int64_t i, int64_t n) {
+  if (i + 4 <= n) return __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(g + i));
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  for (int j = 0; j < 4; ++j)
+    if (i + j < n) v[j] = g[i + j];
+  return v;
 }
+__device__ __forceinline__ uint64_t load_sq(const uint16_t* g, int64_t i, int64_t n) {
+  if (i + 4 <= n) return __builtin_nontemporal_load(reinterpret_cast<const uint64_t*>(g + i));
+  uint64_t v = 0;
+  for (int j = 0; j < 4; ++j)
+    if (i + j < n) v |= uint64_t(g[i + j]) << (16 * j);
+  return v;
+}
+__device__ __forceinline__ float element(const f32x4& v, int j) { return v[j]; }
+__device__ __forceinline__ float element(uint64_t v, int j) { return bf2f(uint16_t(v >> (16 * j))); }
 
 template <bool BF16>
 __global__ __launch_bounds__(kSqThreads) void k_sumsq(SqArgs a) {
@@ -93,12 +89,16 @@ __global__ __launch_bounds__(kSqThreads) void k_sumsq(SqArgs a) {
     const int t = __builtin_amdgcn_readfirstlane(find_tensor(a.first, a.count, c));
     const int64_t i0 = int64_t(c - a.first[t]) * kSqChunk + threadIdx.x * 4, n = a.n[t];
     constexpr int U = kSqChunk / (4 * kSqThreads);
-    float v[U][4];
+    using Elem = std::conditional_t<BF16, uint16_t, float>;
+    std::conditional_t<BF16, uint64_t, f32x4> v[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) load_sq<BF16>(a.g[t], i0 + u * 4 * kSqThreads, n, v[u]);
+    for (int u = 0; u < U; ++u) v[u] = load_sq(static_cast<const Elem*>(a.g[t]), i0 + u * 4 * kSqThreads, n);
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      for (int j = 0; j < 4; ++j) sum = fma(double(v[u][j]), double(v[u][j]), sum);
+      for (int j = 0; j < 4; ++j) {
+        const double x = element(v[u], j);
+        sum = fma(x, x, sum);
+      }
   }
   sum = block_sum(sum);
   // The sums of all workgroups are joined, in the order of their numbers, by the one that comes last; a
@@ -215,39 +215,52 @@ __device__ __forceinline__ void decode4(uint32_t code, uint32_t scale, float (&x
   x[3] = __builtin_amdgcn_cvt_f32_fp8(int(code), 3) * s;
 }
 
-// Four consecutive elements from i on; without FULL, those past n read as zero and are not written. Every
-// byte is used once, so whole accesses pass the caches by (927 us instead of 985 us for 178 M elements with
-// fp32 states, 777 us instead of 868 us for 267 M with 8-bit ones).
+// Four consecutive elements from i on; without FULL (a chunk that ends inside, n > 0), those past n read as
+// zero and are not written, and the others are loaded one by one from clamped addresses: with branches around
+// whole and single loads each load would be waited for before the next. Every byte is used once, so whole
+// accesses pass the caches by (927 us instead of 985 us for 178 M elements with fp32 states, 777 us instead of
+// 868 us for 267 M with 8-bit ones).
 template <bool FULL>
 __device__ __forceinline__ void load4(const float* p, int64_t i, int64_t n, float (&x)[4]) {
-  if (FULL || i + 4 <= n) {
+  if constexpr (FULL) {
     const f32x4 v = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p + i));
 #pragma unroll
     for (int j = 0; j < 4; ++j) x[j] = v[j];
   } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = i + j < n ? p[i + j] : 0.f;
+    for (int j = 0; j < 4; ++j) {
+      const float v = p[min(i + j, n - 1)];
+      x[j] = i + j < n ? v : 0.f;
+    }
   }
 }
 template <bool FULL>
 __device__ __forceinline__ void load4(const uint16_t* p, int64_t i, int64_t n, float (&x)[4]) {
-  if (FULL || i + 4 <= n) {
+  if constexpr (FULL) {
     const uint64_t v = __builtin_nontemporal_load(reinterpret_cast<const uint64_t*>(p + i));
 #pragma unroll
     for (int j = 0; j < 4; ++j) x[j] = bf2f(uint16_t(v >> (16 * j)));
   } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = i + j < n ? bf2f(p[i + j]) : 0.f;
+    for (int j = 0; j < 4; ++j) {
+      const float v = bf2f(p[min(i + j, n - 1)]);
+      x[j] = i + j < n ? v : 0.f;
+    }
   }
 }
 template <bool FULL>
 __device__ __forceinline__ uint32_t load4(const uint8_t* p, int64_t i, int64_t n) {
-  if (FULL || i + 4 <= n) return __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p + i));
-  uint32_t x = 0;
+  if constexpr (FULL) {
+    return __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p + i));
+  } else {
+    uint32_t x = 0;
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (i + j < n) x |= uint32_t(p[i + j]) << (8 * j);
-  return x;
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t v = p[min(i + j, n - 1)];
+      x |= (i + j < n ? v : 0u) << (8 * j);
+    }
+    return x;
+  }
 }
 template <bool FULL>
 __device__ __forceinline__ void store4(float* p, int64_t i, int64_t n, const float (&x)[4]) {
@@ -297,7 +310,8 @@ __device__ __forceinline__ void adamw4(const AdamArgs& a, int t, int64_t i, int6
   if constexpr (MX8) {
     const uint32_t cm = load4<FULL>(static_cast<const uint8_t*>(a.m[t]), i, n);
     const uint32_t cv = load4<FULL>(static_cast<const uint8_t*>(a.v[t]), i, n);
-    const uint32_t sm = FULL || i < n ? a.ms[t][i >> 5] : 0u, sv = FULL || i < n ? a.vs[t][i >> 5] : 0u;
+    const int64_t run = (FULL ? i : min(i, n - 1)) >> 5;
+    const uint32_t sm = a.ms[t][run], sv = a.vs[t][run];
     decode4(cm, sm, m);
     decode4(cv, sv, v);
 #pragma unroll
