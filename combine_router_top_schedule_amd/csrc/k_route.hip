@@ -10,7 +10,7 @@
 // Backward: the chosen weights are q = softmax over the chosen of f(x), f = x or log sigmoid(x), so
 // dx_k = scale q_k (dw_k - sum_j dw_j q_j) f'(x_k) with f' = 1 or sigmoid(-x_k), zero elsewhere; without
 // renormalisation the scores' own derivatives. It is bound by the store of the gradient: 35 us for
-// 131,072 x 256 fp32 (134 MB written; the chosen logits, 32 bytes fetched for each, are another 34 MB), 8.6 us
+// 131,072 x 256 fp32 (134 MB written; 64 bytes fetched around each chosen logit are another 67 MB), 8.6 us
 // for plain softmax weights, 20,011 x 384 bf16 (31 MB).
 #include <cfloat>
 
