@@ -1071,12 +1071,15 @@ hipError_t launch_route_fwd(const mok_route_desc& d, const void* x, const float*
   if (a.gs > 1) a.group_magic = uint32_t(cdiv(int64_t(1) << 32, a.gs));
   if (a.gs >= 4) a.chunk_magic = uint32_t(cdiv(65536, a.gs / 4));
   // One workgroup writes the load by itself; several add to it, which takes a launch that clears it first
-  // (3.8 us). Few enough tokens (4 steps of a workgroup, some 3 us each) are left to one.
+  // (1.9 us in a graph, 3.8 us without). What a workgroup does in two steps, of 2 us (64 experts) to 3.7 us
+  // (256) each, is left to one: 64 tokens take it 6.2 to 10.2 us in a graph, several 6.0 to 8.5 us, but without
+  // a graph the second launch costs more; 128 tokens 10.4 to 17.5 us against 6.4 to 9.0 us. (8 waves in the
+  // one, 5.1 to 8.5 us for 64 tokens, need LDS of a size set at launch, which is 0.7 % of every large call.)
   const int per_step = fast ? kWaves * 64 / lanes : kWaves;
   // as many workgroups as are resident: 4 a CU, 3 of the kernels with more registers (131,072 tokens of 384
   // experts: 60 us, with 4 a CU 65 us)
   const int per_cu = !fast ? 8 : a.E > 512 || (lanes == 8 && a.E > 256) ? 3 : 4;
-  const int grid = load && a.N <= 4 * per_step ? 1 : grid_of(a.N, per_step, per_cu * cus);
+  const int grid = load && a.N <= 2 * per_step ? 1 : grid_of(a.N, per_step, per_cu * cus);
   if (load && (grid > 1 || a.N == 0)) {
     const hipError_t e = launch_fill_u32(reinterpret_cast<uint32_t*>(load), 0u, a.E, s);
     if (e != hipSuccess) return e;
