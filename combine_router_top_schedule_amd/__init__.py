@@ -579,7 +579,8 @@ def mok_grad_sumsq(plan: SumsqPlan, out, ws=None, stream=None):
 class AdamwPlan:
     """The tensors of a mok_adamw call, checked once: lists of equal length of parameters (float32 or
     bfloat16), gradients (float32 or bfloat16), moments (float32; or uint8 E4M3 codes, with their uint8
-    scales of 32 elements in m_scale and v_scale) and, for float32 parameters, bfloat16 copies."""
+    scales of 32 elements in m_scale and v_scale) and, for float32 parameters, bfloat16 copies (None in
+    the place of a parameter that has none)."""
 
     def __init__(self, p, g, m, v, copy=None, m_scale=None, v_scale=None):
         torch = _tch()
@@ -604,10 +605,10 @@ class AdamwPlan:
         for name, ts in self.keep.items():
             counts, dtype, read = runs if name.endswith("_scale") else sizes, types[name], name == "g"
             columns[name] = at = [
+                None if t is None and name == "copy" else
                 t.data_ptr() if t.dtype is dtype and t.numel() == n and t.get_device() == self.dev
                 and t.is_contiguous() else _want(t, name, dtype, n, self.dev) for t, n in zip(ts, counts)]
-            size = ts[0].element_size()
-            spans += [(a, a + n * size, read, name) for a, n in zip(at, counts) if n]
+            spans += [(a, a + n * dtype.itemsize, read, name) for a, n in zip(at, counts) if n and a is not None]
         # what is written overlaps nothing else (gradients may be given twice)
         spans.sort()
         read_end = written_end = 0   # the furthest ends so far

@@ -13,7 +13,7 @@ class MokAdamW:
     """AdamW over parameters updated in place from gradients that stay in the given tensors.
 
     params: float32 masters or bfloat16; grads: float32 or bfloat16; copies: bfloat16 copies of float32
-    masters, written by every step (the layer's weights). state: "float32" or "mxfp8" moments. max_norm
+    masters, written by every step (the layer's weights; None in the place of a master without one). state: "float32" or "mxfp8" moments. max_norm
     clips by the norm of all gradients, which stays on the device; with check_finite (or max_norm) a
     step whose norm is not finite changes nothing."""
 

@@ -20,6 +20,7 @@ if not torch.cuda.is_available():  # pragma: no cover - CPU container
     pytest.skip("needs a GPU", allow_module_level=True)
 
 import combine_router_top_schedule_amd as mok
+from combine_router_top_schedule_amd.optim import MokAdamW
 
 U = 2.0 ** -24
 HYPER = dict(lr=3e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.1)
@@ -336,6 +337,28 @@ def test_bindings_refuse():
     for bad in (dict(out=z(1)), dict(out=z(2, torch.float64)), dict(ws=u8(8))):
         with pytest.raises(ValueError):
             mok.mok_grad_sumsq(sp, **{**dict(out=sq), **bad})
+
+
+def test_copies_of_some():
+    z = lambda n, dt=torch.float32: torch.ones(n, dtype=dt, device="cuda")
+    p, g, c = [z(40), z(50), z(3)], [z(40), z(50), z(3)], [None, z(50, torch.bfloat16), None]
+    mok.mok_adamw(mok.adamw_plan(p=p, g=g, m=[z(40), z(50), z(3)], v=[z(40), z(50), z(3)], copy=c), lr=0.25, step=1)
+    assert all((t < 1).all() for t in p) and torch.equal(c[1], p[1].bfloat16())
+    with pytest.raises(ValueError):
+        mok.adamw_plan(p=[p[0]], g=[g[0]], m=[z(40)], v=[z(40)], copy=[p[0].bfloat16()[:39]])
+    mok.adamw_plan(p=[p[0]], g=[g[0]], m=[z(40)], v=[z(40)], copy=[None])
+
+
+def test_optimizer_object_refuses_to_be_captured(monkeypatch):
+    p, g = torch.ones(40, device="cuda"), torch.ones(40, device="cuda")
+    opt = MokAdamW([p], [g], max_norm=1.0)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    with pytest.raises(RuntimeError):
+        opt.step()
+    monkeypatch.undo()
+    assert opt.steps == 0 and (p == 1).all()
+    opt.step()
+    assert opt.steps == 1 and (p < 1).all()
 
 
 def test_lengths_beyond_32_bits():
