@@ -420,7 +420,7 @@ struct FastLds {   // of one wave
     } slow;
   };
   float group[T][L];
-  int out[T][KM];
+  int2 out[T][KM];              // expert and logit (its bits) of each slot
 };
 
 // What a kernel forms scores of: of nothing (keys are the logits), of nothing but the softmax's sum (for plain
@@ -631,6 +631,7 @@ __global__ __launch_bounds__(64 * kWaves, L * V >= 1024 || V > 32 ? 3 : 4) void 
     }
     wave_sync();
     f32x4 me[SL];
+    float logit_of[SL];
     int rank[SL];
     const bool more = SL > 1 && __any(have > L);
 #pragma unroll
@@ -638,6 +639,7 @@ __global__ __launch_bounds__(64 * kWaves, L * V >= 1024 || V > 32 ? 3 : 4) void 
       const int c = j + L * q;
       me[q] = f32x4{0.f, 0.f, 0.f, __int_as_float(-1)};
       rank[q] = 0;
+      logit_of[q] = 0.f;
       if (q > 0 && !more) break;
       if (c < have) {
         const int e = __float_as_int(s.cand[t][c][3]);
@@ -648,6 +650,7 @@ __global__ __launch_bounds__(64 * kWaves, L * V >= 1024 || V > 32 ? 3 : 4) void 
           k = score32(v) + b;
         }
         me[q] = f32x4{k, v, b, __int_as_float(e)};
+        logit_of[q] = v;
         s.cand[t][c] = me[q];
       }
     }
@@ -726,14 +729,16 @@ __global__ __launch_bounds__(64 * kWaves, L * V >= 1024 || V > 32 ? 3 : 4) void 
     slow = slow || (kBias && (__ballot(unsure) & here) != 0);
 #pragma unroll
     for (int q = 0; q < SL; ++q)
-      if (j + L * q < have && rank[q] < a.K) s.out[t][rank[q]] = __float_as_int(me[q][3]);
+      if (j + L * q < have && rank[q] < a.K)
+        s.out[t][rank[q]] = int2{__float_as_int(me[q][3]), __float_as_int(logit_of[q])};
     // (a token that leaves here may have ranks that do not fill its slots)
     const int filled = slow ? 0 : have < a.K ? have : a.K;
     wave_sync();
     // weights of the slots, one a lane
-    const int e = j < filled ? s.out[t][j] : -1;
+    const int2 slot = j < filled ? s.out[t][j] : int2{-1, __float_as_int(-INFINITY)};
+    const int e = slot.x;
     const bool some = e >= 0;
-    const float v = some ? logit<BF16>(a.x, n * a.ld + e) : -INFINITY;
+    const float v = __int_as_float(slot.y);
     const float w = slot_weight<L>(a, some, v, top, sum);
     if (n < a.N && j < a.K && !slow) {
       a.idx[n * a.K + j] = e;
