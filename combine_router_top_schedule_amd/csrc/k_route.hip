@@ -370,6 +370,14 @@ __device__ __forceinline__ void merge_lanes(float* v) {
   for (int i = 0; i < M; ++i) w[i] = lane_xor<OFF>(v[i]);
   merge_down<M>(v, w);
 }
+// The least of the M largest of two lanes' lists.
+template <int OFF, int M>
+__device__ __forceinline__ float merged_least(const float* v) {
+  float least = fmaxf(v[0], lane_xor<OFF>(v[M - 1]));
+#pragma unroll
+  for (int i = 1; i < M; ++i) least = fminf(least, fmaxf(v[i], lane_xor<OFF>(v[M - 1 - i])));
+  return least;
+}
 
 // The tokens n0 + b / L for the set bits b of `left`, one after the other. Not inlined: the constants of its
 // fp64 exponentials would be kept in 80 registers throughout the tile loop (70 us instead of 61 us for
@@ -594,12 +602,17 @@ __global__ __launch_bounds__(64 * kWaves, L * V >= 1024 || V > 32 ? 3 : 4) void 
     }
     merge_lanes<1, KM>(list);
     merge_lanes<2, KM>(list);
-    merge_lanes<4, KM>(list);
-    if constexpr (L > 8) merge_lanes<8, KM>(list);
-    if constexpr (L > 16) merge_lanes<16, KM>(list);
-    float tau = list[0];
+    if constexpr (L > 8) merge_lanes<4, KM>(list);
+    if constexpr (L > 16) merge_lanes<8, KM>(list);
+    float tau;
+    if (a.K == KM) {   // (the last two lists then need no sorting: 60 us for 131,072 x 256, 61 us with it)
+      tau = merged_least<L / 2, KM>(list);
+    } else {
+      merge_lanes<L / 2, KM>(list);
+      tau = list[0];
 #pragma unroll
-    for (int i = 1; i < KM; ++i) tau = i < a.K ? list[i] : tau;
+      for (int i = 1; i < KM; ++i) tau = i < a.K ? list[i] : tau;
+    }
     const float cut = fmaxf(tau - 2.f * key_eps, -FLT_MAX);
     // a bit per expert of the lane: shifted in with the comparison's carry
     constexpr int W = (V + 31) / 32;
