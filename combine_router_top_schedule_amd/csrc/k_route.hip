@@ -13,6 +13,7 @@
 // 131,072 x 256 fp32 (134 MB written; 64 bytes fetched around each chosen logit are another 67 MB), 8.6 us
 // for plain softmax weights, 20,011 x 384 bf16 (31 MB).
 #include <cfloat>
+#include <type_traits>
 
 #include "mok_internal.h"
 #include "mok_device.h"
@@ -527,26 +528,35 @@ __global__ __launch_bounds__(64 * kWaves, L * V >= 1024 || V > 32 ? 3 : 4) void 
     };
     bool slow = false;
     // keys (in x from here on) and, through LDS, the groups' scores
+    auto form_keys = [&](auto checked) {
 #pragma unroll
-    for (int i = 0; i < V / 4; ++i) {
-      float g[4];
+      for (int i = 0; i < V / 4; ++i) {
+        float g[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float v = x[4 * i + c];
-        float k = v;
-        if constexpr (kBias) k = score32(v) + s_bias[4 * (j + L * i) + c];
-        bool able = v > -INFINITY;                            // NaN is not
-        if constexpr (MODE == kSoftmaxBias) able = able && k > -INFINITY;   // (the row's sum may be NaN)
-        x[4 * i + c] = able ? k : -INFINITY;
-        g[c] = x[4 * i + c];
-        if constexpr (kTop2) g[c] = able ? score32(v) : -INFINITY;
+        for (int c = 0; c < 4; ++c) {
+          const float v = x[4 * i + c];
+          float k = v;
+          if constexpr (kBias) k = score32(v) + s_bias[4 * (j + L * i) + c];
+          bool able = !checked || v > -INFINITY;                // NaN is not
+          if constexpr (MODE == kSoftmaxBias) able = able && k > -INFINITY;   // (the row's sum may be NaN)
+          x[4 * i + c] = able ? k : -INFINITY;
+          g[c] = x[4 * i + c];
+          if constexpr (kTop2) g[c] = able ? score32(v) : -INFINITY;
+        }
+        if (a.G > 1) {
+          const float h0 = fmaxf(g[0], g[1]), l0 = fminf(g[0], g[1]);
+          const float h1 = fmaxf(g[2], g[3]), l1 = fminf(g[2], g[3]);
+          s.pair[t][j + L * i] = float2{fmaxf(h0, h1), fmaxf(fminf(h0, h1), fmaxf(l0, l1))};
+        }
       }
-      if (a.G > 1) {
-        const float h0 = fmaxf(g[0], g[1]), l0 = fminf(g[0], g[1]);
-        const float h1 = fmaxf(g[2], g[3]), l1 = fminf(g[2], g[3]);
-        s.pair[t][j + L * i] = float2{fmaxf(h0, h1), fmaxf(fminf(h0, h1), fmaxf(l0, l1))};
-      }
-    }
+    };
+    // Two instructions an expert bar those of -inf and NaN; one an expert finds that a wave's rows hold none
+    // (131,072 x 384 bf16: 58.9 us, so 56.8 us; x 256: 61.0 us, 60.2 us).
+    float size = 0.f;
+#pragma unroll
+    for (int u = 0; u < V; ++u) size += fabsf(x[u]);
+    if (__any(!(size < INFINITY))) form_keys(std::true_type{});
+    else form_keys(std::false_type{});
     if (a.G > 1) {
       wave_sync();
       float best = -INFINITY, second = -INFINITY;
