@@ -4,9 +4,9 @@
 // keys; weights from s. The choice has to be that of exact arithmetic, and among a few million scores
 // many pairs are closer than fp32 rounding. k_route_fwd compares all keys in fp64, one token a wave
 // (557 us for 131,072 tokens of 256 experts, sigmoid, bias, 8 groups, top 8); k_route_fast lets fp32
-// decide what it can and takes 60 us: 1,480 vector instructions for 8 tokens, issued in 72 % of its
+// decide what it can and takes 60 us: 1,390 vector instructions for 8 tokens, issued in 70 % of its
 // cycles, bound it; reading the logits would take 22 us at 6.2 TB/s. 131,072 x 384 in bf16 (no groups):
-// 60 us.
+// 57 us.
 // Backward: the chosen weights are q = softmax over the chosen of f(x), f = x or log sigmoid(x), so
 // dx_k = scale q_k (dw_k - sum_j dw_j q_j) f'(x_k) with f' = 1 or sigmoid(-x_k), zero elsewhere; without
 // renormalisation the scores' own derivatives. It is bound by the store of the gradient: 35 us for
