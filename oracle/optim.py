@@ -86,8 +86,8 @@ def encode(x, u, positive: bool):
         for j in range(32):
             a = abs(float(x[r, j])) * 2.0 ** -e
             step_ = 2.0 ** (max(math.frexp(a)[1] - 1, -6) - 3) if a else 2.0 ** -9
-            # (fp32 sum: the one place where the order of roundings could show)
-            k = math.floor(float(F(F(a / step_) + F(u[r, j] / 65536))))
+            # (24 and 16 bits, at least 2^-40 away from an integer that they do not reach: fp64 is exact enough)
+            k = math.floor(a / step_ + u[r, j] / 65536)
             if positive and a > 0:
                 k = max(k, 1)
             codes[r, j] = table[k * step_] | (128 if np.signbit(x[r, j]) else 0)
