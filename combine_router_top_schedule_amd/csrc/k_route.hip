@@ -539,9 +539,11 @@ __global__ __launch_bounds__(64 * kWaves, L * V >= 1024 || V > 32 ? 3 : 4) void 
           if constexpr (kBias) k = score32(v) + s_bias[4 * (j + L * i) + c];
           bool able = !checked || v > -INFINITY;                // NaN is not
           if constexpr (MODE == kSoftmaxBias) able = able && k > -INFINITY;   // (the row's sum may be NaN)
+          if constexpr (kTop2) g[c] = score32(v);
+          // (here too: without scores no group is better than another, and none stays)
+          if constexpr (MODE == kSoftmaxTop2) able = able && (!checked || g[c] > -INFINITY);
           x[4 * i + c] = able ? k : -INFINITY;
-          g[c] = x[4 * i + c];
-          if constexpr (kTop2) g[c] = able ? score32(v) : -INFINITY;
+          g[c] = able ? (kTop2 ? g[c] : k) : -INFINITY;
         }
         if (a.G > 1) {
           const float h0 = fmaxf(g[0], g[1]), l0 = fminf(g[0], g[1]);

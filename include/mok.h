@@ -453,8 +453,10 @@ typedef enum { MOK_ELEM_F32 = 0, MOK_ELEM_BF16 = 1 } mok_elem;
  *              part in the choice only.
  * Choices are those of exact arithmetic on the given values: keys that fp32 cannot tell apart are
  * compared in fp64. Weights are fp32 arithmetic; the renormalised ones are formed as a softmax over
- * the chosen of x_e, or of log sigmoid(x_e), so they hold for logits of any size. (A NaN or +inf logit
- * makes the row's softmax weights NaN; with a bias too, such a row chooses nothing.) */
+ * the chosen of x_e, or of log sigmoid(x_e), so they hold for logits of any size. A softmax row with a
+ * NaN or +inf logit has no scores: where scores take part in the choice (a bias, or several groups by
+ * MOK_GROUP_TOP2) it chooses nothing, else it goes by its logits and its weights are NaN, but for
+ * renormalised ones, which are formed of the chosen logits alone and are NaN only with +inf among them. */
 typedef enum { MOK_SCORE_SOFTMAX = 0, MOK_SCORE_SIGMOID = 1 } mok_score;
 typedef enum { MOK_GROUP_MAX = 0, MOK_GROUP_TOP2 = 1 } mok_group_score;
 

@@ -46,7 +46,9 @@ def choose_row(gate: Gate, x, bias=None) -> list:
     b = None if bias is None else np.asarray(bias, np.float64)
     biased = s if b is None else s + b
     key = x if b is None else biased
-    able = [e for e in range(gate.E) if x[e] > -math.inf and key[e] > -math.inf]
+    scored = b is not None or (gate.groups > 1 and gate.group_score == "top2")
+    able = [e for e in range(gate.E)
+            if x[e] > -math.inf and key[e] > -math.inf and (not scored or biased[e] > -math.inf)]
     if gate.groups > 1:
         size = gate.E // gate.groups
         value = []
