@@ -522,7 +522,11 @@ __global__ __launch_bounds__(64 * kWaves, L * V >= 1024 || V > 32 ? 3 : 4) void 
     // largest score, 1 / sum. The sum with the bias is rounded once more, to 1 u of at most 1 + |b|.
     const float eps = (kSigmoid ? 3.f : 100.f * rsum) * 0x1p-24f + (1.f + big) * 0x1p-24f;
     const float key_eps = kBias ? eps : 0.f;
-    const float group_gap = kTop2 || (kBias && a.top2) ? 6.f * eps : 2.f * key_eps;
+    // Groups by their largest key: two fp32 scores are off by eps each, 2 eps apart, and a third takes up the
+    // rounding of score -+ gap (up to half a unit, below eps) ahead of a comparison for less or more. By their two
+    // largest: a sum of two keys is off by 2 eps and its own rounding of (up to 2 (1 + big)) u, two of them by 4 eps
+    // and 4 (1 + big) u; score -+ gap, again a number of that size, by another 2 (1 + big) u; the seventh is slack.
+    const float group_gap = kTop2 || (kBias && a.top2) ? 4.f * eps + 7.f * 0x1p-24f * (1.f + big) : 3.f * key_eps;
     auto score32 = [&](float v) {
       return kSigmoid ? __builtin_amdgcn_rcpf(1.f + __expf(-v)) : __expf(v - top) * rsum;
     };
