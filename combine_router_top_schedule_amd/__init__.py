@@ -634,7 +634,8 @@ def mok_adamw(plan: AdamwPlan, lr, step, beta1: float = 0.9, beta2: float = 0.99
               weight_decay: float = 0.0, seed: int = 0, sumsq=None, max_norm: Optional[float] = None,
               stream=None):
     """One AdamW step over the plan's tensors, in place. `lr` and `step` may be device tensors (float64
-    [1], int64 [1]), read when the step runs (a step's number is then added to `seed`). With `sumsq`
+    [1], int64 [1]), read when the step runs (a step's number is then added to `seed`; a number below 1, or a
+    rate that is negative or not finite, changes nothing). With `sumsq`
     (float64 [1], the squared norm of all gradients) gradients are clipped to `max_norm` (None: not
     clipped) and a step whose norm is not finite changes nothing."""
     torch = _tch()

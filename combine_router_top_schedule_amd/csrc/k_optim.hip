@@ -377,6 +377,7 @@ __global__ __launch_bounds__(256) void k_adamw(AdamArgs a) {
   if (a.lr_dev || a.step_dev) {
     const double lr = a.lr_dev ? *a.lr_dev : a.lr;
     const int64_t number = a.step_dev ? *a.step_dev : a.step;
+    if (!(lr >= 0.0 && lr < INFINITY) || number < 1) return;   // what the host refuses: NaN, too
     // replays of a captured step differ in their step alone, and with the same bits in each of them
     // an element's small updates would be dropped in all of them, or in none
     if (a.step_dev) seed += uint32_t(number);

@@ -546,7 +546,9 @@ typedef struct {
   const double* sumsq_dev;  /* squared norm of all gradients, or NULL (no clipping). When it is not
                                finite the call changes nothing                                   */
   const double* lr_dev;     /* NULL, or where the device finds lr (a captured step whose rate changes) */
-  const int64_t* step_dev;  /* NULL, or where the device finds step (and adds it to the seed)     */
+  const int64_t* step_dev;  /* NULL, or where the device finds step (and adds it to the seed).
+                               With a step below 1, or an lr that is negative or not finite, on the
+                               device the call changes nothing                                   */
 } mok_adamw_config;
 
 /* One AdamW step over all tensors, in few launches (48 tensors each):
