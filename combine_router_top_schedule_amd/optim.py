@@ -12,10 +12,11 @@ from . import adamw_plan, mok_adamw, mok_grad_sumsq, sumsq_plan
 class MokAdamW:
     """AdamW over parameters updated in place from gradients that stay in the given tensors.
 
-    params: float32 masters or bfloat16; grads: float32 or bfloat16; copies: bfloat16 copies of float32
-    masters, written by every step (the layer's weights; None in the place of a master without one). state: "float32" or "mxfp8" moments. max_norm
-    clips by the norm of all gradients, which stays on the device; with check_finite (or max_norm) a
-    step whose norm is not finite changes nothing."""
+    params: float32 masters or bfloat16; grads: float32 or bfloat16 (each list of one type); copies:
+    bfloat16 copies of float32 masters, written by every step (the layer's weights; None in the place of
+    a master without one). state: "float32" or "mxfp8" moments. max_norm clips by the norm of all
+    gradients, which stays on the device; with check_finite (or max_norm) a step whose norm is not finite
+    changes nothing."""
 
     def __init__(self, params, grads, copies=None, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
                  weight_decay: float = 0.0, max_norm: Optional[float] = None, check_finite: bool = False,
@@ -43,12 +44,14 @@ class MokAdamW:
     def step(self, lr: Optional[float] = None):
         """One step; `lr` replaces the rate given at the start, for this step. Rate and step count are
         the host's, which a graph would keep: to capture a step call mok_adamw on this object's
-        plan with both on the device."""
+        plan with both on the device. A step that the device leaves out because its norm is not
+        finite counts, too, as the host does not read the norm."""
         if torch.cuda.is_current_stream_capturing():
             raise RuntimeError("a captured step takes its number from the device: see mok_adamw")
-        self.steps += 1
+        step = self.steps + 1
         if self.sumsq is not None:
             mok_grad_sumsq(self.sumsq_plan, self.sumsq)
-        mok_adamw(self.plan, lr=self.lr if lr is None else lr, step=self.steps, beta1=self.betas[0],
+        mok_adamw(self.plan, lr=self.lr if lr is None else lr, step=step, beta1=self.betas[0],
                   beta2=self.betas[1], eps=self.eps, weight_decay=self.weight_decay,
-                  seed=self.seed + self.steps, sumsq=self.sumsq, max_norm=self.max_norm)
+                  seed=self.seed + step, sumsq=self.sumsq, max_norm=self.max_norm)
+        self.steps = step   # (a refused call is no step)

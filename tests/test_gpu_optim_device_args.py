@@ -11,6 +11,7 @@ if not torch.cuda.is_available():  # pragma: no cover - CPU container
     pytest.skip("needs a GPU", allow_module_level=True)
 
 import combine_router_top_schedule_amd as mok
+from combine_router_top_schedule_amd.optim import MokAdamW
 
 
 def tensors(mx, bf):
@@ -58,3 +59,20 @@ def test_refused_values_change_nothing(mx, bf):
     step.fill_(2 ** 62)
     mok.mok_adamw(plan, lr=lr, step=step)
     assert all(torch.isfinite(a).all() and not torch.equal(a, b) for a, b in zip(t["p"][:1], before["p"][:1]))
+
+
+def test_a_refused_call_is_no_step():
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    new = lambda: torch.randn(100, generator=gen, device="cuda")
+    p, g = new(), new()
+    q = p.clone()
+    opt, ref = MokAdamW([p], [g], max_norm=1.0, state="mxfp8"), MokAdamW([q], [g], max_norm=1.0, state="mxfp8")
+    for bad in (-1.0, math.nan, math.inf):
+        with pytest.raises(mok.MokError):
+            opt.step(lr=bad)
+    assert opt.steps == 0
+    for _ in range(3):
+        opt.step()
+        ref.step()
+    assert opt.steps == ref.steps == 3 and torch.equal(p, q)
+    assert torch.equal(opt.m[0], ref.m[0]) and torch.equal(opt.v[0], ref.v[0])
