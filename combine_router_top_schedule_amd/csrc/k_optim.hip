@@ -374,6 +374,8 @@ __global__ __launch_bounds__(256) void k_adamw(AdamArgs a) {
   }
   float decay = a.decay, rate = a.rate, rbc2 = a.rbc2;
   uint32_t seed = a.seed;
+  // Formed again by every thread: 926 us instead of 899 us for 178 M elements with fp32 moments, 1,374 us instead of
+  // 778 us for 267 M with 8-bit ones, which have more arithmetic in their way already.
   if (a.lr_dev || a.step_dev) {
     const double lr = a.lr_dev ? *a.lr_dev : a.lr;
     const int64_t number = a.step_dev ? *a.step_dev : a.step;

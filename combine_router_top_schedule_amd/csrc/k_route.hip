@@ -1,12 +1,13 @@
 // Expert routing with scores, balancing bias, groups and renormalised weights, and its gradient.
 //
 // Forward, per token: s = sigmoid(x) or softmax(x); keys s + b (or x); the best groups; the K largest
-// keys; weights from s. The choice has to be that of exact arithmetic, and among a few million scores
-// many pairs are closer than fp32 rounding. k_route_fwd compares all keys in fp64, one token a wave
-// (557 us for 131,072 tokens of 256 experts, sigmoid, bias, 8 groups, top 8); k_route_fast lets fp32
-// decide what it can and takes 60 us: 1,390 vector instructions for 8 tokens, issued in 70 % of its
-// cycles, bound it; reading the logits would take 22 us at 6.2 TB/s. 131,072 x 384 in bf16 (no groups):
-// 57 us.
+// keys; weights from s. The choice must not depend on fp32 rounding, and among a few million scores
+// many pairs are closer than that. k_route_fwd compares all keys in fp64, one token a wave (131,072 tokens,
+// top 8: 293 us for 256 experts, sigmoid, bias, 16 groups; 282 us for 8 groups of 31; 665 us for 384 experts in 12
+// groups); k_route_fast lets fp32 decide what it can and takes 60 us for 256 experts in 8 groups: 1,390 vector
+// instructions for 8 tokens, issued in 70 % of its cycles, bound it; reading the logits would take 22 us at
+// 6.2 TB/s. 131,072 x 384 in bf16 (no groups): 57 us. More experts or choices: 113 us for 256 with top 16, 114 us
+// for 512 in 16 groups (154 us with top 16), 229 us for 1024 in 32 groups, 289 us for 1024 in bf16 with top 16.
 // Backward: the chosen weights are q = softmax over the chosen of f(x), f = x or log sigmoid(x), so
 // dx_k = scale q_k (dw_k - sum_j dw_j q_j) f'(x_k) with f' = 1 or sigmoid(-x_k), zero elsewhere; without
 // renormalisation the scores' own derivatives. It is bound by the store of the gradient: 35 us for
@@ -1100,7 +1101,8 @@ hipError_t launch_route_fwd(const mok_route_desc& d, const void* x, const float*
   const int cus = device_cus() > 0 ? device_cus() : 256;
   // lanes of a token: as many as its experts need at 32 a lane, and its choices at one a lane
   const int lanes = a.E <= (a.K <= 8 ? 384 : 0) ? 8 : a.E <= 512 ? 16 : 32;
-  // groups that are not made of whole runs of 4 experts, or more of them than lanes, go one token a wave
+  // groups that are not made of whole runs of 4 experts, or more of them than lanes, go one token a wave (256
+  // experts, top 8: 293 us in 16 groups, which 16 lanes a token would hold, against 60 us in 8)
   const bool fast = a.G == 1 || (a.gs % 4 == 0 && a.G <= lanes);
   if (a.gs > 1) a.group_magic = uint32_t(cdiv(int64_t(1) << 32, a.gs));
   if (a.gs >= 4) a.chunk_magic = uint32_t(cdiv(65536, a.gs / 4));

@@ -451,8 +451,9 @@ typedef enum { MOK_ELEM_F32 = 0, MOK_ELEM_BF16 = 1 } mok_elem;
  *              id; slots that no expert fills get id -1 and weight 0;
  *   weight     renorm: scale * s_e / (sum of s over the chosen); else scale * s_e. The bias takes
  *              part in the choice only.
- * Choices are those of exact arithmetic on the given values: keys that fp32 cannot tell apart are
- * compared in fp64. Weights are fp32 arithmetic; the renormalised ones are formed as a softmax over
+ * Choices do not depend on fp32 rounding: keys and groups' scores that fp32 cannot tell apart are
+ * compared in fp64. What fp64 rounds to one number is a tie (sigmoids of logits above 37 under one bias
+ * are), and what it rounds differently is not (sums of two keys that are equal on paper). Weights are fp32 arithmetic; the renormalised ones are formed as a softmax over
  * the chosen of x_e, or of log sigmoid(x_e), so they hold for logits of any size. A softmax row with a
  * NaN or +inf logit has no scores: where scores take part in the choice (a bias, or several groups by
  * MOK_GROUP_TOP2) it chooses nothing, else it goes by its logits and its weights are NaN, but for
