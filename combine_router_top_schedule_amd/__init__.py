@@ -86,6 +86,11 @@ class MokAdamwConfig(ctypes.Structure):
                 ("state", ctypes.c_int32), ("sumsq_dev", _P), ("lr_dev", _P), ("step_dev", _P)]
 
 
+class MokBlockDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("stride", ctypes.c_int64), ("groups", ctypes.c_int32),
+                ("n", ctypes.c_int32), ("k", ctypes.c_int32), ("elem", ctypes.c_int32)]
+
+
 class MokWeights(ctypes.Structure):
     _fields_ = [(n, _P) for n in ("wg", "wu", "wd", "wg_q", "wg_s", "wu_q", "wu_s", "wd_q",
                                   "wd_s", "wgt_q", "wgt_s", "wut_q", "wut_s", "wdt_q", "wdt_s",
@@ -147,6 +152,11 @@ _SIGS = {
     "mok_sumsq_ws_size": (ctypes.c_int, [ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)]),
     "mok_grad_sumsq": (ctypes.c_int, [ctypes.c_int32, _P, ctypes.c_int32, _P, _P, _P]),
     "mok_adamw": (ctypes.c_int, [ctypes.c_int32, _P, ctypes.POINTER(MokAdamwConfig), _P]),
+    "mok_block_padded_rows": (ctypes.c_int64, [ctypes.c_int64, ctypes.c_int32]),
+    "mok_block_quantize": (ctypes.c_int, [ctypes.POINTER(MokBlockDesc), _P, _P, _P, _P, _P, _P, _P]),
+    "mok_block_quantize_weights": (ctypes.c_int, [ctypes.POINTER(MokBlockDesc), _P, _P, _P, _P, _P, _P]),
+    "mok_block_gemm": (ctypes.c_int, [ctypes.POINTER(MokBlockDesc), _P, _P, _P, _P, _P, _P, _P]),
+    "mok_block_wgrad": (ctypes.c_int, [ctypes.POINTER(MokBlockDesc), _P, _P, _P, _P, _P, _P, ctypes.c_int32, _P]),
     "mok_device_cus": (ctypes.c_int32, []),
     "mok_trace_kernel": (ctypes.c_int, [ctypes.c_int32, _P, _P]),
 }
@@ -659,3 +669,135 @@ def mok_adamw(plan: AdamwPlan, lr, step, beta1: float = 0.9, beta2: float = 0.99
     c.seed = seed & 0xFFFFFFFF
     with _on_device(plan.dev, stream) as s:
         _check("mok_adamw", lib().mok_adamw(len(plan.table), plan.table, ctypes.byref(c), s))
+
+
+# ------------------------------------------------------------------------ linear maps in block-scaled FP8
+
+def _up128(n: int) -> int:
+    return -(-n // 128) * 128
+
+
+def block_padded_rows(rows: int, groups: int = 1) -> int:
+    """Columns of the column codes of `rows` rows in `groups` groups, whatever the groups' sizes."""
+    n = int(lib().mok_block_padded_rows(rows, groups))
+    if n < 0:
+        raise ValueError(f"{rows} rows in {groups} groups are out of range")
+    return n
+
+
+def _rows2d(t, name: str):
+    """(rows, columns, elements from row to row) of a 2-d tensor with contiguous rows."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, not {tuple(t.shape)}")
+    rows, cols = t.shape
+    ld, step = t.stride()
+    if (cols > 1 and step != 1) or (rows > 1 and ld < cols):
+        raise ValueError(f"{name}: rows must be contiguous and must not overlap")
+    return rows, cols, ld if rows > 1 else max(cols, 1)
+
+
+def _offsets(offsets, dev: int):
+    """(groups, address) of the groups' offsets (None: one group of all rows)."""
+    if offsets is None:
+        return 1, None
+    if offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise ValueError(f"offsets must be [groups + 1], not {tuple(offsets.shape)}")
+    return offsets.shape[0] - 1, _want(offsets, "offsets", _torch.int32, offsets.shape[0], dev)
+
+
+def _codes(t, name: str, shape, dev: int):
+    """Address of contiguous uint8 (or float8_e4m3fn) codes of `shape`."""
+    if tuple(t.shape) != tuple(shape) or t.dtype not in (_torch.uint8, _torch.float8_e4m3fn):
+        raise ValueError(f"{name} must be uint8 or float8_e4m3fn {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
+    return _want(t, name, t.dtype, t.numel(), dev)
+
+
+def _scales(t, name: str, shape, dev: int):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, not {tuple(t.shape)}")
+    return _want(t, name, _torch.float32, t.numel(), dev)
+
+
+def mok_block_quantize(x, codes=None, scales=None, codes_t=None, scales_t=None, offsets=None, stream=None):
+    """E4M3 codes of rows x [R][K] (float32 or bfloat16, rows may be strided) with one scale for 128 values. codes
+    [R][up(K)] and scales [up(K) / 128][R] are blocked along the row, for products; codes_t [K][P] and scales_t
+    [P / 128][K], P = block_padded_rows(R, groups), along the rows of each group, for the weight gradient.
+    offsets: int32 [groups + 1] (None: one group of all rows)."""
+    torch, dev = _tch(), _device_of(x)
+    R, K, ld = _rows2d(x, "x")
+    G, off = _offsets(offsets, dev)
+    d = MokBlockDesc(R, ld, G, 1, K, _elem(x, "x"))
+    if (codes is None) != (scales is None) or (codes_t is None) != (scales_t is None):
+        raise ValueError("codes and scales go together")
+    c = s = ct = st = None
+    if codes is not None:
+        c = _codes(codes, "codes", (R, _up128(K)), dev)
+        s = _scales(scales, "scales", (_up128(K) // 128, R), dev)
+    if codes_t is not None:
+        P = block_padded_rows(R, G)
+        ct = _codes(codes_t, "codes_t", (K, P), dev)
+        st = _scales(scales_t, "scales_t", (P // 128, K), dev)
+    with _on_device(dev, stream) as q:
+        _check("mok_block_quantize", lib().mok_block_quantize(ctypes.byref(d), x.data_ptr(), off, c, s, ct, st, q))
+
+
+def mok_block_quantize_weights(w, codes, scales, codes_t=None, scales_t=None, stream=None):
+    """E4M3 codes of weights w [G][N][K] (contiguous, float32 or bfloat16), one scale for 128 x 128 values: codes
+    [G][N][up(K)], scales [G][up(N) / 128][up(K) / 128]; codes_t and scales_t are those of the transposed weights [G][K][N]."""
+    torch, dev = _tch(), _device_of(w)
+    if w.dim() != 3:
+        raise ValueError(f"w must be [groups][N][K], not {tuple(w.shape)}")
+    G, N, K = w.shape
+    src = _want(w, "w", w.dtype, w.numel(), dev)
+    d = MokBlockDesc(0, K, G, N, K, _elem(w, "w"))
+    if (codes_t is None) != (scales_t is None):
+        raise ValueError("codes_t and scales_t go together")
+    kb, nb = _up128(K) // 128, _up128(N) // 128
+    c, s = _codes(codes, "codes", (G, N, kb * 128), dev), _scales(scales, "scales", (G, nb, kb), dev)
+    ct = st = None
+    if codes_t is not None:
+        ct, st = _codes(codes_t, "codes_t", (G, K, nb * 128), dev), _scales(scales_t, "scales_t", (G, kb, nb), dev)
+    with _on_device(dev, stream) as q:
+        _check("mok_block_quantize_weights", lib().mok_block_quantize_weights(ctypes.byref(d), src, c, s, ct, st, q))
+
+
+def mok_block_gemm(x, x_scales, w, w_scales, out, offsets=None, stream=None):
+    """out [R][N] (float32 or bfloat16, rows may be strided) = x w^T by groups of rows: x, x_scales from
+    mok_block_quantize, w, w_scales from mok_block_quantize_weights (their transposed ones give the input gradient). Rows
+    in no group are left as they are."""
+    torch, dev = _tch(), _device_of(x)
+    R, N, ld = _rows2d(out, "out")
+    G, off = _offsets(offsets, dev)
+    if x.dim() != 2 or x.shape[1] % 128 or x.shape[1] == 0:
+        raise ValueError(f"x must be [rows][a multiple of 128], not {tuple(x.shape)}")
+    K = x.shape[1]
+    if out.get_device() != dev:
+        raise ValueError(f"out is on {out.device}, x on device {dev}")
+    d = MokBlockDesc(R, ld, G, N, K, _elem(out, "out"))
+    with _on_device(dev, stream) as q:
+        _check("mok_block_gemm", lib().mok_block_gemm(
+            ctypes.byref(d), _codes(x, "x", (R, K), dev), _scales(x_scales, "x_scales", (K // 128, R), dev),
+            _codes(w, "w", (G, N, K), dev), _scales(w_scales, "w_scales", (G, _up128(N) // 128, K // 128), dev), off,
+            out.data_ptr(), q))
+
+
+def mok_block_wgrad(dy_t, dy_scales, x_t, x_scales, dw, offsets=None, accumulate: bool = False, stream=None):
+    """dw [G][N][K] (float32, contiguous) = dy^T x by groups of rows, or added to with `accumulate`, from the column codes
+    and scales (mok_block_quantize) of dy [R][N] and x [R][K]."""
+    torch, dev = _tch(), _device_of(dw)
+    if dw.dim() != 3:
+        raise ValueError(f"dw must be [groups][N][K], not {tuple(dw.shape)}")
+    G, N, K = dw.shape
+    groups, off = _offsets(offsets, dev)
+    if groups != G:
+        raise ValueError(f"dw has {G} groups, offsets {groups}")
+    P = dy_t.shape[1] if dy_t.dim() == 2 else -1
+    R = P + 127 - 127 * G   # the most rows that need P columns: a bound for the offsets as good as R itself
+    if P < 0 or P % 128 or R < 0:
+        raise ValueError(f"dy_t must be [{N}][block_padded_rows(rows, {G})], not {tuple(dy_t.shape)}")
+    d = MokBlockDesc(R, 0, G, N, K, MOK_ELEM_F32)
+    with _on_device(dev, stream) as q:
+        _check("mok_block_wgrad", lib().mok_block_wgrad(
+            ctypes.byref(d), _codes(dy_t, "dy_t", (N, P), dev), _scales(dy_scales, "dy_scales", (P // 128, N), dev),
+            _codes(x_t, "x_t", (K, P), dev), _scales(x_scales, "x_scales", (P // 128, K), dev), off,
+            _want(dw, "dw", torch.float32, G * N * K, dev), int(accumulate), q))

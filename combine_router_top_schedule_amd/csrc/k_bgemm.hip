@@ -1,0 +1,284 @@
+// Products of E4M3 operands with one fp32 scale for 128 values along the sum:
+//   rows sorted by expert times the experts' weights (scales of 128 x 128 there),
+//     out[r][n] = sum_j xs[j][r] ws[g][n / 128][j] sum_{k in block j} x[r][k] w[g][n][k];
+//   the weight gradient, both operands with their tokens contiguous and scaled in blocks of 128 tokens,
+//     dw[g][n][k] = sum_j dys[j][n] xs[j][k] sum_{t in block j} dy[n][t] x[k][t].
+//
+// A stage of 128 bytes a row is one block of the sum, so each stage's 32 x 32 product of two
+// v_mfma_f32_32x32x64_f8f6f4 starts from zero and is added, times its scales, by one fused multiply-add an element
+// (the weight gradient needs one product of two scales more). The first operand's rows (weights; dy) are the rows of
+// the MFMA's result, which lie in registers, the second's (tokens; x) its columns, which lie in lanes: a lane has one token
+// scale, and a weight scale is the same for a whole wave.
+#include "k_block.h"
+#include "k_gemm.h"
+
+namespace mok {
+namespace {
+
+struct ProductArgs {
+  const uint8_t* a;      // weights [g][n][stride_a], or dy columns [n][stride_a]
+  const float* as;       // weights' scales [g][nb][kb], or dy's [..][n]
+  const uint8_t* b;      // tokens [rows][stride_b], or x columns [k][stride_b]
+  const float* bs;       // [kb][rows], or [..][k]
+  void* out;
+  RowGroups rg;
+  int64_t out_stride, stride_a, stride_b;
+  int n, k, kb;          // k, kb: columns and blocks of the sum (gradient: columns of x)
+  int tiles_n;           // tiles of n
+  int tiles_k;           // gradient: tiles of k
+  int accumulate, bf16;
+};
+
+// WA x WB waves, each FA x FB blocks of 32 x 32.
+template <int WA_, int WB_, int FA_, int FB_>
+struct Shape {
+  static constexpr int WA = WA_, WB = WB_, FA = FA_, FB = FB_;
+  static constexpr int kWaves = WA * WB, kA = WA * FA * 32, kB = WB * FB * 32;
+  struct Lds {
+    uint8_t a[2][kA * kStageRowBytes];
+    uint8_t b[2][kB * kStageRowBytes];
+    float as[2][kA];
+    float bs[2][kB];
+  };
+};
+
+// 128 bytes of each of ROWS rows into an LDS stage, swizzled as swz() reads them; the waves take 8 rows a load in
+// turn. Rows past the resource's end read as zeros.
+template <int ROWS, int WAVES>
+__device__ __forceinline__ void issue_rows(__amdgpu_buffer_rsrc_t r, uint8_t* lds, int stride, int col, int w) {
+  const int L = opaque(int(threadIdx.x) & 63);
+  constexpr int kEach = ROWS / 8 / WAVES;
+#pragma unroll
+  for (int c = 0; c < kEach; ++c) {
+    const int blk = w * kEach + c;
+    const int chunk = (L & 7) ^ (L >> 3) ^ (blk & 1);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(lds + blk * 8 * kStageRowBytes), 16,
+                                             (blk * 8 + (L >> 3)) * stride + col + chunk * 16, 0, 0, 0);
+  }
+}
+
+// COUNT scales (consecutive floats, those from `valid` on zero) into LDS, 64 a wave, by the waves from `first` on.
+template <int COUNT>
+__device__ __forceinline__ void issue_scales(const float* s, int valid, float* lds, int w, int first) {
+  if (w < first || w >= first + COUNT / 64) return;
+  const int L = int(threadIdx.x) & 63, q = (w - first) * 64;
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(s, int64_t(valid) * 4), (lds_void*)(lds + q), 4, (q + L) * 4, 0, 0,
+                                           0);
+}
+
+__device__ __forceinline__ i32x8 load_codes(const uint8_t* lds, int row, int kk, int half) {
+  const u32x4 lo = *reinterpret_cast<const u32x4*>(lds + swz(row, kk * 4 + half));
+  const u32x4 hi = *reinterpret_cast<const u32x4*>(lds + swz(row, kk * 4 + 2 + half));
+  return i32x8{int(lo[0]), int(lo[1]), int(lo[2]), int(lo[3]), int(hi[0]), int(hi[1]), int(hi[2]), int(hi[3])};
+}
+
+// E8M0 127 is 2^0: the codes' products as they are.
+__device__ __forceinline__ f32x16 mfma_codes(const i32x8& a, const i32x8& b, const f32x16& c) {
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, 127, 0, 127);
+}
+
+template <class S, bool GRAD>
+__global__ __launch_bounds__(S::kWaves * 64) void k_block_product(ProductArgs p) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  typename S::Lds& sm = *reinterpret_cast<typename S::Lds*>(smem);
+  const int lane = threadIdx.x & 63, w = wave_id(), wa = w / S::WB, wb = w % S::WB, half = lane >> 5, l32 = lane & 31;
+  const int id = xcd_logical_id();
+  GroupTile gt;
+  int n0, k0 = 0, ksteps, valid_b;
+  const uint8_t *a, *b;
+  const float *as, *bs;
+  if constexpr (GRAD) {
+    const int per = p.tiles_n * p.tiles_k, g = id / per, t = id % per;
+    gt = find_group(p.rg, g);
+    int tn, tk;
+    tile_coords(t, p.tiles_n, p.tiles_k, tn, tk);
+    n0 = tn * S::kA;
+    k0 = tk * S::kB;
+    ksteps = (gt.rows + kBlk - 1) / kBlk;
+    if (ksteps == 0 && p.accumulate) return;
+    valid_b = min(S::kB, p.k - k0);
+    a = p.a + n0 * p.stride_a + gt.pad0;
+    b = p.b + k0 * p.stride_b + gt.pad0;
+    as = p.as + (gt.pad0 / kBlk) * p.n + n0;
+    bs = p.bs + (gt.pad0 / kBlk) * p.k + k0;
+  } else {
+    const int tn = id % p.tiles_n;
+    gt = find_group_tile(p.rg, id / p.tiles_n, S::kB);
+    if (gt.group < 0) return;
+    n0 = tn * S::kA;
+    ksteps = p.kb;
+    valid_b = gt.rows;
+    a = p.a + (int64_t(gt.group) * p.n + n0) * p.stride_a;
+    b = p.b + gt.row0 * p.stride_b;
+    const int blocks = (p.n + kBlk - 1) / kBlk;
+    as = p.as + (int64_t(gt.group) * blocks + min((n0 + wa * S::FA * 32) / kBlk, blocks - 1)) * p.kb;
+    bs = p.bs + gt.row0;
+  }
+  const int valid_a = min(S::kA, p.n - n0);
+  // (the last row ends at its own last block, which is all that is read of it)
+  const auto span = [&](int rows, int64_t stride) { return (rows - 1) * stride + int64_t(ksteps) * kBlk; };
+  const __amdgpu_buffer_rsrc_t ra = make_rsrc(a, span(valid_a, p.stride_a)), rb = make_rsrc(b, span(valid_b, p.stride_b));
+  const int64_t bs_step = GRAD ? p.k : p.rg.rows;
+  const auto issue = [&](int kt, int buf) {
+    issue_rows<S::kA, S::kWaves>(ra, sm.a[buf], int(p.stride_a), kt * kBlk, w);
+    issue_rows<S::kB, S::kWaves>(rb, sm.b[buf], int(p.stride_b), kt * kBlk, w);
+    issue_scales<S::kB>(bs + kt * bs_step, valid_b, sm.bs[buf], w, 0);
+    if (GRAD) issue_scales<S::kA>(as + int64_t(kt) * p.n, valid_a, sm.as[buf], w, S::kB / 64);
+  };
+  f32x16 acc[S::FA][S::FB];
+#pragma unroll
+  for (int i = 0; i < S::FA; ++i)
+#pragma unroll
+    for (int j = 0; j < S::FB; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+  if (ksteps > 0) issue(0, 0);
+  for (int kt = 0; kt < ksteps; ++kt) {
+    const int cur = kt & 1;
+    wait_vmem();
+    __syncthreads();
+    if (kt + 1 < ksteps) issue(kt + 1, cur ^ 1);
+    const float wscale = GRAD ? 1.f : as[kt];
+    i32x8 fa[S::FA][2];
+#pragma unroll
+    for (int i = 0; i < S::FA; ++i)
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) fa[i][kk] = load_codes(sm.a[cur], (wa * S::FA + i) * 32 + l32, kk, half);
+#pragma unroll
+    for (int j = 0; j < S::FB; ++j) {
+      const int col = (wb * S::FB + j) * 32 + l32;
+      const i32x8 fb0 = load_codes(sm.b[cur], col, 0, half), fb1 = load_codes(sm.b[cur], col, 1, half);
+      const float s = sm.bs[cur][col] * wscale;
+#pragma unroll
+      for (int i = 0; i < S::FA; ++i) {
+        f32x16 part;
+#pragma unroll
+        for (int v = 0; v < 16; ++v) part[v] = 0.f;
+        part = mfma_codes(fa[i][0], fb0, part);
+        part = mfma_codes(fa[i][1], fb1, part);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if constexpr (GRAD) {
+            const f32x4 sa = *reinterpret_cast<const f32x4*>(sm.as[cur] + (wa * S::FA + i) * 32 + 8 * q + 4 * half);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) acc[i][j][4 * q + u] = fmaf(part[4 * q + u], s * sa[u], acc[i][j][4 * q + u]);
+          } else {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) acc[i][j][4 * q + u] = fmaf(part[4 * q + u], s, acc[i][j][4 * q + u]);
+          }
+        }
+      }
+    }
+  }
+  const int tid = tile_tid(), el = tid & 31, eh = (tid >> 5) & 1;
+  if constexpr (GRAD) {
+    float* out = static_cast<float*>(p.out) + (int64_t(gt.group) * p.n + n0) * p.k + k0;
+#pragma unroll
+    for (int i = 0; i < S::FA; ++i)
+#pragma unroll
+      for (int j = 0; j < S::FB; ++j) {
+        const int c = (wb * S::FB + j) * 32 + el;
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+          const int r = (wa * S::FA + i) * 32 + 8 * (v >> 2) + 4 * eh + (v & 3);
+          if (r < valid_a && c < valid_b) {
+            float* o = out + int64_t(r) * p.k + c;
+            *o = p.accumulate ? *o + acc[i][j][v] : acc[i][j][v];
+          }
+        }
+      }
+  } else {
+    const bool whole = p.out_stride % 4 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
+#pragma unroll
+    for (int j = 0; j < S::FB; ++j) {
+      const int r = (wb * S::FB + j) * 32 + el;
+      if (r >= valid_b) continue;
+      const int64_t at = (gt.row0 + r) * p.out_stride + n0;
+#pragma unroll
+      for (int i = 0; i < S::FA; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int c = (wa * S::FA + i) * 32 + 8 * q + 4 * eh;
+          const f32x16& y = acc[i][j];
+          if (p.bf16) {
+            uint16_t* o = static_cast<uint16_t*>(p.out) + at + c;
+            if (whole && c + 4 <= valid_a) {
+              *reinterpret_cast<uint2*>(o) = uint2{pack_bf2(y[4 * q], y[4 * q + 1]), pack_bf2(y[4 * q + 2], y[4 * q + 3])};
+            } else {
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                if (c + u < valid_a) o[u] = f2bf(y[4 * q + u]);
+            }
+          } else {
+            float* o = static_cast<float*>(p.out) + at + c;
+            if (whole && c + 4 <= valid_a) {
+              *reinterpret_cast<f32x4*>(o) = f32x4{y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]};
+            } else {
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                if (c + u < valid_a) o[u] = y[4 * q + u];
+            }
+          }
+        }
+    }
+  }
+}
+
+// A dynamic shared memory size above 64 KB has to be allowed once for each kernel and device.
+template <class S, bool GRAD>
+hipError_t launch_product(const ProductArgs& p, int64_t tiles, hipStream_t s) {
+  static std::atomic<bool> done[kMaxDevices];
+  const void* f = reinterpret_cast<const void*>(k_block_product<S, GRAD>);
+  constexpr int bytes = int(sizeof(typename S::Lds));
+  const hipError_t e =
+      once_per_device(done, [&] { return hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, bytes); });
+  if (e != hipSuccess) return e;
+  k_block_product<S, GRAD><<<unsigned(tiles), S::kWaves * 64, bytes, s>>>(p);
+  return hipGetLastError();
+}
+
+using Mid = Shape<2, 2, 2, 2>;   // 128 x 128
+
+}  // namespace
+
+hipError_t launch_block_gemm(const mok_block_desc& d, const uint8_t* x, const float* xs, const uint8_t* w,
+                             const float* ws, const int32_t* offsets, void* out, hipStream_t s) {
+  if (d.rows == 0) return hipSuccess;
+  ProductArgs p{};
+  p.kb = int(cdiv(d.k, kBlk));
+  p.a = w;
+  p.as = ws;
+  p.b = x;
+  p.bs = xs;
+  p.out = out;
+  p.rg = RowGroups{offsets, d.rows, d.groups};
+  p.out_stride = d.stride;
+  p.stride_a = p.stride_b = int64_t(p.kb) * kBlk;
+  p.n = d.n;
+  p.k = d.k;
+  p.bf16 = d.elem == MOK_ELEM_BF16;
+  using S = Mid;
+  p.tiles_n = int(cdiv(d.n, S::kA));
+  return launch_product<S, false>(p, group_tiles_max(d.rows, d.groups, S::kB) * p.tiles_n, s);
+}
+
+hipError_t launch_block_wgrad(const mok_block_desc& d, const uint8_t* dy, const float* dys, const uint8_t* x,
+                              const float* xs, const int32_t* offsets, float* dw, bool accumulate, hipStream_t s) {
+  ProductArgs p{};
+  p.a = dy;
+  p.as = dys;
+  p.b = x;
+  p.bs = xs;
+  p.out = dw;
+  p.rg = RowGroups{offsets, d.rows, d.groups};
+  p.stride_a = p.stride_b = block_padded_rows(d.rows, d.groups);
+  p.n = d.n;
+  p.k = d.k;
+  p.accumulate = accumulate;
+  using S = Mid;
+  p.tiles_n = int(cdiv(d.n, S::kA));
+  p.tiles_k = int(cdiv(d.k, S::kB));
+  return launch_product<S, true>(p, int64_t(d.groups) * p.tiles_n * p.tiles_k, s);
+}
+
+}  // namespace mok

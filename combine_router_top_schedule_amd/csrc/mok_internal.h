@@ -464,6 +464,17 @@ hipError_t launch_sumsq(int count, const mok_sumsq_tensor* t, bool bf16, double*
                         hipStream_t s);
 hipError_t launch_adamw(int count, const mok_adamw_tensor* t, const mok_adamw_config& c, hipStream_t s);
 
+// Block-scaled FP8 (k_bquant.hip, k_bgemm.hip); arguments are checked by mok_block.cpp.
+inline int64_t block_padded_rows(int64_t rows, int groups) { return (rows + int64_t(groups) * 127) / 128 * 128; }
+hipError_t launch_block_quantize(const mok_block_desc& d, const void* x, const int32_t* offsets, uint8_t* codes,
+                                 float* scales, uint8_t* codes_t, float* scales_t, hipStream_t s);
+hipError_t launch_block_quantize_weights(const mok_block_desc& d, const void* w, uint8_t* codes, float* scales,
+                                         uint8_t* codes_t, float* scales_t, hipStream_t s);
+hipError_t launch_block_gemm(const mok_block_desc& d, const uint8_t* x, const float* xs, const uint8_t* w,
+                             const float* ws, const int32_t* offsets, void* out, hipStream_t s);
+hipError_t launch_block_wgrad(const mok_block_desc& d, const uint8_t* dy, const float* dys, const uint8_t* x,
+                              const float* xs, const int32_t* offsets, float* dw, bool accumulate, hipStream_t s);
+
 int device_cus();
 
 // One-time set-up per device (kernel attributes are set for the device that is current when

@@ -565,6 +565,64 @@ typedef struct {
 mok_status mok_adamw(int32_t num_tensors, const mok_adamw_tensor* tensors,
                      const mok_adamw_config* config, void* stream);
 
+/* ---- linear maps of sorted rows in block-scaled FP8 ----------------------------------------------
+ *
+ * E4M3 codes with one fp32 scale for each block of 128 along the axis that a product sums over. A block x is
+ * quantised as amax = max(max |x|, 2^-100), scale = amax / 448, code = e4m3(x * (448 / amax)), nearest even; a NaN stays
+ * NaN where it stands, an infinity makes its own code NaN and its block's scale infinite (so all of it NaN in a product).
+ *
+ * Rows are sorted by group (expert): group g is the rows offsets[g] .. offsets[g + 1] - 1, offsets_dev int32 [groups + 1]
+ * on the device (the offsets of a schedule table are such). Rows before the first or behind the last group belong to
+ * none. Offsets are clamped to 0..rows and one smaller than an earlier one counts as that one. NULL with groups == 1: all
+ * rows.
+ *
+ * Layouts, up(v) = v rounded up to a multiple of 128, R rows, G groups, P = mok_block_padded_rows(R, G):
+ *   row codes      uint8 [R][up(K)], zeros past K;       scales fp32 [up(K) / 128][R]
+ *   column codes   uint8 [K][P]: each group's rows turned to columns, beginning at a multiple of 128 (behind the
+ *                  groups before it, each rounded up to 128), zeros up to the next one; scales fp32 [P / 128][K].
+ *                  What lies behind the last group is neither written nor read.
+ *   weight codes   uint8 [G][N][up(K)], zeros past K;    scales fp32 [G][up(N) / 128][up(K) / 128], blocks of 128 x 128
+ *   transposed     the weight codes of [G][K][N]: same values, scales transposed
+ * Codes are 16-byte aligned, scales and offsets 4-byte. */
+typedef struct {
+  int64_t rows;      /* R; 0..2^28 - 1, and at most 2^22 where column codes are written or read         */
+  int64_t stride;    /* elements from one row of the unquantised operand to the next; >= its columns    */
+  int32_t groups;    /* G; 1..1024                                                                     */
+  int32_t n;         /* N; 1..2^20                                                                     */
+  int32_t k;         /* K; 1..2^20                                                                     */
+  int32_t elem;      /* mok_elem of the unquantised operand                                            */
+} mok_block_desc;
+
+/* P: columns that column codes need for any offsets; a multiple of 128. -1 for arguments out of range. */
+int64_t mok_block_padded_rows(int64_t rows, int32_t groups);
+
+/* Quantises rows x_dev [R][K] (`stride` apart, aligned to their element; n unused): codes_dev and scales_dev (both
+ * or NULL) for every row, codes_t_dev and scales_t_dev (both or NULL) for the rows of groups, which alone
+ * take part in a weight gradient. */
+mok_status mok_block_quantize(const mok_block_desc* desc, const void* x_dev, const int32_t* offsets_dev,
+                              uint8_t* codes_dev, float* scales_dev, uint8_t* codes_t_dev, float* scales_t_dev,
+                              void* stream);
+
+/* Quantises weights w_dev [G][N][K], contiguous and aligned to their element (rows and stride unused). codes_t_dev and
+ * scales_t_dev, both or NULL, get the transposed ones, which the input gradient needs: the same rounding. */
+mok_status mok_block_quantize_weights(const mok_block_desc* desc, const void* w_dev, uint8_t* codes_dev,
+                                      float* scales_dev, uint8_t* codes_t_dev, float* scales_t_dev, void* stream);
+
+/* out[r][n] = sum_k x[r][k] w[g][n][k] for every row r of every group g, of codes times scales, summed in fp32 and rounded
+ * once to `elem`; rows in no group are left as they are. x: row codes and scales; w: weight codes and scales; out_dev rows
+ * are `stride` apart. With the output gradient's row codes and the transposed weights (n and k change places) it
+ * is the input gradient. */
+mok_status mok_block_gemm(const mok_block_desc* desc, const uint8_t* x_dev, const float* x_scales_dev,
+                          const uint8_t* w_dev, const float* w_scales_dev, const int32_t* offsets_dev, void* out_dev,
+                          void* stream);
+
+/* Weight gradient dw[g][n][k] = sum over the rows r of group g of dy[r][n] x[r][k], from column codes and scales of dy
+ * [R][N] and x [R][K] (stride and elem unused). dw_dev fp32 [G][N][K], overwritten (zero for a group without rows), or
+ * with accumulate added to. */
+mok_status mok_block_wgrad(const mok_block_desc* desc, const uint8_t* dy_t_dev, const float* dy_scales_dev,
+                           const uint8_t* x_t_dev, const float* x_scales_dev, const int32_t* offsets_dev,
+                           float* dw_dev, int32_t accumulate, void* stream);
+
 /* Measurement hook (benchmarks only): from the next call on, the library records `before`
  * (a hipEvent_t) on the call's stream right before it launches the kernel `kernel` and `after`
  * right after it; MOK_TRACE_NONE (or NULL events) switches it off. Kernels:
