@@ -59,6 +59,7 @@ MOK_ELEM_F32, MOK_ELEM_BF16 = 0, 1
 MOK_SCORE_SOFTMAX, MOK_SCORE_SIGMOID = 0, 1
 MOK_GROUP_MAX, MOK_GROUP_TOP2 = 0, 1
 MOK_STATE_F32, MOK_STATE_MX8 = 0, 1
+MOK_ADJUST_RMS, MOK_ADJUST_SPECTRAL, MOK_ADJUST_NONE = 0, 1, 2
 
 
 class MokRouteDesc(ctypes.Structure):
@@ -84,6 +85,26 @@ class MokAdamwConfig(ctypes.Structure):
                 ("max_norm", ctypes.c_double), ("step", ctypes.c_int64), ("seed", ctypes.c_uint32),
                 ("grad_elem", ctypes.c_int32), ("param_elem", ctypes.c_int32),
                 ("state", ctypes.c_int32), ("sumsq_dev", _P), ("lr_dev", _P), ("step_dev", _P)]
+
+
+class MokNewtonSchulz(ctypes.Structure):
+    _fields_ = [("eps", ctypes.c_double), ("steps", ctypes.c_int32), ("coefficients", ctypes.c_float * 48)]
+
+
+class MokMuonTensor(ctypes.Structure):
+    _fields_ = [("p", _P), ("copy", _P), ("g", _P), ("m", _P), ("batch", ctypes.c_int32),
+                ("rows", ctypes.c_int32), ("cols", ctypes.c_int32)]
+
+
+class MokMuonConfig(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("momentum", ctypes.c_double), ("weight_decay", ctypes.c_double),
+                ("max_norm", ctypes.c_double), ("nesterov", ctypes.c_int32), ("adjust", ctypes.c_int32),
+                ("grad_elem", ctypes.c_int32), ("ns", MokNewtonSchulz), ("sumsq_dev", _P), ("lr_dev", _P)]
+
+
+class MokOrthogonalizeTensor(ctypes.Structure):
+    _fields_ = [("src", _P), ("out", _P), ("batch", ctypes.c_int32), ("rows", ctypes.c_int32),
+                ("cols", ctypes.c_int32)]
 
 
 class MokBlockDesc(ctypes.Structure):
@@ -152,6 +173,11 @@ _SIGS = {
     "mok_sumsq_ws_size": (ctypes.c_int, [ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)]),
     "mok_grad_sumsq": (ctypes.c_int, [ctypes.c_int32, _P, ctypes.c_int32, _P, _P, _P]),
     "mok_adamw": (ctypes.c_int, [ctypes.c_int32, _P, ctypes.POINTER(MokAdamwConfig), _P]),
+    "mok_muon_ws_size": (ctypes.c_int, [ctypes.c_int32, _P, ctypes.POINTER(ctypes.c_size_t)]),
+    "mok_muon": (ctypes.c_int, [ctypes.c_int32, _P, ctypes.POINTER(MokMuonConfig), _P, _P]),
+    "mok_orthogonalize_ws_size": (ctypes.c_int, [ctypes.c_int32, _P, ctypes.POINTER(ctypes.c_size_t)]),
+    "mok_orthogonalize": (ctypes.c_int, [ctypes.c_int32, _P, ctypes.c_int32, ctypes.POINTER(MokNewtonSchulz), _P,
+                                         _P]),
     "mok_block_padded_rows": (ctypes.c_int64, [ctypes.c_int64, ctypes.c_int32]),
     "mok_block_quantize": (ctypes.c_int, [ctypes.POINTER(MokBlockDesc), _P, _P, _P, _P, _P, _P, _P]),
     "mok_block_quantize_weights": (ctypes.c_int, [ctypes.POINTER(MokBlockDesc), _P, _P, _P, _P, _P, _P]),
@@ -669,6 +695,159 @@ def mok_adamw(plan: AdamwPlan, lr, step, beta1: float = 0.9, beta2: float = 0.99
     c.seed = seed & 0xFFFFFFFF
     with _on_device(plan.dev, stream) as s:
         _check("mok_adamw", lib().mok_adamw(len(plan.table), plan.table, ctypes.byref(c), s))
+
+
+# ------------------------------------------------------------------------ Muon
+
+NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)
+"""Coefficients of a step that takes singular values of 0..1 towards 1, small ones 3.4 times a step."""
+
+
+def _newton_schulz(eps, steps, coefficients) -> MokNewtonSchulz:
+    rows = list(coefficients)
+    if rows and not hasattr(rows[0], "__len__"):
+        rows = [tuple(rows)] * steps
+    if len(rows) != steps or any(len(r) != 3 for r in rows):
+        raise ValueError(f"coefficients are (a, b, c), or {steps} of them")
+    if not 1 <= steps <= 16:
+        raise ValueError(f"steps are 1..16, not {steps}")
+    ns = MokNewtonSchulz(eps, steps)
+    ns.coefficients[:3 * steps] = [float(c) for r in rows for c in r]
+    return ns
+
+
+def _matrices(t, name: str):
+    """(batch, rows, cols) of a tensor [..][rows][cols]."""
+    if t.dim() < 2:
+        raise ValueError(f"{name} must be matrices [..][rows][cols], not {tuple(t.shape)}")
+    batch = 1
+    for n in t.shape[:-2]:
+        batch *= n
+    return batch, t.shape[-2], t.shape[-1]
+
+
+def _no_overlap(spans):
+    """spans: (address, end, read only, name). What is written overlaps nothing else; what is read may be given twice."""
+    spans.sort()
+    read_end = written_end = 0   # the furthest ends so far
+    for a, end, read, name in spans:
+        if a < written_end or a < read_end and not read:
+            raise ValueError(f"memory of {name} is shared with another tensor")
+        if read:
+            read_end = max(read_end, end)
+        else:
+            written_end = max(written_end, end)
+
+
+class MuonPlan:
+    """The tensors of a mok_muon call, checked once, and scratch for it: lists of equal length of float32 parameters
+    [..][rows][cols], gradients (float32 or bfloat16), momenta (float32) and bfloat16 copies (None in the place of a
+    parameter that has none). Calls that may overlap in time need plans of their own."""
+
+    def __init__(self, p, g, m, copy=None):
+        torch = _tch()
+        if not p:
+            raise ValueError("no tensors")
+        lists = dict(p=p, g=g, m=m, copy=copy)
+        self.keep = {k: list(ts) for k, ts in lists.items() if ts is not None}
+        for name, ts in self.keep.items():
+            if len(ts) != len(p):
+                raise ValueError(f"{name} has {len(ts)} tensors, p {len(p)}")
+        self.dev, self.grad = _device_of(p[0]), _elem(g[0], "a gradient")
+        types = dict(p=torch.float32, g=g[0].dtype, m=torch.float32, copy=torch.bfloat16)
+        at, spans = {}, []
+        for name, ts in self.keep.items():
+            at[name] = []
+            for t, like in zip(ts, p):
+                if t is None and name == "copy":
+                    at[name].append(None)
+                    continue
+                if t.shape != like.shape:
+                    raise ValueError(f"{name} must be {tuple(like.shape)}, not {tuple(t.shape)}")
+                a = _want(t, name, types[name], like.numel(), self.dev)
+                at[name].append(a)
+                if t.numel():
+                    spans.append((a, a + t.numel() * t.element_size(), name == "g", name))
+        _no_overlap(spans)
+        none = [None] * len(p)
+        self.table = (MokMuonTensor * len(p))(*[
+            (pp, c, gg, mm, *_matrices(t, "p")) for pp, c, gg, mm, t in zip(
+                at["p"], at.get("copy", none), at["g"], at["m"], p)])
+        n = ctypes.c_size_t()
+        _check("mok_muon_ws_size", lib().mok_muon_ws_size(len(p), self.table, ctypes.byref(n)))
+        self.ws = torch.empty(int(n.value), dtype=torch.uint8, device=p[0].device)
+
+
+def muon_plan(p, g, m, copy=None) -> MuonPlan:
+    return MuonPlan(p, g, m, copy)
+
+
+def mok_muon(plan: MuonPlan, lr, momentum: float = 0.95, nesterov: bool = True, weight_decay: float = 0.0,
+             eps: float = 1e-7, adjust: str = "rms", steps: int = 5, coefficients=NEWTON_SCHULZ, sumsq=None,
+             max_norm: Optional[float] = None, stream=None):
+    """One Muon step over the plan's tensors, in place. adjust: "rms" scales the orthogonalised update by 0.2
+    sqrt(max(rows, cols)), "spectral" by sqrt(max(1, rows / cols)), "none" not at all. `lr` may be a device tensor
+    (float64 [1], read when the step runs; negative or not finite changes nothing). `sumsq` and `max_norm` as
+    in mok_adamw."""
+    torch = _tch()
+    c = MokMuonConfig(momentum=momentum, weight_decay=weight_decay, nesterov=int(nesterov), grad_elem=plan.grad,
+                      adjust={"rms": MOK_ADJUST_RMS, "spectral": MOK_ADJUST_SPECTRAL, "none": MOK_ADJUST_NONE}[adjust],
+                      ns=_newton_schulz(eps, steps, coefficients),
+                      max_norm=float("inf") if max_norm is None else max_norm)
+    if isinstance(lr, torch.Tensor):
+        c.lr_dev = _want(lr, "lr", torch.float64, 1, plan.dev)
+    else:
+        c.lr = lr
+    if sumsq is not None:
+        if not isinstance(sumsq, torch.Tensor):
+            raise ValueError("sumsq is a device tensor")
+        c.sumsq_dev = _want(sumsq, "sumsq", torch.float64, 1, plan.dev)
+    elif max_norm is not None:
+        raise ValueError("max_norm needs sumsq, the squared norm of all gradients")
+    with _on_device(plan.dev, stream) as s:
+        _check("mok_muon", lib().mok_muon(len(plan.table), plan.table, ctypes.byref(c), plan.ws.data_ptr(), s))
+
+
+class OrthogonalizePlan:
+    """The matrices of a mok_orthogonalize call, checked once, and scratch for it: sources (float32 or bfloat16, of one
+    type) [..][rows][cols] and bfloat16 outputs of the same shapes."""
+
+    def __init__(self, src, out):
+        torch = _tch()
+        if not src:
+            raise ValueError("no tensors")
+        if len(src) != len(out):
+            raise ValueError(f"out has {len(out)} tensors, src {len(src)}")
+        self.keep, self.dev, self.elem = (list(src), list(out)), _device_of(src[0]), _elem(src[0], "a source")
+        rows, spans = [], []
+        for a, b in zip(src, out):
+            if a.shape != b.shape:
+                raise ValueError(f"out must be {tuple(a.shape)}, not {tuple(b.shape)}")
+            at = [_want(t, name, dtype, a.numel(), self.dev)
+                  for t, name, dtype in ((a, "src", src[0].dtype), (b, "out", torch.bfloat16))]
+            rows.append((*at, *_matrices(a, "src")))
+            if a.numel():
+                spans += [(at[0], at[0] + a.numel() * a.element_size(), True, "src"),
+                          (at[1], at[1] + b.numel() * 2, False, "out")]
+        _no_overlap(spans)
+        self.table = (MokOrthogonalizeTensor * len(src))(*rows)
+        n = ctypes.c_size_t()
+        _check("mok_orthogonalize_ws_size", lib().mok_orthogonalize_ws_size(len(src), self.table, ctypes.byref(n)))
+        self.ws = torch.empty(int(n.value), dtype=torch.uint8, device=src[0].device)
+
+
+def orthogonalize_plan(src, out) -> OrthogonalizePlan:
+    return OrthogonalizePlan(src, out)
+
+
+def mok_orthogonalize(plan: OrthogonalizePlan, eps: float = 1e-7, steps: int = 5, coefficients=NEWTON_SCHULZ,
+                      stream=None):
+    """Every output of the plan = its source, orthogonalised by `steps` Newton-Schulz steps. coefficients: (a, b, c) of
+    every step, or one such triple for each."""
+    ns = _newton_schulz(eps, steps, coefficients)
+    with _on_device(plan.dev, stream) as s:
+        _check("mok_orthogonalize", lib().mok_orthogonalize(len(plan.table), plan.table, plan.elem, ctypes.byref(ns),
+                                                            plan.ws.data_ptr(), s))
 
 
 # ------------------------------------------------------------------------ linear maps in block-scaled FP8

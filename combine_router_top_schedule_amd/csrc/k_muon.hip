@@ -1,0 +1,534 @@
+// Muon: momentum, and its update orthogonalised by Newton-Schulz products.
+//
+// For a matrix u (the momentum, or with Nesterov the gradient plus mu times it), with X on its smaller side
+// m <= n and X_0 = u / (|u|_F + eps), each step does
+//   A = X X^T,   B = b A + c A A,   X <- a X + B X,
+// an odd polynomial of X's singular values that takes them all towards 1. A step is three launches of products:
+// A and A A are symmetric, so only the tiles on and below the diagonal are computed and both halves written; the last
+// step's product ends in the parameters' update instead of X. All matrices of a call go through the same
+// launches, whatever their shapes: a workgroup finds its matrix by the prefix sums of their tile counts.
+//
+// Precision. X is kept in 22 bits as the sum of two fp16 matrices, hi + lo, times a power of two near sqrt(n) that keeps
+// both in fp16's normal range; a X is formed from both, the products take hi, A and B in fp16 with fp32 sums. Kept in
+// fp16 alone, X's rounding drowns the small singular values of a gradient with a few large ones: 64-bit against
+// 11-bit X differ by 1.3e-2 of the result there (512 x 1792, rank 129 plus 1 % noise), with lo by 8e-4; bf16 everywhere by 1e-1. On the
+// matrix cores fp16 is as fast as bf16.
+#include <algorithm>
+#include <cmath>
+
+#include "k_gemm.h"
+
+namespace mok {
+namespace {
+
+typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
+typedef __attribute__((ext_vector_type(4))) _Float16 f16x4;
+
+constexpr int kMuItems = 40;       // tensors (or parts of their batches) that a launch takes (of 4 KB of arguments)
+constexpr int kMuParts = 256;      // partial sums of a matrix's norm at most
+constexpr int kMuPad = 128;        // matrices are padded to multiples of this with zeros, which stay zeros
+
+struct MuItem {
+  const void* g;      // gradient, or the source
+  float* m;           // momentum; null: orthogonalise g
+  void* p;            // parameters, or the bf16 output
+  uint16_t* copy;
+  uint8_t* ws;        // of the part's first matrix
+  int32_t e0, batch;  // the part's matrices: e0 .. e0 + batch - 1 of the tensor
+  int32_t rows, cols;
+  float adjust;
+};
+
+struct MuArgs {
+  MuItem item[kMuItems];
+  int32_t first[kMuItems + 1];   // tiles (or chunks) before item t
+  int32_t count;
+  int32_t nesterov, gbf;
+  float mu, eps;
+  float a, b, c;                 // the step's coefficients
+  int32_t flip;                  // the step's number, odd or even: which operand buffer holds X
+  double lr, weight_decay, max_norm;
+  const double* sumsq;
+  const double* lr_dev;
+};
+
+// A matrix's buffers in the workspace. `s` is X as its parameters lie ([rows][cols], padded), `t` its transpose. The
+// product with B reads `t` (`s` where rows > cols) while its tiles are written, so that one has a second buffer.
+struct MuBuffers {
+  int64_t plane, gram;           // bytes of X and of A
+  int rows, cols, m, n;          // padded; m = min, n = max
+  __host__ __device__ MuBuffers(int r, int c) {
+    rows = int(align_up(r, kMuPad));
+    cols = int(align_up(c, kMuPad));
+    m = rows < cols ? rows : cols;
+    n = rows < cols ? cols : rows;
+    plane = int64_t(rows) * cols * 2;
+    gram = int64_t(m) * m * 2;
+  }
+  __host__ __device__ int64_t bytes() const { return 4 * plane + 2 * gram + kMuParts * 8; }
+  __device__ bool turned(const MuItem& it) const { return it.rows > it.cols; }
+  __device__ _Float16* s(uint8_t* ws, bool turn, int flip) const { return at(ws, turn && flip ? 3 * plane : 0); }
+  __device__ _Float16* t(uint8_t* ws, bool turn, int flip) const { return at(ws, !turn && flip ? 3 * plane : 2 * plane); }
+  __device__ _Float16* lo(uint8_t* ws) const { return at(ws, plane); }
+  __device__ _Float16* a(uint8_t* ws) const { return at(ws, 4 * plane); }
+  __device__ _Float16* b(uint8_t* ws) const { return at(ws, 4 * plane + gram); }
+  __device__ double* parts(uint8_t* ws) const { return reinterpret_cast<double*>(ws + 4 * plane + 2 * gram); }
+  __device__ static _Float16* at(uint8_t* p, int64_t off) { return reinterpret_cast<_Float16*>(p + off); }
+};
+
+// The power of two that X is stored with: near sqrt(n), so that the result's elements are near 1.
+__host__ __device__ inline float mu_scale(int rows, int cols) {
+  int n = rows > cols ? rows : cols, e = 0;
+  while (n > 1) n >>= 2, ++e;
+  return float(1 << e);
+}
+
+// The item of workgroup c.
+__device__ __forceinline__ int find_item(const MuArgs& a, int c) {
+  const int lane = threadIdx.x & 63;
+  const bool in = lane < a.count && a.first[min(lane, kMuItems)] <= c;
+  return __builtin_amdgcn_readfirstlane(__popcll(__ballot(in)) - 1);
+}
+
+// A step whose gradients' norm is not finite, or whose rate on the device is negative or not finite, changes nothing.
+__device__ __forceinline__ bool left_out(const MuArgs& a) {
+  if (a.sumsq && !isfinite(*a.sumsq)) return true;
+  return a.lr_dev && !(*a.lr_dev >= 0.0 && isfinite(*a.lr_dev));
+}
+__device__ __forceinline__ float clip_factor(const MuArgs& a) {
+  return a.sumsq ? float(fmin(1.0, a.max_norm / sqrt(*a.sumsq))) : 1.f;
+}
+
+__device__ __forceinline__ float element(const void* p, bool bf, int64_t i) {
+  return bf ? bf2f(static_cast<const uint16_t*>(p)[i]) : static_cast<const float*>(p)[i];
+}
+
+// ---- momentum and norm --------------------------------------------------------------------------
+__host__ __device__ inline int64_t mu_chunk(int64_t size) {   // elements of a partial sum
+  const int64_t c = align_up(cdiv(size, kMuParts), 1024);
+  return c < 4096 ? 4096 : c;
+}
+
+// One partial sum of |u|^2 a workgroup, in fp64; with a momentum, also its update.
+__global__ __launch_bounds__(256) void k_muon_norm(MuArgs a) {
+  if (left_out(a)) return;
+  const int t = find_item(a, blockIdx.x);
+  const MuItem& it = a.item[t];
+  const int64_t size = int64_t(it.rows) * it.cols, chunk = mu_chunk(size);
+  const int per = int(cdiv(size, chunk)), q = blockIdx.x - a.first[t], e = q / per;
+  const int64_t base = (it.e0 + e) * size, i0 = base + (q % per) * chunk, i1 = min(i0 + chunk, base + size);
+  const float clip = clip_factor(a);
+  const bool bf = a.gbf;
+  double sum = 0;
+  const auto one = [&](int64_t i, float g, float m) {
+    g *= clip;
+    float u = g;
+    if (it.m) {
+      m = m * a.mu + g;
+      u = a.nesterov ? g + a.mu * m : m;
+    }
+    const double d = u;
+    sum = fma(d, d, sum);
+    return m;
+  };
+  for (int64_t i = (i0 & ~int64_t(3)) + threadIdx.x * 4; i < i1; i += 1024) {
+    if (i >= i0 && i + 4 <= i1) {
+      f32x4 g, m = {0.f, 0.f, 0.f, 0.f};
+      if (bf) {
+        const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(it.g) + i);
+        g = f32x4{bf2f(uint16_t(v.x)), bf2f(uint16_t(v.x >> 16)), bf2f(uint16_t(v.y)), bf2f(uint16_t(v.y >> 16))};
+      } else {
+        g = *reinterpret_cast<const f32x4*>(static_cast<const float*>(it.g) + i);
+      }
+      if (it.m) m = *reinterpret_cast<const f32x4*>(it.m + i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) m[j] = one(i + j, g[j], m[j]);
+      if (it.m) *reinterpret_cast<f32x4*>(it.m + i) = m;
+    } else {
+      for (int j = 0; j < 4; ++j)
+        if (i + j >= i0 && i + j < i1) {
+          const float m = one(i + j, element(it.g, bf, i + j), it.m ? it.m[i + j] : 0.f);
+          if (it.m) it.m[i + j] = m;
+        }
+    }
+  }
+  __shared__ double s[4];
+  for (int off = 32; off; off >>= 1) sum += __shfl_xor(sum, off, 64);
+  if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const MuBuffers b(it.rows, it.cols);
+    b.parts(it.ws + e * align_up(b.bytes(), 256))[q % per] = s[0] + s[1] + s[2] + s[3];
+  }
+}
+
+// ---- X_0 ------------------------------------------------------------------------------------------
+// 64 x 64 elements a workgroup, written as they lie and turned, zeros in the padding.
+__global__ __launch_bounds__(256) void k_muon_start(MuArgs a) {
+  if (left_out(a)) return;
+  const int t = find_item(a, blockIdx.x);
+  const MuItem& it = a.item[t];
+  const MuBuffers b(it.rows, it.cols);
+  const int tc = b.cols / 64, per = (b.rows / 64) * tc, q = blockIdx.x - a.first[t], e = q / per;
+  const int r0 = (q % per) / tc * 64, c0 = (q % per) % tc * 64;
+  const int64_t size = int64_t(it.rows) * it.cols;
+  uint8_t* ws = it.ws + e * align_up(b.bytes(), 256);
+  const int parts = int(cdiv(size, mu_chunk(size)));
+  double sum = int(threadIdx.x) < parts ? b.parts(ws)[threadIdx.x] : 0.0;
+  __shared__ double s[4];
+  for (int off = 32; off; off >>= 1) sum += __shfl_xor(sum, off, 64);
+  if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  const double norm = sqrt(s[0] + s[1] + s[2] + s[3]) + a.eps;
+  const float clip = clip_factor(a), f = float(double(mu_scale(it.rows, it.cols)) / norm);
+  __shared__ _Float16 tile[64][66];
+  const bool turn = b.turned(it);
+  _Float16 *hs = b.s(ws, turn, 0), *lo = b.lo(ws), *ht = b.t(ws, turn, 0);
+  const int c = threadIdx.x & 63;
+#pragma unroll 4
+  for (int r = threadIdx.x >> 6; r < 64; r += 4) {
+    float u = 0.f;
+    if (r0 + r < it.rows && c0 + c < it.cols) {
+      const int64_t i = (it.e0 + e) * size + int64_t(r0 + r) * it.cols + c0 + c;
+      if (it.m) {
+        const float m = it.m[i];
+        u = a.nesterov ? element(it.g, a.gbf, i) * clip + a.mu * m : m;
+      } else {
+        u = element(it.g, a.gbf, i) * clip;
+      }
+    }
+    const float x = u * f;
+    const _Float16 h = _Float16(x);
+    const int64_t at = int64_t(r0 + r) * b.cols + c0 + c;
+    hs[at] = h;
+    lo[at] = _Float16(x - float(h));
+    tile[r][c] = h;
+  }
+  __syncthreads();
+#pragma unroll 4
+  for (int r = threadIdx.x >> 6; r < 64; r += 4) ht[int64_t(c0 + r) * b.rows + r0 + c] = tile[c][r];
+}
+
+// ---- products -------------------------------------------------------------------------------------
+// WA x WB waves of FA x FB blocks of 32 x 32; both operands' rows have the sum's axis contiguous.
+template <int WA_, int WB_, int FA_, int FB_>
+struct MuShape {
+  static constexpr int WA = WA_, WB = WB_, FA = FA_, FB = FB_;
+  static constexpr int kWaves = WA * WB, kA = WA * FA * 32, kB = WB * FB * 32;
+  struct Lds {
+    uint8_t a[2][kA * kStageRowBytes];
+    uint8_t b[2][kB * kStageRowBytes];
+  };
+};
+
+template <int ROWS, int WAVES>
+__device__ __forceinline__ void issue_f16(__amdgpu_buffer_rsrc_t r, uint8_t* lds, int stride, int kt, int w) {
+  const int L = opaque(int(threadIdx.x) & 63);
+  constexpr int kEach = ROWS / 8 / WAVES;
+#pragma unroll
+  for (int c = 0; c < kEach; ++c) {
+    const int blk = w * kEach + c, chunk = (L & 7) ^ (L >> 3) ^ (blk & 1);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(lds + blk * 8 * kStageRowBytes), 16,
+                                             (blk * 8 + (L >> 3)) * stride + kt * kStageRowBytes + chunk * 16, 0, 0, 0);
+  }
+}
+
+// acc = A B^T over k halves (a multiple of 128) of rows of `stride` halves; rows past na, nb count as zeros.
+template <class S>
+__device__ __forceinline__ void tile_f16(typename S::Lds& sm, const _Float16* a, int na, const _Float16* b, int nb, int k,
+                                         f32x16 (&acc)[S::FA][S::FB]) {
+  const int lane = threadIdx.x & 63, w = wave_id(), wa = w / S::WB, wb = w % S::WB, half = lane >> 5, l32 = lane & 31;
+#pragma unroll
+  for (int i = 0; i < S::FA; ++i)
+#pragma unroll
+    for (int j = 0; j < S::FB; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+  const int stride = k * 2, ksteps = stride / kStageRowBytes;
+  const __amdgpu_buffer_rsrc_t ra = make_rsrc(a, int64_t(na) * stride), rb = make_rsrc(b, int64_t(nb) * stride);
+  issue_f16<S::kA, S::kWaves>(ra, sm.a[0], stride, 0, w);
+  issue_f16<S::kB, S::kWaves>(rb, sm.b[0], stride, 0, w);
+  for (int kt = 0; kt < ksteps; ++kt) {
+    const int cur = kt & 1;
+    wait_vmem();
+    __syncthreads();
+    if (kt + 1 < ksteps) {
+      issue_f16<S::kA, S::kWaves>(ra, sm.a[cur ^ 1], stride, kt + 1, w);
+      issue_f16<S::kB, S::kWaves>(rb, sm.b[cur ^ 1], stride, kt + 1, w);
+    }
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      f16x8 fa[S::FA], fb[S::FB];
+#pragma unroll
+      for (int i = 0; i < S::FA; ++i)
+        fa[i] = *reinterpret_cast<const f16x8*>(sm.a[cur] + swz((wa * S::FA + i) * 32 + l32, kk * 2 + half));
+#pragma unroll
+      for (int j = 0; j < S::FB; ++j)
+        fb[j] = *reinterpret_cast<const f16x8*>(sm.b[cur] + swz((wb * S::FB + j) * 32 + l32, kk * 2 + half));
+#pragma unroll
+      for (int i = 0; i < S::FA; ++i)
+#pragma unroll
+        for (int j = 0; j < S::FB; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+    }
+  }
+}
+
+// Tile number q of the lower triangle, rows first: (0,0), (1,0), (1,1), (2,0), ...
+__device__ __forceinline__ void triangle(int q, int& i, int& j) {
+  i = int((sqrtf(8.f * q + 1.f) - 1.f) * 0.5f);
+  while ((i + 1) * (i + 2) / 2 <= q) ++i;
+  while (i * (i + 1) / 2 > q) --i;
+  j = q - i * (i + 1) / 2;
+}
+
+// SECOND false: A = X X^T; true: B = b A + c A A. Both symmetric: tiles with i >= j, written twice.
+template <class S, bool SECOND>
+__global__ __launch_bounds__(S::kWaves * 64) void k_muon_gram(MuArgs a) {
+  static_assert(S::kA == S::kB, "square tiles");
+  if (left_out(a)) return;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  typename S::Lds& sm = *reinterpret_cast<typename S::Lds*>(smem);
+  const int t = find_item(a, blockIdx.x);
+  const MuItem& it = a.item[t];
+  const MuBuffers b(it.rows, it.cols);
+  const int T = (b.m + S::kA - 1) / S::kA, per = T * (T + 1) / 2, q = blockIdx.x - a.first[t], e = q / per;
+  uint8_t* ws = it.ws + e * align_up(b.bytes(), 256);
+  int ti, tj;
+  triangle(q % per, ti, tj);
+  const bool turn = b.turned(it);
+  const int i0 = ti * S::kA, j0 = tj * S::kA, ni = min(S::kA, b.m - i0), nj = min(S::kA, b.m - j0);
+  const int k = SECOND ? b.m : b.n;
+  const _Float16* x = SECOND ? b.a(ws) : turn ? b.t(ws, turn, a.flip) : b.s(ws, turn, a.flip);
+  f32x16 acc[S::FA][S::FB];
+  tile_f16<S>(sm, x + int64_t(i0) * k, ni, x + int64_t(j0) * k, nj, k, acc);
+  const float scale = mu_scale(it.rows, it.cols), down = 1.f / (scale * scale);
+  const _Float16* old = b.a(ws);
+  _Float16* out = SECOND ? b.b(ws) : b.a(ws);
+  const int tid = tile_tid(), lane = tid & 63, w = tid >> 6, wa = w / S::WB, wb = w % S::WB, half = lane >> 5;
+#pragma unroll
+  for (int i = 0; i < S::FA; ++i)
+#pragma unroll
+    for (int j = 0; j < S::FB; ++j) {
+      const int c = j0 + (wb * S::FB + j) * 32 + (lane & 31);
+      if (c >= j0 + nj) continue;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int r = i0 + (wa * S::FA + i) * 32 + 8 * v + 4 * half;
+        if (r >= i0 + ni) continue;
+        f16x4 y;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          float z = acc[i][j][4 * v + u];
+          z = SECOND ? a.c * z + a.b * float(old[int64_t(r + u) * b.m + c]) : z * down;
+          y[u] = _Float16(z);
+          out[int64_t(r + u) * b.m + c] = y[u];
+        }
+        if (ti != tj) *reinterpret_cast<f16x4*>(out + int64_t(c) * b.m + r) = y;
+      }
+    }
+}
+
+// X <- a X + B X, as the parameters lie; LAST: the update of the parameters (or the output) by it instead.
+template <class S, bool LAST>
+__global__ __launch_bounds__(S::kWaves * 64) void k_muon_apply(MuArgs a) {
+  if (left_out(a)) return;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  typename S::Lds& sm = *reinterpret_cast<typename S::Lds*>(smem);
+  const int t = find_item(a, blockIdx.x);
+  const MuItem& it = a.item[t];
+  const MuBuffers b(it.rows, it.cols);
+  const int tr = (b.rows + S::kA - 1) / S::kA, tc = (b.cols + S::kB - 1) / S::kB, per = tr * tc;
+  const int q = blockIdx.x - a.first[t], e = q / per;
+  uint8_t* ws = it.ws + e * align_up(b.bytes(), 256);
+  int ti, tj;
+  tile_coords(q % per, tr, tc, ti, tj);
+  const bool turn = b.turned(it);
+  const int i0 = ti * S::kA, j0 = tj * S::kB, ni = min(S::kA, b.rows - i0), nj = min(S::kB, b.cols - j0);
+  const _Float16 *hi = b.s(ws, turn, a.flip), *lo = b.lo(ws);
+  // the result's rows times its columns: B X, or X B where X is turned
+  const _Float16* left = turn ? hi : b.b(ws);
+  const _Float16* right = turn ? b.b(ws) : b.t(ws, turn, a.flip);
+  f32x16 acc[S::FA][S::FB];
+  tile_f16<S>(sm, left + int64_t(i0) * b.m, ni, right + int64_t(j0) * b.m, nj, b.m, acc);
+  const int tid = tile_tid(), lane = tid & 63, w = tid >> 6, wa = w / S::WB, wb = w % S::WB, half = lane >> 5;
+  const double lr = a.lr_dev ? *a.lr_dev : a.lr;
+  const float decay = float(1.0 - lr * a.weight_decay), scale = mu_scale(it.rows, it.cols);
+  const float rate = it.m ? float(lr * it.adjust / scale) : 1.f / scale;
+  const int64_t base = int64_t(it.e0 + e) * it.rows * it.cols;
+  _Float16 *hs = b.s(ws, turn, a.flip ^ 1), *ht = b.t(ws, turn, a.flip ^ 1), *lw = b.lo(ws);
+#pragma unroll
+  for (int i = 0; i < S::FA; ++i)
+#pragma unroll
+    for (int j = 0; j < S::FB; ++j) {
+      const int c = j0 + (wb * S::FB + j) * 32 + (lane & 31);
+      if (c >= j0 + nj) continue;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int r = i0 + (wa * S::FA + i) * 32 + 8 * v + 4 * half;
+        if (r >= i0 + ni) continue;
+        f16x4 h4;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int64_t at = int64_t(r + u) * b.cols + c;
+          const float x = a.a * (float(hi[at]) + float(lo[at])) + acc[i][j][4 * v + u];
+          if constexpr (LAST) {
+            if (r + u < it.rows && c < it.cols) {
+              const int64_t o = base + int64_t(r + u) * it.cols + c;
+              if (it.m) {
+                float* p = static_cast<float*>(it.p);
+                const float y = p[o] * decay - x * rate;
+                p[o] = y;
+                if (it.copy) it.copy[o] = f2bf(y);
+              } else {
+                static_cast<uint16_t*>(it.p)[o] = f2bf(x * rate);
+              }
+            }
+          } else {
+            const _Float16 h = _Float16(x);
+            h4[u] = h;
+            hs[at] = h;
+            lw[at] = _Float16(x - float(h));
+          }
+        }
+        if constexpr (!LAST) *reinterpret_cast<f16x4*>(ht + int64_t(c) * b.rows + r) = h4;
+      }
+    }
+}
+
+using MuMid = MuShape<2, 2, 2, 2>;   // 128 x 128
+
+template <class F>
+hipError_t allow_lds(F* f, int bytes, std::atomic<bool> (&done)[kMaxDevices]) {
+  return once_per_device(done, [&] {
+    return hipFuncSetAttribute(reinterpret_cast<const void*>(f), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  });
+}
+
+// Runs `kernel` over the tiles that `tiles` counts for each item.
+template <class K, class N>
+hipError_t run(K* kernel, MuArgs& a, int threads, int lds, hipStream_t s, N&& tiles) {
+  int64_t sum = 0;
+  for (int t = 0; t < a.count; ++t) {
+    a.first[t] = int32_t(sum);
+    sum += tiles(a.item[t]) * a.item[t].batch;
+  }
+  a.first[a.count] = int32_t(sum);
+  kernel<<<unsigned(sum), threads, lds, s>>>(a);
+  return hipGetLastError();
+}
+
+template <class S>
+hipError_t steps(MuArgs& a, int count, const float* coef, hipStream_t s) {
+  static std::atomic<bool> done[4][kMaxDevices];
+  constexpr int lds = int(sizeof(typename S::Lds)), threads = S::kWaves * 64;
+  hipError_t e = allow_lds(k_muon_gram<S, false>, lds, done[0]);
+  if (e == hipSuccess) e = allow_lds(k_muon_gram<S, true>, lds, done[1]);
+  if (e == hipSuccess) e = allow_lds(k_muon_apply<S, false>, lds, done[2]);
+  if (e == hipSuccess) e = allow_lds(k_muon_apply<S, true>, lds, done[3]);
+  const auto half = [](const MuItem& it) {
+    const int64_t T = cdiv(MuBuffers(it.rows, it.cols).m, S::kA);
+    return T * (T + 1) / 2;
+  };
+  const auto full = [](const MuItem& it) {
+    const MuBuffers b(it.rows, it.cols);
+    return cdiv(b.rows, S::kA) * cdiv(b.cols, S::kB);
+  };
+  for (int k = 0; k < count && e == hipSuccess; ++k) {
+    a.a = coef[3 * k];
+    a.b = coef[3 * k + 1];
+    a.c = coef[3 * k + 2];
+    a.flip = k & 1;
+    e = run(k_muon_gram<S, false>, a, threads, lds, s, half);
+    if (e == hipSuccess) e = run(k_muon_gram<S, true>, a, threads, lds, s, half);
+    if (e == hipSuccess && k + 1 < count) e = run(k_muon_apply<S, false>, a, threads, lds, s, full);
+    if (e == hipSuccess && k + 1 == count) e = run(k_muon_apply<S, true>, a, threads, lds, s, full);
+  }
+  return e;
+}
+
+// A run: matrices that go through the launches together, at most kMuItems items and as many matrices as this workspace
+// holds (one at least). Tensors are cut between the matrices of their batches where a run is full.
+constexpr int64_t kMuWs = int64_t(2) << 30;
+
+struct MuPart {
+  int tensor, first, count;   // matrices first .. first + count - 1 of a tensor
+  int64_t ws;                 // offset of their buffers
+};
+
+int64_t matrix_bytes(const mok_muon_tensor& t) { return align_up(MuBuffers(t.rows, t.cols).bytes(), 256); }
+
+// Calls go(parts, count, bytes) for each run; stops at an error.
+template <class G>
+hipError_t each_run(int count, const mok_muon_tensor* t, G&& go) {
+  MuPart part[kMuItems];
+  int n = 0;
+  int64_t bytes = 0;
+  for (int k = 0; k < count; ++k) {
+    const int64_t one = matrix_bytes(t[k]);
+    for (int b = 0; b < t[k].batch;) {
+      if (n == kMuItems || (n > 0 && bytes + one > kMuWs)) {
+        const hipError_t e = go(part, n, bytes);
+        if (e != hipSuccess) return e;
+        n = 0;
+        bytes = 0;
+      }
+      const int take = int(std::min<int64_t>(t[k].batch - b, std::max<int64_t>(1, (kMuWs - bytes) / one)));
+      part[n++] = MuPart{k, b, take, bytes};
+      bytes += take * one;
+      b += take;
+    }
+  }
+  return n > 0 ? go(part, n, bytes) : hipSuccess;
+}
+
+double adjustment(int rule, int rows, int cols) {
+  if (rule == MOK_ADJUST_RMS) return 0.2 * std::sqrt(double(std::max(rows, cols)));
+  if (rule == MOK_ADJUST_SPECTRAL) return std::sqrt(std::max(1.0, double(rows) / cols));
+  return 1.0;
+}
+
+}  // namespace
+
+int64_t muon_ws_bytes(int count, const mok_muon_tensor* t) {
+  int64_t most = 0;
+  (void)each_run(count, t, [&](const MuPart*, int, int64_t bytes) {
+    most = std::max(most, bytes);
+    return hipSuccess;
+  });
+  return std::max<int64_t>(most, 256);
+}
+
+hipError_t launch_muon(int count, const mok_muon_tensor* t, const mok_muon_config& c, uint8_t* ws, hipStream_t s) {
+  return each_run(count, t, [&](const MuPart* part, int n, int64_t) {
+    MuArgs a{};
+    for (int k = 0; k < n; ++k) {
+      const mok_muon_tensor& x = t[part[k].tensor];
+      a.item[k] = MuItem{x.g, x.m, x.p, static_cast<uint16_t*>(x.copy), ws + part[k].ws, part[k].first, part[k].count,
+                         x.rows, x.cols, float(adjustment(c.adjust, x.rows, x.cols))};
+    }
+    a.count = n;
+    a.nesterov = c.nesterov;
+    a.gbf = c.grad_elem == MOK_ELEM_BF16;
+    a.mu = float(c.momentum);
+    a.eps = float(c.ns.eps);
+    a.lr = c.lr;
+    a.weight_decay = c.weight_decay;
+    a.max_norm = c.max_norm;
+    a.sumsq = c.sumsq_dev;
+    a.lr_dev = c.lr_dev;
+    hipError_t e = run(k_muon_norm, a, 256, 0, s, [](const MuItem& it) {
+      const int64_t size = int64_t(it.rows) * it.cols;
+      return cdiv(size, mu_chunk(size));
+    });
+    if (e == hipSuccess)
+      e = run(k_muon_start, a, 256, 0, s, [](const MuItem& it) {
+        const MuBuffers b(it.rows, it.cols);
+        return int64_t(b.rows / 64) * (b.cols / 64);
+      });
+    if (e == hipSuccess) e = steps<MuMid>(a, c.ns.steps, &c.ns.coefficients[0][0], s);
+    return e;
+  });
+}
+
+}  // namespace mok

@@ -475,6 +475,10 @@ hipError_t launch_block_gemm(const mok_block_desc& d, const uint8_t* x, const fl
 hipError_t launch_block_wgrad(const mok_block_desc& d, const uint8_t* dy, const float* dys, const uint8_t* x,
                               const float* xs, const int32_t* offsets, float* dw, bool accumulate, hipStream_t s);
 
+// Muon (k_muon.hip). A tensor without a momentum (m null) is orthogonalised from g into bf16 p.
+int64_t muon_ws_bytes(int count, const mok_muon_tensor* t);
+hipError_t launch_muon(int count, const mok_muon_tensor* t, const mok_muon_config& c, uint8_t* ws, hipStream_t s);
+
 int device_cus();
 
 // One-time set-up per device (kernel attributes are set for the device that is current when

@@ -4,6 +4,8 @@
 
 #include <cmath>
 #include <cstdint>
+#include <new>
+#include <vector>
 
 #include "mok_internal.h"
 
@@ -34,6 +36,32 @@ mok_status check_route(const mok_route_desc* d) {
 }
 
 mok_status hip_status(hipError_t e) { return e == hipSuccess ? MOK_OK : MOK_ERR_HIP; }
+
+mok_status check_matrix(int32_t batch, int32_t rows, int32_t cols) {
+  if (batch < 0 || batch > (1 << 20) || rows < 1 || rows > (1 << 16) || cols < 1 || cols > (1 << 16))
+    return MOK_ERR_SHAPE;
+  return int64_t(batch) * rows > kMaxOptElements / cols ? MOK_ERR_SHAPE : MOK_OK;
+}
+
+mok_status check_ns(const mok_newton_schulz& ns) {
+  if (!(float(ns.eps) > 0.f && std::isfinite(float(ns.eps))) || ns.steps < 1 || ns.steps > 16) return MOK_ERR_SHAPE;
+  for (int k = 0; k < ns.steps; ++k)
+    for (float c : ns.coefficients[k])
+      if (!std::isfinite(c)) return MOK_ERR_SHAPE;
+  return MOK_OK;
+}
+
+// The matrices of a mok_orthogonalize call as Muon's kernels take them: no momentum. False without host memory.
+bool as_muon(int32_t n, const mok_orthogonalize_tensor* t, std::vector<mok_muon_tensor>& out) {
+  try {
+    out.resize(size_t(n));
+  } catch (const std::bad_alloc&) {
+    return false;
+  }
+  for (int32_t k = 0; k < n; ++k)
+    out[k] = mok_muon_tensor{t[k].out, nullptr, t[k].src, nullptr, t[k].batch, t[k].rows, t[k].cols};
+  return true;
+}
 
 }  // namespace
 
@@ -116,6 +144,80 @@ mok_status mok_adamw(int32_t num_tensors, const mok_adamw_tensor* tensors,
       return MOK_ERR_ALIGN;
   }
   return hip_status(launch_adamw(num_tensors, tensors, c, static_cast<hipStream_t>(stream)));
+}
+
+mok_status mok_muon_ws_size(int32_t num_tensors, const mok_muon_tensor* tensors, size_t* ws_bytes) {
+  if (!ws_bytes || (num_tensors > 0 && !tensors)) return MOK_ERR_NULL;
+  if (num_tensors < 0) return MOK_ERR_SHAPE;
+  for (int32_t k = 0; k < num_tensors; ++k) {
+    const mok_status st = check_matrix(tensors[k].batch, tensors[k].rows, tensors[k].cols);
+    if (st != MOK_OK) return st;
+  }
+  *ws_bytes = size_t(muon_ws_bytes(num_tensors, tensors));
+  return MOK_OK;
+}
+
+mok_status mok_muon(int32_t num_tensors, const mok_muon_tensor* tensors, const mok_muon_config* config,
+                    void* ws_dev, void* stream) {
+  if (!config) return MOK_ERR_NULL;
+  if (num_tensors < 0) return MOK_ERR_SHAPE;
+  if ((num_tensors > 0 && !tensors) || !ws_dev) return MOK_ERR_NULL;
+  const mok_muon_config& c = *config;
+  if (!is_elem(c.grad_elem)) return MOK_ERR_DTYPE;
+  // (written so that NaN fails)
+  if (!(c.lr >= 0 && std::isfinite(c.lr)) || !(c.weight_decay >= 0 && std::isfinite(c.weight_decay)) ||
+      !(c.momentum >= 0 && c.momentum < 1) || (c.nesterov != 0 && c.nesterov != 1) || c.adjust < MOK_ADJUST_RMS ||
+      c.adjust > MOK_ADJUST_NONE)
+    return MOK_ERR_SHAPE;
+  if (c.sumsq_dev && !(c.max_norm > 0)) return MOK_ERR_SHAPE;
+  mok_status st = check_ns(c.ns);
+  if (st != MOK_OK) return st;
+  if (!aligned(c.sumsq_dev, 8) || !aligned(c.lr_dev, 8) || !aligned(ws_dev, 256)) return MOK_ERR_ALIGN;
+  for (int32_t k = 0; k < num_tensors; ++k) {
+    const mok_muon_tensor& t = tensors[k];
+    st = check_matrix(t.batch, t.rows, t.cols);
+    if (st != MOK_OK) return st;
+    if (t.batch == 0) continue;
+    if (!t.p || !t.g || !t.m) return MOK_ERR_NULL;
+    if (!aligned(t.p, 16) || !aligned(t.copy, 16) || !aligned(t.g, 16) || !aligned(t.m, 16)) return MOK_ERR_ALIGN;
+  }
+  return hip_status(launch_muon(num_tensors, tensors, c, static_cast<uint8_t*>(ws_dev),
+                                static_cast<hipStream_t>(stream)));
+}
+
+mok_status mok_orthogonalize_ws_size(int32_t num_tensors, const mok_orthogonalize_tensor* tensors, size_t* ws_bytes) {
+  if (!ws_bytes || (num_tensors > 0 && !tensors)) return MOK_ERR_NULL;
+  if (num_tensors < 0) return MOK_ERR_SHAPE;
+  std::vector<mok_muon_tensor> t;
+  if (!as_muon(num_tensors, tensors, t)) return MOK_ERR_SHAPE;
+  return mok_muon_ws_size(num_tensors, t.data(), ws_bytes);
+}
+
+mok_status mok_orthogonalize(int32_t num_tensors, const mok_orthogonalize_tensor* tensors, int32_t elem,
+                             const mok_newton_schulz* ns, void* ws_dev, void* stream) {
+  if (!ns) return MOK_ERR_NULL;
+  if (num_tensors < 0) return MOK_ERR_SHAPE;
+  if ((num_tensors > 0 && !tensors) || !ws_dev) return MOK_ERR_NULL;
+  if (!is_elem(elem)) return MOK_ERR_DTYPE;
+  mok_status st = check_ns(*ns);
+  if (st != MOK_OK) return st;
+  if (!aligned(ws_dev, 256)) return MOK_ERR_ALIGN;
+  for (int32_t k = 0; k < num_tensors; ++k) {
+    const mok_orthogonalize_tensor& t = tensors[k];
+    st = check_matrix(t.batch, t.rows, t.cols);
+    if (st != MOK_OK) return st;
+    if (t.batch == 0) continue;
+    if (!t.src || !t.out) return MOK_ERR_NULL;
+    if (!aligned(t.src, 16) || !aligned(t.out, 16)) return MOK_ERR_ALIGN;
+  }
+  std::vector<mok_muon_tensor> t;
+  if (!as_muon(num_tensors, tensors, t)) return MOK_ERR_SHAPE;
+  mok_muon_config c{};
+  c.adjust = MOK_ADJUST_NONE;
+  c.grad_elem = elem;
+  c.ns = *ns;
+  return hip_status(launch_muon(num_tensors, t.data(), c, static_cast<uint8_t*>(ws_dev),
+                                static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -565,6 +565,62 @@ typedef struct {
 mok_status mok_adamw(int32_t num_tensors, const mok_adamw_tensor* tensors,
                      const mok_adamw_config* config, void* stream);
 
+/* ---- Muon: orthogonalised updates -------------------------------------------------------------------
+ * A matrix u [rows][cols] becomes, with X on its smaller side (u, or its transpose where rows > cols),
+ *   X = u / (|u|_F + eps);  then `steps` times  A = X X^T,  X = a X + (b A + c A A) X
+ * with the step's (a, b, c): an odd polynomial of u's singular values. With three-term coefficients that keep singular
+ * values of 0..1 below 16 all the way (the usual 3.4445, -4.7750, 2.0315 keep them below 1.3) no intermediate leaves
+ * its range; larger ones may overflow to infinities. Products take fp16 operands, whose sums are fp32; X is held in 22
+ * bits. A zero matrix stays zero; a NaN or an infinity in u makes its whole matrix NaN. Tensors are batches of
+ * matrices, contiguous [batch][rows][cols], 16-byte aligned (the optimizer's other rules hold here, too). */
+typedef struct {
+  double eps;                /* > 0                                       */
+  int32_t steps;             /* 1..16                                     */
+  float coefficients[16][3]; /* a, b, c of each step; finite              */
+} mok_newton_schulz;
+
+typedef struct {
+  void* p;                   /* fp32 parameters, updated in place         */
+  void* copy;                /* bf16 copy, written; NULL: none            */
+  const void* g;             /* gradient                                  */
+  float* m;                  /* momentum                                  */
+  int32_t batch;             /* 0..2^20                                   */
+  int32_t rows, cols;        /* 1..2^16; batch * rows * cols <= 2^33      */
+} mok_muon_tensor;
+
+/* What the update is scaled by: 0.2 sqrt(max(rows, cols)) (updates of AdamW's size), sqrt(max(1, rows / cols)), or 1. */
+typedef enum { MOK_ADJUST_RMS = 0, MOK_ADJUST_SPECTRAL = 1, MOK_ADJUST_NONE = 2 } mok_muon_adjust;
+
+typedef struct {
+  double lr, momentum, weight_decay;  /* lr, weight_decay >= 0; momentum in [0, 1)                    */
+  double max_norm;          /* as in mok_adamw_config                                                 */
+  int32_t nesterov;         /* 0 or 1                                                                 */
+  int32_t adjust;           /* mok_muon_adjust                                                        */
+  int32_t grad_elem;        /* mok_elem                                                               */
+  mok_newton_schulz ns;
+  const double* sumsq_dev;  /* as in mok_adamw_config: NULL, or the squared norm of all gradients      */
+  const double* lr_dev;     /* NULL, or where the device finds lr; negative or not finite changes nothing */
+} mok_muon_config;
+
+/* One Muon step over all tensors:
+ *   g' = g min(1, max_norm / sqrt(*sumsq)),  m = momentum m + g',  u = nesterov ? g' + momentum m : m,
+ *   p = p (1 - lr weight_decay) - lr adjust orthogonalised(u).
+ * 2 + 3 steps launches for up to 40 tensors whose workspace stays below 2 GiB together.
+ *   ws_dev  mok_muon_ws_size bytes, 256-byte aligned; calls that overlap in time need their own */
+mok_status mok_muon_ws_size(int32_t num_tensors, const mok_muon_tensor* tensors, size_t* ws_bytes);
+mok_status mok_muon(int32_t num_tensors, const mok_muon_tensor* tensors, const mok_muon_config* config,
+                    void* ws_dev, void* stream);
+
+/* out = orthogonalised(src) for every matrix, rounded to bf16 (src: elem; out may not overlap a src). */
+typedef struct {
+  const void* src;
+  void* out;                 /* bf16 */
+  int32_t batch, rows, cols; /* as in mok_muon_tensor */
+} mok_orthogonalize_tensor;
+mok_status mok_orthogonalize_ws_size(int32_t num_tensors, const mok_orthogonalize_tensor* tensors, size_t* ws_bytes);
+mok_status mok_orthogonalize(int32_t num_tensors, const mok_orthogonalize_tensor* tensors, int32_t elem,
+                             const mok_newton_schulz* ns, void* ws_dev, void* stream);
+
 /* ---- linear maps of sorted rows in block-scaled FP8 ----------------------------------------------
  *
  * E4M3 codes with one fp32 scale for each block of 128 along the axis that a product sums over. A block x is
