@@ -9,6 +9,11 @@
 // (the weight gradient needs one product of two scales more). The first operand's rows (weights; dy) are the rows of
 // the MFMA's result, which lie in registers, the second's (tokens; x) its columns, which lie in lanes: a lane has one token
 // scale, and a weight scale is the same for a whole wave.
+//
+// The FP8 instructions cut their products some 20 bits below the largest one of a sum: results are off by 1e-5 to 5e-5 of
+// their size, a hundredth of a bf16 result's rounding. fp32 results (the weight gradient among them) are wanted better:
+// there the codes are widened to fp16, which holds all of them, and multiplied at half the rate with sums as good as
+// fp32.
 #include "k_block.h"
 #include "k_gemm.h"
 
@@ -77,7 +82,58 @@ __device__ __forceinline__ f32x16 mfma_codes(const i32x8& a, const i32x8& b, con
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, 127, 0, 127);
 }
 
-template <class S, bool GRAD>
+typedef __attribute__((ext_vector_type(2))) _Float16 f16x2;
+typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
+
+// A row's 128 codes of a stage as fp16 values, which hold every E4M3 value: a lane has the 16-byte chunks 2 q + half. (Which
+// of them meet in a product does not matter as long as both operands agree.)
+struct WideRow {
+  f16x8 v[8];
+};
+__device__ __forceinline__ f16x8 widen(uint32_t lo, uint32_t hi) {
+  const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(int(lo), 1.f, false);
+  const f16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(int(lo), 1.f, true);
+  const f16x2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(int(hi), 1.f, false);
+  const f16x2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(int(hi), 1.f, true);
+  return f16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+__device__ __forceinline__ WideRow load_wide(const uint8_t* lds, int row, int half) {
+  WideRow r;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const u32x4 x = *reinterpret_cast<const u32x4*>(lds + swz(row, 2 * q + half));
+    r.v[2 * q] = widen(x[0], x[1]);
+    r.v[2 * q + 1] = widen(x[2], x[3]);
+  }
+  return r;
+}
+
+// The same codes for the FP8 instructions.
+struct CodeRow {
+  i32x8 v[2];
+};
+__device__ __forceinline__ CodeRow load_narrow(const uint8_t* lds, int row, int half) {
+  return CodeRow{{load_codes(lds, row, 0, half), load_codes(lds, row, 1, half)}};
+}
+
+__device__ __forceinline__ f32x16 block_product(const CodeRow& a, const CodeRow& b) {
+  f32x16 p;
+#pragma unroll
+  for (int v = 0; v < 16; ++v) p[v] = 0.f;
+  p = mfma_codes(a.v[0], b.v[0], p);
+  return mfma_codes(a.v[1], b.v[1], p);
+}
+__device__ __forceinline__ f32x16 block_product(const WideRow& a, const WideRow& b) {
+  f32x16 p;
+#pragma unroll
+  for (int v = 0; v < 16; ++v) p[v] = 0.f;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) p = __builtin_amdgcn_mfma_f32_32x32x16_f16(a.v[q], b.v[q], p, 0, 0, 0);
+  return p;
+}
+
+// WIDE: the products in fp16 (see the head of the file).
+template <class S, bool GRAD, bool WIDE>
 __global__ __launch_bounds__(S::kWaves * 64) void k_block_product(ProductArgs p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   typename S::Lds& sm = *reinterpret_cast<typename S::Lds*>(smem);
@@ -139,23 +195,22 @@ __global__ __launch_bounds__(S::kWaves * 64) void k_block_product(ProductArgs p)
     __syncthreads();
     if (kt + 1 < ksteps) issue(kt + 1, cur ^ 1);
     const float wscale = GRAD ? 1.f : as[kt];
-    i32x8 fa[S::FA][2];
+    using Row = std::conditional_t<WIDE, WideRow, CodeRow>;
+    const auto load = [&](const uint8_t* lds, int row) {
+      if constexpr (WIDE) return load_wide(lds, row, half);
+      else return load_narrow(lds, row, half);
+    };
+    Row fa[S::FA];
 #pragma unroll
-    for (int i = 0; i < S::FA; ++i)
-#pragma unroll
-      for (int kk = 0; kk < 2; ++kk) fa[i][kk] = load_codes(sm.a[cur], (wa * S::FA + i) * 32 + l32, kk, half);
+    for (int i = 0; i < S::FA; ++i) fa[i] = load(sm.a[cur], (wa * S::FA + i) * 32 + l32);
 #pragma unroll
     for (int j = 0; j < S::FB; ++j) {
       const int col = (wb * S::FB + j) * 32 + l32;
-      const i32x8 fb0 = load_codes(sm.b[cur], col, 0, half), fb1 = load_codes(sm.b[cur], col, 1, half);
+      const Row fb = load(sm.b[cur], col);
       const float s = sm.bs[cur][col] * wscale;
 #pragma unroll
       for (int i = 0; i < S::FA; ++i) {
-        f32x16 part;
-#pragma unroll
-        for (int v = 0; v < 16; ++v) part[v] = 0.f;
-        part = mfma_codes(fa[i][0], fb0, part);
-        part = mfma_codes(fa[i][1], fb1, part);
+        const f32x16 part = block_product(fa[i], fb);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           if constexpr (GRAD) {
@@ -225,15 +280,15 @@ __global__ __launch_bounds__(S::kWaves * 64) void k_block_product(ProductArgs p)
 }
 
 // A dynamic shared memory size above 64 KB has to be allowed once for each kernel and device.
-template <class S, bool GRAD>
+template <class S, bool GRAD, bool WIDE>
 hipError_t launch_product(const ProductArgs& p, int64_t tiles, hipStream_t s) {
   static std::atomic<bool> done[kMaxDevices];
-  const void* f = reinterpret_cast<const void*>(k_block_product<S, GRAD>);
+  const void* f = reinterpret_cast<const void*>(k_block_product<S, GRAD, WIDE>);
   constexpr int bytes = int(sizeof(typename S::Lds));
   const hipError_t e =
       once_per_device(done, [&] { return hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, bytes); });
   if (e != hipSuccess) return e;
-  k_block_product<S, GRAD><<<unsigned(tiles), S::kWaves * 64, bytes, s>>>(p);
+  k_block_product<S, GRAD, WIDE><<<unsigned(tiles), S::kWaves * 64, bytes, s>>>(p);
   return hipGetLastError();
 }
 
@@ -259,7 +314,8 @@ hipError_t launch_block_gemm(const mok_block_desc& d, const uint8_t* x, const fl
   p.bf16 = d.elem == MOK_ELEM_BF16;
   using S = Mid;
   p.tiles_n = int(cdiv(d.n, S::kA));
-  return launch_product<S, false>(p, group_tiles_max(d.rows, d.groups, S::kB) * p.tiles_n, s);
+  const int64_t tiles = group_tiles_max(d.rows, d.groups, S::kB) * p.tiles_n;
+  return p.bf16 ? launch_product<S, false, false>(p, tiles, s) : launch_product<S, false, true>(p, tiles, s);
 }
 
 hipError_t launch_block_wgrad(const mok_block_desc& d, const uint8_t* dy, const float* dys, const uint8_t* x,
@@ -278,7 +334,7 @@ hipError_t launch_block_wgrad(const mok_block_desc& d, const uint8_t* dy, const 
   using S = Mid;
   p.tiles_n = int(cdiv(d.n, S::kA));
   p.tiles_k = int(cdiv(d.k, S::kB));
-  return launch_product<S, true>(p, int64_t(d.groups) * p.tiles_n * p.tiles_k, s);
+  return launch_product<S, true, true>(p, int64_t(d.groups) * p.tiles_n * p.tiles_k, s);
 }
 
 }  // namespace mok
