@@ -21,13 +21,13 @@ namespace mok {
 namespace {
 
 struct ProductArgs {
-  const uint8_t* a;      // weights [g][n][stride_a], or dy columns [n][stride_a]
+  const uint8_t* a;      // weights [g][n][stride], or dy columns [n][stride]
   const float* as;       // weights' scales [g][nb][kb], or dy's [..][n]
-  const uint8_t* b;      // tokens [rows][stride_b], or x columns [k][stride_b]
+  const uint8_t* b;      // tokens [rows][stride], or x columns [k][stride]
   const float* bs;       // [kb][rows], or [..][k]
   void* out;
   RowGroups rg;
-  int64_t out_stride, stride_a, stride_b;
+  int64_t out_stride, stride;   // stride: of a's and b's rows
   int n, k, kb;          // k, kb: columns and blocks of the sum (gradient: columns of x)
   int tiles_n;           // tiles of n
   int tiles_k;           // gradient: tiles of k
@@ -42,86 +42,93 @@ struct Shape {
   struct Lds {
     uint8_t a[2][kA * kStageRowBytes];
     uint8_t b[2][kB * kStageRowBytes];
-    float as[2][kA];
-    float bs[2][kB];
+    float as[4][kA];   // (a stage's scales are read until its last product, when its codes' buffer takes others)
+    float bs[4][kB];
   };
 };
 
-// 128 bytes of each of ROWS rows into an LDS stage, swizzled as swz() reads them; the waves take 8 rows a load in
-// turn. Rows past the resource's end read as zeros.
+// 128 bytes of each of ROWS rows into an LDS stage, swizzled as swz() reads them; a wave takes kEach runs of 8 rows. Rows
+// past the resource's end read as zeros. `lane_off` is lane_offset(stride): a lane's row and chunk in an even run; in an odd
+// one the chunk's lowest bit turns, which is the offset's bit 4, as strides are multiples of 128.
+__device__ __forceinline__ int lane_offset(int stride) {
+  const int L = int(threadIdx.x) & 63;
+  return (L >> 3) * stride + ((L & 7) ^ (L >> 3)) * 16;
+}
 template <int ROWS, int WAVES>
-__device__ __forceinline__ void issue_rows(__amdgpu_buffer_rsrc_t r, uint8_t* lds, int stride, int col, int w) {
-  const int L = opaque(int(threadIdx.x) & 63);
+__device__ __forceinline__ void issue_rows(__amdgpu_buffer_rsrc_t r, uint8_t* lds, int lane_off, int stride, int col,
+                                           int w) {
   constexpr int kEach = ROWS / 8 / WAVES;
+  static_assert(kEach % 2 == 0, "a wave's first run is even");
 #pragma unroll
   for (int c = 0; c < kEach; ++c) {
-    const int blk = w * kEach + c;
-    const int chunk = (L & 7) ^ (L >> 3) ^ (blk & 1);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(lds + blk * 8 * kStageRowBytes), 16,
-                                             (blk * 8 + (L >> 3)) * stride + col + chunk * 16, 0, 0, 0);
+    const int run = w * kEach + c;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(lds + run * 8 * kStageRowBytes), 16,
+                                             (lane_off ^ (c & 1) * 16) + (run * 8 * stride + col), 0, 0, 0);
   }
 }
 
-// COUNT scales (consecutive floats, those from `valid` on zero) into LDS, 64 a wave, by the waves from `first` on.
+// COUNT scales (consecutive floats, those from `valid` on zero) into LDS, 64 a wave (by several waves the same ones: a
+// branch here would cut the stage's code in two, and the compiler then moves products across it).
 template <int COUNT>
-__device__ __forceinline__ void issue_scales(const float* s, int valid, float* lds, int w, int first) {
-  if (w < first || w >= first + COUNT / 64) return;
-  const int L = int(threadIdx.x) & 63, q = (w - first) * 64;
+__device__ __forceinline__ void issue_scales(const float* s, int valid, float* lds, int w) {
+  const int L = int(threadIdx.x) & 63, q = w % (COUNT / 64) * 64;
   __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(s, int64_t(valid) * 4), (lds_void*)(lds + q), 4, (q + L) * 4, 0, 0,
                                            0);
-}
-
-__device__ __forceinline__ i32x8 load_codes(const uint8_t* lds, int row, int kk, int half) {
-  const u32x4 lo = *reinterpret_cast<const u32x4*>(lds + swz(row, kk * 4 + half));
-  const u32x4 hi = *reinterpret_cast<const u32x4*>(lds + swz(row, kk * 4 + 2 + half));
-  return i32x8{int(lo[0]), int(lo[1]), int(lo[2]), int(lo[3]), int(hi[0]), int(hi[1]), int(hi[2]), int(hi[3])};
-}
-
-// E8M0 127 is 2^0: the codes' products as they are.
-__device__ __forceinline__ f32x16 mfma_codes(const i32x8& a, const i32x8& b, const f32x16& c) {
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, 127, 0, 127);
 }
 
 typedef __attribute__((ext_vector_type(2))) _Float16 f16x2;
 typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
 
-// A row's 128 codes of a stage as fp16 values, which hold every E4M3 value: a lane has the 16-byte chunks 2 q + half. (Which
-// of them meet in a product does not matter as long as both operands agree.)
+// A row's 128 codes of a stage: a lane has the 16-byte chunks 2 q + half. (Which of them meet in a product does not matter
+// as long as both operands agree.)
+struct Codes {
+  u32x4 q[4];
+};
+__device__ __forceinline__ Codes load_codes(const uint8_t* lds, int row, int half) {
+  Codes c;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) c.q[q] = *reinterpret_cast<const u32x4*>(lds + swz(row, 2 * q + half));
+  return c;
+}
+
+// The codes as operands of the FP8 instructions, or as fp16 values, which hold every E4M3 value.
+struct NarrowRow {
+  i32x8 v[2];
+  __device__ __forceinline__ explicit NarrowRow(const Codes& c) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        v[h][u] = int(c.q[2 * h][u]);
+        v[h][4 + u] = int(c.q[2 * h + 1][u]);
+      }
+  }
+};
 struct WideRow {
   f16x8 v[8];
-};
-__device__ __forceinline__ f16x8 widen(uint32_t lo, uint32_t hi) {
-  const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(int(lo), 1.f, false);
-  const f16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(int(lo), 1.f, true);
-  const f16x2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(int(hi), 1.f, false);
-  const f16x2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(int(hi), 1.f, true);
-  return f16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-}
-__device__ __forceinline__ WideRow load_wide(const uint8_t* lds, int row, int half) {
-  WideRow r;
+  __device__ __forceinline__ explicit WideRow(const Codes& c) {
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const u32x4 x = *reinterpret_cast<const u32x4*>(lds + swz(row, 2 * q + half));
-    r.v[2 * q] = widen(x[0], x[1]);
-    r.v[2 * q + 1] = widen(x[2], x[3]);
+    for (int q = 0; q < 4; ++q) {
+      v[2 * q] = widen(c.q[q][0], c.q[q][1]);
+      v[2 * q + 1] = widen(c.q[q][2], c.q[q][3]);
+    }
   }
-  return r;
-}
-
-// The same codes for the FP8 instructions.
-struct CodeRow {
-  i32x8 v[2];
+  static __device__ __forceinline__ f16x8 widen(uint32_t lo, uint32_t hi) {
+    const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(int(lo), 1.f, false);
+    const f16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(int(lo), 1.f, true);
+    const f16x2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(int(hi), 1.f, false);
+    const f16x2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(int(hi), 1.f, true);
+    return f16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+  }
 };
-__device__ __forceinline__ CodeRow load_narrow(const uint8_t* lds, int row, int half) {
-  return CodeRow{{load_codes(lds, row, 0, half), load_codes(lds, row, 1, half)}};
-}
 
-__device__ __forceinline__ f32x16 block_product(const CodeRow& a, const CodeRow& b) {
+__device__ __forceinline__ f32x16 block_product(const NarrowRow& a, const NarrowRow& b) {
   f32x16 p;
 #pragma unroll
   for (int v = 0; v < 16; ++v) p[v] = 0.f;
-  p = mfma_codes(a.v[0], b.v[0], p);
-  return mfma_codes(a.v[1], b.v[1], p);
+  // (E8M0 127 is 2^0: the codes' products as they are)
+  p = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a.v[0], b.v[0], p, 0, 0, 0, 127, 0, 127);
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a.v[1], b.v[1], p, 0, 0, 0, 127, 0, 127);
 }
 __device__ __forceinline__ f32x16 block_product(const WideRow& a, const WideRow& b) {
   f32x16 p;
@@ -132,9 +139,14 @@ __device__ __forceinline__ f32x16 block_product(const WideRow& a, const WideRow&
   return p;
 }
 
+__device__ __forceinline__ void add_scaled(f32x16& sum, const f32x16& part, float s) {
+#pragma unroll
+  for (int v = 0; v < 16; ++v) sum[v] = fmaf(part[v], s, sum[v]);
+}
+
 // WIDE: the products in fp16 (see the head of the file).
-template <class S, bool GRAD, bool WIDE>
-__global__ __launch_bounds__(S::kWaves * 64) void k_block_product(ProductArgs p) {
+template <class S, bool GRAD, bool WIDE, bool AHEAD = !WIDE>
+__global__ __launch_bounds__(S::kWaves * 64, 2) void k_block_product(ProductArgs p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   typename S::Lds& sm = *reinterpret_cast<typename S::Lds*>(smem);
   const int lane = threadIdx.x & 63, w = wave_id(), wa = w / S::WB, wb = w % S::WB, half = lane >> 5, l32 = lane & 31;
@@ -153,8 +165,8 @@ __global__ __launch_bounds__(S::kWaves * 64) void k_block_product(ProductArgs p)
     ksteps = (gt.rows + kBlk - 1) / kBlk;
     if (ksteps == 0 && p.accumulate) return;
     valid_b = min(S::kB, p.k - k0);
-    a = p.a + n0 * p.stride_a + gt.pad0;
-    b = p.b + k0 * p.stride_b + gt.pad0;
+    a = p.a + n0 * p.stride + gt.pad0;
+    b = p.b + k0 * p.stride + gt.pad0;
     as = p.as + (gt.pad0 / kBlk) * p.n + n0;
     bs = p.bs + (gt.pad0 / kBlk) * p.k + k0;
   } else {
@@ -164,8 +176,8 @@ __global__ __launch_bounds__(S::kWaves * 64) void k_block_product(ProductArgs p)
     n0 = tn * S::kA;
     ksteps = p.kb;
     valid_b = gt.rows;
-    a = p.a + (int64_t(gt.group) * p.n + n0) * p.stride_a;
-    b = p.b + gt.row0 * p.stride_b;
+    a = p.a + (int64_t(gt.group) * p.n + n0) * p.stride;
+    b = p.b + gt.row0 * p.stride;
     const int blocks = (p.n + kBlk - 1) / kBlk;
     as = p.as + (int64_t(gt.group) * blocks + min((n0 + wa * S::FA * 32) / kBlk, blocks - 1)) * p.kb;
     bs = p.bs + gt.row0;
@@ -173,13 +185,14 @@ __global__ __launch_bounds__(S::kWaves * 64) void k_block_product(ProductArgs p)
   const int valid_a = min(S::kA, p.n - n0);
   // (the last row ends at its own last block, which is all that is read of it)
   const auto span = [&](int rows, int64_t stride) { return (rows - 1) * stride + int64_t(ksteps) * kBlk; };
-  const __amdgpu_buffer_rsrc_t ra = make_rsrc(a, span(valid_a, p.stride_a)), rb = make_rsrc(b, span(valid_b, p.stride_b));
+  const __amdgpu_buffer_rsrc_t ra = make_rsrc(a, span(valid_a, p.stride)), rb = make_rsrc(b, span(valid_b, p.stride));
+  const int stride = int(p.stride), lane_off = lane_offset(stride);
   const int64_t bs_step = GRAD ? p.k : p.rg.rows;
-  const auto issue = [&](int kt, int buf) {
-    issue_rows<S::kA, S::kWaves>(ra, sm.a[buf], int(p.stride_a), kt * kBlk, w);
-    issue_rows<S::kB, S::kWaves>(rb, sm.b[buf], int(p.stride_b), kt * kBlk, w);
-    issue_scales<S::kB>(bs + kt * bs_step, valid_b, sm.bs[buf], w, 0);
-    if (GRAD) issue_scales<S::kA>(as + int64_t(kt) * p.n, valid_a, sm.as[buf], w, S::kB / 64);
+  const auto issue = [&](int kt, int buf, int slot) {
+    issue_rows<S::kA, S::kWaves>(ra, sm.a[buf], lane_off, stride, kt * kBlk, w);
+    issue_rows<S::kB, S::kWaves>(rb, sm.b[buf], lane_off, stride, kt * kBlk, w);
+    issue_scales<S::kB>(bs + kt * bs_step, valid_b, sm.bs[slot], w);
+    if (GRAD) issue_scales<S::kA>(as + int64_t(kt) * p.n, valid_a, sm.as[slot], w);
   };
   f32x16 acc[S::FA][S::FB];
 #pragma unroll
@@ -188,43 +201,94 @@ __global__ __launch_bounds__(S::kWaves * 64) void k_block_product(ProductArgs p)
     for (int j = 0; j < S::FB; ++j)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
-  if (ksteps > 0) issue(0, 0);
+  // One operand's rows of a stage stay in registers (tokens' columns in the gradient, else weights), the other's pass
+  // through them.
+  using Row = std::conditional_t<WIDE, WideRow, NarrowRow>;
+  constexpr int FR = GRAD ? S::FB : S::FA, FT = GRAD ? S::FA : S::FB;
+  const int row_r = (GRAD ? wb * S::FB : wa * S::FA) * 32 + l32, row_t = (GRAD ? wa * S::FA : wb * S::FB) * 32 + l32;
+  const auto lds_r = [&](int buf) { return GRAD ? sm.b[buf] : sm.a[buf]; };
+  const auto lds_t = [&](int buf) { return GRAD ? sm.a[buf] : sm.b[buf]; };
+  Codes cr[FR], ct[2];
+  if (ksteps > 0) {
+    issue(0, 0, 0);
+    if (AHEAD) {
+      issue(min(1, ksteps - 1), 1, 1);
+      wait_vmem();
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < FR; ++i) cr[i] = load_codes(lds_r(0), row_r + 32 * i, half);
+      ct[0] = load_codes(lds_t(0), row_t, half);
+    }
+  }
+  float wscales = 0.f;   // of 64 stages, one a lane
+  const auto load_wscales = [&](int kt) {
+    wscales = kt + lane < ksteps ? as[kt + lane] : 0.f;
+    wait_vmem();   // (here, as the compiler would wait in each stage, for the stage loads, too)
+  };
+  if (!GRAD) load_wscales(0);
+  f32x16 part[2];
+  float part_scale = 0.f;
+#pragma unroll
+  for (int v = 0; v < 16; ++v) part[1][v] = 0.f;
   for (int kt = 0; kt < ksteps; ++kt) {
     const int cur = kt & 1;
-    wait_vmem();
-    __syncthreads();
-    if (kt + 1 < ksteps) issue(kt + 1, cur ^ 1);
-    const float wscale = GRAD ? 1.f : as[kt];
-    using Row = std::conditional_t<WIDE, WideRow, CodeRow>;
-    const auto load = [&](const uint8_t* lds, int row) {
-      if constexpr (WIDE) return load_wide(lds, row, half);
-      else return load_narrow(lds, row, half);
-    };
-    Row fa[S::FA];
+    const bool more = kt + 1 < ksteps;
+    if (!GRAD && kt > 0 && (kt & 63) == 0) load_wscales(kt);
+    const float wscale = GRAD ? 1.f : __int_as_float(__builtin_amdgcn_readlane(__float_as_int(wscales), kt & 63));
+    const float *bsc = sm.bs[kt & 3] + wb * S::FB * 32 + l32, *asc = sm.as[kt & 3] + wa * S::FA * 32 + 4 * half;
+    float sb[S::FB];
+    if constexpr (!AHEAD) {
+      wait_vmem();
+      __syncthreads();
+      issue(more ? kt + 1 : kt, cur ^ 1, (kt + 1) & 3);   // (the last one for nothing)
 #pragma unroll
-    for (int i = 0; i < S::FA; ++i) fa[i] = load(sm.a[cur], (wa * S::FA + i) * 32 + l32);
+      for (int i = 0; i < FR; ++i) cr[i] = load_codes(lds_r(cur), row_r + 32 * i, half);
+      ct[0] = load_codes(lds_t(cur), row_t, half);
+    }
 #pragma unroll
-    for (int j = 0; j < S::FB; ++j) {
-      const int col = (wb * S::FB + j) * 32 + l32;
-      const Row fb = load(sm.b[cur], col);
-      const float s = sm.bs[cur][col] * wscale;
+    for (int j = 0; j < S::FB; ++j) sb[j] = bsc[j * 32] * wscale;
+    Row r[FR] = {Row(cr[0]), Row(cr[1])};
+    static_assert(FR == 2, "two resident rows");
 #pragma unroll
-      for (int i = 0; i < S::FA; ++i) {
-        const f32x16 part = block_product(fa[i], fb);
+    for (int t = 0; t < FT; ++t) {
+      const bool next = AHEAD && t + 1 == FT;   // (in the last stage what is read is not used)
+      if (AHEAD) __builtin_amdgcn_sched_barrier(0);
+      if (t + 1 < FT) ct[(t + 1) & 1] = load_codes(lds_t(cur), row_t + 32 * (t + 1), half);
+      if (next) {
+        wait_vmem();
+        __syncthreads();
+        issue(min(kt + 2, ksteps - 1), cur, (kt + 2) & 3);   // (the last two for nothing)
+        ct[(t + 1) & 1] = load_codes(lds_t(cur ^ 1), row_t, half);
+      }
+      const Row x(ct[t & 1]);
+      f32x4 sa[4];
+      if constexpr (GRAD)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if constexpr (GRAD) {
-            const f32x4 sa = *reinterpret_cast<const f32x4*>(sm.as[cur] + (wa * S::FA + i) * 32 + 8 * q + 4 * half);
+        for (int q = 0; q < 4; ++q) sa[q] = *reinterpret_cast<const f32x4*>(asc + t * 32 + 8 * q);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) acc[i][j][4 * q + u] = fmaf(part[4 * q + u], s * sa[u], acc[i][j][4 * q + u]);
-          } else {
+      for (int i = 0; i < FR; ++i) {
+        if constexpr (AHEAD) {
+          static_assert(!GRAD || !AHEAD);
+          // each product's sum is added while the next one runs
+          constexpr int U = FR * FT;
+          const int u = t * FR + i, before = (u + U - 1) % U;
+          part[u & 1] = block_product(r[i], x);
+          __builtin_amdgcn_sched_barrier(0);
+          if (next) cr[i] = load_codes(lds_r(cur ^ 1), row_r + 32 * i, half);
+          add_scaled(acc[before % FR][before / FR], part[before & 1], part_scale);
+          part_scale = sb[t];
+          __builtin_amdgcn_sched_barrier(0);
+        } else {
+          f32x16& sum = GRAD ? acc[t][i] : acc[i][t];
+          const f32x16 prod = GRAD ? block_product(x, r[i]) : block_product(r[i], x);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) acc[i][j][4 * q + u] = fmaf(part[4 * q + u], s, acc[i][j][4 * q + u]);
-          }
+          for (int v = 0; v < 16; ++v) sum[v] = fmaf(prod[v], GRAD ? sb[i] * sa[v >> 2][v & 3] : sb[t], sum[v]);
         }
       }
     }
   }
+  wait_vmem();   // (loads into LDS do not outlive the workgroup)
+  if constexpr (AHEAD) add_scaled(acc[FR - 1][FT - 1], part[1], part_scale);
   const int tid = tile_tid(), el = tid & 31, eh = (tid >> 5) & 1;
   if constexpr (GRAD) {
     float* out = static_cast<float*>(p.out) + (int64_t(gt.group) * p.n + n0) * p.k + k0;
@@ -292,7 +356,8 @@ hipError_t launch_product(const ProductArgs& p, int64_t tiles, hipStream_t s) {
   return hipGetLastError();
 }
 
-using Mid = Shape<2, 2, 2, 2>;   // 128 x 128
+using Mid = Shape<2, 2, 2, 2>;    // 128 x 128
+using Wide = Shape<4, 2, 2, 4>;   // 256 x 256
 
 }  // namespace
 
@@ -308,10 +373,15 @@ hipError_t launch_block_gemm(const mok_block_desc& d, const uint8_t* x, const fl
   p.out = out;
   p.rg = RowGroups{offsets, d.rows, d.groups};
   p.out_stride = d.stride;
-  p.stride_a = p.stride_b = int64_t(p.kb) * kBlk;
+  p.stride = int64_t(p.kb) * kBlk;
   p.n = d.n;
   p.k = d.k;
   p.bf16 = d.elem == MOK_ELEM_BF16;
+  if (p.bf16 && d.rows >= 8192) {
+    using S = Wide;
+    p.tiles_n = int(cdiv(d.n, S::kA));
+    return launch_product<S, false, false>(p, group_tiles_max(d.rows, d.groups, S::kB) * p.tiles_n, s);
+  }
   using S = Mid;
   p.tiles_n = int(cdiv(d.n, S::kA));
   const int64_t tiles = group_tiles_max(d.rows, d.groups, S::kB) * p.tiles_n;
@@ -327,7 +397,7 @@ hipError_t launch_block_wgrad(const mok_block_desc& d, const uint8_t* dy, const 
   p.bs = xs;
   p.out = dw;
   p.rg = RowGroups{offsets, d.rows, d.groups};
-  p.stride_a = p.stride_b = block_padded_rows(d.rows, d.groups);
+  p.stride = block_padded_rows(d.rows, d.groups);
   p.n = d.n;
   p.k = d.k;
   p.accumulate = accumulate;
