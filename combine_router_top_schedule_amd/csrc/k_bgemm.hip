@@ -56,11 +56,11 @@ __device__ __forceinline__ int lane_offset(int stride) {
 }
 template <int ROWS, int WAVES>
 __device__ __forceinline__ void issue_rows(__amdgpu_buffer_rsrc_t r, uint8_t* lds, int lane_off, int stride, int col,
-                                           int w) {
+                                           int w, int part, int parts) {
   constexpr int kEach = ROWS / 8 / WAVES;
   static_assert(kEach % 2 == 0, "a wave's first run is even");
 #pragma unroll
-  for (int c = 0; c < kEach; ++c) {
+  for (int c = kEach * part / parts; c < kEach * (part + 1) / parts; ++c) {
     const int run = w * kEach + c;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(lds + run * 8 * kStageRowBytes), 16,
                                              (lane_off ^ (c & 1) * 16) + (run * 8 * stride + col), 0, 0, 0);
@@ -126,9 +126,9 @@ __device__ __forceinline__ f32x16 block_product(const NarrowRow& a, const Narrow
   f32x16 p;
 #pragma unroll
   for (int v = 0; v < 16; ++v) p[v] = 0.f;
-  // (E8M0 127 is 2^0: the codes' products as they are)
-  p = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a.v[0], b.v[0], p, 0, 0, 0, 127, 0, 127);
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a.v[1], b.v[1], p, 0, 0, 0, 127, 0, 127);
+  // (no scales: the codes' products as they are)
+  p = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a.v[0], b.v[0], p, 0, 0, 0, 0, 0, 0);
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a.v[1], b.v[1], p, 0, 0, 0, 0, 0, 0);
 }
 __device__ __forceinline__ f32x16 block_product(const WideRow& a, const WideRow& b) {
   f32x16 p;
@@ -150,13 +150,12 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void k_block_product(ProductArgs
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   typename S::Lds& sm = *reinterpret_cast<typename S::Lds*>(smem);
   const int lane = threadIdx.x & 63, w = wave_id(), wa = w / S::WB, wb = w % S::WB, half = lane >> 5, l32 = lane & 31;
-  const int id = xcd_logical_id();
   GroupTile gt;
   int n0, k0 = 0, ksteps, valid_b;
   const uint8_t *a, *b;
   const float *as, *bs;
   if constexpr (GRAD) {
-    const int per = p.tiles_n * p.tiles_k, g = id / per, t = id % per;
+    const int id = xcd_logical_id(), per = p.tiles_n * p.tiles_k, g = id / per, t = id % per;
     gt = find_group(p.rg, g);
     int tn, tk;
     tile_coords(t, p.tiles_n, p.tiles_k, tn, tk);
@@ -170,9 +169,13 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void k_block_product(ProductArgs
     as = p.as + (gt.pad0 / kBlk) * p.n + n0;
     bs = p.bs + (gt.pad0 / kBlk) * p.k + k0;
   } else {
-    const int tn = id % p.tiles_n;
-    gt = find_group_tile(p.rg, id / p.tiles_n, S::kB);
-    if (gt.group < 0) return;
+    // the tiles there are (not the bound that was launched) in runs of equal length for the XCDs
+    const int row_tiles = count_group_tiles(p.rg, S::kB), total = row_tiles * p.tiles_n, run = (total + 7) / 8;
+    const int in = blockIdx.x / kXcds, id = blockIdx.x % kXcds * run + in;
+    if (in >= run || id >= total) return;
+    int tm, tn;
+    tile_coords(id, row_tiles, p.tiles_n, tm, tn);
+    gt = find_group_tile(p.rg, tm, S::kB);
     n0 = tn * S::kA;
     ksteps = p.kb;
     valid_b = gt.rows;
@@ -188,9 +191,13 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void k_block_product(ProductArgs
   const __amdgpu_buffer_rsrc_t ra = make_rsrc(a, span(valid_a, p.stride)), rb = make_rsrc(b, span(valid_b, p.stride));
   const int stride = int(p.stride), lane_off = lane_offset(stride);
   const int64_t bs_step = GRAD ? p.k : p.rg.rows;
-  const auto issue = [&](int kt, int buf, int slot) {
-    issue_rows<S::kA, S::kWaves>(ra, sm.a[buf], lane_off, stride, kt * kBlk, w);
-    issue_rows<S::kB, S::kWaves>(rb, sm.b[buf], lane_off, stride, kt * kBlk, w);
+  // part `part` of `parts` of a stage's loads (scales with the first); past the last stage, the last once more for nothing
+  const auto issue = [&](int kt, int part, int parts) {
+    const int buf = kt & 1, slot = kt & 3;
+    kt = min(kt, ksteps - 1);
+    issue_rows<S::kA, S::kWaves>(ra, sm.a[buf], lane_off, stride, kt * kBlk, w, part, parts);
+    issue_rows<S::kB, S::kWaves>(rb, sm.b[buf], lane_off, stride, kt * kBlk, w, part, parts);
+    if (part > 0) return;
     issue_scales<S::kB>(bs + kt * bs_step, valid_b, sm.bs[slot], w);
     if (GRAD) issue_scales<S::kA>(as + int64_t(kt) * p.n, valid_a, sm.as[slot], w);
   };
@@ -210,9 +217,10 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void k_block_product(ProductArgs
   const auto lds_t = [&](int buf) { return GRAD ? sm.a[buf] : sm.b[buf]; };
   Codes cr[FR], ct[2];
   if (ksteps > 0) {
-    issue(0, 0, 0);
+    issue(0, 0, 1);
     if (AHEAD) {
-      issue(min(1, ksteps - 1), 1, 1);
+      issue(1, 0, 4);
+      issue(1, 1, 4);
       wait_vmem();
       __syncthreads();
 #pragma unroll
@@ -232,7 +240,6 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void k_block_product(ProductArgs
   for (int v = 0; v < 16; ++v) part[1][v] = 0.f;
   for (int kt = 0; kt < ksteps; ++kt) {
     const int cur = kt & 1;
-    const bool more = kt + 1 < ksteps;
     if (!GRAD && kt > 0 && (kt & 63) == 0) load_wscales(kt);
     const float wscale = GRAD ? 1.f : __int_as_float(__builtin_amdgcn_readlane(__float_as_int(wscales), kt & 63));
     const float *bsc = sm.bs[kt & 3] + wb * S::FB * 32 + l32, *asc = sm.as[kt & 3] + wa * S::FA * 32 + 4 * half;
@@ -240,7 +247,7 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void k_block_product(ProductArgs
     if constexpr (!AHEAD) {
       wait_vmem();
       __syncthreads();
-      issue(more ? kt + 1 : kt, cur ^ 1, (kt + 1) & 3);   // (the last one for nothing)
+      issue(kt + 1, 0, 1);
 #pragma unroll
       for (int i = 0; i < FR; ++i) cr[i] = load_codes(lds_r(cur), row_r + 32 * i, half);
       ct[0] = load_codes(lds_t(cur), row_t, half);
@@ -257,7 +264,6 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void k_block_product(ProductArgs
       if (next) {
         wait_vmem();
         __syncthreads();
-        issue(min(kt + 2, ksteps - 1), cur, (kt + 2) & 3);   // (the last two for nothing)
         ct[(t + 1) & 1] = load_codes(lds_t(cur ^ 1), row_t, half);
       }
       const Row x(ct[t & 1]);
@@ -274,6 +280,9 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void k_block_product(ProductArgs
           const int u = t * FR + i, before = (u + U - 1) % U;
           part[u & 1] = block_product(r[i], x);
           __builtin_amdgcn_sched_barrier(0);
+          // (the loads of a stage are spread over four products: in one run they hold the waves up)
+          if (u < 2) issue(kt + 1, 2 + u, 4);
+          if (u >= U - 2) issue(kt + 2, u - (U - 2), 4);
           if (next) cr[i] = load_codes(lds_r(cur ^ 1), row_r + 32 * i, half);
           add_scaled(acc[before % FR][before / FR], part[before & 1], part_scale);
           part_scale = sb[t];

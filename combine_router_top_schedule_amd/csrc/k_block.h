@@ -97,6 +97,26 @@ __device__ __forceinline__ GroupTile find_group_tile(const RowGroups& rg, int t,
   return r;
 }
 
+// Number of tiles that find_group_tile knows. Uniform over the wave.
+__device__ __forceinline__ int count_group_tiles(const RowGroups& rg, int tile) {
+  if (!rg.offsets) return int((rg.rows + tile - 1) / tile);
+  const int lane = threadIdx.x & 63;
+  int prev = clamp_offset(rg.offsets[0], rg.rows), tiles = 0;
+  for (int g0 = 0; g0 < rg.groups; g0 += 64) {
+    const int g = g0 + lane;
+    int end = g < rg.groups ? clamp_offset(rg.offsets[g + 1], rg.rows) : 0;
+    end = wave_scan_max(max(end, prev), lane);
+    int start = __shfl_up(end, 1, 64);
+    if (lane == 0) start = prev;
+    int sum = (end - start + tile - 1) / tile;
+#pragma unroll
+    for (int o = 32; o; o >>= 1) sum += __shfl_xor(sum, o, 64);
+    tiles += sum;
+    prev = __shfl(end, 63, 64);
+  }
+  return __builtin_amdgcn_readfirstlane(tiles);
+}
+
 // Group g: its rows, and where they begin when each group is padded to 128. Uniform over the wave.
 __device__ __forceinline__ GroupTile find_group(const RowGroups& rg, int g) {
   GroupTile r;
