@@ -144,6 +144,50 @@ __device__ __forceinline__ void add_scaled(f32x16& sum, const f32x16& part, floa
   for (int v = 0; v < 16; ++v) sum[v] = fmaf(part[v], s, sum[v]);
 }
 
+// The tile's rows, from registers through LDS to out[row0 ..][n0 ..]: `rows` rows of `cols` elements. 16 bytes a lane where
+// rows begin at multiples of that, else an element a lane.
+template <class S, class T>
+__device__ __forceinline__ void store_rows(uint8_t* smem, const f32x16 (&acc)[S::FA][S::FB], const ProductArgs& p,
+                                           int64_t row0, int n0, int rows, int cols) {
+  constexpr int kPitch = S::kA * int(sizeof(T)) + 16, kChunk = 16 / int(sizeof(T)), kThreads = S::kWaves * 64;
+  static_assert(S::kB * kPitch <= int(sizeof(typename S::Lds)));
+  const int tid = tile_tid(), lane = tid & 63, w = tid >> 6, wa = w / S::WB, wb = w % S::WB, half = lane >> 5;
+  __syncthreads();   // (the other waves' last reads of the stages)
+#pragma unroll
+  for (int j = 0; j < S::FB; ++j) {
+    uint8_t* row = smem + ((wb * S::FB + j) * 32 + (lane & 31)) * kPitch;
+#pragma unroll
+    for (int i = 0; i < S::FA; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        T* o = reinterpret_cast<T*>(row) + (wa * S::FA + i) * 32 + 8 * q + 4 * half;
+        const f32x16& y = acc[i][j];
+        if constexpr (sizeof(T) == 2)
+          *reinterpret_cast<uint2*>(o) = uint2{pack_bf2(y[4 * q], y[4 * q + 1]), pack_bf2(y[4 * q + 2], y[4 * q + 3])};
+        else
+          *reinterpret_cast<f32x4*>(o) = f32x4{y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]};
+      }
+  }
+  __syncthreads();
+  T* out = static_cast<T*>(p.out) + row0 * p.out_stride + n0;
+  if ((reinterpret_cast<uintptr_t>(out) & 15) == 0 && p.out_stride % kChunk == 0) {
+    constexpr int kRun = S::kA / kChunk;   // lanes of a row
+    for (int r = tid / kRun; r < rows; r += kThreads / kRun) {
+      const int c = tid % kRun * kChunk;
+      const T* x = reinterpret_cast<const T*>(smem + r * kPitch) + c;
+      T* o = out + r * p.out_stride + c;
+      if (c + kChunk <= cols) {
+        *reinterpret_cast<u32x4*>(o) = *reinterpret_cast<const u32x4*>(x);
+      } else {
+        for (int u = 0; c + u < cols; ++u) o[u] = x[u];
+      }
+    }
+  } else {
+    for (int r = w; r < rows; r += S::kWaves)
+      for (int c = lane; c < cols; c += 64) out[r * p.out_stride + c] = reinterpret_cast<const T*>(smem + r * kPitch)[c];
+  }
+}
+
 // WIDE: the products in fp16 (see the head of the file).
 template <class S, bool GRAD, bool WIDE, bool AHEAD = !WIDE>
 __global__ __launch_bounds__(S::kWaves * 64, 2) void k_block_product(ProductArgs p) {
@@ -216,6 +260,11 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void k_block_product(ProductArgs
   const auto lds_r = [&](int buf) { return GRAD ? sm.b[buf] : sm.a[buf]; };
   const auto lds_t = [&](int buf) { return GRAD ? sm.a[buf] : sm.b[buf]; };
   Codes cr[FR], ct[2];
+  float sb[S::FB];
+  const auto load_sb = [&](int kt) {
+#pragma unroll
+    for (int j = 0; j < S::FB; ++j) sb[j] = sm.bs[kt & 3][(wb * S::FB + j) * 32 + l32];
+  };
   if (ksteps > 0) {
     issue(0, 0, 1);
     if (AHEAD) {
@@ -223,6 +272,7 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void k_block_product(ProductArgs
       issue(1, 1, 4);
       wait_vmem();
       __syncthreads();
+      load_sb(0);
 #pragma unroll
       for (int i = 0; i < FR; ++i) cr[i] = load_codes(lds_r(0), row_r + 32 * i, half);
       ct[0] = load_codes(lds_t(0), row_t, half);
@@ -242,8 +292,7 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void k_block_product(ProductArgs
     const int cur = kt & 1;
     if (!GRAD && kt > 0 && (kt & 63) == 0) load_wscales(kt);
     const float wscale = GRAD ? 1.f : __int_as_float(__builtin_amdgcn_readlane(__float_as_int(wscales), kt & 63));
-    const float *bsc = sm.bs[kt & 3] + wb * S::FB * 32 + l32, *asc = sm.as[kt & 3] + wa * S::FA * 32 + 4 * half;
-    float sb[S::FB];
+    const float* asc = sm.as[kt & 3] + wa * S::FA * 32 + 4 * half;
     if constexpr (!AHEAD) {
       wait_vmem();
       __syncthreads();
@@ -252,8 +301,10 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void k_block_product(ProductArgs
       for (int i = 0; i < FR; ++i) cr[i] = load_codes(lds_r(cur), row_r + 32 * i, half);
       ct[0] = load_codes(lds_t(cur), row_t, half);
     }
+    if constexpr (!AHEAD) load_sb(kt);
+    float scaled[S::FB];
 #pragma unroll
-    for (int j = 0; j < S::FB; ++j) sb[j] = bsc[j * 32] * wscale;
+    for (int j = 0; j < S::FB; ++j) scaled[j] = sb[j] * wscale;
     Row r[FR] = {Row(cr[0]), Row(cr[1])};
     static_assert(FR == 2, "two resident rows");
 #pragma unroll
@@ -264,6 +315,7 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void k_block_product(ProductArgs
       if (next) {
         wait_vmem();
         __syncthreads();
+        load_sb(kt + 1);
         ct[(t + 1) & 1] = load_codes(lds_t(cur ^ 1), row_t, half);
       }
       const Row x(ct[t & 1]);
@@ -285,21 +337,21 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void k_block_product(ProductArgs
           if (u >= U - 2) issue(kt + 2, u - (U - 2), 4);
           if (next) cr[i] = load_codes(lds_r(cur ^ 1), row_r + 32 * i, half);
           add_scaled(acc[before % FR][before / FR], part[before & 1], part_scale);
-          part_scale = sb[t];
+          part_scale = scaled[t];
           __builtin_amdgcn_sched_barrier(0);
         } else {
           f32x16& sum = GRAD ? acc[t][i] : acc[i][t];
           const f32x16 prod = GRAD ? block_product(x, r[i]) : block_product(r[i], x);
 #pragma unroll
-          for (int v = 0; v < 16; ++v) sum[v] = fmaf(prod[v], GRAD ? sb[i] * sa[v >> 2][v & 3] : sb[t], sum[v]);
+          for (int v = 0; v < 16; ++v) sum[v] = fmaf(prod[v], GRAD ? scaled[i] * sa[v >> 2][v & 3] : scaled[t], sum[v]);
         }
       }
     }
   }
   wait_vmem();   // (loads into LDS do not outlive the workgroup)
   if constexpr (AHEAD) add_scaled(acc[FR - 1][FT - 1], part[1], part_scale);
-  const int tid = tile_tid(), el = tid & 31, eh = (tid >> 5) & 1;
   if constexpr (GRAD) {
+    const int tid = tile_tid(), el = tid & 31, eh = (tid >> 5) & 1;
     float* out = static_cast<float*>(p.out) + (int64_t(gt.group) * p.n + n0) * p.k + k0;
 #pragma unroll
     for (int i = 0; i < S::FA; ++i)
@@ -316,39 +368,9 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void k_block_product(ProductArgs
         }
       }
   } else {
-    const bool whole = p.out_stride % 4 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
-#pragma unroll
-    for (int j = 0; j < S::FB; ++j) {
-      const int r = (wb * S::FB + j) * 32 + el;
-      if (r >= valid_b) continue;
-      const int64_t at = (gt.row0 + r) * p.out_stride + n0;
-#pragma unroll
-      for (int i = 0; i < S::FA; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int c = (wa * S::FA + i) * 32 + 8 * q + 4 * eh;
-          const f32x16& y = acc[i][j];
-          if (p.bf16) {
-            uint16_t* o = static_cast<uint16_t*>(p.out) + at + c;
-            if (whole && c + 4 <= valid_a) {
-              *reinterpret_cast<uint2*>(o) = uint2{pack_bf2(y[4 * q], y[4 * q + 1]), pack_bf2(y[4 * q + 2], y[4 * q + 3])};
-            } else {
-#pragma unroll
-              for (int u = 0; u < 4; ++u)
-                if (c + u < valid_a) o[u] = f2bf(y[4 * q + u]);
-            }
-          } else {
-            float* o = static_cast<float*>(p.out) + at + c;
-            if (whole && c + 4 <= valid_a) {
-              *reinterpret_cast<f32x4*>(o) = f32x4{y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]};
-            } else {
-#pragma unroll
-              for (int u = 0; u < 4; ++u)
-                if (c + u < valid_a) o[u] = y[4 * q + u];
-            }
-          }
-        }
-    }
+    // A lane holds 4 consecutive columns of one row: rows come together in LDS and go out in whole runs.
+    if constexpr (WIDE) store_rows<S, float>(smem, acc, p, gt.row0, n0, valid_b, valid_a);
+    else store_rows<S, uint16_t>(smem, acc, p, gt.row0, n0, valid_b, valid_a);
   }
 }
 
