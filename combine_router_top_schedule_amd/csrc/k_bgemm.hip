@@ -14,6 +14,9 @@
 // their size, a hundredth of a bf16 result's rounding. fp32 results (the weight gradient among them) are wanted better:
 // there the codes are widened to fp16, which holds all of them, and multiplied at half the rate with sums as good as
 // fp32.
+#include <algorithm>
+#include <cmath>
+
 #include "k_block.h"
 #include "k_gemm.h"
 
@@ -387,8 +390,168 @@ hipError_t launch_product(const ProductArgs& p, int64_t tiles, hipStream_t s) {
   return hipGetLastError();
 }
 
+// ---- few rows ------------------------------------------------------------------------------------
+// Up to 16 FT tokens against 16 FN weight rows a workgroup. The weights' bytes bound it: operands go from memory straight
+// into registers, the blocks of the sum are dealt out to the 8 waves in turn (so a workgroup reads runs of 1 KB of a
+// weight row) and kAhead blocks of a wave are in flight; the waves' sums join in LDS in their order. One
+// v_mfma_f32_16x16x128_f8f6f4 is one block: lane l has 32 codes of row l % 16, from 32 (l / 16) on.
+constexpr int kFewWaves = 8;
+
+struct FewCodes {
+  u32x4 lo, hi;
+};
+__device__ __forceinline__ FewCodes load_few(const uint8_t* p) {
+  return FewCodes{*reinterpret_cast<const u32x4*>(p), *reinterpret_cast<const u32x4*>(p + 16)};
+}
+template <bool WIDE>
+__device__ __forceinline__ f32x4 few_product(const FewCodes& a, const FewCodes& b) {
+  f32x4 p = {0.f, 0.f, 0.f, 0.f};
+  if constexpr (WIDE) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const u32x4 x = h ? a.hi : a.lo, y = h ? b.hi : b.lo;
+      p = __builtin_amdgcn_mfma_f32_16x16x32_f16(WideRow::widen(x[0], x[1]), WideRow::widen(y[0], y[1]), p, 0, 0, 0);
+      p = __builtin_amdgcn_mfma_f32_16x16x32_f16(WideRow::widen(x[2], x[3]), WideRow::widen(y[2], y[3]), p, 0, 0, 0);
+    }
+    return p;
+  } else {
+    const auto eight = [](const FewCodes& c) {
+      return i32x8{int(c.lo[0]), int(c.lo[1]), int(c.lo[2]), int(c.lo[3]),
+                   int(c.hi[0]), int(c.hi[1]), int(c.hi[2]), int(c.hi[3])};
+    };
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(eight(a), eight(b), p, 0, 0, 0, 0, 0, 0);
+  }
+}
+
+template <int FN, int FT, bool WIDE>
+__global__ __launch_bounds__(kFewWaves * 64) void k_block_few(ProductArgs p) {
+  __shared__ f32x4 sums[kFewWaves][FN * FT][64];
+  const GroupTile gt = find_group_tile(p.rg, blockIdx.y, 16 * FT);
+  if (gt.group < 0) return;
+  const int lane = threadIdx.x & 63, w = wave_id(), l16 = lane & 15, part = lane >> 4;
+  const int n0 = blockIdx.x * (16 * FN), blocks = (p.n + kBlk - 1) / kBlk;
+  const uint8_t* a[FN];
+  const uint8_t* b[FT];
+  const float* bs[FT];
+  // (rows past the last are the last one's: their results are not stored)
+#pragma unroll
+  for (int i = 0; i < FN; ++i)
+    a[i] = p.a + (int64_t(gt.group) * p.n + min(n0 + 16 * i + l16, p.n - 1)) * p.stride + part * 32;
+#pragma unroll
+  for (int j = 0; j < FT; ++j) {
+    const int64_t row = gt.row0 + min(16 * j + l16, gt.rows - 1);
+    b[j] = p.b + row * p.stride + part * 32;
+    bs[j] = p.bs + row;
+  }
+  const float* as = p.as + (int64_t(gt.group) * blocks + n0 / kBlk) * p.kb;
+  f32x4 acc[FN][FT];
+#pragma unroll
+  for (int i = 0; i < FN; ++i)
+#pragma unroll
+    for (int j = 0; j < FT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  constexpr int kAhead = FN + FT <= 3 ? 4 : 2;
+  for (int k0 = w; k0 < p.kb; k0 += kFewWaves * kAhead) {
+    FewCodes ca[kAhead][FN], cb[kAhead][FT];
+    float sa[kAhead], sb[kAhead][FT];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int k = k0 + u * kFewWaves, at = min(k, p.kb - 1);   // (past the end a block once more, with a scale of zero)
+#pragma unroll
+      for (int i = 0; i < FN; ++i) ca[u][i] = load_few(a[i] + int64_t(at) * kBlk);
+#pragma unroll
+      for (int j = 0; j < FT; ++j) {
+        cb[u][j] = load_few(b[j] + int64_t(at) * kBlk);
+        sb[u][j] = bs[j][int64_t(at) * p.rg.rows];
+      }
+      sa[u] = as[at];
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (k0 + u * kFewWaves >= p.kb) break;
+#pragma unroll
+      for (int j = 0; j < FT; ++j) {
+        const float s = sa[u] * sb[u][j];
+#pragma unroll
+        for (int i = 0; i < FN; ++i) {
+          const f32x4 y = few_product<WIDE>(ca[u][i], cb[u][j]);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(y[v], s, acc[i][j][v]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < FN; ++i)
+#pragma unroll
+    for (int j = 0; j < FT; ++j) sums[w][i * FT + j][lane] = acc[i][j];
+  __syncthreads();
+  // lane l of a block: token l % 16, weight rows 4 (l / 16) ..
+  for (int q = threadIdx.x; q < FN * FT * 64; q += kFewWaves * 64) {
+    const int f = q >> 6, l = q & 63, i = f / FT, j = f % FT;
+    f32x4 y = sums[0][f][l];
+#pragma unroll
+    for (int u = 1; u < kFewWaves; ++u) y += sums[u][f][l];
+    const int r = 16 * j + (l & 15), c = n0 + 16 * i + 4 * (l >> 4);
+    if (r >= gt.rows) continue;
+    const int64_t at = (gt.row0 + r) * p.out_stride + c;
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      if (c + v < p.n) {
+        if constexpr (WIDE) static_cast<float*>(p.out)[at + v] = y[v];
+        else static_cast<uint16_t*>(p.out)[at + v] = f2bf(y[v]);
+      }
+  }
+}
+
+template <int FN, int FT>
+hipError_t launch_few(const ProductArgs& p, hipStream_t s) {
+  const dim3 grid(unsigned(cdiv(p.n, 16 * FN)), unsigned(group_tiles_max(p.rg.rows, p.rg.groups, 16 * FT)));
+  if (p.bf16) k_block_few<FN, FT, false><<<grid, kFewWaves * 64, 0, s>>>(p);
+  else k_block_few<FN, FT, true><<<grid, kFewWaves * 64, 0, s>>>(p);
+  return hipGetLastError();
+}
+
+// Weight rows of a workgroup: 64, 32 or 16, the most that leave a workgroup for every CU (the more of them, the less
+// often the tokens' codes are read).
+template <int FT>
+hipError_t launch_few_n(const ProductArgs& p, hipStream_t s) {
+  const int64_t tiles = group_tiles_max(p.rg.rows, p.rg.groups, 16 * FT);
+  if (cdiv(p.n, 64) * tiles >= 256) return launch_few<4, FT>(p, s);
+  return cdiv(p.n, 32) * tiles >= 256 ? launch_few<2, FT>(p, s) : launch_few<1, FT>(p, s);
+}
+
 using Mid = Shape<2, 2, 2, 2>;    // 128 x 128
 using Wide = Shape<4, 2, 2, 4>;   // 256 x 256
+
+template <class S, bool WIDE>
+hipError_t launch_tiles(ProductArgs p, hipStream_t s) {
+  p.tiles_n = int(cdiv(p.n, S::kA));
+  return launch_product<S, false, WIDE>(p, align_up(group_tiles_max(p.rg.rows, p.rg.groups, S::kB) * p.tiles_n, kXcds), s);
+}
+
+// Which kernel: the one that these estimates call fastest, in microseconds. The tile kernels take so long for a stage of
+// the sum (alone on a CU, or beside another workgroup) and for a tile's beginning and end, in rounds of as many tiles as
+// run at once; the kernel for few rows is bound by what its workgroups read, at 9.5 TB/s from the L2 caches. Measured, bf16:
+// 6 experts of 7168 x 2048: 44 rows 18.9 (few) against 23.4 (128 x 128), 384 rows 23 (128 x 128), 3,000 rows 66 (128 x 128);
+// one of 4096 x 7168: 64 rows 20 (few), 512 rows 49 (128 x 128) against 59 (few); 4 experts, 16,384 rows 505 (256 x 256)
+// against 610 (128 x 128).
+int64_t few_tokens(const mok_block_desc& d) {   // blocks of 16 tokens that a workgroup takes
+  const int64_t each = d.rows / d.groups;
+  return each <= 16 ? 1 : each <= 32 ? 2 : 4;
+}
+double few_us(const mok_block_desc& d, int64_t ft) {
+  const int64_t tiles = cdiv(d.rows, 16 * ft) + (d.groups > 1 ? std::min<int64_t>(d.rows, d.groups) / 2 : 0);
+  const int64_t fn = cdiv(d.n, 64) * tiles >= 256 ? 4 : cdiv(d.n, 32) * tiles >= 256 ? 2 : 1;
+  return double(tiles * cdiv(d.n, 16 * fn) * cdiv(d.k, kBlk) * (fn + ft) * 2048) / 9.5e6 + 3.0;
+}
+template <class S>
+double tiles_us(const mok_block_desc& d, int per_cu, double alone, double beside, double tile) {
+  // (groups end inside tiles: half a tile each on average)
+  const int64_t rows = cdiv(d.rows, S::kB) + (d.groups > 1 ? std::min<int64_t>(d.rows, d.groups) / 2 : 0);
+  const int64_t tiles = rows * cdiv(d.n, S::kA);
+  const double each = double(cdiv(d.k, kBlk)) * (tiles <= 256 ? alone : beside) + tile;
+  return each * (per_cu == 1 ? double(cdiv(tiles, 256)) : std::max(1.0, double(tiles) / (256 * per_cu) + 0.3));
+}
 
 }  // namespace
 
@@ -408,15 +571,15 @@ hipError_t launch_block_gemm(const mok_block_desc& d, const uint8_t* x, const fl
   p.n = d.n;
   p.k = d.k;
   p.bf16 = d.elem == MOK_ELEM_BF16;
-  if (p.bf16 && d.rows >= 8192) {
-    using S = Wide;
-    p.tiles_n = int(cdiv(d.n, S::kA));
-    return launch_product<S, false, false>(p, group_tiles_max(d.rows, d.groups, S::kB) * p.tiles_n, s);
+  const int64_t few_ft = few_tokens(d);
+  const double few = few_us(d, few_ft), mid = tiles_us<Mid>(d, 2, p.bf16 ? 0.77 : 1.1, p.bf16 ? 1.1 : 1.5, 3.0),
+               wide = p.bf16 ? tiles_us<Wide>(d, 1, 1.7, 1.7, 10.0) : INFINITY;
+  if (few <= mid && few <= wide) {
+    if (few_ft == 1) return launch_few_n<1>(p, s);
+    return few_ft == 2 ? launch_few_n<2>(p, s) : launch_few_n<4>(p, s);
   }
-  using S = Mid;
-  p.tiles_n = int(cdiv(d.n, S::kA));
-  const int64_t tiles = group_tiles_max(d.rows, d.groups, S::kB) * p.tiles_n;
-  return p.bf16 ? launch_product<S, false, false>(p, tiles, s) : launch_product<S, false, true>(p, tiles, s);
+  if (!p.bf16) return launch_tiles<Mid, true>(p, s);
+  return mid <= wide ? launch_tiles<Mid, false>(p, s) : launch_tiles<Wide, false>(p, s);
 }
 
 hipError_t launch_block_wgrad(const mok_block_desc& d, const uint8_t* dy, const float* dys, const uint8_t* x,
