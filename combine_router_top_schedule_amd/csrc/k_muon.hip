@@ -185,19 +185,27 @@ __global__ __launch_bounds__(256) void k_muon_start(MuArgs a) {
   const bool turn = b.turned(it);
   _Float16 *hs = b.s(ws, turn, 0), *lo = b.lo(ws), *ht = b.t(ws, turn, 0);
   const int c = threadIdx.x & 63;
-#pragma unroll 4
-  for (int r = threadIdx.x >> 6; r < 64; r += 4) {
-    float u = 0.f;
-    if (r0 + r < it.rows && c0 + c < it.cols) {
-      const int64_t i = (it.e0 + e) * size + int64_t(r0 + r) * it.cols + c0 + c;
-      if (it.m) {
-        const float m = it.m[i];
-        u = a.nesterov ? element(it.g, a.gbf, i) * clip + a.mu * m : m;
-      } else {
-        u = element(it.g, a.gbf, i) * clip;
-      }
-    }
-    const float x = u * f;
+  const int wv = threadIdx.x >> 6;
+  const auto at_edge = [&](int k) {   // (outside: an element of the edge, which is not used)
+    return (it.e0 + e) * size + int64_t(min(r0 + wv + 4 * k, it.rows - 1)) * it.cols + min(c0 + c, it.cols - 1);
+  };
+  float g[16], m[16];
+  if (a.gbf) {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) g[k] = bf2f(static_cast<const uint16_t*>(it.g)[at_edge(k)]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) g[k] = static_cast<const float*>(it.g)[at_edge(k)];
+  }
+  if (it.m)
+#pragma unroll
+    for (int k = 0; k < 16; ++k) m[k] = it.m[at_edge(k)];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const int r = wv + 4 * k;
+    float u = g[k] * clip;
+    if (it.m) u = a.nesterov ? u + a.mu * m[k] : m[k];
+    const float x = r0 + r < it.rows && c0 + c < it.cols ? u * f : 0.f;
     const _Float16 h = _Float16(x);
     const int64_t at = int64_t(r0 + r) * b.cols + c0 + c;
     hs[at] = h;
@@ -310,23 +318,52 @@ __global__ __launch_bounds__(S::kWaves * 64) void k_muon_gram(MuArgs a) {
   for (int i = 0; i < S::FA; ++i)
 #pragma unroll
     for (int j = 0; j < S::FB; ++j) {
-      const int c = j0 + (wb * S::FB + j) * 32 + (lane & 31);
-      if (c >= j0 + nj) continue;
+      const int r0 = i0 + (wa * S::FA + i) * 32 + 4 * half, c = j0 + (wb * S::FB + j) * 32 + (lane & 31);
+      if ((wa * S::FA + i) * 32 >= ni || (wb * S::FB + j) * 32 >= nj) continue;   // (padded sizes are multiples of 128)
+      _Float16 z[16];
+      if constexpr (SECOND)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) z[v] = old[int64_t(r0 + 8 * (v >> 2) + (v & 3)) * b.m + c];
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
-        const int r = i0 + (wa * S::FA + i) * 32 + 8 * v + 4 * half;
-        if (r >= i0 + ni) continue;
         f16x4 y;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          float z = acc[i][j][4 * v + u];
-          z = SECOND ? a.c * z + a.b * float(old[int64_t(r + u) * b.m + c]) : z * down;
-          y[u] = _Float16(z);
-          out[int64_t(r + u) * b.m + c] = y[u];
+          const float g = acc[i][j][4 * v + u];
+          y[u] = _Float16(SECOND ? a.c * g + a.b * float(z[4 * v + u]) : g * down);
+          out[int64_t(r0 + 8 * v + u) * b.m + c] = y[u];
         }
-        if (ti != tj) *reinterpret_cast<f16x4*>(out + int64_t(c) * b.m + r) = y;
+        if (ti != tj) *reinterpret_cast<f16x4*>(out + int64_t(c) * b.m + r0 + 8 * v) = y;
       }
     }
+}
+
+// The update of parameters (or the output) by results value(v) at row r0 + row(v) of column c, v < N. All parameters are loaded
+// before any is used, those outside the matrix from its edge.
+template <int N, class R, class V>
+__device__ __forceinline__ void store_results(const MuItem& it, int64_t base, int r0, int c, R&& row, V&& value, float decay,
+                                              float rate) {
+  const auto at = [&](int v) { return base + int64_t(min(r0 + row(v), it.rows - 1)) * it.cols + min(c, it.cols - 1); };
+  const auto inside = [&](int v) { return r0 + row(v) < it.rows && c < it.cols; };
+  if (it.m) {
+    float* p = static_cast<float*>(it.p);
+    float y[N];
+#pragma unroll
+    for (int v = 0; v < N; ++v) y[v] = p[at(v)];
+#pragma unroll
+    for (int v = 0; v < N; ++v) {
+      y[v] = y[v] * decay - value(v) * rate;
+      if (inside(v)) p[at(v)] = y[v];
+    }
+    if (it.copy)
+#pragma unroll
+      for (int v = 0; v < N; ++v)
+        if (inside(v)) it.copy[at(v)] = f2bf(y[v]);
+  } else {
+#pragma unroll
+    for (int v = 0; v < N; ++v)
+      if (inside(v)) static_cast<uint16_t*>(it.p)[at(v)] = f2bf(value(v) * rate);
+  }
 }
 
 // X <- a X + B X, as the parameters lie; LAST: the update of the parameters (or the output) by it instead.
@@ -361,39 +398,280 @@ __global__ __launch_bounds__(S::kWaves * 64) void k_muon_apply(MuArgs a) {
   for (int i = 0; i < S::FA; ++i)
 #pragma unroll
     for (int j = 0; j < S::FB; ++j) {
-      const int c = j0 + (wb * S::FB + j) * 32 + (lane & 31);
-      if (c >= j0 + nj) continue;
+      const int r0 = i0 + (wa * S::FA + i) * 32 + 4 * half, c = j0 + (wb * S::FB + j) * 32 + (lane & 31);
+      if ((wa * S::FA + i) * 32 >= ni || (wb * S::FB + j) * 32 >= nj) continue;   // (padded sizes are multiples of 128)
+      const auto row = [](int v) { return 8 * (v >> 2) + (v & 3); };
+      _Float16 xh[16], xl[16];
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int r = i0 + (wa * S::FA + i) * 32 + 8 * v + 4 * half;
-        if (r >= i0 + ni) continue;
-        f16x4 h4;
+      for (int v = 0; v < 16; ++v) {
+        const int64_t at = int64_t(r0 + row(v)) * b.cols + c;
+        xh[v] = hi[at];
+        xl[v] = lo[at];
+      }
+      float x[16];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int64_t at = int64_t(r + u) * b.cols + c;
-          const float x = a.a * (float(hi[at]) + float(lo[at])) + acc[i][j][4 * v + u];
-          if constexpr (LAST) {
-            if (r + u < it.rows && c < it.cols) {
-              const int64_t o = base + int64_t(r + u) * it.cols + c;
-              if (it.m) {
-                float* p = static_cast<float*>(it.p);
-                const float y = p[o] * decay - x * rate;
-                p[o] = y;
-                if (it.copy) it.copy[o] = f2bf(y);
-              } else {
-                static_cast<uint16_t*>(it.p)[o] = f2bf(x * rate);
-              }
-            }
-          } else {
-            const _Float16 h = _Float16(x);
+      for (int v = 0; v < 16; ++v) x[v] = a.a * (float(xh[v]) + float(xl[v])) + acc[i][j][v];
+      if constexpr (LAST) {
+        store_results<16>(it, base, r0, c, row, [&](int v) { return x[v]; }, decay, rate);
+      } else {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          f16x4 h4;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int64_t at = int64_t(r0 + 8 * v + u) * b.cols + c;
+            const _Float16 h = _Float16(x[4 * v + u]);
             h4[u] = h;
             hs[at] = h;
-            lw[at] = _Float16(x - float(h));
+            lw[at] = _Float16(x[4 * v + u] - float(h));
           }
+          *reinterpret_cast<f16x4*>(ht + int64_t(c) * b.rows + r0 + 8 * v) = h4;
         }
-        if constexpr (!LAST) *reinterpret_cast<f16x4*>(ht + int64_t(c) * b.rows + r) = h4;
       }
     }
+}
+
+// ---- small matrices -----------------------------------------------------------------------------
+// A matrix whose X and X^T in fp16 fit the LDS beside A takes one workgroup and one launch for everything: X stays in
+// registers in fp32, its fp16 copies, A and then B in LDS. Launches and the way through memory bound the general kernels at
+// such sizes (25 matrices of 256 x 128 and less: 222 us in 17 launches, SMALL_US us here).
+//
+// X is cut into 32 x 32 blocks, 1..4 along its shorter side and up to 32 along the longer one. Wave w takes the
+// longer side's blocks w, w + 8, ..., for each of them all of the shorter side's: four slots at most, which share the
+// operand of their longer side.
+struct SmallShape {
+  int rows, cols, m, n, shorter, longer;   // sizes rounded up to 32, and in blocks
+  __host__ __device__ SmallShape(int r, int c) {
+    rows = int(align_up(r, 32));
+    cols = int(align_up(c, 32));
+    m = rows < cols ? rows : cols;
+    n = rows < cols ? cols : rows;
+    shorter = m / 32;
+    longer = n / 32;
+  }
+  __host__ __device__ bool fits() const { return shorter <= 4 && (longer + 7) / 8 * shorter <= 4; }
+  __host__ __device__ int lds() const { return (2 * m * n + m * m) * 2; }
+};
+
+// Element (row, col) of a matrix in LDS whose rows have `len` halves (a multiple of 32): 16-byte chunks are swapped
+// within runs of 8 (4 where rows are no multiple of 8 chunks) by the row, so that 32 rows of one chunk spread over the banks.
+__device__ __forceinline__ int small_at(int row, int col, int len) {
+  const int mask = len & 63 ? 3 : 7;
+  return row * len + (((col >> 3) ^ (row & mask)) << 3) + (col & 7);
+}
+// A lane's part of a row as an operand: chunk c of it.
+struct SmallRow {
+  const _Float16* p;
+  int turn;
+  __device__ __forceinline__ SmallRow(const _Float16* x, int row, int len)
+      : p(x + row * len), turn(row & (len & 63 ? 3 : 7)) {}
+  __device__ __forceinline__ f16x8 operator()(int c) const { return *reinterpret_cast<const f16x8*>(p + ((c ^ turn) << 3)); }
+};
+
+// N results of 32 rows each, a[i] times b[i / EACH] (or in the other order), over `len` halves; the next slice's operands
+// are read while one is multiplied.
+template <int N, int EACH, bool SWAP>
+__device__ __forceinline__ void small_products(const SmallRow* a, const SmallRow* b, int len, f32x16 (&acc)[N]) {
+  const int half = (threadIdx.x & 63) >> 5;
+  constexpr int M = (N + EACH - 1) / EACH;
+  f16x8 fa[2][N], fb[2][M];
+  const auto load = [&](int buf, int c) {
+#pragma unroll
+    for (int j = 0; j < M; ++j) fb[buf][j] = b[j](c + half);
+#pragma unroll
+    for (int i = 0; i < N; ++i) fa[buf][i] = a[i](c + half);
+  };
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int v = 0; v < 16; ++v) acc[i][v] = 0.f;
+  const int last = len / 8 - 2;
+  load(0, 0);
+#pragma unroll 1
+  for (int c = 0; c <= last; c += 4)   // (two slices, as len is a multiple of 32)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      load(u ^ 1, min(c + 2 * u + 2, last));
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        acc[i] = SWAP ? __builtin_amdgcn_mfma_f32_32x32x16_f16(fb[u][i / EACH], fa[u][i], acc[i], 0, 0, 0)
+                      : __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[u][i], fb[u][i / EACH], acc[i], 0, 0, 0);
+    }
+}
+
+struct MuSteps {
+  int32_t count;
+  float coef[16][3];
+};
+
+// SHORTER: blocks along the shorter side; TURN: that is the columns' side.
+template <int SHORTER, bool TURN>
+__device__ __forceinline__ void muon_small(const MuArgs& a, const MuSteps& st, const MuItem& it, int e) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  constexpr int N = SHORTER == 3 ? 3 : 4;   // slots
+  const SmallShape sh(it.rows, it.cols);
+  _Float16 *xs = reinterpret_cast<_Float16*>(smem), *xt = xs + sh.m * sh.n, *gram = xt + sh.m * sh.n;
+  const int lane = threadIdx.x & 63, w = wave_id(), half = lane >> 5, l32 = lane & 31;
+  const int64_t base = int64_t(it.e0 + e) * it.rows * it.cols;
+  const float scale = mu_scale(it.rows, it.cols), down = 1.f / (scale * scale), clip = clip_factor(a);
+  // element v of slot q is row rq(q) + 8 (v / 4) + 4 half + v % 4, column cq(q) + l32
+  const auto rq = [&](int q) { return (TURN ? w + 8 * (q / SHORTER) : q % SHORTER) * 32; };
+  const auto cq = [&](int q) { return (TURN ? q % SHORTER : w + 8 * (q / SHORTER)) * 32; };
+  float x[N][16];
+  bool live[N];
+  double sum = 0;
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    live[q] = w + 8 * (q / SHORTER) < sh.longer;
+    const int r0 = rq(q) + 4 * half, c0 = cq(q) + l32;
+    float g[16], m[16];
+    const auto inside = [&](int v) { return r0 + 8 * (v >> 2) + (v & 3) < it.rows && c0 < it.cols; };
+    const auto at = [&](int v) {   // (outside: another element of the matrix, which is not used)
+      return base + int64_t(min(r0 + 8 * (v >> 2) + (v & 3), it.rows - 1)) * it.cols + min(c0, it.cols - 1);
+    };
+    // (a branch for all loads of a kind and none around single ones, which would be waited for one by one)
+    if (a.gbf) {
+#pragma unroll
+      for (int v = 0; v < 16; ++v) g[v] = bf2f(static_cast<const uint16_t*>(it.g)[at(v)]);
+    } else {
+#pragma unroll
+      for (int v = 0; v < 16; ++v) g[v] = static_cast<const float*>(it.g)[at(v)];
+    }
+    if (it.m)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) m[v] = it.m[at(v)];
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+      float u = g[v] * clip;
+      if (it.m) {
+        m[v] = m[v] * a.mu + u;
+        if (inside(v)) it.m[at(v)] = m[v];
+        u = a.nesterov ? u + a.mu * m[v] : m[v];
+      }
+      x[q][v] = inside(v) ? u : 0.f;
+      sum = fma(double(x[q][v]), double(x[q][v]), sum);
+    }
+  }
+  for (int off = 32; off; off >>= 1) sum += __shfl_xor(sum, off, 64);
+  double* sums = reinterpret_cast<double*>(gram);
+  if (lane == 0) sums[w] = sum;
+  __syncthreads();
+  double norm = 0;
+  for (int k = 0; k < 8; ++k) norm += sums[k];
+  const float f = float(double(scale) / (sqrt(norm) + a.eps));
+#pragma unroll
+  for (int q = 0; q < N; ++q)
+#pragma unroll
+    for (int v = 0; v < 16; ++v) x[q][v] *= f;
+  constexpr int G = SHORTER * SHORTER > 8 ? 2 : 1;
+  int gr[G], gc[G];
+  bool glive[G];
+#pragma unroll
+  for (int q = 0; q < G; ++q) {
+    const int b = w + 8 * q;
+    glive[q] = b < SHORTER * SHORTER;
+    gr[q] = glive[q] ? b / SHORTER * 32 : 0;
+    gc[q] = glive[q] ? b % SHORTER * 32 : 0;
+  }
+  // (addresses in LDS are formed anew where they are used: hoisted out of the loop they would fill the registers)
+  const auto put_gram = [&](const f32x16 (&g)[G]) {
+    const int tid = tile_tid(), h = (tid >> 5) & 1, c = tid & 31;
+#pragma unroll
+    for (int q = 0; q < G; ++q)
+      if (glive[q])
+#pragma unroll
+        for (int v = 0; v < 16; ++v)
+          gram[small_at(gr[q] + 8 * (v >> 2) + 4 * h + (v & 3), gc[q] + c, sh.m)] = _Float16(g[q][v]);
+  };
+  const _Float16 *across_rows = TURN ? xt : xs, *along_rows = TURN ? xs : xt;   // rows of n, and of m halves
+#pragma unroll 1
+  for (int k = 0; k < st.count; ++k) {
+    const float ca = st.coef[k][0], cb = st.coef[k][1], cc = st.coef[k][2];
+    {
+      const int tid = tile_tid(), h = (tid >> 5) & 1, c = tid & 31;
+#pragma unroll
+      for (int q = 0; q < N; ++q)
+        if (live[q])
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const int r = rq(q) + 8 * v + 4 * h;
+            f16x4 y;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              y[u] = _Float16(x[q][4 * v + u]);
+              xs[small_at(r + u, cq(q) + c, sh.cols)] = y[u];
+            }
+            *reinterpret_cast<f16x4*>(xt + small_at(cq(q) + c, r, sh.rows)) = y;
+          }
+    }
+    __syncthreads();
+    // A, then B in its place: the wave's blocks w and w + 8 of SHORTER x SHORTER
+    f32x16 g[G];
+    if (glive[0]) {
+      const int l = tile_tid() & 31;
+      const SmallRow left[2] = {SmallRow(across_rows, gr[0] + l, sh.n), SmallRow(across_rows, gr[G - 1] + l, sh.n)};
+      const SmallRow right[2] = {SmallRow(across_rows, gc[0] + l, sh.n), SmallRow(across_rows, gc[G - 1] + l, sh.n)};
+      small_products<G, 1, false>(left, right, sh.n, g);
+#pragma unroll
+      for (int q = 0; q < G; ++q) g[q] *= down;
+      put_gram(g);
+    }
+    __syncthreads();
+    if (glive[0]) {
+      const int l = tile_tid() & 31;
+      const SmallRow left[2] = {SmallRow(gram, gr[0] + l, sh.m), SmallRow(gram, gr[G - 1] + l, sh.m)};
+      const SmallRow right[2] = {SmallRow(gram, gc[0] + l, sh.m), SmallRow(gram, gc[G - 1] + l, sh.m)};
+      f32x16 y[G];
+      small_products<G, 1, false>(left, right, sh.m, y);
+#pragma unroll
+      for (int q = 0; q < G; ++q) g[q] = cc * y[q] + cb * g[q];
+    }
+    __syncthreads();
+    if (glive[0]) put_gram(g);
+    __syncthreads();
+    if (live[0]) {
+      const int l = tile_tid() & 31;
+      const auto along = [&](int j) { return SmallRow(along_rows, min(w + 8 * j, sh.longer - 1) * 32 + l, sh.m); };
+      const auto across = [&](int q) { return SmallRow(gram, q % SHORTER * 32 + l, sh.m); };
+      const SmallRow ra[4] = {across(0), across(1), across(2), across(3)};
+      const SmallRow rb[4] = {along(0), along(1), along(2), along(3)};
+      f32x16 y[N];
+      small_products<N, SHORTER, TURN>(ra, rb, sh.m, y);
+#pragma unroll
+      for (int q = 0; q < N; ++q)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) x[q][v] = ca * x[q][v] + y[q][v];
+    }
+    __syncthreads();
+  }
+  const double lr = a.lr_dev ? *a.lr_dev : a.lr;
+  const float decay = float(1.0 - lr * a.weight_decay), rate = it.m ? float(lr * it.adjust / scale) : 1.f / scale;
+#pragma unroll
+  for (int q = 0; q < N; ++q)
+    if (live[q]) {
+      const int r0 = rq(q) + 4 * half, c = cq(q) + l32;
+      store_results<16>(it, base, r0, c, [](int v) { return 8 * (v >> 2) + (v & 3); }, [&](int v) { return x[q][v]; }, decay,
+                        rate);
+    }
+}
+
+__global__ __launch_bounds__(512) void k_muon_small(MuArgs a, MuSteps st) {
+  if (left_out(a)) return;
+  const int t = find_item(a, blockIdx.x);
+  const MuItem& it = a.item[t];
+  const int e = blockIdx.x - a.first[t], shorter = SmallShape(it.rows, it.cols).shorter;
+  const bool turn = it.rows > it.cols;
+  if (turn) {
+    if (shorter == 1) muon_small<1, true>(a, st, it, e);
+    else if (shorter == 2) muon_small<2, true>(a, st, it, e);
+    else if (shorter == 3) muon_small<3, true>(a, st, it, e);
+    else muon_small<4, true>(a, st, it, e);
+  } else {
+    if (shorter == 1) muon_small<1, false>(a, st, it, e);
+    else if (shorter == 2) muon_small<2, false>(a, st, it, e);
+    else if (shorter == 3) muon_small<3, false>(a, st, it, e);
+    else muon_small<4, false>(a, st, it, e);
+  }
 }
 
 using MuMid = MuShape<2, 2, 2, 2>;   // 128 x 128
@@ -456,16 +734,19 @@ struct MuPart {
   int64_t ws;                 // offset of their buffers
 };
 
-int64_t matrix_bytes(const mok_muon_tensor& t) { return align_up(MuBuffers(t.rows, t.cols).bytes(), 256); }
+int64_t matrix_bytes(const mok_muon_tensor& t, bool small) {
+  return small ? 0 : align_up(MuBuffers(t.rows, t.cols).bytes(), 256);
+}
 
-// Calls go(parts, count, bytes) for each run; stops at an error.
+// Calls go(parts, count, bytes) for each run of the small tensors, or of the others; stops at an error.
 template <class G>
-hipError_t each_run(int count, const mok_muon_tensor* t, G&& go) {
+hipError_t each_run(int count, const mok_muon_tensor* t, bool small, G&& go) {
   MuPart part[kMuItems];
   int n = 0;
   int64_t bytes = 0;
   for (int k = 0; k < count; ++k) {
-    const int64_t one = matrix_bytes(t[k]);
+    if (SmallShape(t[k].rows, t[k].cols).fits() != small) continue;
+    const int64_t one = matrix_bytes(t[k], small);
     for (int b = 0; b < t[k].batch;) {
       if (n == kMuItems || (n > 0 && bytes + one > kMuWs)) {
         const hipError_t e = go(part, n, bytes);
@@ -473,7 +754,8 @@ hipError_t each_run(int count, const mok_muon_tensor* t, G&& go) {
         n = 0;
         bytes = 0;
       }
-      const int take = int(std::min<int64_t>(t[k].batch - b, std::max<int64_t>(1, (kMuWs - bytes) / one)));
+      const int64_t room = small ? t[k].batch : std::max<int64_t>(1, (kMuWs - bytes) / one);
+      const int take = int(std::min<int64_t>(t[k].batch - b, room));
       part[n++] = MuPart{k, b, take, bytes};
       bytes += take * one;
       b += take;
@@ -492,7 +774,7 @@ double adjustment(int rule, int rows, int cols) {
 
 int64_t muon_ws_bytes(int count, const mok_muon_tensor* t) {
   int64_t most = 0;
-  (void)each_run(count, t, [&](const MuPart*, int, int64_t bytes) {
+  (void)each_run(count, t, false, [&](const MuPart*, int, int64_t bytes) {
     most = std::max(most, bytes);
     return hipSuccess;
   });
@@ -500,7 +782,7 @@ int64_t muon_ws_bytes(int count, const mok_muon_tensor* t) {
 }
 
 hipError_t launch_muon(int count, const mok_muon_tensor* t, const mok_muon_config& c, uint8_t* ws, hipStream_t s) {
-  return each_run(count, t, [&](const MuPart* part, int n, int64_t) {
+  const auto arguments = [&](const MuPart* part, int n) {
     MuArgs a{};
     for (int k = 0; k < n; ++k) {
       const mok_muon_tensor& x = t[part[k].tensor];
@@ -517,17 +799,40 @@ hipError_t launch_muon(int count, const mok_muon_tensor* t, const mok_muon_confi
     a.max_norm = c.max_norm;
     a.sumsq = c.sumsq_dev;
     a.lr_dev = c.lr_dev;
-    hipError_t e = run(k_muon_norm, a, 256, 0, s, [](const MuItem& it) {
+    return a;
+  };
+  hipError_t e = each_run(count, t, true, [&](const MuPart* part, int n, int64_t) {
+    static std::atomic<bool> done[kMaxDevices];
+    const hipError_t e0 = allow_lds(k_muon_small, 160 << 10, done);
+    if (e0 != hipSuccess) return e0;
+    MuArgs a = arguments(part, n);
+    MuSteps st{};
+    st.count = c.ns.steps;
+    std::copy_n(&c.ns.coefficients[0][0], 3 * st.count, &st.coef[0][0]);
+    int lds = 0, matrices = 0;
+    for (int k = 0; k < n; ++k) {
+      lds = std::max(lds, SmallShape(a.item[k].rows, a.item[k].cols).lds());
+      a.first[k] = matrices;
+      matrices += a.item[k].batch;
+    }
+    a.first[n] = matrices;
+    k_muon_small<<<matrices, 512, lds, s>>>(a, st);
+    return hipGetLastError();
+  });
+  if (e != hipSuccess) return e;
+  return each_run(count, t, false, [&](const MuPart* part, int n, int64_t) {
+    MuArgs a = arguments(part, n);
+    hipError_t e1 = run(k_muon_norm, a, 256, 0, s, [](const MuItem& it) {
       const int64_t size = int64_t(it.rows) * it.cols;
       return cdiv(size, mu_chunk(size));
     });
-    if (e == hipSuccess)
-      e = run(k_muon_start, a, 256, 0, s, [](const MuItem& it) {
+    if (e1 == hipSuccess)
+      e1 = run(k_muon_start, a, 256, 0, s, [](const MuItem& it) {
         const MuBuffers b(it.rows, it.cols);
         return int64_t(b.rows / 64) * (b.cols / 64);
       });
-    if (e == hipSuccess) e = steps<MuMid>(a, c.ns.steps, &c.ns.coefficients[0][0], s);
-    return e;
+    if (e1 == hipSuccess) e1 = steps<MuMid>(a, c.ns.steps, &c.ns.coefficients[0][0], s);
+    return e1;
   });
 }
 
