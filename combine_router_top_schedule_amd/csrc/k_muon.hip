@@ -162,6 +162,76 @@ __global__ __launch_bounds__(256) void k_muon_norm(MuArgs a) {
   }
 }
 
+// A window of rows of a tensor's matrix, from element `first` on: buffer accesses whose bounds are the window's, so that
+// elements outside read as zero and are not written, without branches (around single loads, each would be waited for
+// before the next).
+struct MuWindow {
+  int64_t first, count;   // elements
+  int cols;
+  __device__ __forceinline__ MuWindow(const MuItem& it, int64_t first_, int rows)
+      : first(first_), count(int64_t(rows) * it.cols), cols(it.cols) {}
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t of(const void* p, int size) const {
+    return make_rsrc(static_cast<const uint8_t*>(p) + first * size, count * size);
+  }
+  // of row r and column c; beyond the window's end where c is beyond its columns
+  __device__ __forceinline__ int at(int r, int c) const { return c < cols ? r * cols + c : 1 << 28; }
+};
+__device__ __forceinline__ float load_f32(__amdgpu_buffer_rsrc_t r, int i) {
+  return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, i * 4, 0, 0));
+}
+__device__ __forceinline__ float load_bf16(__amdgpu_buffer_rsrc_t r, int i) {
+  return bf2f(uint16_t(__builtin_amdgcn_raw_buffer_load_b16(r, i * 2, 0, 0)));
+}
+__device__ __forceinline__ void store_f32(__amdgpu_buffer_rsrc_t r, int i, float v) {
+  __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), r, i * 4, 0, 0);
+}
+__device__ __forceinline__ void store_bf16(__amdgpu_buffer_rsrc_t r, int i, float v) {
+  __builtin_amdgcn_raw_buffer_store_b16(f2bf(v), r, i * 2, 0, 0);
+}
+
+// N gradients (or source elements) of rows r0 + row(v) of column c.
+template <int N, class R>
+__device__ __forceinline__ void load_gradients(const MuArgs& a, const MuItem& it, const MuWindow& win, int r0, int c, R&& row,
+                                               float (&g)[N]) {
+  const int at = win.at(r0, c);
+  if (a.gbf) {
+    const __amdgpu_buffer_rsrc_t r = win.of(it.g, 2);
+#pragma unroll
+    for (int v = 0; v < N; ++v) g[v] = load_bf16(r, at + row(v) * win.cols);
+  } else {
+    const __amdgpu_buffer_rsrc_t r = win.of(it.g, 4);
+#pragma unroll
+    for (int v = 0; v < N; ++v) g[v] = load_f32(r, at + row(v) * win.cols);
+  }
+}
+
+// The update of parameters (or the output) by results value(v) at rows r0 + row(v) of column c.
+template <int N, class R, class V>
+__device__ __forceinline__ void store_results(const MuItem& it, const MuWindow& win, int r0, int c, R&& row, V&& value,
+                                              float decay, float rate) {
+  const int at = win.at(r0, c);
+  if (it.m) {
+    const __amdgpu_buffer_rsrc_t p = win.of(it.p, 4);
+    float y[N];
+#pragma unroll
+    for (int v = 0; v < N; ++v) y[v] = load_f32(p, at + row(v) * win.cols);
+#pragma unroll
+    for (int v = 0; v < N; ++v) {
+      y[v] = y[v] * decay - value(v) * rate;
+      store_f32(p, at + row(v) * win.cols, y[v]);
+    }
+    if (it.copy) {
+      const __amdgpu_buffer_rsrc_t q = win.of(it.copy, 2);
+#pragma unroll
+      for (int v = 0; v < N; ++v) store_bf16(q, at + row(v) * win.cols, y[v]);
+    }
+  } else {
+    const __amdgpu_buffer_rsrc_t q = win.of(it.p, 2);
+#pragma unroll
+    for (int v = 0; v < N; ++v) store_bf16(q, at + row(v) * win.cols, value(v) * rate);
+  }
+}
+
 // ---- X_0 ------------------------------------------------------------------------------------------
 // 64 x 64 elements a workgroup, written as they lie and turned, zeros in the padding.
 __global__ __launch_bounds__(256) void k_muon_start(MuArgs a) {
@@ -186,26 +256,21 @@ __global__ __launch_bounds__(256) void k_muon_start(MuArgs a) {
   _Float16 *hs = b.s(ws, turn, 0), *lo = b.lo(ws), *ht = b.t(ws, turn, 0);
   const int c = threadIdx.x & 63;
   const int wv = threadIdx.x >> 6;
-  const auto at_edge = [&](int k) {   // (outside: an element of the edge, which is not used)
-    return (it.e0 + e) * size + int64_t(min(r0 + wv + 4 * k, it.rows - 1)) * it.cols + min(c0 + c, it.cols - 1);
-  };
+  const MuWindow win(it, (it.e0 + e) * size + int64_t(r0) * it.cols, min(64, max(0, it.rows - r0)));
+  const auto row = [](int k) { return 4 * k; };
   float g[16], m[16];
-  if (a.gbf) {
+  load_gradients<16>(a, it, win, wv, c0 + c, row, g);
+  if (it.m) {
+    const __amdgpu_buffer_rsrc_t rm = win.of(it.m, 4);
 #pragma unroll
-    for (int k = 0; k < 16; ++k) g[k] = bf2f(static_cast<const uint16_t*>(it.g)[at_edge(k)]);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 16; ++k) g[k] = static_cast<const float*>(it.g)[at_edge(k)];
+    for (int k = 0; k < 16; ++k) m[k] = load_f32(rm, win.at(wv, c0 + c) + 4 * k * it.cols);
   }
-  if (it.m)
-#pragma unroll
-    for (int k = 0; k < 16; ++k) m[k] = it.m[at_edge(k)];
 #pragma unroll
   for (int k = 0; k < 16; ++k) {
     const int r = wv + 4 * k;
     float u = g[k] * clip;
     if (it.m) u = a.nesterov ? u + a.mu * m[k] : m[k];
-    const float x = r0 + r < it.rows && c0 + c < it.cols ? u * f : 0.f;
+    const float x = u * f;
     const _Float16 h = _Float16(x);
     const int64_t at = int64_t(r0 + r) * b.cols + c0 + c;
     hs[at] = h;
@@ -338,34 +403,6 @@ __global__ __launch_bounds__(S::kWaves * 64) void k_muon_gram(MuArgs a) {
     }
 }
 
-// The update of parameters (or the output) by results value(v) at row r0 + row(v) of column c, v < N. All parameters are loaded
-// before any is used, those outside the matrix from its edge.
-template <int N, class R, class V>
-__device__ __forceinline__ void store_results(const MuItem& it, int64_t base, int r0, int c, R&& row, V&& value, float decay,
-                                              float rate) {
-  const auto at = [&](int v) { return base + int64_t(min(r0 + row(v), it.rows - 1)) * it.cols + min(c, it.cols - 1); };
-  const auto inside = [&](int v) { return r0 + row(v) < it.rows && c < it.cols; };
-  if (it.m) {
-    float* p = static_cast<float*>(it.p);
-    float y[N];
-#pragma unroll
-    for (int v = 0; v < N; ++v) y[v] = p[at(v)];
-#pragma unroll
-    for (int v = 0; v < N; ++v) {
-      y[v] = y[v] * decay - value(v) * rate;
-      if (inside(v)) p[at(v)] = y[v];
-    }
-    if (it.copy)
-#pragma unroll
-      for (int v = 0; v < N; ++v)
-        if (inside(v)) it.copy[at(v)] = f2bf(y[v]);
-  } else {
-#pragma unroll
-    for (int v = 0; v < N; ++v)
-      if (inside(v)) static_cast<uint16_t*>(it.p)[at(v)] = f2bf(value(v) * rate);
-  }
-}
-
 // X <- a X + B X, as the parameters lie; LAST: the update of the parameters (or the output) by it instead.
 template <class S, bool LAST>
 __global__ __launch_bounds__(S::kWaves * 64) void k_muon_apply(MuArgs a) {
@@ -392,7 +429,7 @@ __global__ __launch_bounds__(S::kWaves * 64) void k_muon_apply(MuArgs a) {
   const double lr = a.lr_dev ? *a.lr_dev : a.lr;
   const float decay = float(1.0 - lr * a.weight_decay), scale = mu_scale(it.rows, it.cols);
   const float rate = it.m ? float(lr * it.adjust / scale) : 1.f / scale;
-  const int64_t base = int64_t(it.e0 + e) * it.rows * it.cols;
+  const MuWindow win(it, (int64_t(it.e0 + e) * it.rows + i0) * it.cols, min(ni, max(0, it.rows - i0)));
   _Float16 *hs = b.s(ws, turn, a.flip ^ 1), *ht = b.t(ws, turn, a.flip ^ 1), *lw = b.lo(ws);
 #pragma unroll
   for (int i = 0; i < S::FA; ++i)
@@ -412,7 +449,7 @@ __global__ __launch_bounds__(S::kWaves * 64) void k_muon_apply(MuArgs a) {
 #pragma unroll
       for (int v = 0; v < 16; ++v) x[v] = a.a * (float(xh[v]) + float(xl[v])) + acc[i][j][v];
       if constexpr (LAST) {
-        store_results<16>(it, base, r0, c, row, [&](int v) { return x[v]; }, decay, rate);
+        store_results<16>(it, win, r0 - i0, c, row, [&](int v) { return x[v]; }, decay, rate);
       } else {
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
@@ -440,18 +477,16 @@ __global__ __launch_bounds__(S::kWaves * 64) void k_muon_apply(MuArgs a) {
 // longer side's blocks w, w + 8, ..., for each of them all of the shorter side's: four slots at most, which share the
 // operand of their longer side.
 struct SmallShape {
-  int rows, cols, m, n, shorter, longer;   // sizes rounded up to 32, and in blocks
+  int shorter, longer;   // blocks along the sides
   __host__ __device__ SmallShape(int r, int c) {
-    rows = int(align_up(r, 32));
-    cols = int(align_up(c, 32));
-    m = rows < cols ? rows : cols;
-    n = rows < cols ? cols : rows;
-    shorter = m / 32;
-    longer = n / 32;
+    shorter = ((r < c ? r : c) + 31) / 32;
+    longer = ((r < c ? c : r) + 31) / 32;
   }
   __host__ __device__ bool fits() const { return shorter <= 4 && (longer + 7) / 8 * shorter <= 4; }
-  __host__ __device__ int lds() const { return (2 * m * n + m * m) * 2; }
 };
+// The longest row of the layout in LDS, in halves: that of all rows, so that addresses are constants and a row's base.
+constexpr int small_long(int shorter) { return 256 * (4 / shorter); }
+constexpr int small_lds(int shorter) { return (2 * 32 * shorter * small_long(shorter) + 1024 * shorter * shorter) * 2; }
 
 // Element (row, col) of a matrix in LDS whose rows have `len` halves (a multiple of 32): 16-byte chunks are swapped
 // within runs of 8 (4 where rows are no multiple of 8 chunks) by the row, so that 32 rows of one chunk spread over the banks.
@@ -509,10 +544,12 @@ template <int SHORTER, bool TURN>
 __device__ __forceinline__ void muon_small(const MuArgs& a, const MuSteps& st, const MuItem& it, int e) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   constexpr int N = SHORTER == 3 ? 3 : 4;   // slots
-  const SmallShape sh(it.rows, it.cols);
-  _Float16 *xs = reinterpret_cast<_Float16*>(smem), *xt = xs + sh.m * sh.n, *gram = xt + sh.m * sh.n;
+  constexpr int kShort = 32 * SHORTER, kLong = small_long(SHORTER);   // rows of the matrices in LDS
+  const int longer = SmallShape(it.rows, it.cols).longer, n = longer * 32;
+  _Float16 *xs = reinterpret_cast<_Float16*>(smem), *xt = xs + kShort * kLong, *gram = xt + kShort * kLong;
   const int lane = threadIdx.x & 63, w = wave_id(), half = lane >> 5, l32 = lane & 31;
-  const int64_t base = int64_t(it.e0 + e) * it.rows * it.cols;
+  const MuWindow win(it, int64_t(it.e0 + e) * it.rows * it.cols, it.rows);
+  const auto row = [](int v) { return 8 * (v >> 2) + (v & 3); };
   const float scale = mu_scale(it.rows, it.cols), down = 1.f / (scale * scale), clip = clip_factor(a);
   // element v of slot q is row rq(q) + 8 (v / 4) + 4 half + v % 4, column cq(q) + l32
   const auto rq = [&](int q) { return (TURN ? w + 8 * (q / SHORTER) : q % SHORTER) * 32; };
@@ -522,35 +559,28 @@ __device__ __forceinline__ void muon_small(const MuArgs& a, const MuSteps& st, c
   double sum = 0;
 #pragma unroll
   for (int q = 0; q < N; ++q) {
-    live[q] = w + 8 * (q / SHORTER) < sh.longer;
+    live[q] = w + 8 * (q / SHORTER) < longer;
     const int r0 = rq(q) + 4 * half, c0 = cq(q) + l32;
     float g[16], m[16];
-    const auto inside = [&](int v) { return r0 + 8 * (v >> 2) + (v & 3) < it.rows && c0 < it.cols; };
-    const auto at = [&](int v) {   // (outside: another element of the matrix, which is not used)
-      return base + int64_t(min(r0 + 8 * (v >> 2) + (v & 3), it.rows - 1)) * it.cols + min(c0, it.cols - 1);
-    };
-    // (a branch for all loads of a kind and none around single ones, which would be waited for one by one)
-    if (a.gbf) {
+    load_gradients<16>(a, it, win, r0, c0, row, g);
+    if (it.m) {
+      const __amdgpu_buffer_rsrc_t rm = win.of(it.m, 4);
+      const int at = win.at(r0, c0);
 #pragma unroll
-      for (int v = 0; v < 16; ++v) g[v] = bf2f(static_cast<const uint16_t*>(it.g)[at(v)]);
+      for (int v = 0; v < 16; ++v) m[v] = load_f32(rm, at + row(v) * it.cols);
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        g[v] *= clip;
+        m[v] = m[v] * a.mu + g[v];
+        store_f32(rm, at + row(v) * it.cols, m[v]);
+        x[q][v] = a.nesterov ? g[v] + a.mu * m[v] : m[v];
+      }
     } else {
 #pragma unroll
-      for (int v = 0; v < 16; ++v) g[v] = static_cast<const float*>(it.g)[at(v)];
+      for (int v = 0; v < 16; ++v) x[q][v] = g[v] * clip;
     }
-    if (it.m)
 #pragma unroll
-      for (int v = 0; v < 16; ++v) m[v] = it.m[at(v)];
-#pragma unroll
-    for (int v = 0; v < 16; ++v) {
-      float u = g[v] * clip;
-      if (it.m) {
-        m[v] = m[v] * a.mu + u;
-        if (inside(v)) it.m[at(v)] = m[v];
-        u = a.nesterov ? u + a.mu * m[v] : m[v];
-      }
-      x[q][v] = inside(v) ? u : 0.f;
-      sum = fma(double(x[q][v]), double(x[q][v]), sum);
-    }
+    for (int v = 0; v < 16; ++v) sum = fma(double(x[q][v]), double(x[q][v]), sum);
   }
   for (int off = 32; off; off >>= 1) sum += __shfl_xor(sum, off, 64);
   double* sums = reinterpret_cast<double*>(gram);
@@ -581,7 +611,7 @@ __device__ __forceinline__ void muon_small(const MuArgs& a, const MuSteps& st, c
       if (glive[q])
 #pragma unroll
         for (int v = 0; v < 16; ++v)
-          gram[small_at(gr[q] + 8 * (v >> 2) + 4 * h + (v & 3), gc[q] + c, sh.m)] = _Float16(g[q][v]);
+          gram[small_at(gr[q] + 8 * (v >> 2) + 4 * h + (v & 3), gc[q] + c, kShort)] = _Float16(g[q][v]);
   };
   const _Float16 *across_rows = TURN ? xt : xs, *along_rows = TURN ? xs : xt;   // rows of n, and of m halves
 #pragma unroll 1
@@ -599,9 +629,9 @@ __device__ __forceinline__ void muon_small(const MuArgs& a, const MuSteps& st, c
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
               y[u] = _Float16(x[q][4 * v + u]);
-              xs[small_at(r + u, cq(q) + c, sh.cols)] = y[u];
+              xs[small_at(r + u, cq(q) + c, TURN ? kShort : kLong)] = y[u];
             }
-            *reinterpret_cast<f16x4*>(xt + small_at(cq(q) + c, r, sh.rows)) = y;
+            *reinterpret_cast<f16x4*>(xt + small_at(cq(q) + c, r, TURN ? kLong : kShort)) = y;
           }
     }
     __syncthreads();
@@ -609,9 +639,9 @@ __device__ __forceinline__ void muon_small(const MuArgs& a, const MuSteps& st, c
     f32x16 g[G];
     if (glive[0]) {
       const int l = tile_tid() & 31;
-      const SmallRow left[2] = {SmallRow(across_rows, gr[0] + l, sh.n), SmallRow(across_rows, gr[G - 1] + l, sh.n)};
-      const SmallRow right[2] = {SmallRow(across_rows, gc[0] + l, sh.n), SmallRow(across_rows, gc[G - 1] + l, sh.n)};
-      small_products<G, 1, false>(left, right, sh.n, g);
+      const SmallRow left[2] = {SmallRow(across_rows, gr[0] + l, kLong), SmallRow(across_rows, gr[G - 1] + l, kLong)};
+      const SmallRow right[2] = {SmallRow(across_rows, gc[0] + l, kLong), SmallRow(across_rows, gc[G - 1] + l, kLong)};
+      small_products<G, 1, false>(left, right, n, g);
 #pragma unroll
       for (int q = 0; q < G; ++q) g[q] *= down;
       put_gram(g);
@@ -619,10 +649,10 @@ __device__ __forceinline__ void muon_small(const MuArgs& a, const MuSteps& st, c
     __syncthreads();
     if (glive[0]) {
       const int l = tile_tid() & 31;
-      const SmallRow left[2] = {SmallRow(gram, gr[0] + l, sh.m), SmallRow(gram, gr[G - 1] + l, sh.m)};
-      const SmallRow right[2] = {SmallRow(gram, gc[0] + l, sh.m), SmallRow(gram, gc[G - 1] + l, sh.m)};
+      const SmallRow left[2] = {SmallRow(gram, gr[0] + l, kShort), SmallRow(gram, gr[G - 1] + l, kShort)};
+      const SmallRow right[2] = {SmallRow(gram, gc[0] + l, kShort), SmallRow(gram, gc[G - 1] + l, kShort)};
       f32x16 y[G];
-      small_products<G, 1, false>(left, right, sh.m, y);
+      small_products<G, 1, false>(left, right, kShort, y);
 #pragma unroll
       for (int q = 0; q < G; ++q) g[q] = cc * y[q] + cb * g[q];
     }
@@ -631,12 +661,12 @@ __device__ __forceinline__ void muon_small(const MuArgs& a, const MuSteps& st, c
     __syncthreads();
     if (live[0]) {
       const int l = tile_tid() & 31;
-      const auto along = [&](int j) { return SmallRow(along_rows, min(w + 8 * j, sh.longer - 1) * 32 + l, sh.m); };
-      const auto across = [&](int q) { return SmallRow(gram, q % SHORTER * 32 + l, sh.m); };
+      const auto along = [&](int j) { return SmallRow(along_rows, min(w + 8 * j, longer - 1) * 32 + l, kShort); };
+      const auto across = [&](int q) { return SmallRow(gram, q % SHORTER * 32 + l, kShort); };
       const SmallRow ra[4] = {across(0), across(1), across(2), across(3)};
       const SmallRow rb[4] = {along(0), along(1), along(2), along(3)};
       f32x16 y[N];
-      small_products<N, SHORTER, TURN>(ra, rb, sh.m, y);
+      small_products<N, SHORTER, TURN>(ra, rb, kShort, y);
 #pragma unroll
       for (int q = 0; q < N; ++q)
 #pragma unroll
@@ -650,8 +680,7 @@ __device__ __forceinline__ void muon_small(const MuArgs& a, const MuSteps& st, c
   for (int q = 0; q < N; ++q)
     if (live[q]) {
       const int r0 = rq(q) + 4 * half, c = cq(q) + l32;
-      store_results<16>(it, base, r0, c, [](int v) { return 8 * (v >> 2) + (v & 3); }, [&](int v) { return x[q][v]; }, decay,
-                        rate);
+      store_results<16>(it, win, r0, c, row, [&](int v) { return x[q][v]; }, decay, rate);
     }
 }
 
@@ -811,7 +840,7 @@ hipError_t launch_muon(int count, const mok_muon_tensor* t, const mok_muon_confi
     std::copy_n(&c.ns.coefficients[0][0], 3 * st.count, &st.coef[0][0]);
     int lds = 0, matrices = 0;
     for (int k = 0; k < n; ++k) {
-      lds = std::max(lds, SmallShape(a.item[k].rows, a.item[k].cols).lds());
+      lds = std::max(lds, small_lds(SmallShape(a.item[k].rows, a.item[k].cols).shorter));
       a.first[k] = matrices;
       matrices += a.item[k].batch;
     }
