@@ -112,6 +112,7 @@ __host__ __device__ inline int64_t mu_chunk(int64_t size) {   // elements of a p
 // One partial sum of |u|^2 a workgroup, in fp64; with a momentum, also its update.
 __global__ __launch_bounds__(256) void k_muon_norm(MuArgs a) {
   if (left_out(a)) return;
+  if (int(blockIdx.x) >= a.first[a.count]) return;
   const int t = find_item(a, blockIdx.x);
   const MuItem& it = a.item[t];
   const int64_t size = int64_t(it.rows) * it.cols, chunk = mu_chunk(size);
@@ -236,6 +237,7 @@ __device__ __forceinline__ void store_results(const MuItem& it, const MuWindow& 
 // 64 x 64 elements a workgroup, written as they lie and turned, zeros in the padding.
 __global__ __launch_bounds__(256) void k_muon_start(MuArgs a) {
   if (left_out(a)) return;
+  if (int(blockIdx.x) >= a.first[a.count]) return;
   const int t = find_item(a, blockIdx.x);
   const MuItem& it = a.item[t];
   const MuBuffers b(it.rows, it.cols);
@@ -294,19 +296,24 @@ struct MuShape {
   };
 };
 
+// Part `part` of 4 of a wave's share of a stage (128 bytes of each of ROWS rows), swizzled as swz() reads it. `lane_off` holds
+// the lane's row and chunk in a run of 8 rows of even number; in an odd one the chunk's lowest bit turns.
 template <int ROWS, int WAVES>
-__device__ __forceinline__ void issue_f16(__amdgpu_buffer_rsrc_t r, uint8_t* lds, int stride, int kt, int w) {
-  const int L = opaque(int(threadIdx.x) & 63);
+__device__ __forceinline__ void issue_f16(__amdgpu_buffer_rsrc_t r, uint8_t* lds, int lane_off, int stride, int kt, int w,
+                                          int part) {
   constexpr int kEach = ROWS / 8 / WAVES;
-#pragma unroll
-  for (int c = 0; c < kEach; ++c) {
-    const int blk = w * kEach + c, chunk = (L & 7) ^ (L >> 3) ^ (blk & 1);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(lds + blk * 8 * kStageRowBytes), 16,
-                                             (blk * 8 + (L >> 3)) * stride + kt * kStageRowBytes + chunk * 16, 0, 0, 0);
-  }
+  static_assert(kEach == 4, "one run a part");
+  const int run = w * kEach + part;
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(lds + run * 8 * kStageRowBytes), 16,
+                                           (lane_off ^ (part & 1) * 16) + (run * 8 * stride + kt * kStageRowBytes), 0, 0, 0);
 }
 
 // acc = A B^T over k halves (a multiple of 128) of rows of `stride` halves; rows past na, nb count as zeros.
+//
+// Stages of 64 halves a row are double-buffered in LDS and cut into 4 slices, whose operands are read while the slice
+// before is multiplied. The barrier of a stage stands before its last slice's products: then the next stage has
+// arrived, and this one's buffer takes the stage after the next, a quarter at a time over four slices (in one run the
+// loads hold the waves up).
 template <class S>
 __device__ __forceinline__ void tile_f16(typename S::Lds& sm, const _Float16* a, int na, const _Float16* b, int nb, int k,
                                          f32x16 (&acc)[S::FA][S::FB]) {
@@ -319,32 +326,69 @@ __device__ __forceinline__ void tile_f16(typename S::Lds& sm, const _Float16* a,
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
   const int stride = k * 2, ksteps = stride / kStageRowBytes;
   const __amdgpu_buffer_rsrc_t ra = make_rsrc(a, int64_t(na) * stride), rb = make_rsrc(b, int64_t(nb) * stride);
-  issue_f16<S::kA, S::kWaves>(ra, sm.a[0], stride, 0, w);
-  issue_f16<S::kB, S::kWaves>(rb, sm.b[0], stride, 0, w);
+  const int lane_off = (lane >> 3) * stride + ((lane & 7) ^ (lane >> 3)) * 16;
+  const auto issue = [&](int kt, int part) {   // (past the last stage, the last once more for nothing)
+    const int buf = kt & 1;
+    kt = min(kt, ksteps - 1);
+    issue_f16<S::kA, S::kWaves>(ra, sm.a[buf], lane_off, stride, kt, w, part);
+    issue_f16<S::kB, S::kWaves>(rb, sm.b[buf], lane_off, stride, kt, w, part);
+  };
+  f16x8 fa[2][S::FA], fb[2][S::FB];
+  const auto load = [&](int f, int buf, int kk) {
+#pragma unroll
+    for (int i = 0; i < S::FA; ++i)
+      fa[f][i] = *reinterpret_cast<const f16x8*>(sm.a[buf] + swz((wa * S::FA + i) * 32 + l32, kk * 2 + half));
+#pragma unroll
+    for (int j = 0; j < S::FB; ++j)
+      fb[f][j] = *reinterpret_cast<const f16x8*>(sm.b[buf] + swz((wb * S::FB + j) * 32 + l32, kk * 2 + half));
+  };
+#pragma unroll
+  for (int q = 0; q < 4; ++q) issue(0, q);
+  issue(1, 0);
+  issue(1, 1);
+  wait_vmem();
+  __syncthreads();
+  load(0, 0, 0);
   for (int kt = 0; kt < ksteps; ++kt) {
     const int cur = kt & 1;
-    wait_vmem();
-    __syncthreads();
-    if (kt + 1 < ksteps) {
-      issue_f16<S::kA, S::kWaves>(ra, sm.a[cur ^ 1], stride, kt + 1, w);
-      issue_f16<S::kB, S::kWaves>(rb, sm.b[cur ^ 1], stride, kt + 1, w);
-    }
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
-      f16x8 fa[S::FA], fb[S::FB];
-#pragma unroll
-      for (int i = 0; i < S::FA; ++i)
-        fa[i] = *reinterpret_cast<const f16x8*>(sm.a[cur] + swz((wa * S::FA + i) * 32 + l32, kk * 2 + half));
-#pragma unroll
-      for (int j = 0; j < S::FB; ++j)
-        fb[j] = *reinterpret_cast<const f16x8*>(sm.b[cur] + swz((wb * S::FB + j) * 32 + l32, kk * 2 + half));
+      __builtin_amdgcn_sched_barrier(0);
+      if (kk < 3) {
+        load((kk + 1) & 1, cur, kk + 1);
+      } else {
+        wait_vmem();
+        __syncthreads();
+        load(0, cur ^ 1, 0);   // (in the last stage what is read is not used)
+      }
+      if (kk < 2) issue(kt + 1, 2 + kk);
+      if (kk == 3) {
+        issue(kt + 2, 0);
+        issue(kt + 2, 1);
+      }
 #pragma unroll
       for (int i = 0; i < S::FA; ++i)
 #pragma unroll
         for (int j = 0; j < S::FB; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[kk & 1][i], fb[kk & 1][j], acc[i][j], 0, 0, 0);
+      // one operand read between products
+      constexpr int kReads = S::FA + S::FB, kProducts = S::FA * S::FB;
+#pragma unroll
+      for (int q = 0; q < kReads; ++q) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // LDS read
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // MFMA
+      }
+      if constexpr (kProducts > kReads) __builtin_amdgcn_sched_group_barrier(0x008, kProducts - kReads, 0);
     }
+    __builtin_amdgcn_sched_barrier(0);
   }
+  wait_vmem();   // (loads into LDS do not outlive the workgroup)
+}
+
+// The tile that a workgroup takes: those of one XCD follow one another (they share operands); -1: none.
+__device__ __forceinline__ int xcd_tile(int total) {
+  const int run = (total + kXcds - 1) / kXcds, in = blockIdx.x / kXcds, id = blockIdx.x % kXcds * run + in;
+  return in < run && id < total ? id : -1;
 }
 
 // Tile number q of the lower triangle, rows first: (0,0), (1,0), (1,1), (2,0), ...
@@ -357,15 +401,17 @@ __device__ __forceinline__ void triangle(int q, int& i, int& j) {
 
 // SECOND false: A = X X^T; true: B = b A + c A A. Both symmetric: tiles with i >= j, written twice.
 template <class S, bool SECOND>
-__global__ __launch_bounds__(S::kWaves * 64) void k_muon_gram(MuArgs a) {
+__global__ __launch_bounds__(S::kWaves * 64, 2) void k_muon_gram(MuArgs a) {
   static_assert(S::kA == S::kB, "square tiles");
   if (left_out(a)) return;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   typename S::Lds& sm = *reinterpret_cast<typename S::Lds*>(smem);
-  const int t = find_item(a, blockIdx.x);
+  const int id = xcd_tile(a.first[a.count]);
+  if (id < 0) return;
+  const int t = find_item(a, id);
   const MuItem& it = a.item[t];
   const MuBuffers b(it.rows, it.cols);
-  const int T = (b.m + S::kA - 1) / S::kA, per = T * (T + 1) / 2, q = blockIdx.x - a.first[t], e = q / per;
+  const int T = (b.m + S::kA - 1) / S::kA, per = T * (T + 1) / 2, q = id - a.first[t], e = q / per;
   uint8_t* ws = it.ws + e * align_up(b.bytes(), 256);
   int ti, tj;
   triangle(q % per, ti, tj);
@@ -405,15 +451,17 @@ __global__ __launch_bounds__(S::kWaves * 64) void k_muon_gram(MuArgs a) {
 
 // X <- a X + B X, as the parameters lie; LAST: the update of the parameters (or the output) by it instead.
 template <class S, bool LAST>
-__global__ __launch_bounds__(S::kWaves * 64) void k_muon_apply(MuArgs a) {
+__global__ __launch_bounds__(S::kWaves * 64, 2) void k_muon_apply(MuArgs a) {
   if (left_out(a)) return;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   typename S::Lds& sm = *reinterpret_cast<typename S::Lds*>(smem);
-  const int t = find_item(a, blockIdx.x);
+  const int id = xcd_tile(a.first[a.count]);
+  if (id < 0) return;
+  const int t = find_item(a, id);
   const MuItem& it = a.item[t];
   const MuBuffers b(it.rows, it.cols);
   const int tr = (b.rows + S::kA - 1) / S::kA, tc = (b.cols + S::kB - 1) / S::kB, per = tr * tc;
-  const int q = blockIdx.x - a.first[t], e = q / per;
+  const int q = id - a.first[t], e = q / per;
   uint8_t* ws = it.ws + e * align_up(b.bytes(), 256);
   int ti, tj;
   tile_coords(q % per, tr, tc, ti, tj);
@@ -703,7 +751,8 @@ __global__ __launch_bounds__(512) void k_muon_small(MuArgs a, MuSteps st) {
   }
 }
 
-using MuMid = MuShape<2, 2, 2, 2>;   // 128 x 128
+using MuMid = MuShape<2, 2, 2, 2>;    // 128 x 128
+using MuWide = MuShape<2, 4, 4, 2>;   // 256 x 256
 
 template <class F>
 hipError_t allow_lds(F* f, int bytes, std::atomic<bool> (&done)[kMaxDevices]) {
@@ -721,7 +770,7 @@ hipError_t run(K* kernel, MuArgs& a, int threads, int lds, hipStream_t s, N&& ti
     sum += tiles(a.item[t]) * a.item[t].batch;
   }
   a.first[a.count] = int32_t(sum);
-  kernel<<<unsigned(sum), threads, lds, s>>>(a);
+  kernel<<<unsigned(align_up(sum, kXcds)), threads, lds, s>>>(a);
   return hipGetLastError();
 }
 
@@ -860,7 +909,12 @@ hipError_t launch_muon(int count, const mok_muon_tensor* t, const mok_muon_confi
         const MuBuffers b(it.rows, it.cols);
         return int64_t(b.rows / 64) * (b.cols / 64);
       });
-    if (e1 == hipSuccess) e1 = steps<MuMid>(a, c.ns.steps, &c.ns.coefficients[0][0], s);
+    if (e1 != hipSuccess) return e1;
+    int64_t tiles = 0;   // of 256 x 256 in a step's last product
+    for (int k = 0; k < n; ++k)
+      tiles += cdiv(a.item[k].rows, 256) * cdiv(a.item[k].cols, 256) * a.item[k].batch;
+    e1 = tiles >= 256 ? steps<MuWide>(a, c.ns.steps, &c.ns.coefficients[0][0], s)
+                      : steps<MuMid>(a, c.ns.steps, &c.ns.coefficients[0][0], s);
     return e1;
   });
 }
