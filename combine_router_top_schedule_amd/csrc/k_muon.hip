@@ -8,11 +8,11 @@
 // step's product ends in the parameters' update instead of X. All matrices of a call go through the same
 // launches, whatever their shapes: a workgroup finds its matrix by the prefix sums of their tile counts.
 //
-// Precision. X is kept in 22 bits as the sum of two fp16 matrices, hi + lo, times a power of two near sqrt(n) that keeps
-// both in fp16's normal range; a X is formed from both, the products take hi, A and B in fp16 with fp32 sums. Kept in
-// fp16 alone, X's rounding drowns the small singular values of a gradient with a few large ones: 64-bit against
-// 11-bit X differ by 1.3e-2 of the result there (512 x 1792, rank 129 plus 1 % noise), with lo by 8e-4; bf16 everywhere by 1e-1. On the
-// matrix cores fp16 is as fast as bf16.
+// Precision. X is kept in 19 bits, fp16 and a byte for the bits below, times a power of two near sqrt(n) that keeps it in
+// fp16's normal range; a X is formed from all of them, the products take X, A and B in fp16 with fp32 sums. Kept in
+// fp16 alone, X's rounding drowns the small singular values of a gradient with a few large ones: the result is off by
+// 1.3e-2 there (512 x 1792, rank 129 plus 1 % noise), with the byte by 8e-4, with bf16 everywhere by 1e-1; 1e-3 to 2e-3
+// for random matrices, where A's and B's rounding is what is left. On the matrix cores fp16 is as fast as bf16.
 #include <algorithm>
 #include <cmath>
 
@@ -23,6 +23,7 @@ namespace {
 
 typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
 typedef __attribute__((ext_vector_type(4))) _Float16 f16x4;
+typedef __attribute__((ext_vector_type(2))) _Float16 f16x2;
 
 constexpr int kMuItems = 40;       // tensors (or parts of their batches) that a launch takes (of 4 KB of arguments)
 constexpr int kMuParts = 256;      // partial sums of a matrix's norm at most
@@ -55,7 +56,7 @@ struct MuArgs {
 // A matrix's buffers in the workspace. `s` is X as its parameters lie ([rows][cols], padded), `t` its transpose. The
 // product with B reads `t` (`s` where rows > cols) while its tiles are written, so that one has a second buffer.
 struct MuBuffers {
-  int64_t plane, gram;           // bytes of X and of A
+  int64_t plane, gram;           // bytes of X in fp16 and of A
   int rows, cols, m, n;          // padded; m = min, n = max
   __host__ __device__ MuBuffers(int r, int c) {
     rows = int(align_up(r, kMuPad));
@@ -65,16 +66,29 @@ struct MuBuffers {
     plane = int64_t(rows) * cols * 2;
     gram = int64_t(m) * m * 2;
   }
-  __host__ __device__ int64_t bytes() const { return 4 * plane + 2 * gram + kMuParts * 8; }
+  __host__ __device__ int64_t bytes() const { return parts_at() + kMuParts * 8; }
+  __host__ __device__ int64_t parts_at() const { return 3 * plane + plane / 2 + 2 * gram; }
   __device__ bool turned(const MuItem& it) const { return it.rows > it.cols; }
-  __device__ _Float16* s(uint8_t* ws, bool turn, int flip) const { return at(ws, turn && flip ? 3 * plane : 0); }
-  __device__ _Float16* t(uint8_t* ws, bool turn, int flip) const { return at(ws, !turn && flip ? 3 * plane : 2 * plane); }
-  __device__ _Float16* lo(uint8_t* ws) const { return at(ws, plane); }
-  __device__ _Float16* a(uint8_t* ws) const { return at(ws, 4 * plane); }
-  __device__ _Float16* b(uint8_t* ws) const { return at(ws, 4 * plane + gram); }
-  __device__ double* parts(uint8_t* ws) const { return reinterpret_cast<double*>(ws + 4 * plane + 2 * gram); }
+  __device__ _Float16* s(uint8_t* ws, bool turn, int flip) const { return at(ws, turn && flip ? 2 * plane : 0); }
+  __device__ _Float16* t(uint8_t* ws, bool turn, int flip) const { return at(ws, !turn && flip ? 2 * plane : plane); }
+  __device__ _Float16* a(uint8_t* ws) const { return at(ws, 3 * plane); }
+  __device__ _Float16* b(uint8_t* ws) const { return at(ws, 3 * plane + gram); }
+  __device__ uint8_t* lo(uint8_t* ws) const { return ws + 3 * plane + 2 * gram; }
+  __device__ double* parts(uint8_t* ws) const { return reinterpret_cast<double*>(ws + parts_at()); }
   __device__ static _Float16* at(uint8_t* p, int64_t off) { return reinterpret_cast<_Float16*>(p + off); }
 };
+
+// X's lower bits: what fp16 leaves of x, in 256ths of h's last place (2^-24 for the smallest), one byte.
+__device__ __forceinline__ int exponent_of(_Float16 h) {
+  return max(int(__float_as_uint(float(h)) >> 23 & 0xFF), 113);   // (2^-14, below which fp16's places stay)
+}
+__device__ __forceinline__ int low_bits(float x, _Float16 h) {
+  const float q = rintf((x - float(h)) * __uint_as_float(uint32_t(272 - exponent_of(h)) << 23));
+  return int(fminf(fmaxf(q, -128.f), 127.f));
+}
+__device__ __forceinline__ float with_low(_Float16 h, int low) {
+  return fmaf(float(low), __uint_as_float(uint32_t(exponent_of(h) - 18) << 23), float(h));
+}
 
 // The power of two that X is stored with: near sqrt(n), so that the result's elements are near 1.
 __host__ __device__ inline float mu_scale(int rows, int cols) {
@@ -233,6 +247,42 @@ __device__ __forceinline__ void store_results(const MuItem& it, const MuWindow& 
   }
 }
 
+// The same for N rows from r0 on of columns c and c + 1, where rows have an even number of columns and both are inside.
+template <int N>
+__device__ __forceinline__ void store_pairs(const MuItem& it, const MuWindow& win, int r0, int c, const float (&x)[2][N],
+                                            float decay, float rate) {
+  const int at = win.at(r0, c);
+  if (it.m) {
+    const __amdgpu_buffer_rsrc_t p = win.of(it.p, 4);
+    float y[2][N];
+#pragma unroll
+    for (int v = 0; v < N; ++v) {
+      const auto t = __builtin_amdgcn_raw_buffer_load_b64(p, (at + v * win.cols) * 4, 0, 0);
+      y[0][v] = __uint_as_float(t[0]);
+      y[1][v] = __uint_as_float(t[1]);
+    }
+#pragma unroll
+    for (int v = 0; v < N; ++v) {
+      for (int j = 0; j < 2; ++j) y[j][v] = y[j][v] * decay - x[j][v] * rate;
+      decltype(__builtin_amdgcn_raw_buffer_load_b64(p, 0, 0, 0)) t;
+      t[0] = __float_as_uint(y[0][v]);
+      t[1] = __float_as_uint(y[1][v]);
+      __builtin_amdgcn_raw_buffer_store_b64(t, p, (at + v * win.cols) * 4, 0, 0);
+    }
+    if (it.copy) {
+      const __amdgpu_buffer_rsrc_t q = win.of(it.copy, 2);
+#pragma unroll
+      for (int v = 0; v < N; ++v)
+        __builtin_amdgcn_raw_buffer_store_b32(pack_bf2(y[0][v], y[1][v]), q, (at + v * win.cols) * 2, 0, 0);
+    }
+  } else {
+    const __amdgpu_buffer_rsrc_t q = win.of(it.p, 2);
+#pragma unroll
+    for (int v = 0; v < N; ++v)
+      __builtin_amdgcn_raw_buffer_store_b32(pack_bf2(x[0][v] * rate, x[1][v] * rate), q, (at + v * win.cols) * 2, 0, 0);
+  }
+}
+
 // ---- X_0 ------------------------------------------------------------------------------------------
 // 64 x 64 elements a workgroup, written as they lie and turned, zeros in the padding.
 __global__ __launch_bounds__(256) void k_muon_start(MuArgs a) {
@@ -255,7 +305,8 @@ __global__ __launch_bounds__(256) void k_muon_start(MuArgs a) {
   const float clip = clip_factor(a), f = float(double(mu_scale(it.rows, it.cols)) / norm);
   __shared__ _Float16 tile[64][66];
   const bool turn = b.turned(it);
-  _Float16 *hs = b.s(ws, turn, 0), *lo = b.lo(ws), *ht = b.t(ws, turn, 0);
+  _Float16 *hs = b.s(ws, turn, 0), *ht = b.t(ws, turn, 0);
+  uint8_t* lo = b.lo(ws);
   const int c = threadIdx.x & 63;
   const int wv = threadIdx.x >> 6;
   const MuWindow win(it, (it.e0 + e) * size + int64_t(r0) * it.cols, min(64, max(0, it.rows - r0)));
@@ -276,7 +327,7 @@ __global__ __launch_bounds__(256) void k_muon_start(MuArgs a) {
     const _Float16 h = _Float16(x);
     const int64_t at = int64_t(r0 + r) * b.cols + c0 + c;
     hs[at] = h;
-    lo[at] = _Float16(x - float(h));
+    lo[at] = uint8_t(low_bits(x, h));
     tile[r][c] = h;
   }
   __syncthreads();
@@ -285,10 +336,30 @@ __global__ __launch_bounds__(256) void k_muon_start(MuArgs a) {
 }
 
 // ---- products -------------------------------------------------------------------------------------
-// WA x WB waves of FA x FB blocks of 32 x 32; both operands' rows have the sum's axis contiguous.
-template <int WA_, int WB_, int FA_, int FB_>
+// WA x WB waves of FA x 2 blocks of 32 x 32; both operands' rows have the sum's axis contiguous.
+//
+// Which rows of the operands make a block is chosen for the results, which a lane holds as 4 consecutive rows of one
+// column in each quarter q of each block. Block j of the second operand takes rows 2 l + j of the wave's 64, so a lane has
+// two neighbouring columns, and a row of 32 lanes is a whole cache line of fp16. Block i of the first takes rows
+// q 8 FA + h 4 FA + 4 i + u (lane l = 8 q + 4 h + u), so a lane's FA blocks are runs of 4 FA rows, whole 16 bytes of the
+// transpose.
+template <int WA_, int WB_, int FA_>
 struct MuShape {
-  static constexpr int WA = WA_, WB = WB_, FA = FA_, FB = FB_;
+  static constexpr int WA = WA_, WB = WB_, FA = FA_, FB = 2;
+  static constexpr int kRun = 4 * FA, kTurnBit = FA == 4 ? 4 : 3;   // (see swz_a)
+  static_assert(FA == 2 || FA == 4);
+  // First row (in the wave's share) of the results of quarter q in this half of the lanes, and an operand's row.
+  static __device__ __forceinline__ int result_row(int q, int half) { return q * 2 * kRun + half * kRun; }
+  static __device__ __forceinline__ int row_a(int i, int l) {
+    return (l >> 3) * 2 * kRun + (l >> 2 & 1) * kRun + 4 * i + (l & 3);
+  }
+  static __device__ __forceinline__ int row_b(int j, int l) { return 2 * l + j; }
+  // Place of chunk `chunk` of row `row` in LDS: chunks are swapped by three bits that differ among the rows a block reads,
+  // l's lowest three, so that its reads are free of bank conflicts: for the first operand bits 0, 1 and kTurnBit of the row,
+  // for the second those of swz().
+  static __device__ __forceinline__ int swz_a(int row, int chunk) {
+    return row * kStageRowBytes + ((chunk ^ (row & 3) ^ ((row >> kTurnBit & 1) << 2)) << 4);
+  }
   static constexpr int kWaves = WA * WB, kA = WA * FA * 32, kB = WB * FB * 32;
   struct Lds {
     uint8_t a[2][kA * kStageRowBytes];
@@ -296,16 +367,17 @@ struct MuShape {
   };
 };
 
-// Part `part` of 4 of a wave's share of a stage (128 bytes of each of ROWS rows), swizzled as swz() reads it. `lane_off` holds
-// the lane's row and chunk in a run of 8 rows of even number; in an odd one the chunk's lowest bit turns.
-template <int ROWS, int WAVES>
+// Part `part` of 4 of a wave's share of a stage: a run of 8 rows, 128 bytes each. `lane_off` holds the lane's row and chunk
+// in the first run; TURN: the bits of a chunk's number that turn in this run.
+template <int ROWS, int WAVES, class T>
 __device__ __forceinline__ void issue_f16(__amdgpu_buffer_rsrc_t r, uint8_t* lds, int lane_off, int stride, int kt, int w,
-                                          int part) {
+                                          int part, T&& turn) {
   constexpr int kEach = ROWS / 8 / WAVES;
   static_assert(kEach == 4, "one run a part");
   const int run = w * kEach + part;
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(lds + run * 8 * kStageRowBytes), 16,
-                                           (lane_off ^ (part & 1) * 16) + (run * 8 * stride + kt * kStageRowBytes), 0, 0, 0);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(
+      r, (lds_void*)(lds + run * 8 * kStageRowBytes), 16,
+      (lane_off ^ turn(part) * 16) + (run * 8 * stride + kt * kStageRowBytes), 0, 0, 0);
 }
 
 // acc = A B^T over k halves (a multiple of 128) of rows of `stride` halves; rows past na, nb count as zeros.
@@ -326,21 +398,24 @@ __device__ __forceinline__ void tile_f16(typename S::Lds& sm, const _Float16* a,
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
   const int stride = k * 2, ksteps = stride / kStageRowBytes;
   const __amdgpu_buffer_rsrc_t ra = make_rsrc(a, int64_t(na) * stride), rb = make_rsrc(b, int64_t(nb) * stride);
-  const int lane_off = (lane >> 3) * stride + ((lane & 7) ^ (lane >> 3)) * 16;
+  const int off_a = (lane >> 3) * stride + ((lane & 7) ^ (lane >> 3 & 3)) * 16;
+  const int off_b = (lane >> 3) * stride + ((lane & 7) ^ (lane >> 3)) * 16;
   const auto issue = [&](int kt, int part) {   // (past the last stage, the last once more for nothing)
     const int buf = kt & 1;
     kt = min(kt, ksteps - 1);
-    issue_f16<S::kA, S::kWaves>(ra, sm.a[buf], lane_off, stride, kt, w, part);
-    issue_f16<S::kB, S::kWaves>(rb, sm.b[buf], lane_off, stride, kt, w, part);
+    // (a wave's runs begin at a multiple of 4, so a run's parity, or its half's, is its part's)
+    issue_f16<S::kA, S::kWaves>(ra, sm.a[buf], off_a, stride, kt, w, part,
+                                [](int p) { return (p >> (S::kTurnBit - 3) & 1) * 4; });
+    issue_f16<S::kB, S::kWaves>(rb, sm.b[buf], off_b, stride, kt, w, part, [](int p) { return p & 1; });
   };
   f16x8 fa[2][S::FA], fb[2][S::FB];
   const auto load = [&](int f, int buf, int kk) {
 #pragma unroll
     for (int i = 0; i < S::FA; ++i)
-      fa[f][i] = *reinterpret_cast<const f16x8*>(sm.a[buf] + swz((wa * S::FA + i) * 32 + l32, kk * 2 + half));
+      fa[f][i] = *reinterpret_cast<const f16x8*>(sm.a[buf] + S::swz_a(wa * S::FA * 32 + S::row_a(i, l32), kk * 2 + half));
 #pragma unroll
     for (int j = 0; j < S::FB; ++j)
-      fb[f][j] = *reinterpret_cast<const f16x8*>(sm.b[buf] + swz((wb * S::FB + j) * 32 + l32, kk * 2 + half));
+      fb[f][j] = *reinterpret_cast<const f16x8*>(sm.b[buf] + swz(wb * 64 + S::row_b(j, l32), kk * 2 + half));
   };
 #pragma unroll
   for (int q = 0; q < 4; ++q) issue(0, q);
@@ -425,28 +500,33 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void k_muon_gram(MuArgs a) {
   const _Float16* old = b.a(ws);
   _Float16* out = SECOND ? b.b(ws) : b.a(ws);
   const int tid = tile_tid(), lane = tid & 63, w = tid >> 6, wa = w / S::WB, wb = w % S::WB, half = lane >> 5;
+  // (padded sizes are multiples of 128, which a wave's share does not cross)
+  if (wa * S::FA * 32 >= ni || wb * 64 >= nj) return;
+  const int c = j0 + wb * 64 + 2 * (lane & 31);
 #pragma unroll
-  for (int i = 0; i < S::FA; ++i)
+  for (int q = 0; q < 4; ++q) {
+    const int r0 = i0 + wa * S::FA * 32 + S::result_row(q, half);
+    f16x2 z[S::kRun];
+    if constexpr (SECOND)
 #pragma unroll
-    for (int j = 0; j < S::FB; ++j) {
-      const int r0 = i0 + (wa * S::FA + i) * 32 + 4 * half, c = j0 + (wb * S::FB + j) * 32 + (lane & 31);
-      if ((wa * S::FA + i) * 32 >= ni || (wb * S::FB + j) * 32 >= nj) continue;   // (padded sizes are multiples of 128)
-      _Float16 z[16];
-      if constexpr (SECOND)
+      for (int v = 0; v < S::kRun; ++v) z[v] = *reinterpret_cast<const f16x2*>(old + int64_t(r0 + v) * b.m + c);
+    _Float16 y[2][S::kRun];
 #pragma unroll
-        for (int v = 0; v < 16; ++v) z[v] = old[int64_t(r0 + 8 * (v >> 2) + (v & 3)) * b.m + c];
+    for (int v = 0; v < S::kRun; ++v) {
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        f16x4 y;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float g = acc[i][j][4 * v + u];
-          y[u] = _Float16(SECOND ? a.c * g + a.b * float(z[4 * v + u]) : g * down);
-          out[int64_t(r0 + 8 * v + u) * b.m + c] = y[u];
-        }
-        if (ti != tj) *reinterpret_cast<f16x4*>(out + int64_t(c) * b.m + r0 + 8 * v) = y;
+      for (int j = 0; j < 2; ++j) {
+        const float g = acc[v >> 2][j][4 * q + (v & 3)];
+        y[j][v] = _Float16(SECOND ? a.c * g + a.b * float(z[v][j]) : g * down);
       }
+      *reinterpret_cast<f16x2*>(out + int64_t(r0 + v) * b.m + c) = f16x2{y[0][v], y[1][v]};
     }
+    if (ti != tj)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int v = 0; v < S::kRun; v += 8)
+          *reinterpret_cast<f16x8*>(out + int64_t(c + j) * b.m + r0 + v) = *reinterpret_cast<const f16x8*>(&y[j][v]);
+  }
 }
 
 // X <- a X + B X, as the parameters lie; LAST: the update of the parameters (or the output) by it instead.
@@ -467,7 +547,7 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void k_muon_apply(MuArgs a) {
   tile_coords(q % per, tr, tc, ti, tj);
   const bool turn = b.turned(it);
   const int i0 = ti * S::kA, j0 = tj * S::kB, ni = min(S::kA, b.rows - i0), nj = min(S::kB, b.cols - j0);
-  const _Float16 *hi = b.s(ws, turn, a.flip), *lo = b.lo(ws);
+  const _Float16* hi = b.s(ws, turn, a.flip);
   // the result's rows times its columns: B X, or X B where X is turned
   const _Float16* left = turn ? hi : b.b(ws);
   const _Float16* right = turn ? b.b(ws) : b.t(ws, turn, a.flip);
@@ -478,42 +558,57 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void k_muon_apply(MuArgs a) {
   const float decay = float(1.0 - lr * a.weight_decay), scale = mu_scale(it.rows, it.cols);
   const float rate = it.m ? float(lr * it.adjust / scale) : 1.f / scale;
   const MuWindow win(it, (int64_t(it.e0 + e) * it.rows + i0) * it.cols, min(ni, max(0, it.rows - i0)));
-  _Float16 *hs = b.s(ws, turn, a.flip ^ 1), *ht = b.t(ws, turn, a.flip ^ 1), *lw = b.lo(ws);
+  _Float16 *hs = b.s(ws, turn, a.flip ^ 1), *ht = b.t(ws, turn, a.flip ^ 1);
+  uint8_t* lo = b.lo(ws);
+  if (wa * S::FA * 32 >= ni || wb * 64 >= nj) return;   // (padded sizes are multiples of 128)
+  const int wc = wb * 64 + 2 * (lane & 31), c = j0 + wc;
+  const bool pairs = j0 + S::kB <= it.cols && it.cols % 2 == 0;
 #pragma unroll
-  for (int i = 0; i < S::FA; ++i)
+  for (int q = 0; q < 4; ++q) {
+    const int wr = wa * S::FA * 32 + S::result_row(q, half), r0 = i0 + wr;
+    f16x2 xh[S::kRun];
+    uint16_t xl[S::kRun];
 #pragma unroll
-    for (int j = 0; j < S::FB; ++j) {
-      const int r0 = i0 + (wa * S::FA + i) * 32 + 4 * half, c = j0 + (wb * S::FB + j) * 32 + (lane & 31);
-      if ((wa * S::FA + i) * 32 >= ni || (wb * S::FB + j) * 32 >= nj) continue;   // (padded sizes are multiples of 128)
-      const auto row = [](int v) { return 8 * (v >> 2) + (v & 3); };
-      _Float16 xh[16], xl[16];
-#pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        const int64_t at = int64_t(r0 + row(v)) * b.cols + c;
-        xh[v] = hi[at];
-        xl[v] = lo[at];
-      }
-      float x[16];
-#pragma unroll
-      for (int v = 0; v < 16; ++v) x[v] = a.a * (float(xh[v]) + float(xl[v])) + acc[i][j][v];
-      if constexpr (LAST) {
-        store_results<16>(it, win, r0 - i0, c, row, [&](int v) { return x[v]; }, decay, rate);
-      } else {
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          f16x4 h4;
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int64_t at = int64_t(r0 + 8 * v + u) * b.cols + c;
-            const _Float16 h = _Float16(x[4 * v + u]);
-            h4[u] = h;
-            hs[at] = h;
-            lw[at] = _Float16(x[4 * v + u] - float(h));
-          }
-          *reinterpret_cast<f16x4*>(ht + int64_t(c) * b.rows + r0 + 8 * v) = h4;
-        }
-      }
+    for (int v = 0; v < S::kRun; ++v) {
+      const int64_t at = int64_t(r0 + v) * b.cols + c;
+      xh[v] = *reinterpret_cast<const f16x2*>(hi + at);
+      xl[v] = *reinterpret_cast<const uint16_t*>(lo + at);
     }
+    float x[2][S::kRun];
+#pragma unroll
+    for (int v = 0; v < S::kRun; ++v)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        x[j][v] = a.a * with_low(xh[v][j], int8_t(xl[v] >> (8 * j))) + acc[v >> 2][j][4 * q + (v & 3)];
+    if constexpr (LAST) {
+      if (pairs) {
+        store_pairs<S::kRun>(it, win, wr, c, x, decay, rate);
+      } else {
+        const auto row = [](int v) { return v; };
+#pragma unroll
+        for (int j = 0; j < 2; ++j) store_results<S::kRun>(it, win, wr, c + j, row, [&](int v) { return x[j][v]; }, decay, rate);
+      }
+    } else {
+      _Float16 y[2][S::kRun];
+#pragma unroll
+      for (int v = 0; v < S::kRun; ++v) {
+        const int64_t at = int64_t(r0 + v) * b.cols + c;
+        int low[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          y[j][v] = _Float16(x[j][v]);
+          low[j] = low_bits(x[j][v], y[j][v]);
+        }
+        *reinterpret_cast<f16x2*>(hs + at) = f16x2{y[0][v], y[1][v]};
+        *reinterpret_cast<uint16_t*>(lo + at) = uint16_t((low[0] & 0xFF) | low[1] << 8);
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int v = 0; v < S::kRun; v += 8)
+          *reinterpret_cast<f16x8*>(ht + int64_t(c + j) * b.rows + r0 + v) = *reinterpret_cast<const f16x8*>(&y[j][v]);
+    }
+  }
 }
 
 // ---- small matrices -----------------------------------------------------------------------------
@@ -751,8 +846,8 @@ __global__ __launch_bounds__(512) void k_muon_small(MuArgs a, MuSteps st) {
   }
 }
 
-using MuMid = MuShape<2, 2, 2, 2>;    // 128 x 128
-using MuWide = MuShape<2, 4, 4, 2>;   // 256 x 256
+using MuMid = MuShape<2, 2, 2>;    // 128 x 128
+using MuWide = MuShape<2, 4, 4>;   // 256 x 256
 
 template <class F>
 hipError_t allow_lds(F* f, int bytes, std::atomic<bool> (&done)[kMaxDevices]) {
