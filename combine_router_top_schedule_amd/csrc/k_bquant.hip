@@ -114,6 +114,24 @@ __global__ __launch_bounds__(256) void k_bquant_rows(RowsArgs a) {
   if (i < nb && out < a.rows) a.scales[int64_t(b0 + i) * a.rows + out] = s[i][rr];
 }
 
+// The tiles behind the groups': rows before the first group and behind the last, which only get row codes.
+__device__ __forceinline__ bool find_outside_tile(const RowGroups& rg, int t, GroupTile& gt) {
+  if (!rg.offsets) return false;
+  const int lane = threadIdx.x & 63;
+  int last = clamp_offset(rg.offsets[0], rg.rows);
+  const int head = last;
+  for (int g = lane; g < rg.groups; g += 64) last = max(last, clamp_offset(rg.offsets[g + 1], rg.rows));
+#pragma unroll
+  for (int o = 32; o; o >>= 1) last = max(last, __shfl_xor(last, o, 64));
+  const int before = (head + kBlk - 1) / kBlk, u = t - count_group_tiles(rg, kBlk);
+  const int64_t row0 = u < before ? int64_t(u) * kBlk : last + int64_t(u - before) * kBlk;
+  const int64_t end = u < before ? head : rg.rows;
+  if (row0 >= end) return false;
+  gt.row0 = gt.tile0 = row0;
+  gt.rows = int(min(int64_t(kBlk), end - row0));
+  return true;
+}
+
 struct TileArgs {
   const void* x;
   uint8_t* codes;       // null: not wanted
@@ -156,7 +174,10 @@ __global__ __launch_bounds__(256) void k_bquant_tile(TileArgs a) {
     }
   } else {
     gt = find_group_tile(a.rg, t, kBlk);
-    if (gt.group < 0) return;
+    if (gt.group < 0) {
+      if (!codes || !find_outside_tile(a.rg, t, gt)) return;
+      codes_t = nullptr;
+    }
   }
   const int r0 = (tid >> 4) * 8, c = (tid & 15) * 8, col = jb * kBlk + c;
   Q8 q[8];
@@ -210,7 +231,7 @@ __global__ __launch_bounds__(256) void k_bquant_tile(TileArgs a) {
     for (int j = 0; j < 8; ++j) {
       const float m = fmaxf(fmaxf(s_col[0][c + j], s_col[1][c + j]), fmaxf(s_col[2][c + j], s_col[3][c + j]));
       fc[j] = kBlkTop / m;
-      if (tid < 16 && col + j < a.k) scales_t[(gt.tile0 / kBlk) * int64_t(a.k) + col + j] = m / kBlkTop;
+      if (codes_t && tid < 16 && col + j < a.k) scales_t[(gt.tile0 / kBlk) * int64_t(a.k) + col + j] = m / kBlkTop;
     }
     if (codes && tid < gt.rows) scales[int64_t(jb) * a.rg.rows + gt.row0 + tid] = s_row[tid];
   }
@@ -272,14 +293,13 @@ hipError_t launch_block_quantize(const mok_block_desc& d, const void* x, const i
   if (d.rows == 0) return hipSuccess;
   const bool bf = d.elem == MOK_ELEM_BF16;
   const int kb = int(cdiv(d.k, kBlk));
-  if (codes) {
+  if (!codes_t) {
     const RowsArgs a{x, codes, scales, d.rows, d.stride, d.k, kb};
-    const hipError_t e = bf ? rows_typed<uint16_t>(a, s) : rows_typed<float>(a, s);
-    if (e != hipSuccess || !codes_t) return e;
+    return bf ? rows_typed<uint16_t>(a, s) : rows_typed<float>(a, s);
   }
-  const TileArgs a{x, nullptr, nullptr, codes_t, scales_t, RowGroups{offsets, d.rows, d.groups}, d.stride,
+  const TileArgs a{x, codes, scales, codes_t, scales_t, RowGroups{offsets, d.rows, d.groups}, d.stride,
                    block_padded_rows(d.rows, d.groups), d.k, kb, 0};
-  const int64_t tiles = group_tiles_max(d.rows, d.groups, kBlk);
+  const int64_t tiles = group_tiles_max(d.rows, d.groups, kBlk) + (codes && offsets ? 2 : 0);
   return bf ? tile_typed<uint16_t, false>(a, tiles, s) : tile_typed<float, false>(a, tiles, s);
 }
 
