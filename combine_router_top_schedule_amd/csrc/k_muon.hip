@@ -18,6 +18,10 @@
 
 #include "k_gemm.h"
 
+// What is fused is written so: left to the compiler, the variants of a kernel would round differently, and a matrix's result
+// depend on what else is in the call.
+#pragma clang fp contract(off)
+
 namespace mok {
 namespace {
 
@@ -77,6 +81,13 @@ struct MuBuffers {
   __device__ double* parts(uint8_t* ws) const { return reinterpret_cast<double*>(ws + parts_at()); }
   __device__ static _Float16* at(uint8_t* p, int64_t off) { return reinterpret_cast<_Float16*>(p + off); }
 };
+
+// x rounded to fp16. The compiler would join this with the sum that gives x in an instruction that rounds once, in some
+// variants of a kernel and not in others.
+__device__ __forceinline__ _Float16 to_half(float x) {
+  asm("" : "+v"(x));
+  return _Float16(x);
+}
 
 // X's lower bits: what fp16 leaves of x, in 256ths of h's last place (2^-24 for the smallest), one byte.
 __device__ __forceinline__ int exponent_of(_Float16 h) {
@@ -139,8 +150,8 @@ __global__ __launch_bounds__(256) void k_muon_norm(MuArgs a) {
     g *= clip;
     float u = g;
     if (it.m) {
-      m = m * a.mu + g;
-      u = a.nesterov ? g + a.mu * m : m;
+      m = fmaf(m, a.mu, g);
+      u = a.nesterov ? fmaf(a.mu, m, g) : m;
     }
     const double d = u;
     sum = fma(d, d, sum);
@@ -232,7 +243,7 @@ __device__ __forceinline__ void store_results(const MuItem& it, const MuWindow& 
     for (int v = 0; v < N; ++v) y[v] = load_f32(p, at + row(v) * win.cols);
 #pragma unroll
     for (int v = 0; v < N; ++v) {
-      y[v] = y[v] * decay - value(v) * rate;
+      y[v] = fmaf(-value(v), rate, y[v] * decay);
       store_f32(p, at + row(v) * win.cols, y[v]);
     }
     if (it.copy) {
@@ -263,7 +274,7 @@ __device__ __forceinline__ void store_pairs(const MuItem& it, const MuWindow& wi
     }
 #pragma unroll
     for (int v = 0; v < N; ++v) {
-      for (int j = 0; j < 2; ++j) y[j][v] = y[j][v] * decay - x[j][v] * rate;
+      for (int j = 0; j < 2; ++j) y[j][v] = fmaf(-x[j][v], rate, y[j][v] * decay);
       decltype(__builtin_amdgcn_raw_buffer_load_b64(p, 0, 0, 0)) t;
       t[0] = __float_as_uint(y[0][v]);
       t[1] = __float_as_uint(y[1][v]);
@@ -322,9 +333,9 @@ __global__ __launch_bounds__(256) void k_muon_start(MuArgs a) {
   for (int k = 0; k < 16; ++k) {
     const int r = wv + 4 * k;
     float u = g[k] * clip;
-    if (it.m) u = a.nesterov ? u + a.mu * m[k] : m[k];
+    if (it.m) u = a.nesterov ? fmaf(a.mu, m[k], u) : m[k];
     const float x = u * f;
-    const _Float16 h = _Float16(x);
+    const _Float16 h = to_half(x);
     const int64_t at = int64_t(r0 + r) * b.cols + c0 + c;
     hs[at] = h;
     lo[at] = uint8_t(low_bits(x, h));
@@ -516,7 +527,7 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void k_muon_gram(MuArgs a) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const float g = acc[v >> 2][j][4 * q + (v & 3)];
-        y[j][v] = _Float16(SECOND ? a.c * g + a.b * float(z[v][j]) : g * down);
+        y[j][v] = to_half(SECOND ? fmaf(a.c, g, a.b * float(z[v][j])) : g * down);
       }
       *reinterpret_cast<f16x2*>(out + int64_t(r0 + v) * b.m + c) = f16x2{y[0][v], y[1][v]};
     }
@@ -579,7 +590,7 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void k_muon_apply(MuArgs a) {
     for (int v = 0; v < S::kRun; ++v)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
-        x[j][v] = a.a * with_low(xh[v][j], int8_t(xl[v] >> (8 * j))) + acc[v >> 2][j][4 * q + (v & 3)];
+        x[j][v] = fmaf(a.a, with_low(xh[v][j], int8_t(xl[v] >> (8 * j))), acc[v >> 2][j][4 * q + (v & 3)]);
     if constexpr (LAST) {
       if (pairs) {
         store_pairs<S::kRun>(it, win, wr, c, x, decay, rate);
@@ -596,7 +607,7 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void k_muon_apply(MuArgs a) {
         int low[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          y[j][v] = _Float16(x[j][v]);
+          y[j][v] = to_half(x[j][v]);
           low[j] = low_bits(x[j][v], y[j][v]);
         }
         *reinterpret_cast<f16x2*>(hs + at) = f16x2{y[0][v], y[1][v]};
@@ -714,9 +725,9 @@ __device__ __forceinline__ void muon_small(const MuArgs& a, const MuSteps& st, c
 #pragma unroll
       for (int v = 0; v < 16; ++v) {
         g[v] *= clip;
-        m[v] = m[v] * a.mu + g[v];
+        m[v] = fmaf(m[v], a.mu, g[v]);
         store_f32(rm, at + row(v) * it.cols, m[v]);
-        x[q][v] = a.nesterov ? g[v] + a.mu * m[v] : m[v];
+        x[q][v] = a.nesterov ? fmaf(a.mu, m[v], g[v]) : m[v];
       }
     } else {
 #pragma unroll
@@ -754,7 +765,7 @@ __device__ __forceinline__ void muon_small(const MuArgs& a, const MuSteps& st, c
       if (glive[q])
 #pragma unroll
         for (int v = 0; v < 16; ++v)
-          gram[small_at(gr[q] + 8 * (v >> 2) + 4 * h + (v & 3), gc[q] + c, kShort)] = _Float16(g[q][v]);
+          gram[small_at(gr[q] + 8 * (v >> 2) + 4 * h + (v & 3), gc[q] + c, kShort)] = to_half(g[q][v]);
   };
   const _Float16 *across_rows = TURN ? xt : xs, *along_rows = TURN ? xs : xt;   // rows of n, and of m halves
 #pragma unroll 1
@@ -771,7 +782,7 @@ __device__ __forceinline__ void muon_small(const MuArgs& a, const MuSteps& st, c
             f16x4 y;
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-              y[u] = _Float16(x[q][4 * v + u]);
+              y[u] = to_half(x[q][4 * v + u]);
               xs[small_at(r + u, cq(q) + c, TURN ? kShort : kLong)] = y[u];
             }
             *reinterpret_cast<f16x4*>(xt + small_at(cq(q) + c, r, TURN ? kLong : kShort)) = y;
@@ -797,7 +808,9 @@ __device__ __forceinline__ void muon_small(const MuArgs& a, const MuSteps& st, c
       f32x16 y[G];
       small_products<G, 1, false>(left, right, kShort, y);
 #pragma unroll
-      for (int q = 0; q < G; ++q) g[q] = cc * y[q] + cb * g[q];
+      for (int q = 0; q < G; ++q)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) g[q][v] = fmaf(cc, y[q][v], cb * g[q][v]);
     }
     __syncthreads();
     if (glive[0]) put_gram(g);
@@ -813,7 +826,7 @@ __device__ __forceinline__ void muon_small(const MuArgs& a, const MuSteps& st, c
 #pragma unroll
       for (int q = 0; q < N; ++q)
 #pragma unroll
-        for (int v = 0; v < 16; ++v) x[q][v] = ca * x[q][v] + y[q][v];
+        for (int v = 0; v < 16; ++v) x[q][v] = fmaf(ca, x[q][v], y[q][v]);
     }
     __syncthreads();
   }

@@ -1,12 +1,12 @@
 """Optimizer state for a list of parameters: allocates the moments (with torch, on the parameters'
-device) and calls mok_grad_sumsq and mok_adamw. Argument marshalling only."""
+device) and calls mok_grad_sumsq, mok_adamw and mok_muon. Argument marshalling only."""
 from __future__ import annotations
 
 from typing import Optional
 
 import torch
 
-from . import adamw_plan, mok_adamw, mok_grad_sumsq, sumsq_plan
+from . import adamw_plan, mok_adamw, mok_grad_sumsq, mok_muon, muon_plan, sumsq_plan
 
 
 class MokAdamW:
@@ -55,3 +55,32 @@ class MokAdamW:
                   beta2=self.betas[1], eps=self.eps, weight_decay=self.weight_decay,
                   seed=self.seed + step, sumsq=self.sumsq, max_norm=self.max_norm)
         self.steps = step   # (a refused call is no step)
+
+
+class MokMuon:
+    """Muon over matrices [..][rows][cols] updated in place from gradients that stay in the given tensors: momentum,
+    orthogonalised by Newton-Schulz steps.
+
+    params: float32 masters; grads: float32 or bfloat16 (one type); copies: bfloat16 copies, written by every step (None in
+    the place of a master without one). adjust: "rms" gives updates AdamW's size, so both can share a rate; "spectral",
+    "none". max_norm and check_finite as for MokAdamW."""
+
+    def __init__(self, params, grads, copies=None, lr: float = 1e-3, momentum: float = 0.95, nesterov: bool = True,
+                 weight_decay: float = 0.0, eps: float = 1e-7, adjust: str = "rms", max_norm: Optional[float] = None,
+                 check_finite: bool = False):
+        self.params, self.grads, self.copies, self.lr = list(params), list(grads), copies, lr
+        self.hyper = dict(momentum=momentum, nesterov=nesterov, weight_decay=weight_decay, eps=eps, adjust=adjust)
+        self.max_norm = max_norm
+        self.m = [torch.zeros_like(p) for p in self.params]
+        self.plan = muon_plan(self.params, self.grads, self.m, copies)
+        self.sumsq = None
+        if max_norm is not None or check_finite:
+            self.sumsq_plan = sumsq_plan(self.grads)
+            self.sumsq = torch.zeros(1, dtype=torch.float64, device=self.params[0].device)
+
+    def step(self, lr=None):
+        """One step; `lr` replaces the rate given at the start, for this step, and may be a device tensor (float64 [1]),
+        which a captured step reads when it runs."""
+        if self.sumsq is not None:
+            mok_grad_sumsq(self.sumsq_plan, self.sumsq)
+        mok_muon(self.plan, lr=self.lr if lr is None else lr, sumsq=self.sumsq, max_norm=self.max_norm, **self.hyper)

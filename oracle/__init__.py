@@ -27,6 +27,9 @@ Modules:
   gradient, in fp64.
 * ``optim``       the norm of all gradients and AdamW in fp64, and bit for bit the fp32 and 8-bit
   arithmetic that ``include/mok.h`` states.
+* ``block``       block-scaled FP8 (one fp32 scale for 128 values), bit for bit as ``include/mok.h``
+  states it, and its products by group in fp64.
+* ``muon``        Newton-Schulz steps and the Muon step in fp64, and with the fp16 roundings of a kernel.
 * ``brute``       pure-Python loops over the same definitions, for tiny shapes only; it
   pins ``moe_oracle``.
 """
