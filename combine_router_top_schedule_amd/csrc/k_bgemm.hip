@@ -202,7 +202,11 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void k_block_product(ProductArgs
   const uint8_t *a, *b;
   const float *as, *bs;
   if constexpr (GRAD) {
-    const int id = xcd_logical_id(), per = p.tiles_n * p.tiles_k, g = id / per, t = id % per;
+    // Every XCD takes an eighth of each group's tiles, which follow one another: groups differ in length, and with whole
+    // groups to an XCD the one with the longest would be the last (uneven groups: 694 us instead of 590).
+    const int per = p.tiles_n * p.tiles_k, run = (per + kXcds - 1) / kXcds, in = blockIdx.x / kXcds;
+    const int g = in / run, t = blockIdx.x % kXcds * run + in % run;
+    if (t >= per) return;
     gt = find_group(p.rg, g);
     int tn, tk;
     tile_coords(t, p.tiles_n, p.tiles_k, tn, tk);
@@ -354,22 +358,30 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void k_block_product(ProductArgs
   wait_vmem();   // (loads into LDS do not outlive the workgroup)
   if constexpr (AHEAD) add_scaled(acc[FR - 1][FT - 1], part[1], part_scale);
   if constexpr (GRAD) {
+    // (through a buffer that ends with the tile: what is outside reads as zero and is not written, without branches, around
+    // which loads would be waited for one by one)
     const int tid = tile_tid(), el = tid & 31, eh = (tid >> 5) & 1;
     float* out = static_cast<float*>(p.out) + (int64_t(gt.group) * p.n + n0) * p.k + k0;
+    const __amdgpu_buffer_rsrc_t ro = make_rsrc(out, (int64_t(valid_a - 1) * p.k + valid_b) * 4);
 #pragma unroll
-    for (int i = 0; i < S::FA; ++i)
+    for (int j = 0; j < S::FB; ++j) {
+      const int c = (wb * S::FB + j) * 32 + el;
 #pragma unroll
-      for (int j = 0; j < S::FB; ++j) {
-        const int c = (wb * S::FB + j) * 32 + el;
+      for (int i = 0; i < S::FA; ++i) {
+        const int r0 = (wa * S::FA + i) * 32 + 4 * eh, at = c < valid_b ? (r0 * p.k + c) * 4 : 1 << 30;
+        if (p.accumulate) {
+          float y[16];
 #pragma unroll
-        for (int v = 0; v < 16; ++v) {
-          const int r = (wa * S::FA + i) * 32 + 8 * (v >> 2) + 4 * eh + (v & 3);
-          if (r < valid_a && c < valid_b) {
-            float* o = out + int64_t(r) * p.k + c;
-            *o = p.accumulate ? *o + acc[i][j][v] : acc[i][j][v];
-          }
+          for (int v = 0; v < 16; ++v)
+            y[v] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(ro, at + (8 * (v >> 2) + (v & 3)) * p.k * 4, 0, 0));
+#pragma unroll
+          for (int v = 0; v < 16; ++v) acc[i][j][v] += y[v];
         }
+#pragma unroll
+        for (int v = 0; v < 16; ++v)
+          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(acc[i][j][v]), ro, at + (8 * (v >> 2) + (v & 3)) * p.k * 4, 0, 0);
       }
+    }
   } else {
     // A lane holds 4 consecutive columns of one row: rows come together in LDS and go out in whole runs.
     if constexpr (WIDE) store_rows<S, float>(smem, acc, p, gt.row0, n0, valid_b, valid_a);
@@ -598,7 +610,7 @@ hipError_t launch_block_wgrad(const mok_block_desc& d, const uint8_t* dy, const 
   using S = Mid;
   p.tiles_n = int(cdiv(d.n, S::kA));
   p.tiles_k = int(cdiv(d.k, S::kB));
-  return launch_product<S, true, true>(p, int64_t(d.groups) * p.tiles_n * p.tiles_k, s);
+  return launch_product<S, true, true>(p, int64_t(d.groups) * align_up(int64_t(p.tiles_n) * p.tiles_k, kXcds), s);
 }
 
 }  // namespace mok
