@@ -881,20 +881,29 @@ def _offsets(offsets, dev: int):
         return 1, None
     if offsets.dim() != 1 or offsets.shape[0] < 2:
         raise ValueError(f"offsets must be [groups + 1], not {tuple(offsets.shape)}")
-    return offsets.shape[0] - 1, _want(offsets, "offsets", _torch.int32, offsets.shape[0], dev)
+    n = offsets.shape[0]
+    return n - 1, _want(offsets, "offsets", _torch.int32, n, dev)
 
 
-def _codes(t, name: str, shape, dev: int):
-    """Address of contiguous uint8 (or float8_e4m3fn) codes of `shape`."""
-    if tuple(t.shape) != tuple(shape) or t.dtype not in (_torch.uint8, _torch.float8_e4m3fn):
-        raise ValueError(f"{name} must be uint8 or float8_e4m3fn {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
-    return _want(t, name, t.dtype, t.numel(), dev)
+def _shaped(t, name: str, shape, dev: int, codes: bool):
+    """Address of a contiguous tensor of `shape`, of E4M3 codes (uint8 or float8_e4m3fn) or of float32 scales."""
+    dt = t.dtype
+    if (t.shape != shape or not (dt is _torch.uint8 or dt is _torch.float8_e4m3fn if codes else dt is _torch.float32)
+            or t.get_device() != dev or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {'uint8 or float8_e4m3fn' if codes else 'float32'} tensor "
+                         f"{tuple(shape)} on device {dev}, not {dt} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+    return t.data_ptr()
 
 
-def _scales(t, name: str, shape, dev: int):
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {tuple(shape)}, not {tuple(t.shape)}")
-    return _want(t, name, _torch.float32, t.numel(), dev)
+def _launch(fn: str, dev: int, stream, *args):
+    """Calls the library with the stream last, on the tensors' device (the short way where that is the current one)."""
+    if stream is None and _torch.cuda.current_device() == dev:
+        code = getattr(_lib or lib(), fn)(*args, _raw_stream(dev))
+    else:
+        with _on_device(dev, stream) as s:
+            code = getattr(lib(), fn)(*args, s)
+    if code:
+        raise MokError(fn, code)
 
 
 def mok_block_quantize(x, codes=None, scales=None, codes_t=None, scales_t=None, offsets=None, stream=None):
@@ -902,49 +911,50 @@ def mok_block_quantize(x, codes=None, scales=None, codes_t=None, scales_t=None, 
     [R][up(K)] and scales [up(K) / 128][R] are blocked along the row, for products; codes_t [K][P] and scales_t
     [P / 128][K], P = block_padded_rows(R, groups), along the rows of each group, for the weight gradient.
     offsets: int32 [groups + 1] (None: one group of all rows)."""
-    torch, dev = _tch(), _device_of(x)
+    _tch()
+    dev = _device_of(x)
     R, K, ld = _rows2d(x, "x")
     G, off = _offsets(offsets, dev)
-    d = MokBlockDesc(R, ld, G, 1, K, _elem(x, "x"))
     if (codes is None) != (scales is None) or (codes_t is None) != (scales_t is None):
         raise ValueError("codes and scales go together")
+    kb = -(-K // 128)
     c = s = ct = st = None
     if codes is not None:
-        c = _codes(codes, "codes", (R, _up128(K)), dev)
-        s = _scales(scales, "scales", (_up128(K) // 128, R), dev)
+        c, s = _shaped(codes, "codes", (R, kb * 128), dev, True), _shaped(scales, "scales", (kb, R), dev, False)
     if codes_t is not None:
         P = block_padded_rows(R, G)
-        ct = _codes(codes_t, "codes_t", (K, P), dev)
-        st = _scales(scales_t, "scales_t", (P // 128, K), dev)
-    with _on_device(dev, stream) as q:
-        _check("mok_block_quantize", lib().mok_block_quantize(ctypes.byref(d), x.data_ptr(), off, c, s, ct, st, q))
+        ct, st = _shaped(codes_t, "codes_t", (K, P), dev, True), _shaped(scales_t, "scales_t", (P // 128, K), dev, False)
+    _launch("mok_block_quantize", dev, stream, ctypes.byref(MokBlockDesc(R, ld, G, 1, K, _elem(x, "x"))), x.data_ptr(),
+            off, c, s, ct, st)
 
 
 def mok_block_quantize_weights(w, codes, scales, codes_t=None, scales_t=None, stream=None):
     """E4M3 codes of weights w [G][N][K] (contiguous, float32 or bfloat16), one scale for 128 x 128 values: codes
     [G][N][up(K)], scales [G][up(N) / 128][up(K) / 128]; codes_t and scales_t are those of the transposed weights [G][K][N]."""
-    torch, dev = _tch(), _device_of(w)
+    _tch()
+    dev = _device_of(w)
     if w.dim() != 3:
         raise ValueError(f"w must be [groups][N][K], not {tuple(w.shape)}")
     G, N, K = w.shape
     src = _want(w, "w", w.dtype, w.numel(), dev)
-    d = MokBlockDesc(0, K, G, N, K, _elem(w, "w"))
     if (codes_t is None) != (scales_t is None):
         raise ValueError("codes_t and scales_t go together")
     kb, nb = _up128(K) // 128, _up128(N) // 128
-    c, s = _codes(codes, "codes", (G, N, kb * 128), dev), _scales(scales, "scales", (G, nb, kb), dev)
+    c, s = _shaped(codes, "codes", (G, N, kb * 128), dev, True), _shaped(scales, "scales", (G, nb, kb), dev, False)
     ct = st = None
     if codes_t is not None:
-        ct, st = _codes(codes_t, "codes_t", (G, K, nb * 128), dev), _scales(scales_t, "scales_t", (G, kb, nb), dev)
-    with _on_device(dev, stream) as q:
-        _check("mok_block_quantize_weights", lib().mok_block_quantize_weights(ctypes.byref(d), src, c, s, ct, st, q))
+        ct = _shaped(codes_t, "codes_t", (G, K, nb * 128), dev, True)
+        st = _shaped(scales_t, "scales_t", (G, kb, nb), dev, False)
+    _launch("mok_block_quantize_weights", dev, stream, ctypes.byref(MokBlockDesc(0, K, G, N, K, _elem(w, "w"))), src, c, s,
+            ct, st)
 
 
 def mok_block_gemm(x, x_scales, w, w_scales, out, offsets=None, stream=None):
     """out [R][N] (float32 or bfloat16, rows may be strided) = x w^T by groups of rows: x, x_scales from
     mok_block_quantize, w, w_scales from mok_block_quantize_weights (their transposed ones give the input gradient). Rows
     in no group are left as they are."""
-    torch, dev = _tch(), _device_of(x)
+    _tch()
+    dev = _device_of(x)
     R, N, ld = _rows2d(out, "out")
     G, off = _offsets(offsets, dev)
     if x.dim() != 2 or x.shape[1] % 128 or x.shape[1] == 0:
@@ -952,18 +962,17 @@ def mok_block_gemm(x, x_scales, w, w_scales, out, offsets=None, stream=None):
     K = x.shape[1]
     if out.get_device() != dev:
         raise ValueError(f"out is on {out.device}, x on device {dev}")
-    d = MokBlockDesc(R, ld, G, N, K, _elem(out, "out"))
-    with _on_device(dev, stream) as q:
-        _check("mok_block_gemm", lib().mok_block_gemm(
-            ctypes.byref(d), _codes(x, "x", (R, K), dev), _scales(x_scales, "x_scales", (K // 128, R), dev),
-            _codes(w, "w", (G, N, K), dev), _scales(w_scales, "w_scales", (G, _up128(N) // 128, K // 128), dev), off,
-            out.data_ptr(), q))
+    _launch("mok_block_gemm", dev, stream, ctypes.byref(MokBlockDesc(R, ld, G, N, K, _elem(out, "out"))),
+            _shaped(x, "x", (R, K), dev, True), _shaped(x_scales, "x_scales", (K // 128, R), dev, False),
+            _shaped(w, "w", (G, N, K), dev, True), _shaped(w_scales, "w_scales", (G, -(-N // 128), K // 128), dev, False),
+            off, out.data_ptr())
 
 
 def mok_block_wgrad(dy_t, dy_scales, x_t, x_scales, dw, offsets=None, accumulate: bool = False, stream=None):
     """dw [G][N][K] (float32, contiguous) = dy^T x by groups of rows, or added to with `accumulate`, from the column codes
     and scales (mok_block_quantize) of dy [R][N] and x [R][K]."""
-    torch, dev = _tch(), _device_of(dw)
+    _tch()
+    dev = _device_of(dw)
     if dw.dim() != 3:
         raise ValueError(f"dw must be [groups][N][K], not {tuple(dw.shape)}")
     G, N, K = dw.shape
@@ -974,9 +983,7 @@ def mok_block_wgrad(dy_t, dy_scales, x_t, x_scales, dw, offsets=None, accumulate
     R = P + 127 - 127 * G   # the most rows that need P columns: a bound for the offsets as good as R itself
     if P < 0 or P % 128 or R < 0:
         raise ValueError(f"dy_t must be [{N}][block_padded_rows(rows, {G})], not {tuple(dy_t.shape)}")
-    d = MokBlockDesc(R, 0, G, N, K, MOK_ELEM_F32)
-    with _on_device(dev, stream) as q:
-        _check("mok_block_wgrad", lib().mok_block_wgrad(
-            ctypes.byref(d), _codes(dy_t, "dy_t", (N, P), dev), _scales(dy_scales, "dy_scales", (P // 128, N), dev),
-            _codes(x_t, "x_t", (K, P), dev), _scales(x_scales, "x_scales", (P // 128, K), dev), off,
-            _want(dw, "dw", torch.float32, G * N * K, dev), int(accumulate), q))
+    _launch("mok_block_wgrad", dev, stream, ctypes.byref(MokBlockDesc(R, 0, G, N, K, MOK_ELEM_F32)),
+            _shaped(dy_t, "dy_t", (N, P), dev, True), _shaped(dy_scales, "dy_scales", (P // 128, N), dev, False),
+            _shaped(x_t, "x_t", (K, P), dev, True), _shaped(x_scales, "x_scales", (P // 128, K), dev, False), off,
+            _shaped(dw, "dw", (G, N, K), dev, False), int(accumulate))

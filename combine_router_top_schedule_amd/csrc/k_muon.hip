@@ -747,12 +747,13 @@ __device__ __forceinline__ void muon_small(const MuArgs& a, const MuSteps& st, c
   for (int q = 0; q < N; ++q)
 #pragma unroll
     for (int v = 0; v < 16; ++v) x[q][v] *= f;
-  constexpr int G = SHORTER * SHORTER > 8 ? 2 : 1;
+  // A's blocks of the wave, 32 x 32 of SHORTER x SHORTER: number w, and of those from 8 on one in the same column.
+  constexpr int G = SHORTER > 2 ? 2 : 1;
   int gr[G], gc[G];
   bool glive[G];
 #pragma unroll
   for (int q = 0; q < G; ++q) {
-    const int b = w + 8 * q;
+    const int b = q == 0 || SHORTER == 4 ? w + 8 * q : w == 8 % SHORTER ? 8 : SHORTER * SHORTER;
     glive[q] = b < SHORTER * SHORTER;
     gr[q] = glive[q] ? b / SHORTER * 32 : 0;
     gc[q] = glive[q] ? b % SHORTER * 32 : 0;
@@ -794,8 +795,8 @@ __device__ __forceinline__ void muon_small(const MuArgs& a, const MuSteps& st, c
     if (glive[0]) {
       const int l = tile_tid() & 31;
       const SmallRow left[2] = {SmallRow(across_rows, gr[0] + l, kLong), SmallRow(across_rows, gr[G - 1] + l, kLong)};
-      const SmallRow right[2] = {SmallRow(across_rows, gc[0] + l, kLong), SmallRow(across_rows, gc[G - 1] + l, kLong)};
-      small_products<G, 1, false>(left, right, n, g);
+      const SmallRow right[1] = {SmallRow(across_rows, gc[0] + l, kLong)};   // (two blocks of a wave share their column)
+      small_products<G, G, false>(left, right, n, g);
 #pragma unroll
       for (int q = 0; q < G; ++q) g[q] *= down;
       put_gram(g);
@@ -804,9 +805,9 @@ __device__ __forceinline__ void muon_small(const MuArgs& a, const MuSteps& st, c
     if (glive[0]) {
       const int l = tile_tid() & 31;
       const SmallRow left[2] = {SmallRow(gram, gr[0] + l, kShort), SmallRow(gram, gr[G - 1] + l, kShort)};
-      const SmallRow right[2] = {SmallRow(gram, gc[0] + l, kShort), SmallRow(gram, gc[G - 1] + l, kShort)};
+      const SmallRow right[1] = {SmallRow(gram, gc[0] + l, kShort)};
       f32x16 y[G];
-      small_products<G, 1, false>(left, right, kShort, y);
+      small_products<G, G, false>(left, right, kShort, y);
 #pragma unroll
       for (int q = 0; q < G; ++q)
 #pragma unroll
