@@ -921,8 +921,9 @@ struct MuPart {
   int64_t ws;                 // offset of their buffers
 };
 
+// (small ones need none; counted as 512 bytes, a run has at most 2^22 of them, a workgroup each)
 int64_t matrix_bytes(const mok_muon_tensor& t, bool small) {
-  return small ? 0 : align_up(MuBuffers(t.rows, t.cols).bytes(), 256);
+  return small ? 512 : align_up(MuBuffers(t.rows, t.cols).bytes(), 256);
 }
 
 // Calls go(parts, count, bytes) for each run of the small tensors, or of the others; stops at an error.
@@ -941,8 +942,7 @@ hipError_t each_run(int count, const mok_muon_tensor* t, bool small, G&& go) {
         n = 0;
         bytes = 0;
       }
-      const int64_t room = small ? t[k].batch : std::max<int64_t>(1, (kMuWs - bytes) / one);
-      const int take = int(std::min<int64_t>(t[k].batch - b, room));
+      const int take = int(std::min<int64_t>(t[k].batch - b, std::max<int64_t>(1, (kMuWs - bytes) / one)));
       part[n++] = MuPart{k, b, take, bytes};
       bytes += take * one;
       b += take;

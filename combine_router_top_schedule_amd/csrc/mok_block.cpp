@@ -12,7 +12,7 @@ namespace {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-constexpr int64_t kMaxRows = (int64_t(1) << 28) - 1;      // 16 rows a workgroup, fewer than 2^32 threads
+constexpr int64_t kMaxRows = int64_t(1) << 27;            // 16 rows a workgroup of 256, fewer than 2^32 threads
 constexpr int64_t kMaxColumnRows = int64_t(1) << 22;      // 256 rows of column codes within 32-bit offsets
 constexpr int32_t kMaxWidth = 1 << 20;
 constexpr int64_t kMaxTiles = (int64_t(1) << 22) - 1;     // workgroups of up to 512 threads in a launch

@@ -641,7 +641,7 @@ mok_status mok_orthogonalize(int32_t num_tensors, const mok_orthogonalize_tensor
  *   transposed     the weight codes of [G][K][N]: same values, scales transposed
  * Codes are 16-byte aligned, scales and offsets 4-byte. */
 typedef struct {
-  int64_t rows;      /* R; 0..2^28 - 1, and at most 2^22 where column codes are written or read         */
+  int64_t rows;      /* R; 0..2^27, and at most 2^22 where column codes are written or read             */
   int64_t stride;    /* elements from one row of the unquantised operand to the next; >= its columns    */
   int32_t groups;    /* G; 1..1024                                                                     */
   int32_t n;         /* N; 1..2^20                                                                     */

@@ -433,3 +433,22 @@ def test_binding_refusals():
             f()
         except mok.MokError as e:
             assert e.code in (1, 4)
+
+
+def test_many_rows_and_few_columns():
+    """More row tiles than a grid's second dimension holds."""
+    R, N, K = 5_000_000, 16, 128
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randint(0, 0x7F, (R, K), dtype=torch.uint8, device="cuda", generator=g)
+    xs = torch.rand(1, R, device="cuda", generator=g)
+    w, ws = weights(np.random.default_rng(1), 1, N, K)
+    out = torch.zeros(R, N, dtype=BF, device="cuda")
+    mok.mok_block_gemm(x, xs, w, ws, out)
+    for a in (0, 2_499_990, R - 10):
+        want, size, most = ob.gemm(host(x[a:a + 10]), host(xs[:, a:a + 10]), host(w), host(ws), [0, 10], np.zeros((10, N)))
+        close(host(out[a:a + 10]), want, size, most, K, True)
+    c, s = torch.zeros(R, 128, dtype=torch.uint8, device="cuda"), torch.zeros(1, R, device="cuda")
+    mok.mok_block_quantize(out, c, s)
+    for a in (0, R - 10):
+        rc, rs = ob.quantize_rows(host(out[a:a + 10]))
+        assert same_codes(host(c[a:a + 10]), rc) and np.array_equal(host(s[:, a:a + 10]), rs)

@@ -331,3 +331,15 @@ def test_training_step_of_an_experts_map():
         assert not torch.equal(before, w) and torch.isfinite(w).all()
         seen.append(lin.wq.clone())
     assert all(not torch.equal(a, b) for a, b in zip(seen, seen[1:]))
+
+
+def test_many_small_matrices():
+    """100,000 matrices in one call, the last as alone."""
+    src = torch.empty(100_000, 9, 5, device="cuda").normal_(generator=torch.Generator(device="cuda").manual_seed(2))
+    out = torch.zeros(src.shape, dtype=BF, device="cuda")
+    mok.mok_orthogonalize(mok.orthogonalize_plan([src], [out]))
+    for k in (0, 65_537, 99_999):
+        alone = torch.zeros(9, 5, dtype=BF, device="cuda")
+        mok.mok_orthogonalize(mok.orthogonalize_plan([src[k].clone()], [alone]))
+        x, far = allowed(host(src[k]))
+        assert torch.equal(alone, out[k]) and np.linalg.norm(host(alone) - x) <= far + 2.0 ** -8 * np.linalg.norm(x)
