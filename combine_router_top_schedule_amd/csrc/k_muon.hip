@@ -622,21 +622,352 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void k_muon_apply(MuArgs a) {
   }
 }
 
+struct MuSteps {
+  int32_t count;
+  float coef[16][3];
+};
+
+// ---- matrices with up to 32 rows or columns -------------------------------------------------------
+// Rounding to fp16 averages out over many directions; of a few, each is off by up to 1e-2. A = u u^T is small here, so
+// the steps are taken on it alone, in fp64 on the matrix cores, and u is read twice whatever their number:
+//   Q = a + b A + c A A,   P <- Q P,   A <- Q A Q,   X = P u / (|u| + eps),   |u|^2 the trace of the first A.
+// Errors of A grow by a^2 a step where X is small: 12^4 in five steps, 1e-12 in fp64. Up to kThinLds elements, one workgroup
+// keeps u in LDS and does it all (THIN_US); longer ones take three launches (THIN_LONG_US).
+constexpr int kThin = 32, kThinRow = kThin + 1, kThinMatrix = kThin * kThinRow;   // doubles
+constexpr int kThinLds = ((160 << 10) - 3 * kThinMatrix * 8) / 4;                 // elements of u beside three matrices
+constexpr int kThinParts = 256;                                                  // partial sums of A at most
+constexpr int kThinChunk = 8192;                                                 // elements of a chunk, of whole columns
+
+typedef __attribute__((ext_vector_type(4))) double f64x4;
+
+struct ThinShape {
+  int m, n, stride;          // rows and columns of u as it lies in LDS, and a row's length there
+  int columns, chunks, parts;
+  __host__ __device__ ThinShape(int rows, int cols) {
+    m = rows < cols ? rows : cols;
+    n = rows < cols ? cols : rows;
+    columns = kThinChunk / m & ~15;
+    chunks = int(cdiv(n, columns));
+    parts = chunks < kThinParts ? chunks : kThinParts;
+    stride = columns | 1;
+  }
+  __host__ __device__ bool thin() const { return m <= kThin; }
+  __host__ __device__ bool fits() const { return thin() && int64_t(m) * (n | 1) <= kThinLds; }
+  __host__ __device__ int64_t bytes() const { return int64_t(parts + 1) * m * m * 8; }   // partial sums, P
+  __host__ __device__ int chunk_lds() const { return kThinMatrix * 8 + m * stride * 4; }
+};
+
+// Calls use(elements, their places in LDS, how many of them) for the columns j0 .. j0 + cols - 1, 8 elements a
+// thread at a time, so that their loads are in flight together. Elements past the last one are the first once more.
+template <int THREADS, class U>
+__device__ __forceinline__ void thin_elements(const MuItem& it, int64_t base, int m, int stride, int j0, int cols, U&& use) {
+  const bool turn = it.rows > it.cols;
+  const int inner = turn ? m : cols, total = m * cols, dq = THREADS / inner, dr = THREADS % inner;
+  int q = threadIdx.x / inner, r = threadIdx.x % inner;
+  for (int e = threadIdx.x; e < total; e += 8 * THREADS) {
+    int64_t i[8];
+    int at[8], count = 0;
+#pragma unroll
+    for (int v = 0; v < 8; ++v) {
+      const bool in = e + v * THREADS < total;
+      i[v] = in ? base + (turn ? int64_t(j0) * m + e + v * THREADS : int64_t(q) * it.cols + j0 + r) : base;
+      at[v] = turn ? r * stride + q : q * stride + r;
+      count += in;
+      q += dq;
+      r += dr;
+      if (r >= inner) r -= inner, ++q;
+    }
+    use(i, at, count);
+  }
+}
+
+template <int THREADS, bool UPDATE>
+__device__ __forceinline__ void thin_load(const MuArgs& a, const MuItem& it, int64_t base, int m, int stride, int j0, int cols,
+                                          float* u) {
+  const float clip = clip_factor(a);
+  thin_elements<THREADS>(it, base, m, stride, j0, cols, [&](const int64_t (&i)[8], const int (&at)[8], int count) {
+    float g[8], mm[8];
+    if (a.gbf) {
+#pragma unroll
+      for (int v = 0; v < 8; ++v) g[v] = element(it.g, true, i[v]);
+    } else {
+#pragma unroll
+      for (int v = 0; v < 8; ++v) g[v] = element(it.g, false, i[v]);
+    }
+    if (it.m) {
+#pragma unroll
+      for (int v = 0; v < 8; ++v) mm[v] = it.m[i[v]];
+    }
+#pragma unroll
+    for (int v = 0; v < 8; ++v)
+      if (v < count) {
+        float x = g[v] * clip;
+        if (it.m) {
+          if constexpr (UPDATE) it.m[i[v]] = mm[v] = fmaf(mm[v], a.mu, x);
+          x = a.nesterov ? fmaf(a.mu, mm[v], x) : mm[v];
+        }
+        u[at[v]] = x;
+      }
+  });
+}
+
+// The update (or the output) by the results in LDS.
+template <int THREADS>
+__device__ __forceinline__ void thin_store(const MuArgs& a, const MuItem& it, int64_t base, int m, int stride, int j0, int cols,
+                                           const float* u) {
+  const double lr = a.lr_dev ? *a.lr_dev : a.lr;
+  const float decay = float(1.0 - lr * a.weight_decay), rate = float(lr * it.adjust);
+  thin_elements<THREADS>(it, base, m, stride, j0, cols, [&](const int64_t (&i)[8], const int (&at)[8], int count) {
+    float* p = static_cast<float*>(it.p);
+    float y[8];
+    if (it.m)
+#pragma unroll
+      for (int v = 0; v < 8; ++v) y[v] = p[i[v]];
+#pragma unroll
+    for (int v = 0; v < 8; ++v)
+      if (v < count) {
+        const float x = u[at[v]];
+        if (it.m) {
+          p[i[v]] = y[v] = fmaf(-x, rate, y[v] * decay);
+          if (it.copy) it.copy[i[v]] = f2bf(y[v]);
+        } else {
+          static_cast<uint16_t*>(it.p)[i[v]] = f2bf(x);
+        }
+      }
+  });
+}
+
+// The lane's part of a 16 x 16 product in fp64: operands' row (or column) lane % 16 at k = lane / 16 of 4; element i of
+// a result is in row 4 i + lane / 16, column lane % 16.
+__device__ __forceinline__ f64x4 thin_mfma(double x, double y, f64x4 c) {
+  return __builtin_amdgcn_mfma_f64_16x16x4f64(x, y, c, 0, 0, 0);
+}
+
+// acc += u u^T over the columns in LDS, blocks (0, 0), (1, 0) and (1, 1); each wave takes every WAVES-th 4 columns.
+template <int WAVES>
+__device__ __forceinline__ void thin_gram(const float* u, int m, int stride, int cols, f64x4 (&acc)[3]) {
+  const int lane = threadIdx.x & 63, r = lane & 15;
+  for (int k0 = wave_id() * 4; k0 < cols; k0 += WAVES * 4) {
+    const int k = k0 + (lane >> 4);
+    const double x = r < m && k < cols ? double(u[r * stride + k]) : 0.0;
+    acc[0] = thin_mfma(x, x, acc[0]);
+    if (m > 16) {
+      const double y = r + 16 < m && k < cols ? double(u[(r + 16) * stride + k]) : 0.0;
+      acc[1] = thin_mfma(y, x, acc[1]);
+      acc[2] = thin_mfma(y, y, acc[2]);
+    }
+  }
+}
+
+// Adds the waves' blocks up in LDS, one wave after another, so that the order is always the same.
+template <int WAVES>
+__device__ __forceinline__ void thin_gather(const f64x4 (&acc)[3], int m, double* sum) {
+  const int lane = threadIdx.x & 63, c = lane & 15, w = wave_id();
+  for (int t = 0; t < WAVES; ++t) {
+    if (t == w)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 4 * i + (lane >> 4);
+        const auto add = [&](int row, int col, double v) {
+          double& d = sum[row * kThinRow + col];
+          d = t ? d + v : v;
+        };
+        add(r, c, acc[0][i]);
+        if (m > 16) {
+          add(r + 16, c, acc[1][i]);
+          add(c, r + 16, acc[1][i]);
+          add(r + 16, c + 16, acc[2][i]);
+        }
+      }
+    __syncthreads();
+  }
+}
+
+// From A = u u^T in LDS: P / (|u| + eps) in `p`. Eight waves; `q` is scratch. The matrices are symmetric (and polynomials of
+// one matrix), so an operand's columns are read as its rows.
+__device__ __forceinline__ void thin_steps(const MuSteps& st, double eps, int m, double* a, double* q, double* p) {
+  const int lane = threadIdx.x & 63, c = lane & 15, w = wave_id(), tiles = m > 16 ? 2 : 1;
+  const int ti = (w & 3) >> 1, tj = w & 1;
+  const bool mine = ti < tiles && tj < tiles;
+  double norm = 0;
+  for (int i = 0; i < m; ++i) norm += a[i * kThinRow + i];
+  norm = sqrt(norm) + eps;
+  __syncthreads();
+  for (int i = threadIdx.x; i < kThinMatrix; i += 512) a[i] = a[i] / norm / norm;
+  __syncthreads();
+  const auto product = [&](const double* x, const double* y) {
+    f64x4 s = {0, 0, 0, 0};
+    for (int k = lane >> 4; k < tiles * 16; k += 4)
+      s = thin_mfma(x[(ti * 16 + c) * kThinRow + k], y[(tj * 16 + c) * kThinRow + k], s);
+    return s;
+  };
+  const auto place = [&](int i) { return (ti * 16 + 4 * i + (lane >> 4)) * kThinRow + tj * 16 + c; };
+  const auto put = [&](double* x, const f64x4& s) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[place(i)] = s[i];
+  };
+  f64x4 s;
+  for (int k = 0; k < st.count; ++k) {
+    const double ca = st.coef[k][0], cb = st.coef[k][1], cc = st.coef[k][2];
+    if (mine && w < 4) {
+      s = product(a, a);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int at = place(i);
+        const bool diagonal = ti == tj && 4 * i + (lane >> 4) == c;
+        s[i] = (diagonal ? ca : 0.0) + cb * a[at] + cc * s[i];
+      }
+      put(q, s);
+    }
+    __syncthreads();
+    if (mine) s = w < 4 ? product(q, a) : k ? product(p, q) : f64x4{q[place(0)], q[place(1)], q[place(2)], q[place(3)]};
+    __syncthreads();
+    if (mine) put(w < 4 ? a : p, s);
+    __syncthreads();
+    if (k + 1 < st.count) {
+      if (mine && w < 4) s = product(a, q);
+      __syncthreads();
+      if (mine && w < 4) put(a, s);
+      __syncthreads();
+    }
+  }
+  if (mine && w >= 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[place(i)] /= norm;
+  }
+  __syncthreads();
+}
+
+// u <- P u, for the columns in LDS; a wave takes 16 at a time.
+template <int WAVES>
+__device__ __forceinline__ void thin_apply(const double* p, float* u, int m, int stride, int cols) {
+  const int lane = threadIdx.x & 63, c = lane & 15;
+  for (int j0 = wave_id() * 16; j0 < cols; j0 += WAVES * 16) {
+    const int j = j0 + c;
+    f64x4 s[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+    for (int k = lane >> 4; k < (m + 3 & ~3); k += 4) {
+      const double x = k < m && j < cols ? double(u[k * stride + j]) : 0.0;
+      s[0] = thin_mfma(p[c * kThinRow + k], x, s[0]);
+      if (m > 16) s[1] = thin_mfma(p[(c + 16) * kThinRow + k], x, s[1]);
+    }
+    if (j < cols)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = 4 * i + (lane >> 4);
+        if (r < m) u[r * stride + j] = float(s[i >> 2][i & 3]);
+      }
+  }
+}
+
+// All of it in one workgroup of eight waves.
+__device__ __forceinline__ void muon_thin(const MuArgs& a, const MuSteps& st, const MuItem& it, int e) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  double *sum = reinterpret_cast<double*>(smem), *q = sum + kThinMatrix, *p = q + kThinMatrix;
+  float* u = reinterpret_cast<float*>(p + kThinMatrix);
+  const ThinShape sh(it.rows, it.cols);
+  const int64_t base = int64_t(it.e0 + e) * it.rows * it.cols;
+  const int stride = sh.n | 1;
+  thin_load<512, true>(a, it, base, sh.m, stride, 0, sh.n, u);
+  __syncthreads();
+  f64x4 acc[3] = {{0, 0, 0, 0}, {0, 0, 0, 0}, {0, 0, 0, 0}};
+  thin_gram<8>(u, sh.m, stride, sh.n, acc);
+  thin_gather<8>(acc, sh.m, sum);
+  thin_steps(st, a.eps, sh.m, sum, q, p);
+  thin_apply<8>(p, u, sh.m, stride, sh.n);
+  __syncthreads();
+  thin_store<512>(a, it, base, sh.m, stride, 0, sh.n, u);
+}
+
+// Partial sums of A: part `blockIdx`'s chunks, every parts-th one; with a momentum, also its update.
+__global__ __launch_bounds__(256) void k_thin_gram(MuArgs a) {
+  if (left_out(a)) return;
+  if (int(blockIdx.x) >= a.first[a.count]) return;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  double* sum = reinterpret_cast<double*>(smem);
+  float* u = reinterpret_cast<float*>(sum + kThinMatrix);
+  const int t = find_item(a, blockIdx.x);
+  const MuItem& it = a.item[t];
+  const ThinShape sh(it.rows, it.cols);
+  const int id = blockIdx.x - a.first[t], e = id / sh.parts, part = id % sh.parts;
+  const int64_t base = int64_t(it.e0 + e) * it.rows * it.cols;
+  f64x4 acc[3] = {{0, 0, 0, 0}, {0, 0, 0, 0}, {0, 0, 0, 0}};
+  for (int c = part; c < sh.chunks; c += sh.parts) {
+    const int j0 = c * sh.columns, cols = min(sh.columns, sh.n - j0);
+    thin_load<256, true>(a, it, base, sh.m, sh.stride, j0, cols, u);
+    __syncthreads();
+    thin_gram<4>(u, sh.m, sh.stride, cols, acc);
+    __syncthreads();
+  }
+  thin_gather<4>(acc, sh.m, sum);
+  double* out = reinterpret_cast<double*>(it.ws + e * align_up(sh.bytes(), 256)) + int64_t(part) * sh.m * sh.m;
+  for (int i = threadIdx.x; i < sh.m * sh.m; i += 256) out[i] = sum[i / sh.m * kThinRow + i % sh.m];
+}
+
+// P of each matrix, from its partial sums.
+__global__ __launch_bounds__(512) void k_thin_steps(MuArgs a, MuSteps st) {
+  if (left_out(a)) return;
+  if (int(blockIdx.x) >= a.first[a.count]) return;
+  __shared__ double sum[kThinMatrix], q[kThinMatrix], p[kThinMatrix];
+  const int t = find_item(a, blockIdx.x), e = blockIdx.x - a.first[t];
+  const MuItem& it = a.item[t];
+  const ThinShape sh(it.rows, it.cols);
+  double* ws = reinterpret_cast<double*>(it.ws + e * align_up(sh.bytes(), 256));
+  const int mm = sh.m * sh.m;
+  for (int i = threadIdx.x; i < kThinMatrix; i += 512) sum[i] = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < mm; i += 512) {
+    double v = 0;
+    for (int part = 0; part < sh.parts; ++part) v += ws[int64_t(part) * mm + i];
+    sum[i / sh.m * kThinRow + i % sh.m] = v;
+  }
+  __syncthreads();
+  thin_steps(st, a.eps, sh.m, sum, q, p);
+  for (int i = threadIdx.x; i < mm; i += 512) ws[int64_t(sh.parts) * mm + i] = p[i / sh.m * kThinRow + i % sh.m];
+}
+
+// The results, a chunk a workgroup.
+__global__ __launch_bounds__(256) void k_thin_apply(MuArgs a) {
+  if (left_out(a)) return;
+  if (int(blockIdx.x) >= a.first[a.count]) return;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  double* p = reinterpret_cast<double*>(smem);
+  float* u = reinterpret_cast<float*>(p + kThinMatrix);
+  const int t = find_item(a, blockIdx.x);
+  const MuItem& it = a.item[t];
+  const ThinShape sh(it.rows, it.cols);
+  const int id = blockIdx.x - a.first[t], e = id / sh.chunks, j0 = id % sh.chunks * sh.columns;
+  const int cols = min(sh.columns, sh.n - j0);
+  const int64_t base = int64_t(it.e0 + e) * it.rows * it.cols;
+  const double* ws = reinterpret_cast<const double*>(it.ws + e * align_up(sh.bytes(), 256)) + int64_t(sh.parts) * sh.m * sh.m;
+  for (int i = threadIdx.x; i < kThin * kThin; i += 256) {
+    const int r = i / kThin, c = i % kThin;
+    p[r * kThinRow + c] = r < sh.m && c < sh.m ? ws[r * sh.m + c] : 0.0;
+  }
+  thin_load<256, false>(a, it, base, sh.m, sh.stride, j0, cols, u);
+  __syncthreads();
+  thin_apply<4>(p, u, sh.m, sh.stride, cols);
+  __syncthreads();
+  thin_store<256>(a, it, base, sh.m, sh.stride, j0, cols, u);
+}
+
 // ---- small matrices -----------------------------------------------------------------------------
 // A matrix whose X and X^T in fp16 fit the LDS beside A takes one workgroup and one launch for everything: X stays in
 // registers in fp32, its fp16 copies, A and then B in LDS. Launches and the way through memory bound the general kernels at
 // such sizes (25 matrices of 256 x 128 and less: 222 us in 17 launches, SMALL_US us here).
 //
-// X is cut into 32 x 32 blocks, 1..4 along its shorter side and up to 32 along the longer one. Wave w takes the
+// X is cut into 32 x 32 blocks, 2..4 along its shorter side and up to 16 along the longer one. Wave w takes the
 // longer side's blocks w, w + 8, ..., for each of them all of the shorter side's: four slots at most, which share the
 // operand of their longer side.
 struct SmallShape {
   int shorter, longer;   // blocks along the sides
-  __host__ __device__ SmallShape(int r, int c) {
+  bool one_workgroup;
+  __host__ __device__ SmallShape(int r, int c) : one_workgroup(ThinShape(r, c).fits()) {
     shorter = ((r < c ? r : c) + 31) / 32;
     longer = ((r < c ? c : r) + 31) / 32;
   }
-  __host__ __device__ bool fits() const { return shorter <= 4 && (longer + 7) / 8 * shorter <= 4; }
+  __host__ __device__ bool fits() const {
+    return shorter == 1 ? one_workgroup : shorter <= 4 && (longer + 7) / 8 * shorter <= 4;
+  }
 };
 // The longest row of the layout in LDS, in halves: that of all rows, so that addresses are constants and a row's base.
 constexpr int small_long(int shorter) { return 256 * (4 / shorter); }
@@ -687,11 +1018,6 @@ __device__ __forceinline__ void small_products(const SmallRow* a, const SmallRow
                       : __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[u][i], fb[u][i / EACH], acc[i], 0, 0, 0);
     }
 }
-
-struct MuSteps {
-  int32_t count;
-  float coef[16][3];
-};
 
 // SHORTER: blocks along the shorter side; TURN: that is the columns' side.
 template <int SHORTER, bool TURN>
@@ -846,15 +1172,14 @@ __global__ __launch_bounds__(512) void k_muon_small(MuArgs a, MuSteps st) {
   const int t = find_item(a, blockIdx.x);
   const MuItem& it = a.item[t];
   const int e = blockIdx.x - a.first[t], shorter = SmallShape(it.rows, it.cols).shorter;
-  const bool turn = it.rows > it.cols;
-  if (turn) {
-    if (shorter == 1) muon_small<1, true>(a, st, it, e);
-    else if (shorter == 2) muon_small<2, true>(a, st, it, e);
+  if (shorter == 1) {
+    muon_thin(a, st, it, e);
+  } else if (it.rows > it.cols) {
+    if (shorter == 2) muon_small<2, true>(a, st, it, e);
     else if (shorter == 3) muon_small<3, true>(a, st, it, e);
     else muon_small<4, true>(a, st, it, e);
   } else {
-    if (shorter == 1) muon_small<1, false>(a, st, it, e);
-    else if (shorter == 2) muon_small<2, false>(a, st, it, e);
+    if (shorter == 2) muon_small<2, false>(a, st, it, e);
     else if (shorter == 3) muon_small<3, false>(a, st, it, e);
     else muon_small<4, false>(a, st, it, e);
   }
@@ -871,15 +1196,15 @@ hipError_t allow_lds(F* f, int bytes, std::atomic<bool> (&done)[kMaxDevices]) {
 }
 
 // Runs `kernel` over the tiles that `tiles` counts for each item.
-template <class K, class N>
-hipError_t run(K* kernel, MuArgs& a, int threads, int lds, hipStream_t s, N&& tiles) {
+template <class K, class N, class... More>
+hipError_t run(K* kernel, MuArgs& a, int threads, int lds, hipStream_t s, N&& tiles, const More&... more) {
   int64_t sum = 0;
   for (int t = 0; t < a.count; ++t) {
     a.first[t] = int32_t(sum);
     sum += tiles(a.item[t]) * a.item[t].batch;
   }
   a.first[a.count] = int32_t(sum);
-  kernel<<<unsigned(align_up(sum, kXcds)), threads, lds, s>>>(a);
+  kernel<<<unsigned(align_up(sum, kXcds)), threads, lds, s>>>(a, more...);
   return hipGetLastError();
 }
 
@@ -921,20 +1246,27 @@ struct MuPart {
   int64_t ws;                 // offset of their buffers
 };
 
-// (small ones need none; counted as 512 bytes, a run has at most 2^22 of them, a workgroup each)
-int64_t matrix_bytes(const mok_muon_tensor& t, bool small) {
-  return small ? 512 : align_up(MuBuffers(t.rows, t.cols).bytes(), 256);
+enum class MuSize { Small, Thin, General };
+MuSize size_of(const mok_muon_tensor& t) {
+  if (SmallShape(t.rows, t.cols).fits()) return MuSize::Small;
+  return ThinShape(t.rows, t.cols).thin() ? MuSize::Thin : MuSize::General;
 }
 
-// Calls go(parts, count, bytes) for each run of the small tensors, or of the others; stops at an error.
+// (small ones need none; counted as 512 bytes, a run has at most 2^22 of them, a workgroup each)
+int64_t matrix_bytes(const mok_muon_tensor& t, MuSize size) {
+  if (size == MuSize::Small) return 512;
+  return align_up(size == MuSize::Thin ? ThinShape(t.rows, t.cols).bytes() : MuBuffers(t.rows, t.cols).bytes(), 256);
+}
+
+// Calls go(parts, count, bytes) for each run of the tensors of a size; stops at an error.
 template <class G>
-hipError_t each_run(int count, const mok_muon_tensor* t, bool small, G&& go) {
+hipError_t each_run(int count, const mok_muon_tensor* t, MuSize size, G&& go) {
   MuPart part[kMuItems];
   int n = 0;
   int64_t bytes = 0;
   for (int k = 0; k < count; ++k) {
-    if (SmallShape(t[k].rows, t[k].cols).fits() != small) continue;
-    const int64_t one = matrix_bytes(t[k], small);
+    if (size_of(t[k]) != size) continue;
+    const int64_t one = matrix_bytes(t[k], size);
     for (int b = 0; b < t[k].batch;) {
       if (n == kMuItems || (n > 0 && bytes + one > kMuWs)) {
         const hipError_t e = go(part, n, bytes);
@@ -961,10 +1293,11 @@ double adjustment(int rule, int rows, int cols) {
 
 int64_t muon_ws_bytes(int count, const mok_muon_tensor* t) {
   int64_t most = 0;
-  (void)each_run(count, t, false, [&](const MuPart*, int, int64_t bytes) {
-    most = std::max(most, bytes);
-    return hipSuccess;
-  });
+  for (const MuSize size : {MuSize::Thin, MuSize::General})
+    (void)each_run(count, t, size, [&](const MuPart*, int, int64_t bytes) {
+      most = std::max(most, bytes);
+      return hipSuccess;
+    });
   return std::max<int64_t>(most, 256);
 }
 
@@ -988,17 +1321,20 @@ hipError_t launch_muon(int count, const mok_muon_tensor* t, const mok_muon_confi
     a.lr_dev = c.lr_dev;
     return a;
   };
-  hipError_t e = each_run(count, t, true, [&](const MuPart* part, int n, int64_t) {
+  MuSteps st{};
+  st.count = c.ns.steps;
+  std::copy_n(&c.ns.coefficients[0][0], 3 * st.count, &st.coef[0][0]);
+  hipError_t e = each_run(count, t, MuSize::Small, [&](const MuPart* part, int n, int64_t) {
     static std::atomic<bool> done[kMaxDevices];
     const hipError_t e0 = allow_lds(k_muon_small, 160 << 10, done);
     if (e0 != hipSuccess) return e0;
     MuArgs a = arguments(part, n);
-    MuSteps st{};
-    st.count = c.ns.steps;
-    std::copy_n(&c.ns.coefficients[0][0], 3 * st.count, &st.coef[0][0]);
     int lds = 0, matrices = 0;
     for (int k = 0; k < n; ++k) {
-      lds = std::max(lds, small_lds(SmallShape(a.item[k].rows, a.item[k].cols).shorter));
+      const MuItem& it = a.item[k];
+      const ThinShape thin(it.rows, it.cols);
+      lds = std::max(lds, thin.thin() ? (3 * kThinMatrix * 8 + thin.m * (thin.n | 1) * 4)
+                                      : small_lds(SmallShape(it.rows, it.cols).shorter));
       a.first[k] = matrices;
       matrices += a.item[k].batch;
     }
@@ -1006,8 +1342,19 @@ hipError_t launch_muon(int count, const mok_muon_tensor* t, const mok_muon_confi
     k_muon_small<<<matrices, 512, lds, s>>>(a, st);
     return hipGetLastError();
   });
+  if (e == hipSuccess)
+    e = each_run(count, t, MuSize::Thin, [&](const MuPart* part, int n, int64_t) {
+      MuArgs a = arguments(part, n);
+      int lds = 0;
+      for (int k = 0; k < n; ++k) lds = std::max(lds, ThinShape(a.item[k].rows, a.item[k].cols).chunk_lds());
+      hipError_t e1 = run(k_thin_gram, a, 256, lds, s, [](const MuItem& it) { return int64_t(ThinShape(it.rows, it.cols).parts); });
+      if (e1 == hipSuccess) e1 = run(k_thin_steps, a, 512, 0, s, [](const MuItem&) { return int64_t(1); }, st);
+      if (e1 == hipSuccess)
+        e1 = run(k_thin_apply, a, 256, lds, s, [](const MuItem& it) { return int64_t(ThinShape(it.rows, it.cols).chunks); });
+      return e1;
+    });
   if (e != hipSuccess) return e;
-  return each_run(count, t, false, [&](const MuPart* part, int n, int64_t) {
+  return each_run(count, t, MuSize::General, [&](const MuPart* part, int n, int64_t) {
     MuArgs a = arguments(part, n);
     hipError_t e1 = run(k_muon_norm, a, 256, 0, s, [](const MuItem& it) {
       const int64_t size = int64_t(it.rows) * it.cols;
