@@ -11,8 +11,10 @@
 // Precision. X is kept in 19 bits, fp16 and a byte for the bits below, times a power of two near sqrt(n) that keeps it in
 // fp16's normal range; a X is formed from all of them, the products take X, A and B in fp16 with fp32 sums. Kept in
 // fp16 alone, X's rounding drowns the small singular values of a gradient with a few large ones: the result is off by
-// 1.3e-2 there (512 x 1792, rank 129 plus 1 % noise), with the byte by 8e-4, with bf16 everywhere by 1e-1; 1e-3 to 2e-3
-// for random matrices, where A's and B's rounding is what is left. On the matrix cores fp16 is as fast as bf16.
+// 1.3e-2 there (512 x 1792, rank 129 plus 1 % noise), with the byte by 8e-4, with bf16 everywhere by 1e-1. A's and B's
+// diagonals hold most of them where singular values are alike: they are kept apart in fp32 (fp16 holds zeros), and their parts
+// of the products added to the sums, with the same fp16 as the products take: so a direction that A lacks stays one in A A
+// and B X. Random matrices are off by 1e-3 so, by 2e-3 to 4e-3 without. On the matrix cores fp16 is as fast as bf16.
 #include <algorithm>
 #include <cmath>
 
@@ -71,13 +73,16 @@ struct MuBuffers {
     gram = int64_t(m) * m * 2;
   }
   __host__ __device__ int64_t bytes() const { return parts_at() + kMuParts * 8; }
-  __host__ __device__ int64_t parts_at() const { return 3 * plane + plane / 2 + 2 * gram; }
+  __host__ __device__ int64_t parts_at() const { return 3 * plane + plane / 2 + 2 * (gram + m * 4); }
   __device__ bool turned(const MuItem& it) const { return it.rows > it.cols; }
   __device__ _Float16* s(uint8_t* ws, bool turn, int flip) const { return at(ws, turn && flip ? 2 * plane : 0); }
   __device__ _Float16* t(uint8_t* ws, bool turn, int flip) const { return at(ws, !turn && flip ? 2 * plane : plane); }
   __device__ _Float16* a(uint8_t* ws) const { return at(ws, 3 * plane); }
   __device__ _Float16* b(uint8_t* ws) const { return at(ws, 3 * plane + gram); }
   __device__ uint8_t* lo(uint8_t* ws) const { return ws + 3 * plane + 2 * gram; }
+  __device__ float* diagonal(uint8_t* ws, bool of_b) const {
+    return reinterpret_cast<float*>(lo(ws) + plane / 2) + (of_b ? m : 0);
+  }
   __device__ double* parts(uint8_t* ws) const { return reinterpret_cast<double*>(ws + parts_at()); }
   __device__ static _Float16* at(uint8_t* p, int64_t off) { return reinterpret_cast<_Float16*>(p + off); }
 };
@@ -514,29 +519,48 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void k_muon_gram(MuArgs a) {
   // (padded sizes are multiples of 128, which a wave's share does not cross)
   if (wa * S::FA * 32 >= ni || wb * 64 >= nj) return;
   const int c = j0 + wb * 64 + 2 * (lane & 31);
+  const float* da = b.diagonal(ws, false);
+  float* diagonal = b.diagonal(ws, SECOND);
+  float dc[2] = {0.f, 0.f};
+  if constexpr (SECOND) {
+    dc[0] = da[c];
+    dc[1] = da[c + 1];
+  }
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int r0 = i0 + wa * S::FA * 32 + S::result_row(q, half);
-    f16x2 z[S::kRun];
+  for (int p = 0; p < S::kRun / 2; ++p) {   // 8 rows at a time
+    const int v0 = p * 8 % S::kRun, q = p * 8 / S::kRun, r0 = i0 + wa * S::FA * 32 + S::result_row(q, half) + v0;
+    const int64_t at = int64_t(r0) * b.m + c;
+    f16x2 z[8];
+    float dr[8];
     if constexpr (SECOND)
 #pragma unroll
-      for (int v = 0; v < S::kRun; ++v) z[v] = *reinterpret_cast<const f16x2*>(old + int64_t(r0 + v) * b.m + c);
-    _Float16 y[2][S::kRun];
+      for (int v = 0; v < 8; ++v) {
+        z[v] = *reinterpret_cast<const f16x2*>(old + at + v * b.m);
+        dr[v] = da[r0 + v];
+      }
+    _Float16 y[2][8];
 #pragma unroll
-    for (int v = 0; v < S::kRun; ++v) {
+    for (int v = 0; v < 8; ++v) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const float g = acc[v >> 2][j][4 * q + (v & 3)];
-        y[j][v] = to_half(SECOND ? fmaf(a.c, g, a.b * float(z[v][j])) : g * down);
+        const float g = acc[(v0 + v) >> 2][j][4 * q + (v & 3)];
+        const bool on = ti == tj && r0 + v == c + j;   // (where the matrix in fp16 holds zero)
+        float f;
+        if constexpr (SECOND) {
+          const float x = on ? dr[v] : float(z[v][j]);
+          f = fmaf(a.c, fmaf(on ? x : dr[v] + dc[j], x, g), a.b * x);
+        } else {
+          f = g * down;
+        }
+        y[j][v] = to_half(on ? 0.f : f);
+        if (on) diagonal[c + j] = f;
       }
-      *reinterpret_cast<f16x2*>(out + int64_t(r0 + v) * b.m + c) = f16x2{y[0][v], y[1][v]};
+      *reinterpret_cast<f16x2*>(out + at + v * b.m) = f16x2{y[0][v], y[1][v]};
     }
     if (ti != tj)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int v = 0; v < S::kRun; v += 8)
-          *reinterpret_cast<f16x8*>(out + int64_t(c + j) * b.m + r0 + v) = *reinterpret_cast<const f16x8*>(&y[j][v]);
+        *reinterpret_cast<f16x8*>(out + int64_t(c + j) * b.m + r0) = *reinterpret_cast<const f16x8*>(y[j]);
   }
 }
 
@@ -574,10 +598,15 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void k_muon_apply(MuArgs a) {
   if (wa * S::FA * 32 >= ni || wb * 64 >= nj) return;   // (padded sizes are multiples of 128)
   const int wc = wb * 64 + 2 * (lane & 31), c = j0 + wc;
   const bool pairs = j0 + S::kB <= it.cols && it.cols % 2 == 0;
+  const float* diagonal = b.diagonal(ws, true);   // along the side of m
+  const float dc[2] = {turn ? diagonal[c] : 0.f, turn ? diagonal[c + 1] : 0.f};
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const int wr = wa * S::FA * 32 + S::result_row(q, half), r0 = i0 + wr;
     f16x2 xh[S::kRun];
+    float dr[S::kRun];
+#pragma unroll
+    for (int v = 0; v < S::kRun; ++v) dr[v] = turn ? 0.f : diagonal[r0 + v];
     uint16_t xl[S::kRun];
 #pragma unroll
     for (int v = 0; v < S::kRun; ++v) {
@@ -590,7 +619,8 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void k_muon_apply(MuArgs a) {
     for (int v = 0; v < S::kRun; ++v)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
-        x[j][v] = fmaf(a.a, with_low(xh[v][j], int8_t(xl[v] >> (8 * j))), acc[v >> 2][j][4 * q + (v & 3)]);
+        x[j][v] = fmaf(a.a, with_low(xh[v][j], int8_t(xl[v] >> (8 * j))),
+                       fmaf(turn ? dc[j] : dr[v], float(xh[v][j]), acc[v >> 2][j][4 * q + (v & 3)]));
     if constexpr (LAST) {
       if (pairs) {
         store_pairs<S::kRun>(it, win, wr, c, x, decay, rate);
@@ -631,12 +661,14 @@ struct MuSteps {
 // Rounding to fp16 averages out over many directions; of a few, each is off by up to 1e-2. A = u u^T is small here, so
 // the steps are taken on it alone, in fp64 on the matrix cores, and u is read twice whatever their number:
 //   Q = a + b A + c A A,   P <- Q P,   A <- Q A Q,   X = P u / (|u| + eps),   |u|^2 the trace of the first A.
-// Errors of A grow by a^2 a step where X is small: 12^4 in five steps, 1e-12 in fp64. Up to kThinLds elements, one workgroup
-// keeps u in LDS and does it all (THIN_US); longer ones take three launches (THIN_LONG_US).
+// Errors of A grow by a^2 a step where X is small: 12^4 in five steps, 1e-12 in fp64. Up to kThinElements, one workgroup
+// keeps u in LDS and does it all (8 x 128: 13 us, 32 x 250: 27 us, of which two thirds are the steps, latency); longer ones take
+// three launches (32 x 5,000: 46 us, 2 x 50,000: 40 us; the general kernels' 17 take 170 to 200 us there). One workgroup for
+// 8,000 columns took 57 us, three launches take 27 us.
 constexpr int kThin = 32, kThinRow = kThin + 1, kThinMatrix = kThin * kThinRow;   // doubles
-constexpr int kThinLds = ((160 << 10) - 3 * kThinMatrix * 8) / 4;                 // elements of u beside three matrices
-constexpr int kThinParts = 256;                                                  // partial sums of A at most
-constexpr int kThinChunk = 8192;                                                 // elements of a chunk, of whole columns
+constexpr int kThinElements = 8192, kThinColumns = 1024;                         // of u in one workgroup, at most
+constexpr int kThinParts = 128;                                                  // partial sums of A at most
+constexpr int kThinChunk = 2048;                                                 // elements of a chunk: 64 to 512 columns
 
 typedef __attribute__((ext_vector_type(4))) double f64x4;
 
@@ -646,13 +678,13 @@ struct ThinShape {
   __host__ __device__ ThinShape(int rows, int cols) {
     m = rows < cols ? rows : cols;
     n = rows < cols ? cols : rows;
-    columns = kThinChunk / m & ~15;
+    columns = kThinChunk / (m < 4 ? 4 : m) & ~15;
     chunks = int(cdiv(n, columns));
     parts = chunks < kThinParts ? chunks : kThinParts;
     stride = columns | 1;
   }
   __host__ __device__ bool thin() const { return m <= kThin; }
-  __host__ __device__ bool fits() const { return thin() && int64_t(m) * (n | 1) <= kThinLds; }
+  __host__ __device__ bool fits() const { return thin() && n <= kThinColumns && m * n <= kThinElements; }
   __host__ __device__ int64_t bytes() const { return int64_t(parts + 1) * m * m * 8; }   // partial sums, P
   __host__ __device__ int chunk_lds() const { return kThinMatrix * 8 + m * stride * 4; }
 };
@@ -743,25 +775,38 @@ __device__ __forceinline__ f64x4 thin_mfma(double x, double y, f64x4 c) {
   return __builtin_amdgcn_mfma_f64_16x16x4f64(x, y, c, 0, 0, 0);
 }
 
-// acc += u u^T over the columns in LDS, blocks (0, 0), (1, 0) and (1, 1); each wave takes every WAVES-th 4 columns.
+// acc += u u^T over the columns in LDS, blocks (0, 0), (1, 0) and (1, 1); each wave takes every WAVES-th 16 columns, in two
+// sums, so that neither loads nor instructions wait for one another.
 template <int WAVES>
-__device__ __forceinline__ void thin_gram(const float* u, int m, int stride, int cols, f64x4 (&acc)[3]) {
+__device__ __forceinline__ void thin_gram(const float* u, int m, int stride, int cols, f64x4 (&acc)[2][3]) {
   const int lane = threadIdx.x & 63, r = lane & 15;
-  for (int k0 = wave_id() * 4; k0 < cols; k0 += WAVES * 4) {
-    const int k = k0 + (lane >> 4);
-    const double x = r < m && k < cols ? double(u[r * stride + k]) : 0.0;
-    acc[0] = thin_mfma(x, x, acc[0]);
+  const float *ur = u + min(r, m - 1) * stride, *ul = u + min(r + 16, m - 1) * stride;
+  for (int k0 = wave_id() * 16; k0 < cols; k0 += WAVES * 16) {
+    float x[4], y[4];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) x[v] = ur[min(k0 + 4 * v + (lane >> 4), cols - 1)];
     if (m > 16) {
-      const double y = r + 16 < m && k < cols ? double(u[(r + 16) * stride + k]) : 0.0;
-      acc[1] = thin_mfma(y, x, acc[1]);
-      acc[2] = thin_mfma(y, y, acc[2]);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) y[v] = ul[min(k0 + 4 * v + (lane >> 4), cols - 1)];
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const bool in = k0 + 4 * v + (lane >> 4) < cols;
+      const double a = in && r < m ? double(x[v]) : 0.0;
+      acc[v & 1][0] = thin_mfma(a, a, acc[v & 1][0]);
+      if (m > 16) {
+        const double b = in && r + 16 < m ? double(y[v]) : 0.0;
+        acc[v & 1][1] = thin_mfma(b, a, acc[v & 1][1]);
+        acc[v & 1][2] = thin_mfma(b, b, acc[v & 1][2]);
+      }
     }
   }
 }
 
 // Adds the waves' blocks up in LDS, one wave after another, so that the order is always the same.
 template <int WAVES>
-__device__ __forceinline__ void thin_gather(const f64x4 (&acc)[3], int m, double* sum) {
+__device__ __forceinline__ void thin_gather(const f64x4 (&parts)[2][3], int m, double* sum) {
+  const f64x4 acc[3] = {parts[0][0] + parts[1][0], parts[0][1] + parts[1][1], parts[0][2] + parts[1][2]};
   const int lane = threadIdx.x & 63, c = lane & 15, w = wave_id();
   for (int t = 0; t < WAVES; ++t) {
     if (t == w)
@@ -784,22 +829,26 @@ __device__ __forceinline__ void thin_gather(const f64x4 (&acc)[3], int m, double
 }
 
 // From A = u u^T in LDS: P / (|u| + eps) in `p`. Eight waves; `q` is scratch. The matrices are symmetric (and polynomials of
-// one matrix), so an operand's columns are read as its rows.
+// one matrix), so an operand's columns are read as its rows. TILES: 16 x 16 blocks along a side.
+template <int TILES>
 __device__ __forceinline__ void thin_steps(const MuSteps& st, double eps, int m, double* a, double* q, double* p) {
-  const int lane = threadIdx.x & 63, c = lane & 15, w = wave_id(), tiles = m > 16 ? 2 : 1;
-  const int ti = (w & 3) >> 1, tj = w & 1;
-  const bool mine = ti < tiles && tj < tiles;
-  double norm = 0;
-  for (int i = 0; i < m; ++i) norm += a[i * kThinRow + i];
-  norm = sqrt(norm) + eps;
+  const int lane = threadIdx.x & 63, c = lane & 15, w = wave_id(), ti = (w & 3) >> 1, tj = w & 1;
+  const bool mine = ti < TILES && tj < TILES;
+  double norm = lane < m ? a[lane * kThinRow + lane] : 0.0;
+  for (int off = 16; off; off >>= 1) norm += __shfl_xor(norm, off, 64);
+  norm = 1.0 / (sqrt(__shfl(norm, 0, 64)) + eps);
   __syncthreads();
-  for (int i = threadIdx.x; i < kThinMatrix; i += 512) a[i] = a[i] / norm / norm;
+  for (int i = threadIdx.x; i < TILES * 16 * kThinRow; i += 512) a[i] *= norm * norm;
   __syncthreads();
   const auto product = [&](const double* x, const double* y) {
-    f64x4 s = {0, 0, 0, 0};
-    for (int k = lane >> 4; k < tiles * 16; k += 4)
-      s = thin_mfma(x[(ti * 16 + c) * kThinRow + k], y[(tj * 16 + c) * kThinRow + k], s);
-    return s;
+    const double *xr = x + (ti * 16 + c) * kThinRow + (lane >> 4), *yr = y + (tj * 16 + c) * kThinRow + (lane >> 4);
+    double fx[TILES * 4], fy[TILES * 4];
+#pragma unroll
+    for (int k = 0; k < TILES * 4; ++k) fx[k] = xr[4 * k], fy[k] = yr[4 * k];
+    f64x4 s[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};   // (two sums: an instruction does not wait for the one before)
+#pragma unroll
+    for (int k = 0; k < TILES * 4; ++k) s[k & 1] = thin_mfma(fx[k], fy[k], s[k & 1]);
+    return s[0] + s[1];
   };
   const auto place = [&](int i) { return (ti * 16 + 4 * i + (lane >> 4)) * kThinRow + tj * 16 + c; };
   const auto put = [&](double* x, const f64x4& s) {
@@ -813,49 +862,58 @@ __device__ __forceinline__ void thin_steps(const MuSteps& st, double eps, int m,
       s = product(a, a);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int at = place(i);
         const bool diagonal = ti == tj && 4 * i + (lane >> 4) == c;
-        s[i] = (diagonal ? ca : 0.0) + cb * a[at] + cc * s[i];
+        s[i] = (diagonal ? ca : 0.0) + cb * a[place(i)] + cc * s[i];
       }
       put(q, s);
     }
     __syncthreads();
-    if (mine) s = w < 4 ? product(q, a) : k ? product(p, q) : f64x4{q[place(0)], q[place(1)], q[place(2)], q[place(3)]};
+    const bool more = k + 1 < st.count;
+    if (mine && w < 4 && more) s = product(q, a);
+    if (mine && w >= 4) s = k ? product(p, q) : f64x4{q[place(0)], q[place(1)], q[place(2)], q[place(3)]};
     __syncthreads();
-    if (mine) put(w < 4 ? a : p, s);
+    if (mine && w < 4 && more) put(a, s);
+    if (mine && w >= 4) put(p, more ? s : s * norm);
     __syncthreads();
-    if (k + 1 < st.count) {
+    if (more) {
       if (mine && w < 4) s = product(a, q);
       __syncthreads();
       if (mine && w < 4) put(a, s);
       __syncthreads();
     }
   }
-  if (mine && w >= 4) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p[place(i)] /= norm;
-  }
-  __syncthreads();
+}
+__device__ __forceinline__ void thin_steps(const MuSteps& st, double eps, int m, double* a, double* q, double* p) {
+  if (m > 16) thin_steps<2>(st, eps, m, a, q, p);
+  else thin_steps<1>(st, eps, m, a, q, p);
 }
 
-// u <- P u, for the columns in LDS; a wave takes 16 at a time.
+// u <- P u, for the columns in LDS; a wave takes 64 at a time, as four operands of 16.
 template <int WAVES>
 __device__ __forceinline__ void thin_apply(const double* p, float* u, int m, int stride, int cols) {
   const int lane = threadIdx.x & 63, c = lane & 15;
-  for (int j0 = wave_id() * 16; j0 < cols; j0 += WAVES * 16) {
-    const int j = j0 + c;
-    f64x4 s[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+  for (int j0 = wave_id() * 64; j0 < cols; j0 += WAVES * 64) {
+    f64x4 s[4][2] = {};
     for (int k = lane >> 4; k < (m + 3 & ~3); k += 4) {
-      const double x = k < m && j < cols ? double(u[k * stride + j]) : 0.0;
-      s[0] = thin_mfma(p[c * kThinRow + k], x, s[0]);
-      if (m > 16) s[1] = thin_mfma(p[(c + 16) * kThinRow + k], x, s[1]);
-    }
-    if (j < cols)
+      float x[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = 4 * i + (lane >> 4);
-        if (r < m) u[r * stride + j] = float(s[i >> 2][i & 3]);
+      for (int g = 0; g < 4; ++g) x[g] = u[min(k, m - 1) * stride + min(j0 + 16 * g + c, cols - 1)];
+      const double p0 = p[c * kThinRow + k], p1 = p[(c + 16) * kThinRow + k];   // (rows past m are not used)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const double b = k < m ? double(x[g]) : 0.0;   // (P's columns past m are zero but for its diagonal)
+        s[g][0] = thin_mfma(p0, b, s[g][0]);
+        if (m > 16) s[g][1] = thin_mfma(p1, b, s[g][1]);
       }
+    }
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      if (const int j = j0 + 16 * g + c; j < cols)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = 4 * i + (lane >> 4);
+          if (r < m) u[r * stride + j] = float(s[g][i >> 2][i & 3]);
+        }
   }
 }
 
@@ -869,7 +927,7 @@ __device__ __forceinline__ void muon_thin(const MuArgs& a, const MuSteps& st, co
   const int stride = sh.n | 1;
   thin_load<512, true>(a, it, base, sh.m, stride, 0, sh.n, u);
   __syncthreads();
-  f64x4 acc[3] = {{0, 0, 0, 0}, {0, 0, 0, 0}, {0, 0, 0, 0}};
+  f64x4 acc[2][3] = {};
   thin_gram<8>(u, sh.m, stride, sh.n, acc);
   thin_gather<8>(acc, sh.m, sum);
   thin_steps(st, a.eps, sh.m, sum, q, p);
@@ -890,7 +948,7 @@ __global__ __launch_bounds__(256) void k_thin_gram(MuArgs a) {
   const ThinShape sh(it.rows, it.cols);
   const int id = blockIdx.x - a.first[t], e = id / sh.parts, part = id % sh.parts;
   const int64_t base = int64_t(it.e0 + e) * it.rows * it.cols;
-  f64x4 acc[3] = {{0, 0, 0, 0}, {0, 0, 0, 0}, {0, 0, 0, 0}};
+  f64x4 acc[2][3] = {};
   for (int c = part; c < sh.chunks; c += sh.parts) {
     const int j0 = c * sh.columns, cols = min(sh.columns, sh.n - j0);
     thin_load<256, true>(a, it, base, sh.m, sh.stride, j0, cols, u);
@@ -915,11 +973,23 @@ __global__ __launch_bounds__(512) void k_thin_steps(MuArgs a, MuSteps st) {
   const int mm = sh.m * sh.m;
   for (int i = threadIdx.x; i < kThinMatrix; i += 512) sum[i] = 0;
   __syncthreads();
-  for (int i = threadIdx.x; i < mm; i += 512) {
-    double v = 0;
-    for (int part = 0; part < sh.parts; ++part) v += ws[int64_t(part) * mm + i];
-    sum[i / sh.m * kThinRow + i % sh.m] = v;
+  constexpr int kAhead = 16;   // parts loaded together, added in order
+  double v[2] = {0, 0};        // of elements threadIdx and threadIdx + 512
+  for (int part = 0; part < sh.parts; part += kAhead) {
+    double x[2][kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        x[h][k] = ws[int64_t(min(part + k, sh.parts - 1)) * mm + min(int(threadIdx.x) + 512 * h, mm - 1)];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) v[h] += part + k < sh.parts ? x[h][k] : 0.0;
   }
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    if (const int i = threadIdx.x + 512 * h; i < mm) sum[i / sh.m * kThinRow + i % sh.m] = v[h];
   __syncthreads();
   thin_steps(st, a.eps, sh.m, sum, q, p);
   for (int i = threadIdx.x; i < mm; i += 512) ws[int64_t(sh.parts) * mm + i] = p[i / sh.m * kThinRow + i % sh.m];
@@ -953,7 +1023,7 @@ __global__ __launch_bounds__(256) void k_thin_apply(MuArgs a) {
 // ---- small matrices -----------------------------------------------------------------------------
 // A matrix whose X and X^T in fp16 fit the LDS beside A takes one workgroup and one launch for everything: X stays in
 // registers in fp32, its fp16 copies, A and then B in LDS. Launches and the way through memory bound the general kernels at
-// such sizes (25 matrices of 256 x 128 and less: 222 us in 17 launches, SMALL_US us here).
+// such sizes (25 matrices of 256 x 128 and less: 222 us in 17 launches, 62 us here).
 //
 // X is cut into 32 x 32 blocks, 2..4 along its shorter side and up to 16 along the longer one. Wave w takes the
 // longer side's blocks w, w + 8, ..., for each of them all of the shorter side's: four slots at most, which share the
@@ -1094,7 +1164,37 @@ __device__ __forceinline__ void muon_small(const MuArgs& a, const MuSteps& st, c
         for (int v = 0; v < 16; ++v)
           gram[small_at(gr[q] + 8 * (v >> 2) + 4 * h + (v & 3), gc[q] + c, kShort)] = to_half(g[q][v]);
   };
-  const _Float16 *across_rows = TURN ? xt : xs, *along_rows = TURN ? xs : xt;   // rows of n, and of m halves
+  _Float16 *across_rows = TURN ? xt : xs, *along_rows = TURN ? xs : xt;   // rows of n, and of m halves
+  // A's and B's diagonals, in place of the former once A is made
+  float *diag_a = reinterpret_cast<float*>(across_rows), *diag_b = diag_a + kShort;
+  // A wave has one block on the diagonal at most. Its lanes' elements there (of half the lanes), and their places
+  int dq = -1;
+#pragma unroll
+  for (int q = 0; q < G; ++q)
+    if (glive[q] && gr[q] == gc[q]) dq = q;
+  const auto on_diagonal = [&](const f32x16 (&g)[G]) {
+    const int c = tile_tid() & 31, on = (c >> 3) * 4 + (c & 3);
+    float f = 0.f;
+#pragma unroll
+    for (int q = 0; q < G; ++q)
+      if (q == dq)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) f = v == on ? g[q][v] : f;
+    return f;
+  };
+  const auto diagonal_place = [&] { return gc[G - 1 == dq ? G - 1 : 0] + (tile_tid() & 31); };
+  const auto put_diagonal = [&](float* d, float f) {
+    const int tid = tile_tid();
+    if ((tid >> 2 & 1) == (tid >> 5 & 1)) d[diagonal_place()] = f;
+  };
+  const auto clear_diagonal = [&] {
+    const int tid = tile_tid(), c = diagonal_place();
+    if ((tid >> 2 & 1) == (tid >> 5 & 1)) gram[small_at(c, c, kShort)] = 0;
+  };
+  // four of a diagonal's elements, for elements 4 v .. 4 v + 3 of a lane in a block whose first row is r
+  const auto four = [&](const float* d, int r, int v) {
+    return *reinterpret_cast<const f32x4*>(d + r + 8 * v + 4 * (tile_tid() >> 5 & 1));
+  };
 #pragma unroll 1
   for (int k = 0; k < st.count; ++k) {
     const float ca = st.coef[k][0], cb = st.coef[k][1], cc = st.coef[k][2];
@@ -1126,21 +1226,43 @@ __device__ __forceinline__ void muon_small(const MuArgs& a, const MuSteps& st, c
 #pragma unroll
       for (int q = 0; q < G; ++q) g[q] *= down;
       put_gram(g);
+      if (dq >= 0) clear_diagonal();
     }
     __syncthreads();
+    f32x16 aa[G];
+    float d = 0.f;
+    if (dq >= 0) {
+      d = on_diagonal(g);
+      put_diagonal(diag_a, fmaf(cc, d, 0.5f * cb));   // (two of these make an element's factor)
+    }
     if (glive[0]) {
       const int l = tile_tid() & 31;
       const SmallRow left[2] = {SmallRow(gram, gr[0] + l, kShort), SmallRow(gram, gr[G - 1] + l, kShort)};
       const SmallRow right[1] = {SmallRow(gram, gc[0] + l, kShort)};
-      f32x16 y[G];
-      small_products<G, G, false>(left, right, kShort, y);
-#pragma unroll
-      for (int q = 0; q < G; ++q)
-#pragma unroll
-        for (int v = 0; v < 16; ++v) g[q][v] = fmaf(cc, y[q][v], cb * g[q][v]);
+      small_products<G, G, false>(left, right, kShort, aa);
     }
     __syncthreads();
-    if (glive[0]) put_gram(g);
+    if (glive[0]) {
+      const int c = tile_tid() & 31;
+#pragma unroll
+      for (int q = 0; q < G; ++q) {
+        const float dc = diag_a[gc[q] + c];
+#pragma unroll
+        for (int v = 0; v < 16; v += 4) {
+          const f32x4 dr = four(diag_a, gr[q], v >> 2);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float x = float(to_half(g[q][v + u]));
+            g[q][v + u] = fmaf(dr[u] + dc, x, cc * aa[q][v + u]);
+          }
+        }
+      }
+      put_gram(g);
+      if (dq >= 0) {
+        clear_diagonal();
+        put_diagonal(diag_b, fmaf(cc, fmaf(d, d, on_diagonal(aa)), cb * d));
+      }
+    }
     __syncthreads();
     if (live[0]) {
       const int l = tile_tid() & 31;
@@ -1151,9 +1273,16 @@ __device__ __forceinline__ void muon_small(const MuArgs& a, const MuSteps& st, c
       f32x16 y[N];
       small_products<N, SHORTER, TURN>(ra, rb, kShort, y);
 #pragma unroll
-      for (int q = 0; q < N; ++q)
+      for (int q = 0; q < N; ++q) {
+        const float dc = diag_b[q % SHORTER * 32 + l];
 #pragma unroll
-        for (int v = 0; v < 16; ++v) x[q][v] = fmaf(ca, x[q][v], y[q][v]);
+        for (int v = 0; v < 16; v += 4) {
+          const f32x4 dr = TURN ? f32x4{dc, dc, dc, dc} : four(diag_b, q % SHORTER * 32, v >> 2);
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            x[q][v + u] = fmaf(ca, x[q][v + u], fmaf(dr[u], float(to_half(x[q][v + u])), y[q][v + u]));
+        }
+      }
     }
     __syncthreads();
   }

@@ -570,8 +570,9 @@ mok_status mok_adamw(int32_t num_tensors, const mok_adamw_tensor* tensors,
  *   X = u / (|u|_F + eps);  then `steps` times  A = X X^T,  X = a X + (b A + c A A) X
  * with the step's (a, b, c): an odd polynomial of u's singular values. With three-term coefficients that keep singular
  * values of 0..1 below 16 all the way (the usual 3.4445, -4.7750, 2.0315 keep them below 1.3) no intermediate leaves
- * its range; larger ones may overflow to infinities. Products take fp16 operands, whose sums are fp32; X is held in 22
- * bits. A zero matrix stays zero; a NaN or an infinity in u makes its whole matrix NaN. Tensors are batches of
+ * its range; larger ones may overflow to infinities. Products take fp16 operands, whose sums are fp32; X is held in 19
+ * bits (in fp32 up to 128 x 256), the diagonals of A and B in fp32. Matrices of up to 32 rows or columns take their steps in
+ * fp64. A zero matrix stays zero; a NaN or an infinity in u makes its whole matrix NaN. Tensors are batches of
  * matrices, contiguous [batch][rows][cols], 16-byte aligned (the optimizer's other rules hold here, too). */
 typedef struct {
   double eps;                /* > 0                                       */
@@ -605,7 +606,8 @@ typedef struct {
 /* One Muon step over all tensors:
  *   g' = g min(1, max_norm / sqrt(*sumsq)),  m = momentum m + g',  u = nesterov ? g' + momentum m : m,
  *   p = p (1 - lr weight_decay) - lr adjust orthogonalised(u).
- * 2 + 3 steps launches for up to 40 tensors whose workspace stays below 2 GiB together.
+ * One launch for up to 40 tensors of small matrices, 3 for those of up to 32 rows or columns, 2 + 3 steps for others whose
+ * workspace stays below 2 GiB together.
  *   ws_dev  mok_muon_ws_size bytes, 256-byte aligned; calls that overlap in time need their own */
 mok_status mok_muon_ws_size(int32_t num_tensors, const mok_muon_tensor* tensors, size_t* ws_bytes);
 mok_status mok_muon(int32_t num_tensors, const mok_muon_tensor* tensors, const mok_muon_config* config,

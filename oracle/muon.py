@@ -1,8 +1,8 @@
 """Muon in fp64, and with the roundings that a kernel makes.
 
 `orthogonalize` is the definition. `rounded` does the same steps with X, A = X X^T and B = b A + c A A
-rounded to fp16 where they are operands, sums exact: how far it is from the definition is what those
-roundings cost.
+rounded to fp16 where they are operands, but for A's and B's diagonals, sums exact: how far it is from the definition is
+what those roundings cost. Matrices of up to 32 rows or columns are not rounded.
 """
 from __future__ import annotations
 
@@ -36,9 +36,17 @@ def _nineteen(x):
     return h + np.clip(np.rint((x - h) / place * 256), -128, 127) / 256 * place
 
 
+def _half_beside(x):
+    """fp16, but on the diagonal."""
+    d = np.diag(np.diag(x))
+    return _half(x - d) + d
+
+
 def rounded(u, eps=1e-7, steps=5, coefficients=None, small=False):
-    """`small`: X kept in fp32 and B formed from A before its rounding; else X kept in 19 bits."""
+    """`small`: X kept in fp32; else in 19 bits."""
     u = np.asarray(u, np.float64)
+    if min(u.shape) <= 32:
+        return orthogonalize(u, eps, steps, coefficients)
     if u.shape[0] > u.shape[1]:
         return rounded(u.T, eps, steps, coefficients, small).T
     n, scale = u.shape[1], 1.0
@@ -48,9 +56,8 @@ def rounded(u, eps=1e-7, steps=5, coefficients=None, small=False):
     x = keep(u * (scale / (math.sqrt(float((u * u).sum())) + eps)))
     for a, b, c in coefficients or [JORDAN] * steps:
         h = _half(x)
-        g = h @ h.T / scale ** 2
-        g16 = _half(g)
-        x = keep(a * x + _half(b * (g if small else g16) + c * (g16 @ g16)) @ h)
+        g = _half_beside(h @ h.T / scale ** 2)
+        x = keep(a * x + _half_beside(b * g + c * (g @ g)) @ h)
     return x / scale
 
 

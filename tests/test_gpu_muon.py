@@ -343,3 +343,79 @@ def test_many_small_matrices():
         mok.mok_orthogonalize(mok.orthogonalize_plan([src[k].clone()], [alone]))
         x, far = allowed(host(src[k]))
         assert torch.equal(alone, out[k]) and np.linalg.norm(host(alone) - x) <= far + 2.0 ** -8 * np.linalg.norm(x)
+
+
+# (the call takes its coefficients in fp32)
+COEFFICIENTS = [tuple(float(F(c)) for c in om.JORDAN)] * 5
+THIN = [(1, 1), (1, 1024), (1025, 1), (2, 3), (5, 5), (7, 1024), (8, 1025), (9, 1000), (16, 512), (513, 16), (17, 31), (32, 32),
+        (256, 32), (32, 257), (20, 2360), (2360, 19), (31, 5001), (2, 65536), (65536, 32)]
+
+
+@pytest.mark.parametrize("kind", ["features", "low"])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("shape", THIN)
+def test_thin_matrices_element_by_element(shape, dtype, kind):
+    """Up to 32 rows or columns: the source is exact in fp64 and so are the steps (to 1e-12, errors of A growing by 3.44^2 in
+    each of five); what is rounded is the result, to fp32 and then by half a step of bf16, 2^-8, at most (2^-133 below 2^-126)."""
+    src = up(gradient(np.random.default_rng(sum(shape)), 2, *shape, kind=kind)).to(getattr(torch, dtype))
+    out = torch.zeros(src.shape, dtype=BF, device="cuda")
+    mok.mok_orthogonalize(mok.orthogonalize_plan([src], [out]))
+    for s, o in zip(host(src), host(out)):
+        x = om.orthogonalize(s, coefficients=COEFFICIENTS)
+        assert (np.abs(o - x) <= (2.0 ** -8 + 2.0 ** -23) * np.abs(x) + 1e-9 * np.abs(x).max()).all()
+
+
+@pytest.mark.parametrize("shape", [(3, 5), (24, 300), (300, 24), (32, 700), (3000, 7)])
+def test_thin_update(shape):
+    """Momentum and gradient that make u without a rounding (multiples of 2^-12 below 1, momentum 1/2): the update has those of
+    the rate, the result, the decay factor and two products and a sum, each 2^-24 of what it rounds."""
+    rng = np.random.default_rng(shape[0])
+    g, m = (np.rint(rng.uniform(-1, 1, shape) * 4096) / 4096 for _ in range(2))
+    p = rng.standard_normal(shape)
+    tp, tg, tm = up(p), up(g), up(m)
+    p = host(tp)
+    mok.mok_muon(mok.muon_plan([tp], [tg], [tm]), lr=0.01, momentum=0.5, weight_decay=0.1, adjust="spectral")
+    want, mw, _ = om.step(p, g, m, 0.01, momentum=0.5, weight_decay=0.1, adjust="spectral", coefficients=COEFFICIENTS)
+    assert np.array_equal(host(tm), mw)
+    assert (np.abs(host(tp) - want) <= 4 * 2.0 ** -24 * (np.abs(p) + np.abs(want - p * (1 - 0.001))) + 1e-11).all()
+
+
+def test_thin_zero_and_not_finite():
+    for shape in ((4, 6), (5, 3000)):
+        src = torch.randn(3, *shape, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1))
+        src[0] = 0
+        src[1, 2, 1] = float("inf")
+        out = torch.full(src.shape, -7.0, dtype=BF, device="cuda")
+        mok.mok_orthogonalize(mok.orthogonalize_plan([src], [out]))
+        assert (out[0] == 0).all() and out[1].isnan().all() and out[2].isfinite().all()
+
+
+def test_thin_and_others_in_one_graph():
+    """Small, long thin and large matrices of one call, captured and replayed."""
+    shapes = [(2, 6, 40), (1, 30, 3000), (2, 300, 260), (1, 100, 90), (1, 2000, 3)]
+    a, b = Case(shapes, seed=8), Case(shapes, seed=8)
+    mok.mok_muon(b.plan, lr=1e-3)
+    graph = torch.cuda.CUDAGraph()
+    mine = Case(shapes, seed=9)
+    mok.mok_muon(mine.plan, lr=1e-3)
+    with torch.cuda.graph(graph):
+        mok.mok_muon(a.plan, lr=1e-3)
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(a.p + a.m + a.c, b.p + b.m + b.c):
+            assert torch.equal(x, y)
+        for x in a.g + b.g:
+            x.mul_(0.75)
+        mok.mok_muon(b.plan, lr=1e-3)
+        torch.cuda.synchronize()
+
+
+def test_matrices_of_a_few_more_rows_than_thin():
+    """33 to 64 rows, in one workgroup or the general kernels."""
+    for shape in ((33, 40), (33, 257), (40, 700), (700, 40), (33, 5000), (64, 64)):
+        src = up(gradient(np.random.default_rng(3), *shape))
+        out = torch.zeros(shape, dtype=BF, device="cuda")
+        mok.mok_orthogonalize(mok.orthogonalize_plan([src], [out]))
+        x, far = allowed(host(src))
+        assert np.linalg.norm(host(out) - x) <= far + 2.0 ** -8 * np.linalg.norm(x)
