@@ -14,6 +14,12 @@
 // their size, a hundredth of a bf16 result's rounding. fp32 results (the weight gradient among them) are wanted better:
 // there the codes are widened to fp16, which holds all of them, and multiplied at half the rate with sums as good as
 // fp32.
+//
+// Measured: 16,384 rows of 4 experts, 4096 x 7168, bf16: 497 us, 1.94 PFLOP/s, the matrix cores busy in 58 % of the cycles of a
+// clock that falls to 1.6 GHz (one 256 x 256 tile a CU; without the next product beside an addition 872 us). Weight gradient of
+// 4 experts of 7168 x 2048 over them: 490 to 610 us by the card, 0.8 to 1.0 PFLOP/s in fp16, 51 % (128 x 128, two on a CU;
+// 256 x 128 and products one ahead were equal or slower). 44 rows of 6 experts, 7168 x 2048: 19 us, 74 MB at 3.9 TB/s; one row
+// of 4096 x 7168: 7.2 us, 29 MB at 4.1 TB/s, launch included.
 #include <algorithm>
 #include <cmath>
 
@@ -203,7 +209,7 @@ __global__ __launch_bounds__(S::kWaves * 64, 2) void k_block_product(ProductArgs
   const float *as, *bs;
   if constexpr (GRAD) {
     // Every XCD takes an eighth of each group's tiles, which follow one another: groups differ in length, and with whole
-    // groups to an XCD the one with the longest would be the last (uneven groups: 694 us instead of 590).
+    // groups to an XCD the one with the longest would be the last (4 uneven groups, 7168 x 2048: 694 us instead of 608).
     const int per = p.tiles_n * p.tiles_k, run = (per + kXcds - 1) / kXcds, in = blockIdx.x / kXcds;
     const int g = in / run, t = blockIdx.x % kXcds * run + in % run;
     if (t >= per) return;

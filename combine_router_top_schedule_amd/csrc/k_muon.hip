@@ -15,6 +15,11 @@
 // diagonals hold most of them where singular values are alike: they are kept apart in fp32 (fp16 holds zeros), and their parts
 // of the products added to the sums, with the same fp16 as the products take: so a direction that A lacks stays one in A A
 // and B X. Random matrices are off by 1e-3 so, by 2e-3 to 4e-3 without. On the matrix cores fp16 is as fast as bf16.
+//
+// Measured, 12 matrices of 2048 x 7168 and a small one, 5 steps, 8.64 ms: X X^T 410 us (880 TFLOP/s on the half that is
+// computed; 433 tiles of 256 x 256 on 256 CUs make two rounds, the second 69 % full), A A 133 us, B X 985 us (730 TFLOP/s; 600 us
+// of it the products, the rest X in and out, 2.6 GB through HBM), once a call the norm 447 us and X_0 537 us, both at 4.7 TB/s.
+// 256 x 256 tiles have one workgroup a CU, 128 x 128 two: B X takes 1,256 us so, but calls with under 256 large tiles less.
 #include <algorithm>
 #include <cmath>
 
@@ -359,7 +364,8 @@ __global__ __launch_bounds__(256) void k_muon_start(MuArgs a) {
 // two neighbouring columns, and a row of 32 lanes is a whole cache line of fp16. Block i of the first takes rows
 // q 8 FA + h 4 FA + 4 i + u (lane l = 8 q + 4 h + u), so a lane's FA blocks are runs of 4 FA rows, whole 16 bytes of the
 // transpose. In LDS a wave's share lies block by block, so that lanes read rows that follow one another: the loads that fill it
-// take the rows in that order (in the matrix's order, lanes two rows apart halve the reads' rate: 425 us instead of 410 for 12 of 2048 x 7168).
+// take the rows in that order (in the matrix's order, lanes two rows apart halve the reads' rate: X X^T of 12 matrices of 2048 x
+// 7168 took 425 us instead of 410).
 template <int WA_, int WB_, int FA_>
 struct MuShape {
   static constexpr int WA = WA_, WB = WB_, FA = FA_, FB = 2;
