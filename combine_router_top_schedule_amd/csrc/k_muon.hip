@@ -1380,10 +1380,13 @@ MuSize size_of(const mok_muon_tensor& t) {
   return ThinShape(t.rows, t.cols).thin() ? MuSize::Thin : MuSize::General;
 }
 
-// (small ones need none; counted as 512 bytes, a run has at most 2^22 of them, a workgroup each)
+// (A launch has fewer than 2^32 threads. Small ones need none; counted as 512 bytes, a run has at most 2^22 of them, a
+// workgroup each. Long thin ones are counted as 256 bytes a chunk at least: 2^23 workgroups of 256 threads.)
 int64_t matrix_bytes(const mok_muon_tensor& t, MuSize size) {
   if (size == MuSize::Small) return 512;
-  return align_up(size == MuSize::Thin ? ThinShape(t.rows, t.cols).bytes() : MuBuffers(t.rows, t.cols).bytes(), 256);
+  if (size == MuSize::General) return align_up(MuBuffers(t.rows, t.cols).bytes(), 256);
+  const ThinShape sh(t.rows, t.cols);
+  return std::max<int64_t>(align_up(sh.bytes(), 256), sh.chunks * int64_t(256));
 }
 
 // Calls go(parts, count, bytes) for each run of the tensors of a size; stops at an error.
