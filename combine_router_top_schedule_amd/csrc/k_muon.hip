@@ -156,7 +156,7 @@ __global__ __launch_bounds__(256) void k_muon_norm(MuArgs a) {
   const float clip = clip_factor(a);
   const bool bf = a.gbf;
   double sum = 0;
-  const auto one = [&](int64_t i, float g, float m) {
+  const auto one = [&](float g, float m) {
     g *= clip;
     float u = g;
     if (it.m) {
@@ -178,12 +178,12 @@ __global__ __launch_bounds__(256) void k_muon_norm(MuArgs a) {
       }
       if (it.m) m = *reinterpret_cast<const f32x4*>(it.m + i);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) m[j] = one(i + j, g[j], m[j]);
+      for (int j = 0; j < 4; ++j) m[j] = one(g[j], m[j]);
       if (it.m) *reinterpret_cast<f32x4*>(it.m + i) = m;
     } else {
       for (int j = 0; j < 4; ++j)
         if (i + j >= i0 && i + j < i1) {
-          const float m = one(i + j, element(it.g, bf, i + j), it.m ? it.m[i + j] : 0.f);
+          const float m = one(element(it.g, bf, i + j), it.m ? it.m[i + j] : 0.f);
           if (it.m) it.m[i + j] = m;
         }
     }
@@ -1042,18 +1042,32 @@ struct SmallShape {
 constexpr int small_long(int shorter) { return 256 * (4 / shorter); }
 constexpr int small_lds(int shorter) { return (2 * 32 * shorter * small_long(shorter) + 1024 * shorter * shorter) * 2; }
 
-// Element (row, col) of a matrix in LDS whose rows have `len` halves (a multiple of 32): 16-byte chunks are swapped
-// within runs of 8 (4 where rows are no multiple of 8 chunks) by the row, so that 32 rows of one chunk spread over the banks.
-__device__ __forceinline__ int small_at(int row, int col, int len) {
-  const int mask = len & 63 ? 3 : 7;
-  return row * len + (((col >> 3) ^ (row & mask)) << 3) + (col & 7);
+// Element (row, col) of a matrix in LDS whose rows have `len` halves (128, 256, 512; 64; 96): 16-byte chunks are swapped by
+// the row so that 16 rows of one chunk, which the LDS serves in a cycle, lie in different banks (rows of 256 bytes begin in the same
+// one, those of 128 in every other, of 192 in every fourth).
+__device__ __forceinline__ int small_turn(int row, int len) {
+  return len % 128 == 0 ? row & 15 : len == 64 ? (row & 7) ^ (row >> 3 & 1) : row >> 2 & 3;
 }
+__device__ __forceinline__ int small_at(int row, int col, int len) {
+  return row * len + (((col >> 3) ^ small_turn(row, len)) << 3) + (col & 7);
+}
+// The same for a lane's elements of a 32 x 32 block of results: rows row + 8 v + u (row: a multiple of 4) of one column. What a
+// row adds to an address is a multiple of what turns in it, so one exclusive or and a constant make an element's from the first.
+template <int LEN>
+struct SmallColumn {
+  uint8_t* x;
+  int first;
+  __device__ __forceinline__ SmallColumn(_Float16* m, int row, int col)
+      : x(reinterpret_cast<uint8_t*>(m)), first((row * LEN + col) * 2 ^ small_turn(row, LEN) << 4) {}
+  __device__ __forceinline__ _Float16& operator()(int v, int u) const {
+    return *reinterpret_cast<_Float16*>(x + (first ^ small_turn(8 * v + u, LEN) << 4) + (8 * v + u) * LEN * 2);
+  }
+};
 // A lane's part of a row as an operand: chunk c of it.
 struct SmallRow {
   const _Float16* p;
   int turn;
-  __device__ __forceinline__ SmallRow(const _Float16* x, int row, int len)
-      : p(x + row * len), turn(row & (len & 63 ? 3 : 7)) {}
+  __device__ __forceinline__ SmallRow(const _Float16* x, int row, int len) : p(x + row * len), turn(small_turn(row, len)) {}
   __device__ __forceinline__ f16x8 operator()(int c) const { return *reinterpret_cast<const f16x8*>(p + ((c ^ turn) << 3)); }
 };
 
@@ -1158,10 +1172,11 @@ __device__ __forceinline__ void muon_small(const MuArgs& a, const MuSteps& st, c
     const int tid = tile_tid(), h = (tid >> 5) & 1, c = tid & 31;
 #pragma unroll
     for (int q = 0; q < G; ++q)
-      if (glive[q])
+      if (glive[q]) {
+        const SmallColumn<kShort> column(gram, gr[q] + 4 * h, gc[q] + c);
 #pragma unroll
-        for (int v = 0; v < 16; ++v)
-          gram[small_at(gr[q] + 8 * (v >> 2) + 4 * h + (v & 3), gc[q] + c, kShort)] = to_half(g[q][v]);
+        for (int v = 0; v < 16; ++v) column(v >> 2, v & 3) = to_half(g[q][v]);
+      }
   };
   _Float16 *across_rows = TURN ? xt : xs, *along_rows = TURN ? xs : xt;   // rows of n, and of m halves
   // A's and B's diagonals, in place of the former once A is made
@@ -1201,18 +1216,19 @@ __device__ __forceinline__ void muon_small(const MuArgs& a, const MuSteps& st, c
       const int tid = tile_tid(), h = (tid >> 5) & 1, c = tid & 31;
 #pragma unroll
       for (int q = 0; q < N; ++q)
-        if (live[q])
+        if (live[q]) {
+          const SmallColumn<TURN ? kShort : kLong> column(xs, rq(q) + 4 * h, cq(q) + c);
+          // (rows of xt are columns of xs: four runs of 4 elements, a chunk apart)
+          uint8_t* turned = reinterpret_cast<uint8_t*>(xt);
+          const int first = small_at(cq(q) + c, rq(q) + 4 * h, TURN ? kLong : kShort) * 2;
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
-            const int r = rq(q) + 8 * v + 4 * h;
             f16x4 y;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              y[u] = to_half(x[q][4 * v + u]);
-              xs[small_at(r + u, cq(q) + c, TURN ? kShort : kLong)] = y[u];
-            }
-            *reinterpret_cast<f16x4*>(xt + small_at(cq(q) + c, r, TURN ? kLong : kShort)) = y;
+            for (int u = 0; u < 4; ++u) column(v, u) = y[u] = to_half(x[q][4 * v + u]);
+            *reinterpret_cast<f16x4*>(turned + (first ^ v << 4)) = y;
           }
+        }
     }
     __syncthreads();
     // A, then B in its place: the wave's blocks w and w + 8 of SHORTER x SHORTER
