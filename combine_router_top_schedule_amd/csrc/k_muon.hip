@@ -1022,7 +1022,8 @@ __global__ __launch_bounds__(256) void k_thin_apply(MuArgs a) {
 // ---- small matrices -----------------------------------------------------------------------------
 // A matrix whose X and X^T in fp16 fit the LDS beside A takes one workgroup and one launch for everything: X stays in
 // registers in fp32, its fp16 copies, A and then B in LDS. Launches and the way through memory bound the general kernels at
-// such sizes (25 matrices of 256 x 128 and less: 222 us in 17 launches, 62 us here).
+// such sizes (25 matrices of 256 x 128 and less: 222 us in 17 launches, 56 us here).
+// Vector instructions bound it (60 % of the cycles of 8 waves): conversions, addresses, and the diagonals' parts.
 //
 // X is cut into 32 x 32 blocks, 2..4 along its shorter side and up to 16 along the longer one. Wave w takes the
 // longer side's blocks w, w + 8, ..., for each of them all of the shorter side's: four slots at most, which share the
