@@ -968,9 +968,12 @@ def mok_block_gemm(x, x_scales, w, w_scales, out, offsets=None, stream=None):
             off, out.data_ptr())
 
 
-def mok_block_wgrad(dy_t, dy_scales, x_t, x_scales, dw, offsets=None, accumulate: bool = False, stream=None):
+def mok_block_wgrad(dy_t, dy_scales, x_t, x_scales, dw, offsets=None, accumulate: bool = False, stream=None,
+                    rows: Optional[int] = None):
     """dw [G][N][K] (float32, contiguous) = dy^T x by groups of rows, or added to with `accumulate`, from the column codes
-    and scales (mok_block_quantize) of dy [R][N] and x [R][K]."""
+    and scales (mok_block_quantize) of dy [R][N] and x [R][K]. rows: R, to which offsets are clamped as they were in
+    mok_block_quantize. Without it they must not go past R: the codes' width tells R only to 127 rows, and a group made
+    longer than it was would take columns that were never written."""
     _tch()
     dev = _device_of(dw)
     if dw.dim() != 3:
@@ -980,9 +983,10 @@ def mok_block_wgrad(dy_t, dy_scales, x_t, x_scales, dw, offsets=None, accumulate
     if groups != G:
         raise ValueError(f"dw has {G} groups, offsets {groups}")
     P = dy_t.shape[1] if dy_t.dim() == 2 else -1
-    R = P + 127 - 127 * G   # the most rows that need P columns: a bound for the offsets as good as R itself
-    if P < 0 or P % 128 or R < 0:
-        raise ValueError(f"dy_t must be [{N}][block_padded_rows(rows, {G})], not {tuple(dy_t.shape)}")
+    R = P + 127 - 127 * G if rows is None else rows   # (the most rows that need P columns)
+    if P < 0 or P % 128 or R < 0 or (R + 127 * G) // 128 * 128 != P:
+        raise ValueError(f"dy_t must be [{N}][block_padded_rows({'rows' if rows is None else rows}, {G})], "
+                         f"not {tuple(dy_t.shape)}")
     _launch("mok_block_wgrad", dev, stream, ctypes.byref(MokBlockDesc(R, 0, G, N, K, MOK_ELEM_F32)),
             _shaped(dy_t, "dy_t", (N, P), dev, True), _shaped(dy_scales, "dy_scales", (P // 128, N), dev, False),
             _shaped(x_t, "x_t", (K, P), dev, True), _shaped(x_scales, "x_scales", (P // 128, K), dev, False), off,

@@ -53,4 +53,5 @@ class MokBlockLinear:
         if dx is not None:
             mok_block_gemm(self.yq, self.ys, self.wt, self.wts, dx, offsets=offsets)
         if dw is not None:
-            mok_block_wgrad(self.yt, self.yts, self.xt, self.xts, dw, offsets=offsets, accumulate=accumulate)
+            mok_block_wgrad(self.yt, self.yts, self.xt, self.xts, dw, offsets=offsets, accumulate=accumulate,
+                            rows=self.rows)
