@@ -983,7 +983,8 @@ def mok_block_wgrad(dy_t, dy_scales, x_t, x_scales, dw, offsets=None, accumulate
     if groups != G:
         raise ValueError(f"dw has {G} groups, offsets {groups}")
     P = dy_t.shape[1] if dy_t.dim() == 2 else -1
-    R = P + 127 - 127 * G if rows is None else rows   # (the most rows that need P columns)
+    # (the most rows that need P columns, of the 2^22 that column codes have at most)
+    R = min(P + 127 - 127 * G, 1 << 22) if rows is None else rows
     if P < 0 or P % 128 or R < 0 or (R + 127 * G) // 128 * 128 != P:
         raise ValueError(f"dy_t must be [{N}][block_padded_rows({'rows' if rows is None else rows}, {G})], "
                          f"not {tuple(dy_t.shape)}")
