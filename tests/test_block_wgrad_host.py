@@ -15,8 +15,8 @@ def rows_of(monkeypatch):
     seen = []
     monkeypatch.setattr(mok, "_launch", lambda fn, dev, stream, desc, *a: seen.append(desc._obj.rows))
 
-    def call(rows, groups, **kw):
-        P = mok.block_padded_rows(rows, groups)
+    def call(held, groups, **kw):
+        P = mok.block_padded_rows(held, groups)
         c, s = torch.empty(1, P, dtype=torch.uint8), torch.empty(P // 128, 1)
         mok.mok_block_wgrad(c, s, c, s, torch.empty(groups, 1, 1), offsets=torch.zeros(groups + 1, dtype=torch.int32), **kw)
         return seen.pop()
