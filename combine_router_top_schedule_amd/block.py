@@ -9,6 +9,11 @@ from . import (_up128, block_padded_rows, mok_block_gemm, mok_block_quantize, mo
                mok_block_wgrad)
 
 
+def _shape(t, name: str, *shape: int):
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {shape}, not {tuple(t.shape)}")
+
+
 class MokBlockLinear:
     """y[r] = x[r] w[g]^T for the rows r of every group (expert) g, weights w [G][N][K] float32 or bfloat16 kept by
     the caller. Rows [rows] are sorted by group, offsets int32 [G + 1] on the device as in a schedule table. With
@@ -31,12 +36,22 @@ class MokBlockLinear:
             self.yt, self.yts = u8(N, P), f32(pb, N)
         self.refresh_weights()
 
+    def _check_rows(self, t, name: str, columns: int, offsets):
+        """Codes round widths up to 128, so the library's calls take some other widths for these."""
+        _shape(t, name, self.rows, columns)
+        if offsets is not None:
+            _shape(offsets, "offsets", self.w.shape[0] + 1)
+        elif self.w.shape[0] > 1:
+            raise ValueError(f"offsets of {self.w.shape[0]} groups are needed")
+
     def refresh_weights(self):
         """After an update of w in place (an optimizer step): quantises it again."""
         mok_block_quantize_weights(self.w, self.wq, self.ws, codes_t=self.wt, scales_t=self.wts)
 
     def forward(self, x, out, offsets=None):
         """out [rows][N] = x [rows][K] w^T (each float32 or bfloat16); rows in no group are left as they are."""
+        self._check_rows(x, "x", self.w.shape[2], offsets)
+        _shape(out, "out", self.rows, self.w.shape[1])
         mok_block_quantize(x, self.xq, self.xs, codes_t=self.xt, scales_t=self.xts, offsets=offsets)
         mok_block_gemm(self.xq, self.xs, self.wq, self.ws, out, offsets=offsets)
 
@@ -45,6 +60,11 @@ class MokBlockLinear:
         [G][N][K] float32 = dy^T x (None: not wanted), or added to."""
         if not self.train:
             raise RuntimeError("the map was made without train")
+        self._check_rows(dy, "dy", self.w.shape[1], offsets)
+        if dx is not None:
+            _shape(dx, "dx", self.rows, self.w.shape[2])
+        if dw is not None:
+            _shape(dw, "dw", *self.w.shape)
         cols = (self.yt, self.yts) if dw is not None else (None, None)
         rows = (self.yq, self.ys) if dx is not None else (None, None)
         if dx is None and dw is None:
