@@ -118,6 +118,10 @@ __host__ __device__ inline float mu_scale(int rows, int cols) {
   return float(1 << e);
 }
 
+// What u is multiplied by before it is divided by `size` = |u| + eps, whose reciprocal is beyond fp32 below some 2^-120: a
+// power of two, so nothing is rounded, and nothing overflows as no element of u is larger than `size`.
+__device__ __forceinline__ float mu_lift(double size) { return size < 0x1p-100 ? 0x1p100f : 1.f; }
+
 // The item of workgroup c.
 __device__ __forceinline__ int find_item(const MuArgs& a, int c) {
   const int lane = threadIdx.x & 63;
@@ -323,7 +327,7 @@ __global__ __launch_bounds__(256) void k_muon_start(MuArgs a) {
   if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = sum;
   __syncthreads();
   const double norm = sqrt(s[0] + s[1] + s[2] + s[3]) + a.eps;
-  const float clip = clip_factor(a), f = float(double(mu_scale(it.rows, it.cols)) / norm);
+  const float clip = clip_factor(a), lift = mu_lift(norm), f = float(double(mu_scale(it.rows, it.cols)) / (norm * lift));
   __shared__ _Float16 tile[64][66];
   const bool turn = b.turned(it);
   _Float16 *hs = b.s(ws, turn, 0), *ht = b.t(ws, turn, 0);
@@ -344,7 +348,7 @@ __global__ __launch_bounds__(256) void k_muon_start(MuArgs a) {
     const int r = wv + 4 * k;
     float u = g[k] * clip;
     if (it.m) u = a.nesterov ? fmaf(a.mu, m[k], u) : m[k];
-    const float x = u * f;
+    const float x = u * lift * f;
     const _Float16 h = to_half(x);
     const int64_t at = int64_t(r0 + r) * b.cols + c0 + c;
     hs[at] = h;
@@ -1152,11 +1156,12 @@ __device__ __forceinline__ void muon_small(const MuArgs& a, const MuSteps& st, c
   __syncthreads();
   double norm = 0;
   for (int k = 0; k < 8; ++k) norm += sums[k];
-  const float f = float(double(scale) / (sqrt(norm) + a.eps));
+  norm = sqrt(norm) + a.eps;
+  const float lift = mu_lift(norm), f = float(double(scale) / (norm * lift));
 #pragma unroll
   for (int q = 0; q < N; ++q)
 #pragma unroll
-    for (int v = 0; v < 16; ++v) x[q][v] *= f;
+    for (int v = 0; v < 16; ++v) x[q][v] = x[q][v] * lift * f;
   // A's blocks of the wave, 32 x 32 of SHORTER x SHORTER: number w, and of those from 8 on one in the same column.
   constexpr int G = SHORTER > 2 ? 2 : 1;
   int gr[G], gc[G];
