@@ -60,6 +60,7 @@ MOK_SCORE_SOFTMAX, MOK_SCORE_SIGMOID = 0, 1
 MOK_GROUP_MAX, MOK_GROUP_TOP2 = 0, 1
 MOK_STATE_F32, MOK_STATE_MX8 = 0, 1
 MOK_ADJUST_RMS, MOK_ADJUST_SPECTRAL, MOK_ADJUST_NONE = 0, 1, 2
+MOK_BLOCK_FEW_ROWS, MOK_BLOCK_TILES_128, MOK_BLOCK_TILES_256 = 0, 1, 2
 
 
 class MokRouteDesc(ctypes.Structure):
@@ -182,6 +183,7 @@ _SIGS = {
     "mok_block_quantize": (ctypes.c_int, [ctypes.POINTER(MokBlockDesc), _P, _P, _P, _P, _P, _P, _P]),
     "mok_block_quantize_weights": (ctypes.c_int, [ctypes.POINTER(MokBlockDesc), _P, _P, _P, _P, _P, _P]),
     "mok_block_gemm": (ctypes.c_int, [ctypes.POINTER(MokBlockDesc), _P, _P, _P, _P, _P, _P, _P]),
+    "mok_block_gemm_kernel": (ctypes.c_int32, [ctypes.POINTER(MokBlockDesc)]),
     "mok_block_wgrad": (ctypes.c_int, [ctypes.POINTER(MokBlockDesc), _P, _P, _P, _P, _P, _P, ctypes.c_int32, _P]),
     "mok_device_cus": (ctypes.c_int32, []),
     "mok_trace_kernel": (ctypes.c_int, [ctypes.c_int32, _P, _P]),

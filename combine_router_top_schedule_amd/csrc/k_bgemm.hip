@@ -577,6 +577,16 @@ double tiles_us(const mok_block_desc& d, int per_cu, double alone, double beside
 
 }  // namespace
 
+mok_block_kernel block_gemm_kernel(const mok_block_desc& d) {
+  const bool bf = d.elem == MOK_ELEM_BF16;
+  const int64_t few_ft = few_tokens(d);
+  const double few = few_us(d, few_ft), mid = tiles_us<Mid>(d, 2, bf ? 0.77 : 1.1, bf ? 1.1 : 1.5, 3.0),
+               wide = bf ? tiles_us<Wide>(d, 1, 1.7, 1.7, 10.0) : INFINITY;
+  if (few <= mid && few <= wide && group_tiles_max(d.rows, d.groups, int(16 * few_ft)) * cdiv(d.n, 16) < kMaxFewTiles)
+    return MOK_BLOCK_FEW_ROWS;
+  return mid <= wide ? MOK_BLOCK_TILES_128 : MOK_BLOCK_TILES_256;
+}
+
 hipError_t launch_block_gemm(const mok_block_desc& d, const uint8_t* x, const float* xs, const uint8_t* w,
                              const float* ws, const int32_t* offsets, void* out, hipStream_t s) {
   if (d.rows == 0) return hipSuccess;
@@ -593,15 +603,14 @@ hipError_t launch_block_gemm(const mok_block_desc& d, const uint8_t* x, const fl
   p.n = d.n;
   p.k = d.k;
   p.bf16 = d.elem == MOK_ELEM_BF16;
-  const int64_t few_ft = few_tokens(d);
-  const double few = few_us(d, few_ft), mid = tiles_us<Mid>(d, 2, p.bf16 ? 0.77 : 1.1, p.bf16 ? 1.1 : 1.5, 3.0),
-               wide = p.bf16 ? tiles_us<Wide>(d, 1, 1.7, 1.7, 10.0) : INFINITY;
-  if (few <= mid && few <= wide && group_tiles_max(d.rows, d.groups, int(16 * few_ft)) * cdiv(d.n, 16) < kMaxFewTiles) {
-    if (few_ft == 1) return launch_few_n<1>(p, s);
-    return few_ft == 2 ? launch_few_n<2>(p, s) : launch_few_n<4>(p, s);
+  switch (block_gemm_kernel(d)) {
+    case MOK_BLOCK_FEW_ROWS: {
+      const int64_t ft = few_tokens(d);
+      return ft == 1 ? launch_few_n<1>(p, s) : ft == 2 ? launch_few_n<2>(p, s) : launch_few_n<4>(p, s);
+    }
+    case MOK_BLOCK_TILES_128: return p.bf16 ? launch_tiles<Mid, false>(p, s) : launch_tiles<Mid, true>(p, s);
+    default: return launch_tiles<Wide, false>(p, s);
   }
-  if (!p.bf16) return launch_tiles<Mid, true>(p, s);
-  return mid <= wide ? launch_tiles<Mid, false>(p, s) : launch_tiles<Wide, false>(p, s);
 }
 
 hipError_t launch_block_wgrad(const mok_block_desc& d, const uint8_t* dy, const float* dys, const uint8_t* x,

@@ -21,11 +21,15 @@ bool width_ok(int32_t v) { return v >= 1 && v <= kMaxWidth; }
 bool elem_ok(int32_t e) { return e == MOK_ELEM_F32 || e == MOK_ELEM_BF16; }
 uintptr_t elem_size(int32_t e) { return e == MOK_ELEM_BF16 ? 2 : 4; }
 
+bool rows_ok(const mok_block_desc& d, bool columns) {
+  return d.rows >= 0 && d.rows <= (columns ? kMaxColumnRows : kMaxRows) && d.groups >= 1 && d.groups <= 1024 &&
+         width_ok(d.k);
+}
+
 // Rows, groups and offsets, common to all calls on rows.
 mok_status check_rows(const mok_block_desc* d, const int32_t* offsets, bool columns) {
   if (!d) return MOK_ERR_NULL;
-  if (d->rows < 0 || d->rows > (columns ? kMaxColumnRows : kMaxRows)) return MOK_ERR_SHAPE;
-  if (d->groups < 1 || d->groups > 1024 || !width_ok(d->k)) return MOK_ERR_SHAPE;
+  if (!rows_ok(*d, columns)) return MOK_ERR_SHAPE;
   if (!offsets && d->groups != 1) return MOK_ERR_NULL;
   return aligned(offsets, 4) ? MOK_OK : MOK_ERR_ALIGN;
 }
@@ -89,6 +93,11 @@ mok_status mok_block_gemm(const mok_block_desc* desc, const uint8_t* x_dev, cons
   if ((desc->rows / 128 + desc->groups) * cdiv(desc->n, 128) > kMaxTiles) return MOK_ERR_SHAPE;
   return hip_status(launch_block_gemm(*desc, x_dev, x_scales_dev, w_dev, w_scales_dev, offsets_dev, out_dev,
                                       static_cast<hipStream_t>(stream)));
+}
+
+int32_t mok_block_gemm_kernel(const mok_block_desc* desc) {
+  if (!desc || !rows_ok(*desc, false) || !width_ok(desc->n) || !elem_ok(desc->elem)) return -1;
+  return block_gemm_kernel(*desc);
 }
 
 mok_status mok_block_wgrad(const mok_block_desc* desc, const uint8_t* dy_t_dev, const float* dy_scales_dev,

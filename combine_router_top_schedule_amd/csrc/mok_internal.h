@@ -470,6 +470,7 @@ hipError_t launch_block_quantize(const mok_block_desc& d, const void* x, const i
                                  float* scales, uint8_t* codes_t, float* scales_t, hipStream_t s);
 hipError_t launch_block_quantize_weights(const mok_block_desc& d, const void* w, uint8_t* codes, float* scales,
                                          uint8_t* codes_t, float* scales_t, hipStream_t s);
+mok_block_kernel block_gemm_kernel(const mok_block_desc& d);
 hipError_t launch_block_gemm(const mok_block_desc& d, const uint8_t* x, const float* xs, const uint8_t* w,
                              const float* ws, const int32_t* offsets, void* out, hipStream_t s);
 hipError_t launch_block_wgrad(const mok_block_desc& d, const uint8_t* dy, const float* dys, const uint8_t* x,

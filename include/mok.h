@@ -674,6 +674,11 @@ mok_status mok_block_gemm(const mok_block_desc* desc, const uint8_t* x_dev, cons
                           const uint8_t* w_dev, const float* w_scales_dev, const int32_t* offsets_dev, void* out_dev,
                           void* stream);
 
+/* The kernel that mok_block_gemm takes for these rows, groups, n, k and elem (the rest plays no part), as tests and
+ * measurements ask: the one whose estimated time is the least. -1 for a descriptor out of range. */
+typedef enum { MOK_BLOCK_FEW_ROWS = 0, MOK_BLOCK_TILES_128 = 1, MOK_BLOCK_TILES_256 = 2 } mok_block_kernel;
+int32_t mok_block_gemm_kernel(const mok_block_desc* desc);
+
 /* Weight gradient dw[g][n][k] = sum over the rows r of group g of dy[r][n] x[r][k], from column codes and scales of dy
  * [R][N] and x [R][K] (stride and elem unused). dw_dev fp32 [G][N][K], overwritten (zero for a group without rows), or
  * with accumulate added to. */
