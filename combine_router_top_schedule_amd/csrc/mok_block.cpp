@@ -17,6 +17,10 @@ constexpr int64_t kMaxColumnRows = int64_t(1) << 22;      // 256 rows of column 
 constexpr int32_t kMaxWidth = 1 << 20;
 constexpr int64_t kMaxTiles = (int64_t(1) << 22) - 1;     // workgroups of up to 512 threads in a launch
 
+// Tiles that the rows of d have at most.
+int64_t row_tiles(const mok_block_desc& d) { return d.rows / 128 + d.groups; }
+bool product_fits(const mok_block_desc& d) { return row_tiles(d) * cdiv(d.n, 128) <= kMaxTiles; }
+
 bool width_ok(int32_t v) { return v >= 1 && v <= kMaxWidth; }
 bool elem_ok(int32_t e) { return e == MOK_ELEM_F32 || e == MOK_ELEM_BF16; }
 uintptr_t elem_size(int32_t e) { return e == MOK_ELEM_BF16 ? 2 : 4; }
@@ -58,7 +62,7 @@ mok_status mok_block_quantize(const mok_block_desc* desc, const void* x_dev, con
   if (!aligned(x_dev, elem_size(desc->elem)) || !aligned(codes_dev, 16) || !aligned(codes_t_dev, 16) ||
       !aligned(scales_dev, 4) || !aligned(scales_t_dev, 4))
     return MOK_ERR_ALIGN;
-  if (codes_t_dev && (cdiv(desc->rows, 128) + desc->groups + 2) * cdiv(desc->k, 128) > kMaxTiles) return MOK_ERR_SHAPE;
+  if (codes_t_dev && (row_tiles(*desc) + 2) * cdiv(desc->k, 128) > kMaxTiles) return MOK_ERR_SHAPE;
   return hip_status(launch_block_quantize(*desc, x_dev, offsets_dev, codes_dev, scales_dev, codes_t_dev, scales_t_dev,
                                           static_cast<hipStream_t>(stream)));
 }
@@ -90,13 +94,13 @@ mok_status mok_block_gemm(const mok_block_desc* desc, const uint8_t* x_dev, cons
   if (!aligned(x_dev, 16) || !aligned(w_dev, 16) || !aligned(x_scales_dev, 4) || !aligned(w_scales_dev, 4) ||
       !aligned(out_dev, elem_size(desc->elem)))
     return MOK_ERR_ALIGN;
-  if ((desc->rows / 128 + desc->groups) * cdiv(desc->n, 128) > kMaxTiles) return MOK_ERR_SHAPE;
+  if (!product_fits(*desc)) return MOK_ERR_SHAPE;
   return hip_status(launch_block_gemm(*desc, x_dev, x_scales_dev, w_dev, w_scales_dev, offsets_dev, out_dev,
                                       static_cast<hipStream_t>(stream)));
 }
 
 int32_t mok_block_gemm_kernel(const mok_block_desc* desc) {
-  if (!desc || !rows_ok(*desc, false) || !width_ok(desc->n) || !elem_ok(desc->elem)) return -1;
+  if (!desc || !rows_ok(*desc, false) || !width_ok(desc->n) || !elem_ok(desc->elem) || !product_fits(*desc)) return -1;
   return block_gemm_kernel(*desc);
 }
 

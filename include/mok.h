@@ -641,7 +641,11 @@ mok_status mok_orthogonalize(int32_t num_tensors, const mok_orthogonalize_tensor
  *                  What lies behind the last group is neither written nor read.
  *   weight codes   uint8 [G][N][up(K)], zeros past K;    scales fp32 [G][up(N) / 128][up(K) / 128], blocks of 128 x 128
  *   transposed     the weight codes of [G][K][N]: same values, scales transposed
- * Codes are 16-byte aligned, scales and offsets 4-byte. */
+ * Codes are 16-byte aligned, scales and offsets 4-byte.
+ *
+ * A call takes fewer than 2^22 blocks of 128 x 128 (2^23 when weights are quantised), MOK_ERR_SHAPE above: of a product
+ * (R / 128 + G) up(N) / 128, of column codes (R / 128 + G + 2) up(K) / 128, of weights and of a weight gradient
+ * G up(N) / 128 up(K) / 128. */
 typedef struct {
   int64_t rows;      /* R; 0..2^27, and at most 2^22 where column codes are written or read             */
   int64_t stride;    /* elements from one row of the unquantised operand to the next; >= its columns    */
