@@ -56,7 +56,7 @@ class MokBlockLinear:
         mok_block_gemm(self.xq, self.xs, self.wq, self.ws, out, offsets=offsets)
 
     def backward(self, dy, dx=None, dw=None, offsets=None, accumulate: bool = False):
-        """Of the last forward: dx [rows][K] = dy w (None: not wanted; rows in no group are left as they are) and dw
+        """Of the last forward, with its offsets: dx [rows][K] = dy w (None: not wanted; rows in no group are left as they are) and dw
         [G][N][K] float32 = dy^T x (None: not wanted), or added to."""
         if not self.train:
             raise RuntimeError("the map was made without train")

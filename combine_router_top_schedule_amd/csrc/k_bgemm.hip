@@ -15,11 +15,12 @@
 // there the codes are widened to fp16, which holds all of them, and multiplied at half the rate with sums as good as
 // fp32.
 //
-// Measured: 16,384 rows of 4 experts, 4096 x 7168, bf16: 497 us, 1.94 PFLOP/s, the matrix cores busy in 58 % of the cycles of a
-// clock that falls to 1.6 GHz (one 256 x 256 tile a CU; without the next product beside an addition 872 us). Weight gradient of
-// 4 experts of 7168 x 2048 over them: 490 to 610 us by the card, 0.8 to 1.0 PFLOP/s in fp16, 51 % (128 x 128, two on a CU;
+// Measured: 16,384 rows of 4 uneven experts, 4096 x 7168, bf16: 497 us, 1.94 PFLOP/s, the matrix cores busy in 58 % of the cycles
+// of a clock that falls to 1.6 GHz (one 256 x 256 tile a CU, four rounds of them and a fifth of 32 tiles; equal experts, four full
+// rounds, took 405 us where uneven ones took 479; without the next product beside an addition 872 us). Weight gradient of
+// 4 experts of 7168 x 2048 over them: 475 to 610 us by the card, 0.8 to 1.0 PFLOP/s in fp16, 51 % (128 x 128, two on a CU;
 // 256 x 128 and products one ahead were equal or slower). 44 rows of 6 experts, 7168 x 2048: 19 us, 74 MB at 3.9 TB/s; one row
-// of 4096 x 7168: 7.2 us, 29 MB at 4.1 TB/s, launch included.
+// of 4096 x 7168: 7.2 us, 29 MB at 4.1 TB/s, launch included (20 and 9.3 us with weights that are in no cache).
 #include <algorithm>
 #include <cmath>
 
